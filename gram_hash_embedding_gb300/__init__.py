@@ -14,6 +14,9 @@ the lookup (:func:`engram_project`, :func:`engram_gate`,
 :func:`engram_lookup_project`, :func:`engram_lookup_project_gate`), and the
 row-sharded lookup's two ends (:func:`engram_shard_pack`,
 :func:`engram_shard_unpack`). :class:`EngramHash` bundles a state with them.
+Training the front end: :func:`engram_embed` (trainable rows) with its gradient
+:func:`engram_embed_grad` / :func:`engram_embed_grad_dense`,
+:func:`engram_gate_grad`, :func:`engram_grad_norm` and :func:`engram_grad_clip`.
 
 Method: the "DeepSeek V4.1" pages -- blocks/stack-hashes page (the n-gram hash
 ``forward``, ``Engram.forward``) and engram-first/lookup page
@@ -38,6 +41,9 @@ __all__ = [
     "engram_project_gate_workspace", "engram_device_status", "STATUS_TIMEOUT", "engram_shard_pack",
     "engram_shard_unpack", "shard_part", "sharded_lookup", "dist_exchange", "engram_lookup_project",
     "engram_lookup_project_workspace", "engram_lookup_project_gate", "engram_lookup_project_gate_workspace",
+    "engram_embed", "engram_embed_grad", "engram_embed_grad_dense", "engram_embed_grad_workspace", "engram_gate_grad",
+    "engram_gate_grad_workspace", "engram_grad_norm", "engram_grad_clip", "engram_grad_norm_workspace",
+    "TYPE_F32", "TYPE_BF16", "TYPE_F16", "NORM_L2", "NORM_MAX",
 ]
 
 OK, ERR_INVALID, ERR_RANGE, ERR_CUDA, ERR_NOMEM, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
@@ -53,6 +59,10 @@ _SCALE_BYTES = {SCALE_F32: 4, SCALE_BF16: 2, SCALE_E8M0: 1, SCALE_E4M3: 1}
 _SCALE_OF_DTYPE = {torch.float32: SCALE_F32, torch.bfloat16: SCALE_BF16, torch.float8_e4m3fn: SCALE_E4M3}
 if hasattr(torch, "float8_e8m0fnu"):
     _SCALE_OF_DTYPE[torch.float8_e8m0fnu] = SCALE_E8M0
+# value types of the training operators' tensors (ENGRAM_TYPE_*) and their norms (ENGRAM_NORM_*)
+TYPE_F32, TYPE_BF16, TYPE_F16 = 0, 1, 2
+_TYPE_OF_DTYPE = {torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16, torch.float16: TYPE_F16}
+NORM_L2, NORM_MAX = 2, 0
 MAX_LAYERS = 8
 
 
@@ -72,6 +82,12 @@ class _Layout(ctypes.Structure):
 class _Table(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("S", ctypes.c_void_p), ("rows", ctypes.c_int64),
                 ("head_dim", ctypes.c_int32), ("block", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("rows_used", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("row_len", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -119,6 +135,22 @@ def _lib():
         L.engram_shard_pack_workspace.restype = ctypes.c_uint64
         L.engram_shard_pack.argtypes = [_P, _I64, _I64, _I32, _P, _P, _P, _P, ctypes.c_uint64, _P]
         L.engram_shard_unpack.argtypes = [_P, _P, _I64, _I64, _I32, _P, _P]
+        _F = ctypes.c_float
+        L.engram_embed.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _I32, _I64, _I32, _F, _P, _I32, _P]
+        L.engram_embed_grad_workspace.argtypes = [_I64, _I64, _I32]
+        L.engram_embed_grad_workspace.restype = ctypes.c_uint64
+        L.engram_embed_grad.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _I32, _I64, _I32, _F, _P, _P, _I32, _P, _P,
+                                        ctypes.c_uint64, _P]
+        L.engram_embed_grad_dense.argtypes = [_P, _I64, _I64, _I32, _P, _I64, _I32, _I64, _I32, _F, _P, _I64, _I32,
+                                              _I32, _P, ctypes.c_uint64, _P]
+        L.engram_gate_grad_workspace.argtypes = [_I64, _I32, _I32]
+        L.engram_gate_grad_workspace.restype = ctypes.c_uint64
+        L.engram_gate_grad.argtypes = [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _F, _P, _P, _P, _P, _P,
+                                       ctypes.c_uint64, _P]
+        L.engram_grad_norm_workspace.argtypes = [_I32]
+        L.engram_grad_norm_workspace.restype = ctypes.c_uint64
+        L.engram_grad_norm.argtypes = [_P, _I32, _I32, _P, _P, ctypes.c_uint64, _P]
+        L.engram_grad_clip.argtypes = [_P, _I32, _I32, _F, _P, _P, ctypes.c_uint64, _P]
         L.engram_strerror.argtypes = [ctypes.c_int]
         L.engram_set_l2_fetch_granularity.argtypes = [_I32, ctypes.POINTER(_I32)]
         L.engram_strerror.restype = ctypes.c_char_p
@@ -126,7 +158,8 @@ def _lib():
                      "engram_hash", "engram_lookup", "engram_hash_lookup", "engram_state_layout",
                      "engram_hash_varlen", "engram_hash_lookup_varlen", "engram_gate", "engram_project",
                      "engram_project_gate", "engram_device_status", "engram_shard_pack", "engram_shard_unpack",
-                     "engram_lookup_project", "engram_lookup_project_gate"):
+                     "engram_lookup_project", "engram_lookup_project_gate", "engram_embed", "engram_embed_grad",
+                     "engram_embed_grad_dense", "engram_gate_grad", "engram_grad_norm", "engram_grad_clip"):
             getattr(L, name).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -732,6 +765,253 @@ def sharded_lookup(idx: torch.Tensor, W_shard: torch.Tensor, S_shard: torch.Tens
     found = lookup(wanted, W_shard, S_shard).reshape(-1, D)  # this shard's rows for them
     back = exchange(found, recv, send)                      # this rank's rows, in packed order
     return unpack(back, positions, m, D).reshape(tuple(idx.shape) + (D,))
+
+
+# ----------------------------------------------------------------------------- training operators
+def _float_type(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _TYPE_OF_DTYPE:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPE_OF_DTYPE[t.dtype]
+
+
+def _embed_ids(idx: torch.Tensor):
+    """Row ids of a lookup: int64 [T, C] with unit stride along C, or any contiguous shape (then one
+    column): (pointer, row stride, T, C)."""
+    if not isinstance(idx, torch.Tensor) or not idx.is_cuda or idx.dtype != torch.int64:
+        raise TypeError("idx must be an int64 CUDA tensor")
+    if idx.dim() == 2 and idx.shape[1] > 0 and not idx.is_contiguous():
+        return _hash_ids(idx)
+    if not idx.is_contiguous():
+        raise ValueError(f"idx must be contiguous, or [T, C] with unit stride along C, got strides {idx.stride()}")
+    return (idx.data_ptr(),) + ((idx.shape[1], *idx.shape) if idx.dim() == 2 and idx.shape[1] > 0
+                                else (1, idx.numel(), 1))
+
+
+def _rows_of(t: torch.Tensor, name: str):
+    """A table [rows, dim] with unit stride along dim: (pointer, rows, dim, row stride)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, dim] with unit stride along dim, got shape {tuple(t.shape)} "
+                         f"strides {t.stride()}")
+    rows, dim = t.shape
+    stride = t.stride(0) if rows > 1 else dim
+    if stride < dim:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), rows, dim, stride
+
+
+def engram_embed(idx: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """Rows of a trainable table: out[..., k] = scale * W[idx[...], k], +0 rows where idx is outside the
+    table. idx int64 [T, C] (unit stride along C, e.g. one layer of an engram_hash output) or any
+    contiguous shape; W float32, bfloat16 or float16 [rows, dim] (rows may be a stride apart).
+    Returns (or fills) idx.shape + (dim,) of out_dtype (W's dtype when neither out nor out_dtype is given)."""
+    wt = _float_type(W, "W")
+    wp, rows, dim, stride = _rows_of(W, "W")
+    ip, istride, T, C = _embed_ids(idx)
+    temps = []
+    if out is None:
+        out = torch.empty(tuple(idx.shape) + (dim,), dtype=out_dtype or W.dtype, device=idx.device)
+        temps.append(out)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    _size(out, T * C * dim, "out")
+    ot = _float_type(out, "out")
+    _check(_lib().engram_embed(ip, istride, T, C, wp, rows, dim, stride, wt, float(scale), _dev(out, out.dtype, "out"),
+                               ot, _launch_stream(stream, temps)), "engram_embed")
+    return out
+
+
+def engram_embed_grad_workspace(n: int, rows: int, dim: int) -> int:
+    """Bytes of workspace that engram_embed_grad and engram_embed_grad_dense need for n ids."""
+    return int(_lib().engram_embed_grad_workspace(int(n), int(rows), int(dim)))
+
+
+def _embed_dout(dout: torch.Tensor, T: int, C: int):
+    """The gradient of a lookup's output: contiguous, or [T, C * dim] / [T, C, dim] whose tokens are a
+    stride apart: (pointer, token stride, dim)."""
+    n = T * C
+    if dout.dim() == 0 or (n and dout.numel() % n):
+        raise ValueError(f"dout {tuple(dout.shape)} does not hold one row for each of {n} ids")
+    dim = dout.numel() // n if n else dout.shape[-1]
+    if dout.is_contiguous():
+        return dout.data_ptr(), C * dim, dim
+    inner = dout.dim() == 2 and dout.shape == (T, C * dim) and (dout.shape[1] == 1 or dout.stride(1) == 1)
+    inner = inner or (dout.dim() == 3 and dout.shape == (T, C, dim) and (dim == 1 or dout.stride(2) == 1)
+                      and (C == 1 or dout.stride(1) == dim))
+    if not inner or (T > 1 and dout.stride(0) < C * dim):
+        raise ValueError(f"dout must be contiguous, or [T, C, dim] with only its tokens a stride apart, got shape "
+                         f"{tuple(dout.shape)} strides {dout.stride()}")
+    return dout.data_ptr(), dout.stride(0) if T > 1 else C * dim, dim
+
+
+def engram_embed_grad(idx: torch.Tensor, dout: torch.Tensor, rows: int, scale: float = 1.0,
+                      grad_dtype: torch.dtype | None = None, grad_rows: torch.Tensor | None = None,
+                      grad: torch.Tensor | None = None, count: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of engram_embed for a table of `rows` rows, as the rows that occur. idx as in
+    engram_embed; dout: the gradient of its output, float32, bfloat16 or float16 (tokens may be a stride
+    apart). Returns (or fills) grad_rows int64 [n] (the distinct ids ascending, then -1), grad [n, dim]
+    (grad[u] belongs to grad_rows[u]; float32 unless given; rows from count on are not written) and count
+    int64 [1], n = idx.numel(). The sums are fp32 in an order fixed by the ids."""
+    ip, istride, T, C = _embed_ids(idx)
+    dt = _float_type(dout, "dout")
+    dp, dstride, dim = _embed_dout(dout, T, C)
+    n, dev, temps = T * C, idx.device, []
+    if grad_rows is None:
+        grad_rows = torch.empty(n, dtype=torch.int64, device=dev)
+        temps.append(grad_rows)
+    if grad is None:
+        grad = torch.empty((n, dim), dtype=grad_dtype or torch.float32, device=dev)
+        temps.append(grad)
+    elif grad_dtype is not None and grad.dtype != grad_dtype:
+        raise TypeError(f"grad is {grad.dtype}, not {grad_dtype}")
+    if count is None:
+        count = torch.empty(1, dtype=torch.int64, device=dev)
+        temps.append(count)
+    _size(grad_rows, n, "grad_rows")
+    _size(grad, n * dim, "grad")
+    _size(count, 1, "count")
+    ws, nbytes = _workspace(workspace, engram_embed_grad_workspace(n, rows, dim), dev, temps)
+    _check(_lib().engram_embed_grad(ip, istride, T, C, dp, dstride, dt, int(rows), dim, float(scale),
+                                    _dev(grad_rows, torch.int64, "grad_rows"), _dev(grad, grad.dtype, "grad"),
+                                    _float_type(grad, "grad"), _dev(count, torch.int64, "count"), ws, nbytes,
+                                    _launch_stream(stream, temps)), "engram_embed_grad")
+    return grad_rows, grad, count
+
+
+def engram_embed_grad_dense(idx: torch.Tensor, dout: torch.Tensor, grad: torch.Tensor, scale: float = 1.0,
+                            accumulate: bool = False, workspace: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """The gradient of engram_embed as a whole table: grad [rows, dim] (float32, bfloat16 or float16; rows
+    may be a stride apart) is written, zeros where no id named the row; with accumulate the gradient is
+    added to what grad holds. Other arguments as engram_embed_grad. Returns grad."""
+    ip, istride, T, C = _embed_ids(idx)
+    dt, gt = _float_type(dout, "dout"), _float_type(grad, "grad")
+    gp, rows, dim, gstride = _rows_of(grad, "grad")
+    dp, dstride, ddim = _embed_dout(dout, T, C)
+    if ddim != dim:
+        raise ValueError(f"dout has rows of {ddim} values, grad of {dim}")
+    temps = []
+    ws, nbytes = _workspace(workspace, engram_embed_grad_workspace(T * C, rows, dim), idx.device, temps)
+    _check(_lib().engram_embed_grad_dense(ip, istride, T, C, dp, dstride, dt, rows, dim, float(scale), gp, gstride, gt,
+                                          int(bool(accumulate)), ws, nbytes, _launch_stream(stream, temps)),
+           "engram_embed_grad_dense")
+    return grad
+
+
+def engram_gate_grad_workspace(T: int, hc: int, dim: int) -> int:
+    """Bytes of workspace engram_gate_grad needs (0 for T == 0 or an unsupported hc / dim)."""
+    return int(_lib().engram_gate_grad_workspace(int(T), int(hc), int(dim)))
+
+
+def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                     dout: torch.Tensor, mask: torch.Tensor | None = None, eps: float = 1e-20,
+                     dx: torch.Tensor | None = None, dkv: torch.Tensor | None = None,
+                     dq_weight: torch.Tensor | None = None, dk_weight: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of engram_gate (same x, kv, weights, mask, eps) for dout, the gradient of its output.
+    Returns (or fills) dx bf16 like x (may be dout), dkv bf16 like kv, and dq_weight, dk_weight float32
+    [hc, dim], summed over the tokens in a fixed order. A masked token passes dout through."""
+    hc, dim = x.shape[-2], x.shape[-1]
+    T = x.numel() // (hc * dim)
+    temps = []
+    if dx is None:
+        dx = torch.empty_like(x)
+        temps.append(dx)
+    if dkv is None:
+        dkv = torch.empty_like(kv)
+        temps.append(dkv)
+    if dq_weight is None:
+        dq_weight = torch.empty((hc, dim), dtype=torch.float32, device=x.device)
+        temps.append(dq_weight)
+    if dk_weight is None:
+        dk_weight = torch.empty((hc, dim), dtype=torch.float32, device=x.device)
+        temps.append(dk_weight)
+    for name, t, n in (("kv", kv, T * (hc + 1) * dim), ("dkv", dkv, T * (hc + 1) * dim), ("dout", dout, T * hc * dim),
+                       ("dx", dx, T * hc * dim), ("q_weight", q_weight, hc * dim), ("k_weight", k_weight, hc * dim),
+                       ("dq_weight", dq_weight, hc * dim), ("dk_weight", dk_weight, hc * dim), ("mask", mask, T)):
+        _size(t, n, name)
+    bf, f32 = torch.bfloat16, torch.float32
+    m = None if mask is None else _dev(_as_u8(mask), torch.uint8, "mask")
+    ptr = [_dev(x, bf, "x"), _dev(kv, bf, "kv"), _dev(q_weight, bf, "q_weight"), _dev(k_weight, bf, "k_weight"),
+           _dev(dout, bf, "dout"), m, T, hc, dim, float(eps), _dev(dx, bf, "dx"), _dev(dkv, bf, "dkv"),
+           _dev(dq_weight, f32, "dq_weight"), _dev(dk_weight, f32, "dk_weight")]
+    ws, nbytes = _workspace(workspace, engram_gate_grad_workspace(T, hc, dim), x.device, temps)
+    _check(_lib().engram_gate_grad(*ptr, ws, nbytes, _launch_stream(stream, temps)), "engram_gate_grad")
+    return dx, dkv, dq_weight, dk_weight
+
+
+def engram_grad_norm_workspace(n_tensors: int) -> int:
+    """Bytes of workspace engram_grad_norm and engram_grad_clip need."""
+    return int(_lib().engram_grad_norm_workspace(int(n_tensors)))
+
+
+_NORM_OF = {2: NORM_L2, 2.0: NORM_L2, float("inf"): NORM_MAX}
+
+
+def _tensor_list(grads, out, counts):
+    n = len(grads)
+    if (out is not None and len(out) != n) or (counts is not None and len(counts) != n):
+        raise ValueError(f"out and counts need one entry per gradient ({n})")
+    arr = (_Tensor * n)()
+    for i, g in enumerate(grads):
+        a = arr[i]
+        a.type = _float_type(g, "grads")
+        if not g.is_contiguous():
+            raise ValueError("grads must be contiguous")
+        a.data, a.n = g.data_ptr(), g.numel()
+        if out is not None and out[i] is not None:
+            o = out[i]
+            a.out_type = _float_type(o, "out")
+            if o.numel() != a.n or not o.is_contiguous():
+                raise ValueError(f"out[{i}] must be contiguous and hold {a.n} values")
+            a.out = o.data_ptr()
+        if counts is not None and counts[i] is not None:
+            _size(counts[i], 1, "counts")
+            a.rows_used = _dev(counts[i], torch.int64, "counts")
+            if g.dim() < 2 or g.numel() == 0:
+                raise ValueError("a gradient with a count must be [n, dim]")
+            a.row_len = a.n // g.shape[0]
+    return arr, n
+
+
+def _norm_call(grads, norm_type, counts, norm, workspace, stream, out=None, max_norm=None):
+    if norm_type not in _NORM_OF:
+        raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+    grads = list(grads)
+    arr, n = _tensor_list(grads, out, counts)
+    dev = grads[0].device if n else (norm.device if norm is not None else torch.device("cuda"))
+    temps = []
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        temps.append(norm)
+    _size(norm, 1, "norm")
+    ws, nbytes = _workspace(workspace, engram_grad_norm_workspace(n), dev, temps)
+    args = (_dev(norm, torch.float32, "norm"), ws, nbytes, _launch_stream(stream, temps))
+    if max_norm is None:
+        _check(_lib().engram_grad_norm(arr, n, _NORM_OF[norm_type], *args), "engram_grad_norm")
+    else:
+        _check(_lib().engram_grad_clip(arr, n, _NORM_OF[norm_type], float(max_norm), *args), "engram_grad_clip")
+    return norm
+
+
+def engram_grad_norm(grads, norm_type: float = 2.0, counts=None, norm: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The norm over all values of a list of contiguous float32, bfloat16 or float16 CUDA tensors
+    (norm_type 2 or inf), as a float32 scalar tensor on the device. counts: None, or per tensor None or an
+    int64 [1] CUDA tensor saying how many of its leading rows count (engram_embed_grad's count)."""
+    return _norm_call(grads, norm_type, counts, norm, workspace, stream)
+
+
+def engram_grad_clip(grads, max_norm: float, norm_type: float = 2.0, out=None, counts=None,
+                     norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Multiply the gradients by min(1, max_norm / (norm + 1e-6)), norm as engram_grad_norm (returned, as
+    it was before clipping). In place, or into `out`: per gradient a tensor of the same size in any of the
+    three types, or None for in place. Rows past a gradient's count are neither read nor written."""
+    return _norm_call(grads, norm_type, counts, norm, workspace, stream, out, max_norm)
 
 
 class PreparedHashLookup:

@@ -1,5 +1,6 @@
 // C ABI of libengram: state management, host-side argument checks, launches.
 // Declarations and the contract of every entry point are in include/engram.h.
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -9,6 +10,7 @@
 
 #include "engram_internal.cuh"
 #include "proj.cuh"
+#include "train.cuh"
 
 struct engram_state {
   engram_layout lay;
@@ -667,6 +669,183 @@ int engram_shard_unpack(const uint16_t* rows, const int64_t* positions, int64_t 
   if (n > ((int64_t)1 << 40)) return ENGRAM_ERR_UNSUPPORTED;
   return launched(launch_rc(engram::launch_shard_unpack(rows, positions, m, n, head_dim, out, (cudaStream_t)stream)),
                   (cudaStream_t)stream, {span(out, (uint64_t)n * head_dim * 2)});
+}
+
+// ------------------------------------------------------------------------------------------------
+// Training operators (embed.cu, gate_grad.cu, grad_norm.cu)
+namespace {
+
+inline bool type_ok(int32_t t) { return t == ENGRAM_TYPE_F32 || t == ENGRAM_TYPE_BF16 || t == ENGRAM_TYPE_F16; }
+inline bool type_aligned(const void* p, int32_t t) { return aligned(p, engram::type_bytes(t)); }
+
+// sizes and ids shared by the lookup and its gradient
+int check_embed(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, int64_t rows, int32_t dim,
+                float scale) {
+  if (T < 0 || n_cols < 1 || rows < 0 || dim < 1 || idx_stride < n_cols || !std::isfinite(scale))
+    return ENGRAM_ERR_INVALID;
+  if (dim > ENGRAM_MAX_EMBED_DIM || T > INT32_MAX / n_cols || rows >= (int64_t)UINT32_MAX) return ENGRAM_ERR_UNSUPPORTED;
+  if (T > 0 && (idx == nullptr || !aligned(idx, 8))) return ENGRAM_ERR_INVALID;
+  return ENGRAM_OK;
+}
+
+int check_embed_grad(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* dout,
+                     int64_t dout_stride, int32_t dout_type, int64_t rows, int32_t dim, float scale,
+                     int32_t grad_type, const void* workspace, uint64_t workspace_bytes) {
+  if (!type_ok(dout_type) || !type_ok(grad_type)) return ENGRAM_ERR_INVALID;
+  const int rc = check_embed(idx, idx_stride, T, n_cols, rows, dim, scale);
+  if (rc != ENGRAM_OK) return rc;
+  if (dout_stride < (int64_t)n_cols * dim) return ENGRAM_ERR_INVALID;
+  if (T == 0) return ENGRAM_OK;
+  if (dout == nullptr || !type_aligned(dout, dout_type) || workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < engram_embed_grad_workspace(T * n_cols, rows, dim))
+    return ENGRAM_ERR_INVALID;
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+int engram_embed(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* W, int64_t rows,
+                 int32_t dim, int64_t row_stride, int32_t w_type, float scale, void* out, int32_t out_type,
+                 engram_stream_t stream) {
+  if (!type_ok(w_type) || !type_ok(out_type)) return ENGRAM_ERR_INVALID;
+  const int rc = check_embed(idx, idx_stride, T, n_cols, rows, dim, scale);
+  if (rc != ENGRAM_OK) return rc;
+  if (row_stride < dim) return ENGRAM_ERR_INVALID;
+  if (T == 0) return ENGRAM_OK;
+  if ((rows > 0 && W == nullptr) || !type_aligned(W, w_type) || out == nullptr || !type_aligned(out, out_type))
+    return ENGRAM_ERR_INVALID;
+  const engram::EmbedArgs a{idx, idx_stride, T, n_cols, rows, dim, scale};
+  return launched(launch_rc(engram::launch_embed(a, W, row_stride, w_type, out, out_type, (cudaStream_t)stream)),
+                  (cudaStream_t)stream, {span(out, (uint64_t)T * n_cols * dim * engram::type_bytes(out_type))});
+}
+
+uint64_t engram_embed_grad_workspace(int64_t n, int64_t rows, int32_t dim) {
+  if (n <= 0 || n > INT32_MAX || rows < 0 || dim < 1) return 0;
+  return engram::embed_grad_workspace(n, rows, dim);
+}
+
+int engram_embed_grad(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* dout,
+                      int64_t dout_stride, int32_t dout_type, int64_t rows, int32_t dim, float scale,
+                      int64_t* grad_rows, void* grad, int32_t grad_type, int64_t* count, void* workspace,
+                      uint64_t workspace_bytes, engram_stream_t stream) {
+  const int rc = check_embed_grad(idx, idx_stride, T, n_cols, dout, dout_stride, dout_type, rows, dim, scale,
+                                  grad_type, workspace, workspace_bytes);
+  if (rc != ENGRAM_OK) return rc;
+  if (count == nullptr || !aligned(count, 8)) return ENGRAM_ERR_INVALID;
+  if (T > 0 && (grad_rows == nullptr || !aligned(grad_rows, 8) || grad == nullptr || !type_aligned(grad, grad_type)))
+    return ENGRAM_ERR_INVALID;
+  const int64_t n = T * n_cols;
+  const engram::EmbedGradArgs a{{idx, idx_stride, T, n_cols, rows, dim, scale}, dout, dout_stride, dout_type,
+                                grad, dim, grad_type, grad_rows, count, 0};
+  return launched(launch_rc(engram::launch_embed_grad(a, workspace, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(count, 8), span(grad_rows, (uint64_t)n * 8),
+                   span(grad, (uint64_t)n * dim * engram::type_bytes(grad_type)), span(workspace, workspace_bytes)});
+}
+
+int engram_embed_grad_dense(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* dout,
+                            int64_t dout_stride, int32_t dout_type, int64_t rows, int32_t dim, float scale,
+                            void* grad, int64_t grad_stride, int32_t grad_type, int32_t accumulate, void* workspace,
+                            uint64_t workspace_bytes, engram_stream_t stream) {
+  const int rc = check_embed_grad(idx, idx_stride, T, n_cols, dout, dout_stride, dout_type, rows, dim, scale,
+                                  grad_type, workspace, workspace_bytes);
+  if (rc != ENGRAM_OK) return rc;
+  if (grad_stride < dim) return ENGRAM_ERR_INVALID;
+  if (rows == 0 || (T == 0 && accumulate != 0)) return ENGRAM_OK;
+  if (grad == nullptr || !type_aligned(grad, grad_type)) return ENGRAM_ERR_INVALID;
+  const engram::EmbedGradArgs a{{idx, idx_stride, T, n_cols, rows, dim, scale}, dout, dout_stride, dout_type,
+                                grad, grad_stride, grad_type, nullptr, nullptr, accumulate != 0};
+  return launched(launch_rc(engram::launch_embed_grad(a, workspace, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(grad, (uint64_t)rows * grad_stride * engram::type_bytes(grad_type)),
+                   span(workspace, workspace_bytes)});
+}
+
+namespace {
+inline bool gate_grad_shape_ok(int64_t T, int32_t hc, int32_t dim) {
+  return (hc == 1 || hc == 2 || hc == 4 || hc == 8) && dim >= 8 && dim % 8 == 0 && dim <= ENGRAM_MAX_GATE_GRAD_DIM &&
+         T <= INT32_MAX;
+}
+}  // namespace
+
+uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
+  if (T <= 0 || !gate_grad_shape_ok(T, hc, dim)) return 0;
+  return engram::gate_grad_workspace(T, hc, dim);
+}
+
+int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
+                     const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
+                     uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
+                     uint64_t workspace_bytes, engram_stream_t stream) {
+  if (T < 0) return ENGRAM_ERR_INVALID;
+  if (!gate_grad_shape_ok(T, hc, dim)) return ENGRAM_ERR_UNSUPPORTED;
+  if (q_weight == nullptr || k_weight == nullptr || dq_weight == nullptr || dk_weight == nullptr ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(dq_weight, 16) || !aligned(dk_weight, 16))
+    return ENGRAM_ERR_INVALID;
+  if (T > 0) {
+    if (x == nullptr || kv == nullptr || dout == nullptr || dx == nullptr || dkv == nullptr || workspace == nullptr)
+      return ENGRAM_ERR_INVALID;
+    if (!aligned(x, 16) || !aligned(kv, 16) || !aligned(dout, 16) || !aligned(dx, 16) || !aligned(dkv, 16) ||
+        !aligned(workspace, 256) || workspace_bytes < engram_gate_grad_workspace(T, hc, dim))
+      return ENGRAM_ERR_INVALID;
+  }
+  const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
+  const uint64_t w = (uint64_t)hc * dim * 4;
+  return launched(launch_rc(engram::launch_gate_grad(a, workspace, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(dx, (uint64_t)T * hc * dim * 2), span(dkv, (uint64_t)T * (hc + 1) * dim * 2),
+                   span(dq_weight, w), span(dk_weight, w), span(workspace, T > 0 ? workspace_bytes : 0)});
+}
+
+namespace {
+
+int check_tensors(const engram_tensor* t, int32_t n, int32_t norm_type, const float* norm, const void* workspace,
+                  uint64_t workspace_bytes, bool clip) {
+  if (n < 0 || (n > 0 && t == nullptr) || (norm_type != ENGRAM_NORM_L2 && norm_type != ENGRAM_NORM_MAX) ||
+      norm == nullptr || !aligned(norm, 4))
+    return ENGRAM_ERR_INVALID;
+  if (n > 0 && (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < engram_grad_norm_workspace(n)))
+    return ENGRAM_ERR_INVALID;
+  for (int32_t i = 0; i < n; ++i) {
+    const engram_tensor& x = t[i];
+    if (x.n < 0 || !type_ok(x.type)) return ENGRAM_ERR_INVALID;
+    if (x.n > ((int64_t)1 << 36)) return ENGRAM_ERR_UNSUPPORTED;
+    if (x.n > 0 && (x.data == nullptr || !type_aligned(x.data, x.type))) return ENGRAM_ERR_INVALID;
+    if (x.rows_used != nullptr && (!aligned(x.rows_used, 8) || x.row_len < 1 || x.n % x.row_len != 0))
+      return ENGRAM_ERR_INVALID;
+    if (clip && x.out != nullptr &&
+        (!type_ok(x.out_type) || !type_aligned(x.out, x.out_type) || (x.out == x.data && x.out_type != x.type)))
+      return ENGRAM_ERR_INVALID;
+  }
+  return ENGRAM_OK;
+}
+
+}  // namespace
+
+uint64_t engram_grad_norm_workspace(int32_t n_tensors) {
+  return n_tensors > 0 ? round256(engram::grad_norm_workspace(n_tensors)) : 0;
+}
+
+int engram_grad_norm(const engram_tensor* tensors, int32_t n_tensors, int32_t norm_type, float* norm,
+                     void* workspace, uint64_t workspace_bytes, engram_stream_t stream) {
+  const int rc = check_tensors(tensors, n_tensors, norm_type, norm, workspace, workspace_bytes, false);
+  if (rc != ENGRAM_OK) return rc;
+  return launched(launch_rc(engram::launch_grad_norm(tensors, n_tensors, norm_type, false, 0.f, norm, workspace,
+                                                     (cudaStream_t)stream)),
+                  (cudaStream_t)stream, {span(norm, 4), span(workspace, n_tensors > 0 ? workspace_bytes : 0)});
+}
+
+int engram_grad_clip(const engram_tensor* tensors, int32_t n_tensors, int32_t norm_type, float max_norm,
+                     float* norm, void* workspace, uint64_t workspace_bytes, engram_stream_t stream) {
+  const int rc = check_tensors(tensors, n_tensors, norm_type, norm, workspace, workspace_bytes, true);
+  if (rc != ENGRAM_OK) return rc;
+  if (!(max_norm >= 0.f) || !std::isfinite(max_norm)) return ENGRAM_ERR_INVALID;
+  std::vector<Span> writes = {span(norm, 4), span(workspace, n_tensors > 0 ? workspace_bytes : 0)};
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    const engram_tensor& x = tensors[i];
+    writes.push_back(x.out != nullptr ? span(x.out, (uint64_t)x.n * engram::type_bytes(x.out_type))
+                                      : span(x.data, (uint64_t)x.n * engram::type_bytes(x.type)));
+  }
+  return launched(launch_rc(engram::launch_grad_norm(tensors, n_tensors, norm_type, true, max_norm, norm, workspace,
+                                                     (cudaStream_t)stream)),
+                  (cudaStream_t)stream, std::move(writes));
 }
 
 int engram_set_l2_fetch_granularity(int32_t bytes, int32_t* previous) {

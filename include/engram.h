@@ -87,6 +87,18 @@ typedef struct engram_state engram_state;
 /* head_dim must be one of 16, 32, 64, 128, 256, 512; block must divide head_dim and be a multiple of 8. */
 #define ENGRAM_GATE_MAX_COPIES 8  /* engram_gate: residual copies hc in {1, 2, 4, 8}; dim a multiple of 8 */
 #define ENGRAM_MAX_SHARDS 64      /* engram_shard_pack: ranks a table is split over */
+#define ENGRAM_MAX_EMBED_DIM 65536 /* engram_embed and its gradient: values per row */
+#define ENGRAM_MAX_GATE_GRAD_DIM 16384 /* engram_gate_grad: columns of a residual copy */
+
+/* Value types of the training operators' tensors. Reads widen to fp32 exactly; a result is rounded
+ * once, to nearest even. */
+#define ENGRAM_TYPE_F32 0
+#define ENGRAM_TYPE_BF16 1
+#define ENGRAM_TYPE_F16 2
+
+/* Norms of engram_grad_norm and engram_grad_clip. */
+#define ENGRAM_NORM_L2 2  /* sqrt(sum g^2) */
+#define ENGRAM_NORM_MAX 0 /* max |g| */
 
 typedef struct engram_layout {
   int32_t n_layers;    /* engram layers hashed per call (the config's engram_layer_ids count) */
@@ -435,6 +447,126 @@ int engram_shard_pack_static(const int64_t* idx, int64_t n, int64_t rows, int32_
  */
 int engram_shard_unpack(const uint16_t* rows, const int64_t* positions, int64_t m, int64_t n, int32_t head_dim,
                         uint16_t* out, engram_stream_t stream);
+
+/*
+ * Training the front end. The pages are inference code; the calls below are the gradients of what
+ * they compute, for tables held in a trainable float type instead of fp8 codes with scales.
+ *
+ * engram_embed: the lookup of trainable rows with a scale (`ParallelEngramEmbedding.forward` with the
+ * dequantisation replaced by one factor; also a token embedding, n_cols = 1):
+ *   out[t][c][k] = round(scale * W[idx[t * idx_stride + c]][k])          (one fp32 multiply)
+ *   idx         device int64: token t's n_cols row ids at idx[t * idx_stride + c] (idx_stride >= n_cols), e.g.
+ *               one layer's slice of engram_hash's output; an id outside [0, rows) gives a row of +0
+ *   W           device [rows] rows of dim values of w_type, row_stride values apart (row_stride >= dim)
+ *   out         device [T][n_cols][dim] of out_type, written
+ * Any dim >= 1 and any alignment to the type's width; rows on 16-byte boundaries with dim a multiple of 8
+ * move in 16-byte accesses, others value by value. T == 0 is a no-op. Errors: _INVALID (null or misaligned
+ * pointer, negative size, a stride below its row, an unknown type, scale not finite), _UNSUPPORTED (dim >
+ * ENGRAM_MAX_EMBED_DIM, T * n_cols >= 2^31, rows >= 2^32 - 1), _CUDA.
+ */
+int engram_embed(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* W, int64_t rows,
+                 int32_t dim, int64_t row_stride, int32_t w_type, float scale, void* out, int32_t out_type,
+                 engram_stream_t stream);
+
+/* Bytes of device workspace that either form of engram_embed's gradient needs for n = T * n_cols ids
+ * (a multiple of 256; 0 for n <= 0). */
+uint64_t engram_embed_grad_workspace(int64_t n, int64_t rows, int32_t dim);
+
+/*
+ * The gradient of engram_embed by sorted row ids:
+ *   G[r] = scale * sum over (t, c) with idx[t * idx_stride + c] == r of dout[t * dout_stride + c * dim ..]
+ * Ids outside [0, rows) take no part. The sums are fp32 in an order that depends on the ids alone, so the
+ * same inputs give the same bits; the result is rounded once to grad_type.
+ *
+ * engram_embed_grad, the sparse form: only the rows that occur, for tables whose dense gradient would not fit.
+ *   dout        device: token t's n_cols gradients of dim values of dout_type at dout + t * dout_stride
+ *               (dout_stride >= n_cols * dim)
+ *   grad_rows   device int64 [T * n_cols], written: the distinct row ids in ascending order, then -1
+ *   grad        device [T * n_cols][dim] of grad_type: grad[u] belongs to row grad_rows[u]; rows from *count
+ *               on are not written
+ *   count       device int64, written: the distinct rows (0 for T == 0)
+ *   workspace   engram_embed_grad_workspace(T * n_cols, rows, dim) bytes, 256-byte aligned, owned by the
+ *               caller; calls that use one workspace must not overlap on the GPU
+ *
+ * engram_embed_grad_dense, the dense form: grad is device [rows] rows of dim values of grad_type, grad_stride
+ * values apart. accumulate == 0: every row is written, +0 where no id named it. accumulate != 0: G is added
+ * (in fp32, rounded once) to what grad holds, and only rows that occur are touched.
+ * Errors: as engram_embed, and _INVALID for a workspace that is too small or misaligned.
+ */
+int engram_embed_grad(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* dout,
+                      int64_t dout_stride, int32_t dout_type, int64_t rows, int32_t dim, float scale,
+                      int64_t* grad_rows, void* grad, int32_t grad_type, int64_t* count, void* workspace,
+                      uint64_t workspace_bytes, engram_stream_t stream);
+int engram_embed_grad_dense(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const void* dout,
+                            int64_t dout_stride, int32_t dout_type, int64_t rows, int32_t dim, float scale,
+                            void* grad, int64_t grad_stride, int32_t grad_type, int32_t accumulate, void* workspace,
+                            uint64_t workspace_bytes, engram_stream_t stream);
+
+/* Bytes of device workspace that engram_gate_grad needs (a multiple of 256; 0 for T <= 0 or an
+ * unsupported hc or dim). */
+uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
+
+/*
+ * The gradient of engram_gate (blocks/stack-hashes page, `Engram.forward` after the projection), from the
+ * forward's inputs and the gradient of its output. With h = x[t][i], u = dout[t][i], w = q_weight[i] *
+ * k_weight[i], A = mean(h^2) + eps, B = mean(key_i^2) + eps, r = (A * B * dim)^-1/2, dot = r * sum(h * w * key_i):
+ *   gate as engram_gate; ddot = sum(u * value) * gate * (1 - gate) * (|dot| >= 1e-6 ? 0.5 / sqrt(|dot|) : 0)
+ *   dx[t][i]     = u + ddot * (r * w * key_i - dot / (A * dim) * h)
+ *   dkv key i    = ddot * (r * w * h - dot / (B * dim) * key_i)
+ *   dkv value    = sum over i of gate_i * u_i
+ *   dq_weight[i] = k_weight[i] * sum over t of ddot * r * h * key_i;   dk_weight[i]: with q_weight[i]
+ * in fp32. A token whose mask is 0 has a constant gate: dx = dout bit for bit, its dkv is +0 and it takes no
+ * part in the weights' gradients, whatever its x, key and value hold.
+ *   x, kv, q_weight, k_weight, mask, hc, eps  as engram_gate; dim a multiple of 8, <= ENGRAM_MAX_GATE_GRAD_DIM
+ *   dout       device bf16 [T][hc][dim]
+ *   dx         device bf16 [T][hc][dim], written; may be the same buffer as dout
+ *   dkv        device bf16 [T][(hc+1)*dim], written
+ *   dq_weight, dk_weight  device fp32 [hc][dim], written (+0 for T == 0)
+ *   workspace  engram_gate_grad_workspace(T, hc, dim) bytes, 256-byte aligned, owned by the caller; calls
+ *              that use one workspace must not overlap on the GPU (may be NULL for T == 0)
+ * Every pointer but mask 16-byte aligned. The sums over tokens run in a fixed order: the same inputs give
+ * the same bits. Errors: _INVALID, _UNSUPPORTED (hc, dim, T >= 2^31), _CUDA.
+ */
+int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
+                     const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
+                     uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
+                     uint64_t workspace_bytes, engram_stream_t stream);
+
+/* One gradient of engram_grad_norm / engram_grad_clip. */
+typedef struct engram_tensor {
+  const void* data;         /* device: n contiguous values of `type`, aligned to its width; may be NULL for n == 0 */
+  void* out;                /* engram_grad_clip: where the clipped values go; NULL: in place */
+  const int64_t* rows_used; /* device int64 or NULL: only the first *rows_used rows of row_len values count (at
+                               most n / row_len, none if negative), e.g. the count of engram_embed_grad */
+  int64_t n;
+  int32_t row_len;          /* with rows_used: values per row, n a multiple of it; else unused */
+  int32_t type;             /* ENGRAM_TYPE_* of data */
+  int32_t out_type;         /* ENGRAM_TYPE_* of out (unused in place) */
+} engram_tensor;
+
+/* Bytes of device workspace that engram_grad_norm and engram_grad_clip need (a multiple of 256). */
+uint64_t engram_grad_norm_workspace(int32_t n_tensors);
+
+/*
+ * The global norm over a list of gradients, and clipping by it:
+ *   norm = sqrt(sum over all values g^2) (ENGRAM_NORM_L2) or max |g| (ENGRAM_NORM_MAX); 0 for no values
+ *   engram_grad_clip: out = round(g * min(1, max_norm / (norm + 1e-6)))
+ * A value's square is formed in fp32 (|g| above 1.8e19 makes the norm infinite); blocks' sums are joined in
+ * 64 bits in a fixed order. A NaN anywhere makes the norm NaN and every clipped value NaN; an infinite norm
+ * makes the factor 0, so finite values become 0 and infinite ones NaN. Values past *rows_used are neither
+ * counted nor written.
+ *   tensors    host array of n_tensors descriptions, read during the call only. The tensors of one call
+ *              must not overlap; an out may be its own data (then of the same type) and nothing else's
+ *   norm_type  ENGRAM_NORM_*;  max_norm >= 0 and finite
+ *   norm       device fp32, written (before clipping)
+ *   workspace  engram_grad_norm_workspace(n_tensors) bytes, 256-byte aligned, owned by the caller; calls that
+ *              use one workspace must not overlap on the GPU
+ * Errors: _INVALID, _UNSUPPORTED (a tensor of more than 2^36 values), _CUDA.
+ */
+int engram_grad_norm(const engram_tensor* tensors, int32_t n_tensors, int32_t norm_type, float* norm,
+                     void* workspace, uint64_t workspace_bytes, engram_stream_t stream);
+int engram_grad_clip(const engram_tensor* tensors, int32_t n_tensors, int32_t norm_type, float max_norm,
+                     float* norm, void* workspace, uint64_t workspace_bytes, engram_stream_t stream);
 
 /*
  * Set the L2 fetch granularity limit of the current device's context (cudaLimitMaxL2FetchGranularity:
