@@ -203,8 +203,11 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const EmbedArgs 
 }
 
 // -------------------------------------------------------------------------------------- segments
-// A segment is the run of one row id in the sorted keys; its number among the segments is `slot`.
+// A segment is the run of one row id in the sorted keys. The sparse form numbers the segments: ids[i] is
+// the number of the segment that sorted pair i belongs to (kNone outside the table). The dense form
+// needs no numbers: there the keys themselves serve as ids.
 constexpr int kSegTile = 2048;
+constexpr uint32_t kNone = 0xffffffffu;
 
 __device__ __forceinline__ bool is_head(const uint32_t* key, int64_t i, uint32_t rows) {
   const uint32_t k = key[i];
@@ -223,12 +226,11 @@ __global__ void __launch_bounds__(kThreads) head_count_kernel(const uint32_t* __
   if (threadIdx.x == 0) heads[blockIdx.x] = (uint32_t)c;
 }
 
-// seg_start[u] = first sorted pair of segment u (seg_start[count] = the pairs inside the table);
-// the sparse form's grad_rows (-1 past the count) and count
+// ids, and the sparse form's grad_rows (-1 past the count) and count
 __global__ void __launch_bounds__(kThreads)
     segments_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t rows, const uint32_t* __restrict__ heads,
-                    int32_t tiles, uint32_t* __restrict__ seg_start, uint32_t* __restrict__ n_seg,
-                    int64_t* __restrict__ grad_rows, int64_t* __restrict__ count) {
+                    int32_t tiles, uint32_t* __restrict__ ids, int64_t* __restrict__ grad_rows,
+                    int64_t* __restrict__ count) {
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t sum_s[2];
@@ -250,19 +252,14 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t i = (int64_t)blockIdx.x * kSegTile + j;
     const bool h = i < n && is_head(key, i, rows);
     const uint32_t off = block_exclusive(h ? 1u : 0u, warp_sums);
-    if (h) {
-      seg_start[u + off] = (uint32_t)i;
-      if (grad_rows != nullptr) grad_rows[u + off] = key[i];
+    if (h) grad_rows[u + off] = key[i];
+    if (i < n) {
+      ids[i] = key[i] < rows ? u + off - (h ? 0u : 1u) : kNone;
+      if (i >= (int64_t)total) grad_rows[i] = -1;
     }
-    if (i < n && key[i] >= rows && (i == 0 || key[i - 1] < rows)) seg_start[total] = (uint32_t)i;
-    if (i == n - 1 && key[i] < rows) seg_start[total] = (uint32_t)n;
-    if (grad_rows != nullptr && i < n && i >= (int64_t)total) grad_rows[i] = -1;
     u += __syncthreads_count(h);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *n_seg = total;
-    if (count != nullptr) *count = total;
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *count = total;
 }
 
 __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
@@ -271,55 +268,385 @@ __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
   if (threadIdx.x == 0) *count = 0;
 }
 
+// Calls of up to kSmall ids: the whole sort and the numbering in one CTA, the pairs in shared memory.
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallPer = 8;
+constexpr int kSmall = kSmallThreads * kSmallPer;
+constexpr int kSmallSmem = kSmall * 4 + kSmall * 2 + (kSmallThreads / 32) * kMaxBins * 2 + kMaxBins * 4 + 64 * 4;
+
+__global__ void __launch_bounds__(kSmallThreads)
+    sort_small_kernel(const EmbedArgs e, const int n, const int passes, const int width, uint32_t* __restrict__ key_out,
+                      uint32_t* __restrict__ pos_out, uint32_t* __restrict__ ids, int64_t* __restrict__ grad_rows,
+                      int64_t* __restrict__ count) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kWarps = kSmallThreads / 32;
+  extern __shared__ uint32_t smem[];
+  uint32_t* sk = smem;                                         // [kSmall] keys
+  uint32_t* start = sk + kSmall;                               // [kMaxBins] first place of each digit
+  uint32_t* warp_sums = start + kMaxBins;                      // [64]
+  uint16_t* sp = reinterpret_cast<uint16_t*>(warp_sums + 64);  // [kSmall] positions
+  uint16_t* wh = sp + kSmall;                                  // [kWarps][kMaxBins] counts, then starts
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rows = (uint32_t)e.rows;
+  uint32_t key[kSmallPer];
+  uint16_t pos[kSmallPer];
+  const int base = warp * 32 * kSmallPer + lane;  // (warp, step, lane) is position order
+#pragma unroll
+  for (int j = 0; j < kSmallPer; ++j) {
+    const int i = base + j * 32;
+    key[j] = rows;
+    pos[j] = (uint16_t)i;
+    if (i < n) {
+      const int t = i / e.n_cols;
+      const int64_t r = e.idx[t * e.idx_stride + (i - t * e.n_cols)];
+      if (r >= 0 && r < e.rows) key[j] = (uint32_t)r;
+    }
+  }
+  for (int q = 0; q < passes; ++q) {
+    const int shift = q * width, bins = 1 << width;
+    for (int b = tid; b < kWarps * kMaxBins / 2; b += kSmallThreads) reinterpret_cast<uint32_t*>(wh)[b] = 0;
+    __syncthreads();
+    uint16_t rank[kSmallPer];
+#pragma unroll
+    for (int j = 0; j < kSmallPer; ++j) {
+      const bool in = base + j * 32 < n;
+      const uint32_t d = in ? (key[j] >> shift) & (bins - 1) : 0xffffffffu;
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      uint32_t have = 0;
+      if (in) have = wh[warp * kMaxBins + d];
+      __syncwarp();
+      if (in && before == 0) wh[warp * kMaxBins + d] = (uint16_t)(have + __popc(same));
+      __syncwarp();
+      rank[j] = (uint16_t)(have + before);
+    }
+    __syncthreads();
+    // per digit: exclusive sums over the warps
+    uint32_t total = 0;
+    if (tid < bins) {
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t c = wh[w * kMaxBins + tid];
+        wh[w * kMaxBins + tid] = (uint16_t)total;
+        total += c;
+      }
+    }
+    const uint32_t first = block_exclusive(tid < bins ? total : 0u, warp_sums);
+    if (tid < bins) start[tid] = first;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSmallPer; ++j) {
+      if (base + j * 32 < n) {
+        const uint32_t d = (key[j] >> shift) & (bins - 1);
+        const uint32_t at = start[d] + wh[warp * kMaxBins + d] + rank[j];
+        sk[at] = key[j];
+        sp[at] = pos[j];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kSmallPer; ++j) {
+      if (base + j * 32 < n) {
+        key[j] = sk[base + j * 32];
+        pos[j] = sp[base + j * 32];
+      }
+    }
+  }
+  // a thread's kSmallPer consecutive pairs of the sorted order
+  const int i0 = tid * kSmallPer;
+  uint32_t heads = 0;
+  for (int j = 0; j < kSmallPer; ++j) {
+    const int i = i0 + j;
+    if (i < n && sk[i] < rows && (i == 0 || sk[i - 1] != sk[i])) heads++;
+  }
+  uint32_t u = block_exclusive(heads, warp_sums);
+  if (tid == kSmallThreads - 1) start[0] = u + heads;
+  for (int j = 0; j < kSmallPer; ++j) {
+    const int i = i0 + j;
+    if (i >= n) break;
+    const uint32_t k = sk[i];
+    key_out[i] = k;
+    pos_out[i] = sp[i];
+    if (grad_rows != nullptr) {
+      const bool h = k < rows && (i == 0 || sk[i - 1] != k);
+      if (h) grad_rows[u++] = k;
+      ids[i] = k < rows ? u - 1 : kNone;
+    }
+  }
+  __syncthreads();
+  if (grad_rows != nullptr) {
+    for (int i = tid; i < n; i += kSmallThreads)
+      if (i >= (int)start[0]) grad_rows[i] = -1;
+    if (tid == 0) *count = start[0];
+  }
+}
+
 // ------------------------------------------------------------------------------------ segment sums
-// one warp per (segment, 32 * V columns)
+// The sorted pairs are cut into units of `per_unit` consecutive ones, whatever segments they belong to,
+// so a row named a million times and a million rows named once cost the same. A group of 2^glog lanes
+// takes one unit and V columns a lane, with kBatch rows of dout in flight; it writes the segments that
+// lie inside its unit. What is left are runs that cross a unit's ends: the CTA joins its units' parts in
+// shared memory, in order, and leaves at most two parts for the kernel that joins the CTAs' (segments
+// that span CTAs). Every sum's order follows from the sorted ids alone.
+constexpr int kBatch = 8;
+
+struct SumArgs {
+  const uint32_t* ids;
+  const uint32_t* pos;
+  uint32_t limit;  // ids from here on are no rows
+  int64_t n;
+  int32_t glog, per_unit, chunks;
+  int64_t tiles;
+  float* lead;   // [tiles][dim4]: the part of a segment that began in an earlier tile
+  float* trail;  // [tiles][dim4]: the part of a segment that goes on in the next tile
+  int32_t dim4;  // dim rounded up to 4
+  uint8_t* flags;  // [tiles] kOpen, kCloses, kThrough
+  // dense form without accumulation: CTAs from tiles * chunks on write the rows that no id names
+  int32_t zero_rows;  // rows per such CTA
+};
+constexpr int kOpen = 1;     // a segment that begins here goes on in the next unit (tile)
+constexpr int kCloses = 2;   // the segment that began earlier ends here
+constexpr int kThrough = 4;  // it neither begins nor ends here
+
+template <int GT, int V>
+__device__ __forceinline__ void finish_row(const EmbedGradArgs& a, uint32_t row, int k, float* acc) {
+  typename Elem<GT>::type* g = static_cast<typename Elem<GT>::type*>(a.grad) + (int64_t)row * a.grad_stride + k;
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] *= a.e.scale;
+  if (a.accumulate) {
+    Raw<GT, V> raw;
+    raw.load(g);
+    float f[V];
+    raw.widen(f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] += f[j];
+  }
+  store_vals<GT, V>(g, acc);
+}
+
+template <int GT>
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
+  // rows without ids: row r has one exactly if the first sorted id >= r is r
+  __shared__ uint8_t named[kThreads];
+  const int64_t r0 = block * s.zero_rows;
+  const int m = (int)min((int64_t)s.zero_rows, a.e.rows - r0);
+  if ((int)threadIdx.x < m) {
+    const uint32_t r = (uint32_t)(r0 + threadIdx.x);
+    int64_t lo = 0, hi = s.n;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (s.ids[mid] < r) lo = mid + 1; else hi = mid;
+    }
+    named[threadIdx.x] = lo < s.n && s.ids[lo] == r;
+  }
+  __syncthreads();
+  using G = typename Elem<GT>::type;
+  G* g = static_cast<G*>(a.grad);
+  constexpr int kPer = 16 / sizeof(G);
+  const bool wide = (reinterpret_cast<uintptr_t>(g) % 16 == 0) && a.grad_stride % kPer == 0 && a.e.dim % kPer == 0;
+  for (int r = 0; r < m; ++r) {
+    if (named[r]) continue;
+    G* row = g + (r0 + r) * a.grad_stride;
+    if (wide) {
+      for (int k = threadIdx.x; k < a.e.dim / kPer; k += kThreads)
+        reinterpret_cast<uint4*>(row)[k] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      for (int k = threadIdx.x; k < a.e.dim; k += kThreads) Elem<GT>::store(row + k, 0.f);
+    }
+  }
+}
+
 template <int DT, int GT, int V>
-__global__ void __launch_bounds__(kThreads)
-    segment_sum_kernel(const EmbedGradArgs a, const uint32_t* __restrict__ key, const uint32_t* __restrict__ pos,
-                       const uint32_t* __restrict__ seg_start, const uint32_t* __restrict__ n_seg) {
+__global__ void __launch_bounds__(kThreads) segment_sum_kernel(const EmbedGradArgs a, const SumArgs s) {
   pdl_wait();
   pdl_trigger();
   using D = typename Elem<DT>::type;
-  using G = typename Elem<GT>::type;
-  const int lane = threadIdx.x & 31;
-  const int k = ((int)blockIdx.y * 32 + lane) * V;
-  const uint32_t total = *n_seg;
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < total;
-       u += (int64_t)gridDim.x * (kThreads / 32)) {
-    const uint32_t i0 = seg_start[u], i1 = seg_start[u + 1];
-    float acc[V] = {};
-    for (uint32_t i = i0; i < i1; ++i) {
-      const uint32_t p = pos[i], t = p / (uint32_t)a.e.n_cols;
-      if (k < a.e.dim) {
-        Raw<DT, V> raw;
-        raw.load((const D*)a.dout + t * a.dout_stride + (int64_t)(p - t * a.e.n_cols) * a.e.dim + k);
-        float f[V];
-        raw.widen(f);
+  __shared__ float lead_s[kThreads * V];  // [unit][column of the chunk]
+  __shared__ uint8_t flag_s[kThreads];
+  const int64_t work = s.tiles * s.chunks;
+  if ((int64_t)blockIdx.x >= work) {
+    zero_rows<GT>(a, s, (int64_t)blockIdx.x - work);
+    return;
+  }
+  const int64_t tile = blockIdx.x / s.chunks;
+  const int chunk = (int)(blockIdx.x - tile * s.chunks);
+  const int G = 1 << s.glog, units = kThreads >> s.glog;
+  const int unit = threadIdx.x >> s.glog, gl = threadIdx.x & (G - 1);
+  const int k = (chunk * G + gl) * V;
+  const bool on = k < a.e.dim;
+  const int64_t i0 = min(s.n, (tile * units + unit) * s.per_unit), i1 = min(s.n, i0 + s.per_unit);
+  const D* dout = static_cast<const D*>(a.dout) + k;
+  const bool packed = a.dout_stride == (int64_t)a.e.n_cols * a.e.dim;
+
+  float acc[V];
+  uint32_t cur = kNone;  // the running segment
+  bool leading = i0 > 0 && i0 < i1 && s.ids[i0 - 1] == s.ids[i0];
+  int flag = 0;
+  auto put_lead = [&]() {
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += f[j];
+    for (int j = 0; j < V; ++j) lead_s[threadIdx.x * V + j] = acc[j];
+  };
+  auto close = [&]() {  // the running segment ends inside this unit
+    if (leading) {
+      put_lead();
+      flag |= kCloses;
+      leading = false;
+    } else if (on) {
+      finish_row<GT, V>(a, cur, k, acc);
+    }
+  };
+  for (int64_t i = i0; i < i1; i += kBatch) {
+    uint32_t id[kBatch];
+    Raw<DT, V> raw[kBatch];
+    // per_unit is a multiple of kBatch, so these are aligned; the arrays reach a batch past n
+    const uint4 a0 = *reinterpret_cast<const uint4*>(s.ids + i), a1 = *reinterpret_cast<const uint4*>(s.ids + i + 4);
+    const uint4 p0 = *reinterpret_cast<const uint4*>(s.pos + i), p1 = *reinterpret_cast<const uint4*>(s.pos + i + 4);
+    const uint32_t ia[kBatch] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    const uint32_t pa[kBatch] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      id[j] = i + j < i1 && ia[j] < s.limit ? ia[j] : kNone;
+      raw[j].zero();
+      if (id[j] != kNone && on) {
+        int64_t at = (int64_t)pa[j] * a.e.dim;
+        if (!packed) {
+          const uint32_t t = pa[j] / (uint32_t)a.e.n_cols;
+          at = (int64_t)t * a.dout_stride + (int64_t)(pa[j] - t * a.e.n_cols) * a.e.dim;
+        }
+        raw[j].load(dout + at);
       }
     }
-    if (k < a.e.dim) {
-      const int64_t row = a.grad_rows != nullptr ? u : (int64_t)key[i0];
-      G* g = (G*)a.grad + row * a.grad_stride + k;
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] *= a.e.scale;
-      if (a.accumulate) {
-        Raw<GT, V> raw;
-        raw.load(g);
-        float f[V];
-        raw.widen(f);
+    for (int j = 0; j < kBatch; ++j) {
+      float f[V];
+      raw[j].widen(f);
+      if (id[j] != cur) {
+        if (cur != kNone) close();
+        cur = id[j];
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = f[j] + acc[j];
+        for (int q = 0; q < V; ++q) acc[q] = f[q];
+      } else {
+#pragma unroll
+        for (int q = 0; q < V; ++q) acc[q] += f[q];
       }
-      store_vals<GT, V>(g, acc);
     }
+    if (id[kBatch - 1] == kNone) break;
+  }
+  if (cur != kNone) {
+    if (i1 < s.n && s.ids[i1] == cur) {
+      if (leading) put_lead();
+      flag |= leading ? kThrough : kOpen;
+    } else {
+      close();
+    }
+  }
+  if (gl == 0) flag_s[unit] = (uint8_t)flag;
+  __syncthreads();
+
+  auto lead_of = [&](int u) { return lead_s + ((u << s.glog) + gl) * V; };
+  auto part = [&](float* to) {
+    if (!on) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) to[tile * s.dim4 + k + j] = acc[j];
+  };
+  if (flag & kOpen) {  // acc holds the trailing part
+    int v = unit + 1;
+    for (; v < units; ++v) {
+      const float* l = lead_of(v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] += l[j];
+      if (flag_s[v] & kCloses) break;
+    }
+    if (v == units) part(s.trail);
+    else if (on) finish_row<GT, V>(a, cur, k, acc);
+  }
+  if (unit == 0 && (flag & (kCloses | kThrough))) {
+    const float* l0 = lead_of(0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = l0[j];
+    for (int v = 1; v < units && !(flag_s[v - 1] & kCloses); ++v) {
+      const float* l = lead_of(v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] += l[j];
+    }
+    part(s.lead);
+  }
+  if (threadIdx.x == 0 && chunk == 0) {
+    int f = 0, v = 0;
+    while (v < units && (flag_s[v] & kThrough)) ++v;
+    if (v == units) f = kThrough;
+    else if (flag_s[v] & kCloses) f = kCloses;
+    for (v = units - 1; v > 0 && (flag_s[v] & kThrough); --v) {}
+    if (flag_s[v] & kOpen) f |= kOpen;
+    s.flags[tile] = (uint8_t)f;
+  }
+}
+
+// Segments that span tiles: the CTA of the tile where one begins adds the parts of the tiles it crosses.
+// 8 warps take consecutive eighths of the parts, and the eighths are added in order.
+constexpr int kJoinCols = 128;
+template <int GT>
+__global__ void __launch_bounds__(kThreads) segment_join_kernel(const EmbedGradArgs a, const SumArgs s) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float4 part[kWarps][32];
+  __shared__ int last_s;
+  const int64_t b = blockIdx.x;
+  if (!(s.flags[b] & kOpen)) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the tile where the segment ends: the first one after b that it does not go through
+  int64_t last = b + 1;
+  for (;; last += kThreads) {
+    if (threadIdx.x == 0) last_s = kThreads;
+    __syncthreads();
+    const int64_t t = last + threadIdx.x;
+    if (t >= s.tiles || !(s.flags[t] & kThrough)) atomicMin(&last_s, (int)threadIdx.x);
+    __syncthreads();
+    const int at = last_s;
+    __syncthreads();
+    if (at < kThreads) {
+      last += at;
+      break;
+    }
+  }
+  const int64_t m = last - b;  // parts after the first
+  const int k = blockIdx.y * kJoinCols + lane * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (k < a.e.dim) {
+    const int64_t j0 = m * warp / kWarps, j1 = m * (warp + 1) / kWarps;
+    if (warp == 0) sum = *reinterpret_cast<const float4*>(s.trail + b * s.dim4 + k);
+#pragma unroll 8
+    for (int64_t j = j0; j < j1; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(s.lead + (b + 1 + j) * s.dim4 + k);
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || k >= a.e.dim) return;
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 v = part[w][lane];
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  const int64_t per_tile = (int64_t)(kThreads >> s.glog) * s.per_unit;
+  const uint32_t row = s.ids[(b + 1) * per_tile - 1];
+  const float f[4] = {sum.x, sum.y, sum.z, sum.w};
+  for (int j = 0; j < 4 && k + j < a.e.dim; ++j) {
+    float v = f[j];
+    finish_row<GT, 1>(a, row, k + j, &v);
   }
 }
 
 template <int GT>
 __global__ void __launch_bounds__(kThreads)
-    zero_rows_kernel(typename Elem<GT>::type* grad, int64_t rows, int32_t dim, int64_t stride) {
+    all_zero_kernel(typename Elem<GT>::type* grad, int64_t rows, int32_t dim, int64_t stride) {
   pdl_wait();
   pdl_trigger();
   const int64_t units = rows * dim;
@@ -332,10 +659,30 @@ __global__ void __launch_bounds__(kThreads)
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-struct Layout {  // byte offsets into the workspace
-  uint64_t key[2], pos[2], counts, totals, heads, seg_start, n_seg, end;
+// How the sums are cut up: 2^glog lanes a unit, per_unit pairs a unit, chunks of columns, tiles of units
+struct Cut {
+  int glog, per_unit, chunks;
+  int64_t tiles;
 };
-Layout layout_of(int64_t n) {
+constexpr int64_t kWantCtas = 1216;  // 8 CTAs on each of the 152 SMs
+Cut cut_of(int64_t n, int32_t dim, int v) {
+  Cut c;
+  const int lanes = (dim + v - 1) / v;
+  c.glog = 0;
+  while (c.glog < 5 && (1 << c.glog) < lanes) ++c.glog;
+  c.chunks = (int)ceil_div(lanes, 1 << c.glog);
+  const int units = kThreads >> c.glog;
+  // the longest units that still give every SM work; a unit of one batch where there is too little
+  c.per_unit = 64;
+  while (c.per_unit > kBatch && ceil_div(n, (int64_t)units * c.per_unit) * c.chunks < kWantCtas) c.per_unit >>= 1;
+  c.tiles = ceil_div(n, (int64_t)units * c.per_unit);
+  return c;
+}
+
+struct Layout {  // byte offsets into the workspace
+  uint64_t key[2], pos[2], ids, counts, totals, heads, lead, trail, flags, end;
+};
+Layout layout_of(int64_t n, int32_t dim) {
   Layout l;
   uint64_t at = 0;
   auto take = [&](uint64_t bytes) {
@@ -344,14 +691,18 @@ Layout layout_of(int64_t n) {
     return p;
   };
   for (int i = 0; i < 2; ++i) {
-    l.key[i] = take((uint64_t)n * 4);
-    l.pos[i] = take((uint64_t)n * 4);
+    l.key[i] = take((uint64_t)(n + kBatch) * 4);
+    l.pos[i] = take((uint64_t)(n + kBatch) * 4);
   }
+  l.ids = take((uint64_t)(n + kBatch) * 4);
   l.counts = take((uint64_t)ceil_div(n, kTile) * kMaxBins * 4);
   l.totals = take(kMaxBins * 4);
   l.heads = take((uint64_t)ceil_div(n, kSegTile) * 4);
-  l.seg_start = take((uint64_t)(n + 1) * 4);
-  l.n_seg = take(4);
+  const uint64_t tiles = (uint64_t)std::max(cut_of(n, dim, 1).tiles, cut_of(n, dim, 8).tiles);
+  const uint64_t dim4 = (uint64_t)ceil_div(dim, 4) * 4;
+  l.lead = take(tiles * dim4 * 4);
+  l.trail = take(tiles * dim4 * 4);
+  l.flags = take(tiles);
   l.end = at;
   return l;
 }
@@ -381,69 +732,99 @@ cudaError_t launch_embed(const EmbedArgs& a, const void* W, int64_t row_stride, 
   });
 }
 
-uint64_t embed_grad_workspace(int64_t n, int64_t, int32_t) { return n > 0 ? layout_of(n).end : 0; }
+uint64_t embed_grad_workspace(int64_t n, int64_t, int32_t dim) { return n > 0 ? layout_of(n, dim).end : 0; }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStream_t s) {
   const int64_t n = a.e.T * a.e.n_cols;
   const bool sparse = a.grad_rows != nullptr || a.count != nullptr;
-  cudaError_t e = cudaSuccess;
-  if (!sparse && !a.accumulate && a.e.rows > 0) {
-    e = with_type(a.grad_type, [&](auto gt) {
+  const bool zero = !sparse && !a.accumulate;
+  if (n == 0) {
+    if (sparse) return launch_pdl(no_segments_kernel, dim3(1), dim3(32), 0, s, a.count);
+    return with_type(a.grad_type, [&](auto gt) {
       using G = typename Elem<gt()>::type;
       const int64_t grid = std::min<int64_t>(ceil_div(a.e.rows * a.e.dim, kThreads), 152 * 16);
-      return launch_pdl(zero_rows_kernel<gt()>, dim3((unsigned)grid), dim3(kThreads), 0, s, (G*)a.grad, a.e.rows,
+      return launch_pdl(all_zero_kernel<gt()>, dim3((unsigned)grid), dim3(kThreads), 0, s, (G*)a.grad, a.e.rows,
                         a.e.dim, a.grad_stride);
     });
-    if (e != cudaSuccess) return e;
   }
-  if (n == 0) {
-    if (!sparse) return cudaSuccess;
-    return launch_pdl(no_segments_kernel, dim3(1), dim3(32), 0, s, a.count);
-  }
-  const Layout l = layout_of(n);
+  const Layout l = layout_of(n, a.e.dim);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   auto u32 = [&](uint64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
+  cudaError_t e = cudaSuccess;
   int bits = 1;
   while (bits < 32 && ((uint64_t)a.e.rows >> bits) != 0) ++bits;  // `rows` itself is a key
   const int passes = (bits + kMaxBits - 1) / kMaxBits, width = (bits + passes - 1) / passes;
-  const int tiles = (int)ceil_div(n, kTile);
-  for (int q = 0; q < passes; ++q) {
-    SortPass p;
-    p.key_in = q == 0 ? nullptr : u32(l.key[q & 1]);
-    p.pos_in = q == 0 ? nullptr : u32(l.pos[q & 1]);
-    p.key_out = u32(l.key[(q + 1) & 1]);
-    p.pos_out = u32(l.pos[(q + 1) & 1]);
-    p.counts = u32(l.counts);
-    p.totals = u32(l.totals);
-    p.n = n;
-    p.tiles = tiles;
-    p.shift = q * width;
-    p.bins = 1 << std::min(width, 32 - q * width);
-    e = launch_pdl(sort_count_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+  const uint32_t *key, *pos, *ids;
+  if (n <= kSmall) {
+    e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(p.bins, kThreads / 32)), dim3(kThreads), 0, s, p);
+    e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), kSmallSmem, s, a.e, (int)n, passes, width,
+                   u32(l.key[0]), u32(l.pos[0]), u32(l.ids), a.grad_rows, a.count);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(sort_scatter_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
-    if (e != cudaSuccess) return e;
+    key = u32(l.key[0]);
+    pos = u32(l.pos[0]);
+  } else {
+    const int tiles = (int)ceil_div(n, kTile);
+    for (int q = 0; q < passes; ++q) {
+      SortPass p;
+      p.key_in = q == 0 ? nullptr : u32(l.key[q & 1]);
+      p.pos_in = q == 0 ? nullptr : u32(l.pos[q & 1]);
+      p.key_out = u32(l.key[(q + 1) & 1]);
+      p.pos_out = u32(l.pos[(q + 1) & 1]);
+      p.counts = u32(l.counts);
+      p.totals = u32(l.totals);
+      p.n = n;
+      p.tiles = tiles;
+      p.shift = q * width;
+      p.bins = 1 << std::min(width, 32 - q * width);
+      e = launch_pdl(sort_count_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+      if (e != cudaSuccess) return e;
+      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(p.bins, kThreads / 32)), dim3(kThreads), 0, s, p);
+      if (e != cudaSuccess) return e;
+      e = launch_pdl(sort_scatter_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+      if (e != cudaSuccess) return e;
+    }
+    key = u32(l.key[passes & 1]);
+    pos = u32(l.pos[passes & 1]);
+    if (sparse) {
+      const int seg_tiles = (int)ceil_div(n, kSegTile);
+      e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
+                     u32(l.heads));
+      if (e != cudaSuccess) return e;
+      e = launch_pdl(segments_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
+                     (const uint32_t*)u32(l.heads), seg_tiles, u32(l.ids), a.grad_rows, a.count);
+      if (e != cudaSuccess) return e;
+    }
   }
-  const uint32_t *key = u32(l.key[passes & 1]), *pos = u32(l.pos[passes & 1]);
-  const int seg_tiles = (int)ceil_div(n, kSegTile);
-  e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows, u32(l.heads));
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(segments_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
-                 (const uint32_t*)u32(l.heads), seg_tiles, u32(l.seg_start), u32(l.n_seg), a.grad_rows, a.count);
-  if (e != cudaSuccess) return e;
+  ids = sparse ? u32(l.ids) : key;
   const bool v8 = wide(a.dout, a.dout_stride, a.e.dim, a.dout_type) && wide(a.grad, a.grad_stride, a.e.dim, a.grad_type);
-  const unsigned chunks = (unsigned)ceil_div(a.e.dim, 32 * (v8 ? 8 : 1));
-  const unsigned gx = (unsigned)std::min<int64_t>(ceil_div(n, kThreads / 32), 152 * 8);
-  return with_type(a.dout_type, [&](auto dt) {
-    return with_type(a.grad_type, [&](auto gt) {
+  const Cut c = cut_of(n, a.e.dim, v8 ? 8 : 1);
+  SumArgs m;
+  m.ids = ids;
+  m.pos = pos;
+  m.limit = sparse ? kNone : (uint32_t)a.e.rows;
+  m.n = n;
+  m.glog = c.glog;
+  m.per_unit = c.per_unit;
+  m.chunks = c.chunks;
+  m.tiles = c.tiles;
+  m.lead = reinterpret_cast<float*>(ws + l.lead);
+  m.trail = reinterpret_cast<float*>(ws + l.trail);
+  m.dim4 = (int32_t)ceil_div(a.e.dim, 4) * 4;
+  m.flags = ws + l.flags;
+  const int64_t row_bytes = (int64_t)a.e.dim * type_bytes(a.grad_type);
+  m.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads, (128 << 10) / row_bytes));
+  const int64_t grid = c.tiles * c.chunks + (zero ? ceil_div(a.e.rows, m.zero_rows) : 0);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return with_type(a.grad_type, [&](auto gt) {
+    cudaError_t r = with_type(a.dout_type, [&](auto dt) {
       if (v8)
-        return launch_pdl(segment_sum_kernel<dt(), gt(), 8>, dim3(gx, chunks), dim3(kThreads), 0, s, a, key, pos,
-                          (const uint32_t*)u32(l.seg_start), (const uint32_t*)u32(l.n_seg));
-      return launch_pdl(segment_sum_kernel<dt(), gt(), 1>, dim3(gx, chunks), dim3(kThreads), 0, s, a, key, pos,
-                        (const uint32_t*)u32(l.seg_start), (const uint32_t*)u32(l.n_seg));
+        return launch_pdl(segment_sum_kernel<dt(), gt(), 8>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, m);
+      return launch_pdl(segment_sum_kernel<dt(), gt(), 1>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, m);
     });
+    if (r != cudaSuccess || c.tiles == 1) return r;
+    return launch_pdl(segment_join_kernel<gt()>, dim3((unsigned)c.tiles, (unsigned)ceil_div(a.e.dim, kJoinCols)),
+                      dim3(kThreads), 0, s, a, m);
   });
 }
 
