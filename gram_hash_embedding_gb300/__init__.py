@@ -24,6 +24,7 @@ Method: the "DeepSeek V4.1" pages -- blocks/stack-hashes page (the n-gram hash
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -951,30 +952,51 @@ def engram_grad_norm_workspace(n_tensors: int) -> int:
 _NORM_OF = {2: NORM_L2, 2.0: NORM_L2, float("inf"): NORM_MAX}
 
 
+def _list_part(ts, name: str):
+    """(types, pointers, sizes) of a list of tensors; checked in passes over the whole list, since a model
+    has hundreds of gradients and a Python call for each check of each would outlast the kernels."""
+    try:
+        types = [_TYPE_OF_DTYPE[t.dtype] for t in ts]
+        fine = all([t.is_cuda for t in ts])
+    except (AttributeError, KeyError):
+        fine = False
+    if not fine:
+        for t in ts:
+            _float_type(t, name)
+    if not all(map(torch.Tensor.is_contiguous, ts)):
+        raise ValueError(f"{name} must be contiguous")
+    return types, map(torch.Tensor.data_ptr, ts), list(map(torch.Tensor.numel, ts))
+
+
 def _tensor_list(grads, out, counts):
+    """A list's engram_tensor array, packed as 64-bit words: data, out, rows_used, n, row_len | type << 32,
+    out_type."""
     n = len(grads)
     if (out is not None and len(out) != n) or (counts is not None and len(counts) != n):
         raise ValueError(f"out and counts need one entry per gradient ({n})")
-    arr = (_Tensor * n)()
-    for i, g in enumerate(grads):
-        a = arr[i]
-        a.type = _float_type(g, "grads")
-        if not g.is_contiguous():
-            raise ValueError("grads must be contiguous")
-        a.data, a.n = g.data_ptr(), g.numel()
-        if out is not None and out[i] is not None:
-            o = out[i]
-            a.out_type = _float_type(o, "out")
-            if o.numel() != a.n or not o.is_contiguous():
-                raise ValueError(f"out[{i}] must be contiguous and hold {a.n} values")
-            a.out = o.data_ptr()
-        if counts is not None and counts[i] is not None:
-            _size(counts[i], 1, "counts")
-            a.rows_used = _dev(counts[i], torch.int64, "counts")
-            if g.dim() < 2 or g.numel() == 0:
+    words = [0] * (6 * n)
+    types, words[0::6], sizes = _list_part(grads, "grads")
+    words[3::6] = sizes
+    words[4::6] = [t << 32 for t in types]
+    if out is not None:
+        at = [i for i in range(n) if out[i] is not None]
+        given = [out[i] for i in at]
+        types, ptrs, osizes = _list_part(given, "out")
+        for i, t, p, m in zip(at, types, ptrs, osizes):
+            if m != sizes[i]:
+                raise ValueError(f"out[{i}] has {m} elements, expected {sizes[i]}")
+            words[6 * i + 1] = p
+            words[6 * i + 5] = t
+    if counts is not None:
+        for i, c in enumerate(counts):
+            if c is None:
+                continue
+            _size(c, 1, "counts")
+            if grads[i].dim() < 2 or sizes[i] == 0:
                 raise ValueError("a gradient with a count must be [n, dim]")
-            a.row_len = a.n // g.shape[0]
-    return arr, n
+            words[6 * i + 2] = _dev(c, torch.int64, "counts")
+            words[6 * i + 4] |= sizes[i] // grads[i].shape[0]
+    return array.array("q", words), n
 
 
 def _norm_call(grads, norm_type, counts, norm, workspace, stream, out=None, max_norm=None):
@@ -982,6 +1004,7 @@ def _norm_call(grads, norm_type, counts, norm, workspace, stream, out=None, max_
         raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
     grads = list(grads)
     arr, n = _tensor_list(grads, out, counts)
+    ap = arr.buffer_info()[0]
     dev = grads[0].device if n else (norm.device if norm is not None else torch.device("cuda"))
     temps = []
     if norm is None:
@@ -991,9 +1014,9 @@ def _norm_call(grads, norm_type, counts, norm, workspace, stream, out=None, max_
     ws, nbytes = _workspace(workspace, engram_grad_norm_workspace(n), dev, temps)
     args = (_dev(norm, torch.float32, "norm"), ws, nbytes, _launch_stream(stream, temps))
     if max_norm is None:
-        _check(_lib().engram_grad_norm(arr, n, _NORM_OF[norm_type], *args), "engram_grad_norm")
+        _check(_lib().engram_grad_norm(ap, n, _NORM_OF[norm_type], *args), "engram_grad_norm")
     else:
-        _check(_lib().engram_grad_clip(arr, n, _NORM_OF[norm_type], float(max_norm), *args), "engram_grad_clip")
+        _check(_lib().engram_grad_clip(ap, n, _NORM_OF[norm_type], float(max_norm), *args), "engram_grad_clip")
     return norm
 
 

@@ -9,18 +9,37 @@
 //   dq     = k_weight * sum_t c * h * key,  dk = q_weight * the same sum
 // in fp32, everything recomputed from the forward's inputs. A masked token's gate is the constant 0:
 // dh = u, dkey = dvalue = 0 and no part in dq and dk, whatever its key and value hold.
+//
+// Design: bound by memory (a token reads (3 hc + 1) dim and writes (2 hc + 1) dim bf16 values, once), but
+// every output needs sums over the whole row first, and the weights' gradients are sums over all tokens
+// in hc * dim accumulators. So a cluster of CTAs takes whole tokens, in turn with the other clusters: bulk
+// copies bring a token's rows into shared memory two tokens ahead, and a thread owns the same 8 columns of
+// every copy from the first token to the last, with its part of the weights' sums in registers. Per token
+// there is one exchange, of the 4 hc sums: a reduce-scatter in each warp, then every warp sends its sums into
+// the shared memory of each CTA of the cluster (asynchronous stores that count their bytes on an mbarrier; a
+// cluster barrier would wait for the thread's global stores of the token before), and one warp of each CTA
+// forms the token's scalars. That chain is what limits the rate, so it is kept short: approximate reciprocal
+// roots, no integer division. The cluster is as small as registers and shared memory allow (2 CTAs at dim
+// 5120 and 4 copies: one cluster on each pair of SMs).
+// 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 537 us, 3.55 GB at
+// 6.6 TB/s (0.99 of the copy bandwidth). Tried: copies
+// of 16 bytes by each thread into its own slots instead of bulk copies 735 us; a cluster barrier and IEEE
+// roots and divisions in every warp 796 us; two groups of threads with two copies each 683 us; clusters
+// of 4, two to an SM, 690 us where all of them fit and 1,217 us where 2 of 76 had to wait.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
 #include "engram_internal.cuh"
+#include "proj.cuh"
+#include "tc_ptx.cuh"
 #include "train.cuh"
 
 namespace engram {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSplits = 64;  // parts of the token axis in the weights' sums
+constexpr int kSms = 152;
+constexpr int kMaxSmem = 226 << 10;
 
 struct CopyGrad {
   float gate, c, ea, eb;  // gate, c, e / A, e / B
@@ -29,186 +48,418 @@ struct CopyGrad {
 // The scalars of one residual copy from its four sums
 __device__ __forceinline__ CopyGrad copy_grad(float sh, float sk, float sd, float su, float rd, float eps,
                                               float inv_sqrt_dim) {
-  const float A = sh * rd + eps, B = sk * rd + eps;
-  const float r = (1.0f / sqrtf(A)) * (1.0f / sqrtf(B)) * inv_sqrt_dim;
+  const float ra = rsqrtf(sh * rd + eps), rb = rsqrtf(sk * rd + eps);
+  const float r = ra * rb * inv_sqrt_dim;
   const float dot = sd * r;
-  const float m = fabsf(dot), root = sqrtf(fmaxf(m, 1e-6f));
+  const float m = fabsf(dot), ri = rsqrtf(fmaxf(m, 1e-6f));  // 1 / |z|
   CopyGrad g;
   // from exp(-|z|), so that neither the gate nor 1 - gate cancels: gate (1 - gate) = x / (1 + x)^2
-  const float x = expf(-root), y = 1.0f / (1.0f + x);
+  const float x = expf(-fmaxf(m, 1e-6f) * ri), y = __frcp_rn(1.0f + x);
   g.gate = dot < 0.f ? x * y : y;
-  const float ddot = m >= 1e-6f ? su * (x * y * y) * (0.5f / root) : 0.f;
+  const float ddot = m >= 1e-6f ? su * (x * y * y) * (0.5f * ri) : 0.f;
   const float e = ddot * dot * rd;
   g.c = ddot * r;
-  g.ea = e / A;
-  g.eb = e / B;
+  g.ea = e * ra * ra;
+  g.eb = e * rb * rb;
   return g;
 }
 
-__device__ __forceinline__ void bf16x8(const uint16_t* p, float* f) {
-  Raw<ENGRAM_TYPE_BF16, 8> r;
-  r.load(reinterpret_cast<const __nv_bfloat16*>(p));
-  r.widen(f);
+// 8 bf16 values as 4 pairs: the arithmetic runs two values an instruction (the packed fp32 forms), which
+// round like the single ones
+struct Vec8 {
+  float2 p[4];
+};
+
+__device__ __forceinline__ Vec8 widen8(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return r;
 }
 
-__device__ __forceinline__ void st8(uint16_t* p, const float* f) {
-  store_vals<ENGRAM_TYPE_BF16, 8>(reinterpret_cast<__nv_bfloat16*>(p), f);
+__device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack2<ENGRAM_TYPE_BF16>(v.p[i].x, v.p[i].y);
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// one CTA per token; cs[t][i] = c for the weights' sums
-template <int HC>
-__global__ void __launch_bounds__(kThreads) gate_grad_kernel(const GateGradArgs a, const float rd,
-                                                             const float inv_sqrt_dim, float* __restrict__ cs) {
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// one row's part of a token into shared memory, counted in bytes on `bar`
+__device__ __forceinline__ void copy_row(uint4* dst, const uint16_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Sums of N values over the warp, N a power of two <= 32: lane l ends with the total of value
+// l / (32 / N), in N - 1 + log2(32 / N) shuffles instead of 5 N.
+template <int N>
+__device__ __forceinline__ float warp_reduce_scatter(float (&s)[N], int lane) {
+#pragma unroll
+  for (int w = N / 2, off = 16; w >= 1; w /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float give = up ? s[j] : s[j + w];
+      const float keep = up ? s[j + w] : s[j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+  float r = s[0];
+#pragma unroll
+  for (int off = 16 / N; off >= 1; off /= 2) r += __shfl_xor_sync(0xffffffffu, r, off);
+  return r;
+}
+
+// Write v to the same shared variable of CTA `rank` and count its 4 bytes on that CTA's mbarrier. Unlike a
+// cluster barrier's release this waits for none of the thread's global stores.
+__device__ __forceinline__ void send(float* p, uint32_t bar, uint32_t rank, float v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(
+                   tc::map_to_rank(tc::smem_u32(p), rank)),
+               "f"(v), "r"(tc::map_to_rank(bar, rank))
+               : "memory");
+}
+
+// the most threads of a CTA, one per vector of 8 columns: what the registers allow
+constexpr int max_threads(int hc) { return hc <= 2 ? 640 : 320; }
+
+// HC copies, S stages
+template <int HC, int S>
+__global__ void __launch_bounds__(max_threads(HC))
+    gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int cs,
+                     float* __restrict__ part, unsigned int* __restrict__ status) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float red[4 * HC][kThreads / 32];
-  __shared__ CopyGrad gs[HC];
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nvec = a.dim >> 3;
-  const uint16_t* xt = a.x + t * HC * a.dim;
-  const uint16_t* ut = a.dout + t * HC * a.dim;
-  const uint16_t* kt = a.kv + t * (HC + 1) * a.dim;
-  const uint16_t* vt = kt + (int64_t)HC * a.dim;
-  uint16_t* dxt = a.dx + t * HC * a.dim;
-  uint16_t* dkt = a.dkv + t * (HC + 1) * a.dim;
-  const bool open = a.mask == nullptr || a.mask[t] != 0;
-  if (!open) {
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    for (int v = tid; v < nvec * HC; v += kThreads)
-      reinterpret_cast<uint4*>(dxt)[v] = reinterpret_cast<const uint4*>(ut)[v];
-    for (int v = tid; v < nvec * (HC + 1); v += kThreads) reinterpret_cast<uint4*>(dkt)[v] = z;
-    if (tid < HC) cs[t * HC + tid] = 0.f;
-    return;
+  constexpr int kArrays = 3 * HC + 1;   // rows of a token: h, keys and douts of the copies, the value
+  constexpr int N = 4 * HC;             // sums of a token
+  constexpr bool kKeepW = HC <= 4;      // the weights stay in registers; 8 copies read them again (L1, L2)
+  extern __shared__ uint4 smem[];
+  __shared__ float4 scal[2][HC];
+  __shared__ volatile int dead;  // a wait has run out: nothing more is fetched, the results are not to be used
+  __shared__ __align__(8) uint64_t bars[2 + S];  // of red's two halves: the bytes of a token's sums; of the stages
+  const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
+  const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
+  const uint32_t rank = blockIdx.x % cs;
+  float* red = reinterpret_cast<float*>(smem + (size_t)S * kArrays * nv);  // [2][cs][nw][N]
+  const int cnt = min(nv, (a.dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
+  const bool on = tid < cnt;
+  const int me = min(tid, cnt - 1);  // threads past the row read its last vector and use nothing of it
+  const int64_t row0 = 8 * (int64_t)rank * nv;   // its first column
+  const int64_t col = row0 + 8 * tid;
+  const uint32_t bar0 = tc::smem_u32(bars);
+  auto slot = [&](int st, int j) -> const uint4& { return smem[(st * kArrays + j) * nv + me]; };
+  // one thread starts a token's copies
+  uint32_t last = ~0u;  // (that thread's) bit st: the parity of the stage's last copies
+  auto fetch = [&](int64_t t, int st, bool open) {
+    if (t >= a.T || dead) return;
+    last ^= 1u << st;
+    const uint32_t bytes = 16 * cnt, bar = bar0 + 16 + 8 * st;
+    uint4* to = smem + (size_t)st * kArrays * nv;
+    tc::mbar_arrive_expect_tx(bar, bytes * (open ? kArrays : HC));
+    const uint16_t* u = a.dout + t * HC * a.dim + row0;
+    for (int i = 0; i < HC; ++i) copy_row(to + (2 * HC + i) * nv, u + (int64_t)i * a.dim, bytes, bar);
+    if (open) {
+      const uint16_t* h = a.x + t * HC * a.dim + row0;
+      const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
+      for (int i = 0; i < HC; ++i) {
+        copy_row(to + i * nv, h + (int64_t)i * a.dim, bytes, bar);
+        copy_row(to + (HC + i) * nv, k + (int64_t)i * a.dim, bytes, bar);
+      }
+      copy_row(to + 3 * HC * nv, k + (int64_t)HC * a.dim, bytes, bar);
+    }
+  };
+  auto open_at = [&](int64_t t) { return t < a.T && (a.mask == nullptr || a.mask[t] != 0) ? 1u : 0u; };
+
+  auto load_weights = [&](int i) {
+    Vec8 w = {};
+    if (on) {
+      const Vec8 q = widen8(__ldg(reinterpret_cast<const uint4*>(a.qw + col + (int64_t)i * a.dim)));
+      const Vec8 k = widen8(__ldg(reinterpret_cast<const uint4*>(a.kw + col + (int64_t)i * a.dim)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w.p[e] = __fmul2_rn(q.p[e], k.p[e]);
+    }
+    return w;
+  };
+  Vec8 w_kept[kKeepW ? HC : 1];
+  if constexpr (kKeepW) {
+#pragma unroll
+    for (int i = 0; i < HC; ++i) w_kept[i] = load_weights(i);
   }
-  float s[HC][4] = {};
-  for (int v = tid; v < nvec; v += kThreads) {
-    float val[8];
-    bf16x8(vt + 8 * v, val);
+  auto weights = [&](int i) {
+    if constexpr (kKeepW) return w_kept[i];
+    else return load_weights(i);
+  };
+  Vec8 dw[HC] = {};
+  if (tid == 0) {
+    dead = 0;
+    for (int i = 0; i < 2 + S; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+    tc::fence_barrier_init();
+  }
+  if (cs > 1) tc::cluster_sync();  // every CTA's barriers exist before another CTA sends to them
+  else __syncthreads();
+  // bit j of `open`: the mask of the cluster's token j places on
+  uint32_t open = 0;
 #pragma unroll
-    for (int i = 0; i < HC; ++i) {
-      const int64_t o = (int64_t)i * a.dim + 8 * v;
-      float h[8], k[8], u[8], q[8], w[8];
-      bf16x8(xt + o, h);
-      bf16x8(kt + o, k);
-      bf16x8(ut + o, u);
-      bf16x8(a.qw + o, q);
-      bf16x8(a.kw + o, w);
+  for (int j = 0; j < S; ++j) open |= open_at(cluster + (int64_t)j * nc) << j;
+  if (tid == 0)
+    for (int j = 0; j < S - 1; ++j) fetch(cluster + (int64_t)j * nc, j, (open >> j) & 1);
+  int st = 0, buf = 0;
+  uint32_t phase = 0;   // bit b: the parity of bars[b]'s current phase
+  auto wait = [&](int b) {
+    if (!dead && !tc::mbar_wait(bar0 + 8 * b, (phase >> b) & 1, const_cast<const volatile int*>(&dead))) {
+      dead = 1;
+      atomicOr(status, ENGRAM_STATUS_TIMEOUT);
+    }
+    phase ^= 1u << b;
+  };
+  for (int64_t t = cluster; t < a.T; t += nc) {
+    const uint32_t next = open_at(t + (int64_t)S * nc);
+    wait(2 + st);
+    // the stage of the token before is free once every thread has passed this token's first barrier
+    auto refill = [&]() {
+      if (tid == 0) fetch(t + (int64_t)(S - 1) * nc, st == 0 ? S - 1 : st - 1, (open >> (S - 1)) & 1);
+    };
+    uint16_t* dxt = a.dx + t * HC * a.dim + col;
+    uint16_t* dkt = a.dkv + t * (HC + 1) * a.dim + col;
+    if (open & 1) {
+      float s[N];
+      {
+        const Vec8 v = widen8(slot(st, 3 * HC));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s[i][0] = fmaf(h[e], h[e], s[i][0]);
-        s[i][1] = fmaf(k[e], k[e], s[i][1]);
-        s[i][2] = fmaf(h[e] * (q[e] * w[e]), k[e], s[i][2]);
-        s[i][3] = fmaf(u[e], val[e], s[i][3]);
+        for (int i = 0; i < HC; ++i) {
+          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), u = widen8(slot(st, 2 * HC + i));
+          const Vec8 w = weights(i);
+          float2 q[4] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            q[0] = __ffma2_rn(h.p[e], h.p[e], q[0]);
+            q[1] = __ffma2_rn(k.p[e], k.p[e], q[1]);
+            q[2] = __ffma2_rn(__fmul2_rn(h.p[e], w.p[e]), k.p[e], q[2]);
+            q[3] = __ffma2_rn(u.p[e], v.p[e], q[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: what the slots hold
+        }
+      }
+      const float mine = warp_reduce_scatter<N>(s, lane);
+      float* to = red + ((buf * cs + rank) * nw + warp) * N + lane / (32 / N);
+      if (lane % (32 / N) == 0) {
+        if (cs == 1) *to = mine;
+        else
+          for (int r = 0; r < cs; ++r) send(to, bar0 + 8 * buf, r, mine);
+      }
+      if (cs == 1) __syncthreads();
+      // red[buf] is written again two tokens on: whoever does has the sums of the token between from every CTA,
+      // each sent past the barrier below that follows the reads here
+      if (warp == nw - 1) {
+        if (cs > 1) {
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * N * 4));
+          wait(buf);
+        }
+        // lane l: every (32 / N)-th of the warps' parts of sum l % N (no division here: with one per part this
+        // warp held the others up and the call took 696 us instead of 537)
+        const float* from = red + buf * cs * nw * N + lane % N;
+        const int parts_of_token = cs * nw;
+        float sum = 0.f;
+#pragma unroll 5
+        for (int j = lane / N; j < parts_of_token; j += 32 / N) sum += from[j * N];
+#pragma unroll
+        for (int off = N; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __shfl_sync(0xffffffffu, sum, 4 * (lane % HC) + e);
+        const CopyGrad g = copy_grad(f[0], f[1], f[2], f[3], rd, a.eps, inv_sqrt_dim);
+        if (lane < HC) scal[buf][lane] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+      }
+      __syncthreads();
+      refill();
+      if (on) {
+        Vec8 dv = {};
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          const float4 g = scal[buf][i];  // gate, c, -e / A, -e / B
+          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), u = widen8(slot(st, 2 * HC + i));
+          const Vec8 w = weights(i);
+          Vec8 dh, dk;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 ch = __fmul2_rn(both(g.y), h.p[e]), ck = __fmul2_rn(both(g.y), k.p[e]);
+            dh.p[e] = __ffma2_rn(w.p[e], ck, __ffma2_rn(both(g.z), h.p[e], u.p[e]));
+            dk.p[e] = __ffma2_rn(w.p[e], ch, __fmul2_rn(both(g.w), k.p[e]));
+            dv.p[e] = __ffma2_rn(both(g.x), u.p[e], dv.p[e]);
+            dw[i].p[e] = __ffma2_rn(ch, k.p[e], dw[i].p[e]);
+          }
+          st8(dxt + i * a.dim, dh);
+          st8(dkt + i * a.dim, dk);
+        }
+        st8(a.dkv + (t * (HC + 1) + HC) * a.dim + col, dv);
+      }
+      buf ^= 1;
+    } else {  // the whole cluster skips the sums
+      __syncthreads();
+      refill();
+      if (on) {
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          *reinterpret_cast<uint4*>(dxt + i * a.dim) = slot(st, 2 * HC + i);
+          *reinterpret_cast<uint4*>(dkt + i * a.dim) = z;
+        }
+        *reinterpret_cast<uint4*>(a.dkv + (t * (HC + 1) + HC) * a.dim + col) = z;
       }
     }
+    open = open >> 1 | next << (S - 1);
+    st = st == S - 1 ? 0 : st + 1;
   }
-#pragma unroll
-  for (int i = 0; i < HC; ++i)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s[i][q] += __shfl_xor_sync(0xffffffffu, s[i][q], o);
-      if (lane == 0) red[4 * i + q][warp] = s[i][q];
-    }
-  __syncthreads();
-  if (tid < HC) {
-    float f[4];
-    for (int q = 0; q < 4; ++q) {
-      f[q] = 0.f;
-      for (int w = 0; w < kThreads / 32; ++w) f[q] += red[4 * tid + q][w];
-    }
-    gs[tid] = copy_grad(f[0], f[1], f[2], f[3], rd, a.eps, inv_sqrt_dim);
-    cs[t * HC + tid] = gs[tid].c;
-  }
-  __syncthreads();
-  for (int v = tid; v < nvec; v += kThreads) {
-    float dv[8] = {};
+  if (on) {
 #pragma unroll
     for (int i = 0; i < HC; ++i) {
-      const int64_t o = (int64_t)i * a.dim + 8 * v;
-      const CopyGrad g = gs[i];
-      float h[8], k[8], u[8], q[8], w[8], dh[8], dk[8];
-      bf16x8(xt + o, h);
-      bf16x8(kt + o, k);
-      bf16x8(ut + o, u);
-      bf16x8(a.qw + o, q);
-      bf16x8(a.kw + o, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float cw = g.c * (q[e] * w[e]);
-        dh[e] = u[e] + (cw * k[e] - g.ea * h[e]);
-        dk[e] = cw * h[e] - g.eb * k[e];
-        dv[e] = fmaf(g.gate, u[e], dv[e]);
-      }
-      st8(dxt + o, dh);
-      st8(dkt + o, dk);
+      float* to = part + (int64_t)cluster * HC * a.dim + col + (int64_t)i * a.dim;
+      const float2* d = dw[i].p;
+      *reinterpret_cast<float4*>(to) = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
+      *reinterpret_cast<float4*>(to + 4) = make_float4(d[2].x, d[2].y, d[3].x, d[3].y);
     }
-    st8(dkt + (int64_t)HC * a.dim + 8 * v, dv);
   }
+  if (tid == 0 && dead)  // copies may still be on their way into this CTA's memory
+    for (int st = 0; st < S; ++st)
+      if (cluster + (int64_t)st * nc < a.T) tc::mbar_wait(bar0 + 16 + 8 * st, (last >> st) & 1, nullptr);
+  if (cs > 1) tc::cluster_sync();  // and other CTAs' sums
 }
 
-// part[split][i][col] = sum over the split's tokens of c * h * key
-__global__ void __launch_bounds__(kThreads) gate_weight_sums_kernel(const GateGradArgs a, const float* __restrict__ cs,
-                                                                    float* __restrict__ part) {
+// The weights' gradients from the clusters' parts: a CTA takes 128 columns, its 8 warps take every 8th part
+// each, and the warps' sums are added in order.
+constexpr int kFinishThreads = 256;
+__global__ void __launch_bounds__(kFinishThreads) gate_weight_finish_kernel(const GateGradArgs a,
+                                                                            const float* __restrict__ part, int parts) {
   pdl_wait();
   pdl_trigger();
-  const int col = blockIdx.x * kThreads + threadIdx.x, i = blockIdx.y;
-  if (col >= a.dim) return;
-  const int64_t t0 = a.T * blockIdx.z / gridDim.z, t1 = a.T * (blockIdx.z + 1) / gridDim.z;
-  float acc = 0.f;
-  for (int64_t t = t0; t < t1; ++t) {
-    if (a.mask != nullptr && a.mask[t] == 0) continue;
-    const float h = __uint_as_float((uint32_t)a.x[(t * a.hc + i) * a.dim + col] << 16);
-    const float k = __uint_as_float((uint32_t)a.kv[(t * (a.hc + 1) + i) * a.dim + col] << 16);
-    acc = fmaf(cs[t * a.hc + i] * h, k, acc);
+  constexpr int kWarps = kFinishThreads / 32;
+  __shared__ float4 sum_s[kWarps][32];
+  const int n = a.hc * a.dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j = (blockIdx.x * 32 + lane) * 4;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < n) {
+#pragma unroll 8
+    for (int z = warp; z < parts; z += kWarps) {
+      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)z * n + j);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
   }
-  part[((int64_t)blockIdx.z * a.hc + i) * a.dim + col] = acc;
-}
-
-__global__ void __launch_bounds__(kThreads) gate_weight_finish_kernel(const GateGradArgs a, const float* __restrict__ part,
-                                                                      int splits) {
-  pdl_wait();
-  pdl_trigger();
-  const int n = a.hc * a.dim, j = blockIdx.x * kThreads + threadIdx.x;
-  if (j >= n) return;
-  float acc = 0.f;
-  for (int z = 0; z < splits; ++z) acc += part[(int64_t)z * n + j];
-  a.dq[j] = acc * __uint_as_float((uint32_t)a.kw[j] << 16);
-  a.dk[j] = acc * __uint_as_float((uint32_t)a.qw[j] << 16);
+  sum_s[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || j >= n) return;
+  for (int w = 1; w < kWarps; ++w) {
+    const float4 v = sum_s[w][lane];
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const uint2 q = *reinterpret_cast<const uint2*>(a.qw + j), k = *reinterpret_cast<const uint2*>(a.kw + j);
+  auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
+  auto hi = [](uint32_t v) { return __uint_as_float(v & 0xffff0000u); };
+  *reinterpret_cast<float4*>(a.dq + j) = make_float4(s.x * lo(k.x), s.y * hi(k.x), s.z * lo(k.y), s.w * hi(k.y));
+  *reinterpret_cast<float4*>(a.dk + j) = make_float4(s.x * lo(q.x), s.y * hi(q.x), s.z * lo(q.y), s.w * hi(q.y));
 }
 
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 
+struct Shape {
+  int cs, nv, threads, stages;  // CTAs per cluster, vectors and threads per CTA
+  int64_t smem, clusters;
+};
+
+// The smallest cluster whose CTAs hold their columns in registers and three stages of shared memory (8
+// copies of more than 10,000 columns or so: two); more CTAs a token when there are too few tokens for every
+// SM. Few clusters rather than many when every cluster would see few tokens: each leaves hc * dim partial
+// sums behind.
+Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
+  Shape s;
+  const int nvec = dim / 8;
+  auto set = [&](int cs, int stages) {
+    s.cs = cs;
+    s.stages = stages;
+    s.nv = (nvec + cs - 1) / cs;
+    s.threads = (s.nv + 31) / 32 * 32;
+    s.smem = (int64_t)stages * (3 * hc + 1) * s.nv * 16 + 2ll * cs * (s.threads / 32) * 4 * hc * 4;
+    return s.threads <= max_threads(hc) && s.smem <= kMaxSmem;
+  };
+  int cs = 1;
+  while (cs < 8 && !set(cs, 3)) cs *= 2;
+  while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
+  if (!set(cs, 3)) set(cs, 2);
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(kMaxSmem / s.smem, max_threads(hc) / s.threads));
+  s.clusters = std::min({T, std::max<int64_t>(1, kSms * resident / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
+  return s;
+}
+
+template <int HC, int S>
+cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, cudaStream_t s) {
+  auto kern = gate_grad_kernel<HC, S>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = ENGRAM_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = sh.cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(sh.threads);
+  cfg.dynamicSmemBytes = sh.smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // no more clusters than can be resident: one that had to wait would run its share of the tokens alone
+  cfg.gridDim = dim3((unsigned)(sh.clusters * sh.cs));
+  int64_t clusters = sh.clusters;
+  if (sh.cs > 1 && clusters > 1) {
+    int resident = 0;
+    e = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    clusters = std::max<int64_t>(1, std::min<int64_t>(clusters, resident));
+  }
+  unsigned int* status = nullptr;
+  e = device_status_word(&status);
+  if (e != cudaSuccess) return e;
+  *parts = (int)clusters;
+  cfg.gridDim = dim3((unsigned)(clusters * sh.cs));
+  return cudaLaunchKernelEx(&cfg, kern, a, 1.0f / (float)a.dim, (float)(1.0 / sqrt((double)a.dim)), sh.nv, sh.cs, part,
+                            status);
+}
+
 }  // namespace
 
 uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
-  return round256((uint64_t)T * hc * 4) + round256((uint64_t)kSplits * hc * dim * 4);
+  return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
 }
 
 cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s) {
-  float* cs = static_cast<float*>(workspace);
-  float* part = cs + round256((uint64_t)a.T * a.hc * 4) / 4;
-  const float rd = 1.0f / (float)a.dim, isd = (float)(1.0 / sqrt((double)a.dim));
-  const int splits = (int)std::min<int64_t>(a.T, kSplits);
-  cudaError_t e = cudaSuccess;
+  float* part = static_cast<float*>(workspace);
+  int parts = 0;
   if (a.T > 0) {
-    auto go = [&](auto hc) {
-      return launch_pdl(gate_grad_kernel<hc()>, dim3((unsigned)a.T), dim3(kThreads), 0, s, a, rd, isd, cs);
-    };
+    const Shape sh = shape_of(a.T, a.hc, a.dim);
+    cudaError_t e = cudaErrorInvalidValue;
     switch (a.hc) {
-      case 1: e = go(std::integral_constant<int, 1>{}); break;
-      case 2: e = go(std::integral_constant<int, 2>{}); break;
-      case 4: e = go(std::integral_constant<int, 4>{}); break;
-      case 8: e = go(std::integral_constant<int, 8>{}); break;
-      default: return cudaErrorInvalidValue;
+      case 1: e = launch_shape<1, 3>(a, sh, part, &parts, s); break;
+      case 2: e = launch_shape<2, 3>(a, sh, part, &parts, s); break;
+      case 4: e = launch_shape<4, 3>(a, sh, part, &parts, s); break;
+      case 8:
+        e = sh.stages == 3 ? launch_shape<8, 3>(a, sh, part, &parts, s) : launch_shape<8, 2>(a, sh, part, &parts, s);
+        break;
     }
     if (e != cudaSuccess) return e;
-    e = launch_pdl(gate_weight_sums_kernel, dim3((a.dim + kThreads - 1) / kThreads, a.hc, splits), dim3(kThreads), 0,
-                   s, a, (const float*)cs, part);
-    if (e != cudaSuccess) return e;
   }
-  return launch_pdl(gate_weight_finish_kernel, dim3((a.hc * a.dim + kThreads - 1) / kThreads), dim3(kThreads), 0, s, a,
-                    (const float*)part, splits);
+  return launch_pdl(gate_weight_finish_kernel, dim3((a.hc * a.dim + 127) / 128), dim3(kFinishThreads), 0, s, a,
+                    (const float*)part, parts);
 }
 
 }  // namespace engram

@@ -34,6 +34,7 @@
 // flight, frees its tensor memory and exits.
 #include <cuda.h>
 
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -965,6 +966,27 @@ __global__ void device_status_take_kernel(int clear) {
   g_device_status_taken = clear ? atomicExch(&g_device_status, 0u) : atomicOr(&g_device_status, 0u);
 }
 }  // namespace
+
+// The device address of the status word on the current device, for kernels of other files that give up
+// a wait (looked up once per device).
+cudaError_t device_status_word(unsigned int** out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<unsigned int*> words[kMaxDevices];
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  unsigned int* p = words[dev].load(std::memory_order_relaxed);
+  if (p == nullptr) {
+    void* q = nullptr;
+    e = cudaGetSymbolAddress(&q, g_device_status);
+    if (e != cudaSuccess) return e;
+    p = static_cast<unsigned int*>(q);
+    words[dev].store(p, std::memory_order_relaxed);
+  }
+  *out = p;
+  return cudaSuccess;
+}
 
 // Read (and optionally clear, in one atomic step) the device status word, ordered after the work
 // already on stream s; synchronises s.

@@ -49,6 +49,8 @@ cudaError_t launch_lookup_project_gate_sums(const uint16_t* x, const LookupArgs&
 cudaError_t launch_gate_finish(const uint16_t* x, const uint16_t* value, const float* part, const uint8_t* mask,
                                int64_t T, int hc, int dim, float eps, uint16_t* out, cudaStream_t s);
 
+// the word that ENGRAM_STATUS_TIMEOUT is raised in
+cudaError_t device_status_word(unsigned int** out);
 cudaError_t device_status_take(unsigned int* flags, int clear, cudaStream_t s);
 
 // sharded lookup: segments of the pack's count pass (one int32 count per segment and bucket)
