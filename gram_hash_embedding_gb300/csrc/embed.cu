@@ -46,44 +46,69 @@ __global__ void __launch_bounds__(kThreads)
 // -------------------------------------------------------------------------------------- radix sort
 // Least significant digit first, up to kMaxBits bits a pass; per pass a count of every digit per
 // tile, a scan over the tiles of each digit, and a stable scatter. Keys are row ids as 32-bit values,
-// with `rows` itself standing for every id outside the table, so those sort to the end.
-constexpr int kMaxBits = 8;
+// with `rows` itself standing for every id outside the table, so those sort to the end. The first count
+// also writes the keys, so that the ids are read once.
+constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kPerThread = 16;
 constexpr int kTile = kThreads * kPerThread;  // pairs per tile (one CTA)
 
 struct SortPass {
-  const uint32_t* key_in;  // null in the first pass: keys come from the ids, positions are implicit
-  const uint32_t* pos_in;
+  uint32_t* key_in;        // written by the first pass's count
+  const uint32_t* pos_in;  // null in the first pass: the positions are 0, 1, 2, ...
   uint32_t* key_out;
   uint32_t* pos_out;
   uint32_t* counts;  // [bins][tiles]
   uint32_t* totals;  // [bins]
   int64_t n;
-  int32_t tiles, shift, bins;
+  int32_t tiles, shift, bits;
 };
 
-__device__ __forceinline__ uint32_t key_at(const EmbedArgs& e, const SortPass& p, int64_t i) {
-  if (p.key_in != nullptr) return p.key_in[i];
-  const int64_t t = i / e.n_cols;
-  const int64_t r = e.idx[t * e.idx_stride + (i - t * e.n_cols)];
+__device__ __forceinline__ uint32_t key_of_id(const EmbedArgs& e, uint32_t i) {
+  int64_t at = i;
+  if (e.idx_stride != e.n_cols) {
+    const uint32_t t = i / (uint32_t)e.n_cols;
+    at = (int64_t)t * e.idx_stride + (i - t * (uint32_t)e.n_cols);
+  }
+  const int64_t r = e.idx[at];
   return r >= 0 && r < e.rows ? (uint32_t)r : (uint32_t)e.rows;
 }
 
+// lanes of the warp with the same `bits`-bit digit (a ballot per bit)
+__device__ __forceinline__ unsigned same_digit(uint32_t d, int bits, unsigned in) {
+  unsigned m = in;
+  for (int b = 0; b < bits; ++b) {
+    const unsigned v = __ballot_sync(0xffffffffu, (d >> b) & 1);
+    m &= (d >> b) & 1 ? v : ~v;
+  }
+  return m;
+}
+
+template <bool FIRST>
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const EmbedArgs e, const SortPass p) {
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t hist[kMaxBins];
-  for (int b = threadIdx.x; b < p.bins; b += kThreads) hist[b] = 0;
+  const int bins = 1 << p.bits;
+  for (int b = threadIdx.x; b < bins; b += kThreads) hist[b] = 0;
   __syncthreads();
-  const int64_t base = (int64_t)blockIdx.x * kTile;
-#pragma unroll 4
+  const uint32_t base = blockIdx.x * (uint32_t)kTile, n = (uint32_t)p.n;
+  uint32_t key[kPerThread];
+#pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const int64_t i = base + j * kThreads + threadIdx.x;
-    if (i < p.n) atomicAdd(&hist[(key_at(e, p, i) >> p.shift) & (p.bins - 1)], 1u);
+    const uint32_t i = base + j * kThreads + threadIdx.x;
+    if (i < n) key[j] = FIRST ? key_of_id(e, i) : p.key_in[i];
+  }
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const uint32_t i = base + j * kThreads + threadIdx.x;
+    if (i < n) {
+      if (FIRST) p.key_in[i] = key[j];
+      atomicAdd(&hist[(key[j] >> p.shift) & (bins - 1)], 1u);
+    }
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < p.bins; b += kThreads) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
+  for (int b = threadIdx.x; b < bins; b += kThreads) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
 }
 
 // one warp per digit: counts[b][tile] becomes the pairs of digit b in the tiles before
@@ -91,25 +116,32 @@ __global__ void __launch_bounds__(kThreads) sort_scan_kernel(const SortPass p) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= p.bins) return;
+  if (b >= 1 << p.bits) return;
   uint32_t* c = p.counts + (int64_t)b * p.tiles;
   uint32_t run = 0;
-  for (int t0 = 0; t0 < p.tiles; t0 += 32) {
-    const int t = t0 + lane;
-    const uint32_t v = t < p.tiles ? c[t] : 0u;
-    uint32_t x = v;
+  constexpr int kAhead = 4;
+  for (int t0 = 0; t0 < p.tiles; t0 += 32 * kAhead) {
+    uint32_t v[kAhead];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    for (int j = 0; j < kAhead; ++j) v[j] = t0 + 32 * j + lane < p.tiles ? c[t0 + 32 * j + lane] : 0u;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = t0 + 32 * j + lane;
+      uint32_t x = v[j];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (t < p.tiles) c[t] = run + x - v[j];
+      run += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (t < p.tiles) c[t] = run + x - v;
-    run += __shfl_sync(0xffffffffu, x, 31);
   }
   if (lane == 0) p.totals[b] = run;
 }
 
-// exclusive scan over the block of one value per thread
+// exclusive scan over the block of one value per thread; warp_sums: 32 words
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t x = v;
@@ -120,83 +152,131 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_sums[w];
+  // every warp sums the warps before it
+  uint32_t s = lane < warp && lane < THREADS / 32 ? warp_sums[lane] : 0u;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   __syncthreads();
-  return before + x - v;
+  return s + x - v;
 }
 
-__global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const EmbedArgs e, const SortPass p) {
+// The places of a CTA's pairs in its sorted tile: WARPS warps of 32 * PER consecutive pairs, taken 32 at a time,
+// so (warp, step, lane) is their order. wh: [WARPS][1 << bits]; start: [1 << bits], on return
+// the first place of each digit.
+template <int WARPS, int PER>
+__device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], uint32_t (&place)[PER], int left, int shift,
+                                          int bits, uint16_t* wh, uint32_t* start, uint32_t* warp_sums) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = 1 << bits;
+  uint32_t* wz = reinterpret_cast<uint32_t*>(wh);
+  for (int b = tid; b < (WARPS << bits) / 2; b += WARPS * 32) wz[b] = 0;
+  __syncthreads();
+  uint16_t* mine = wh + (warp << bits);
+  const int base = warp * 32 * PER + lane;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool in = base + j * 32 < left;
+    const uint32_t d = (key[j] >> shift) & (bins - 1);
+    const unsigned same = same_digit(d, bits, __ballot_sync(0xffffffffu, in));
+    const int before = __popc(same & ((1u << lane) - 1u));
+    uint32_t have = 0;
+    if (in) have = mine[d];
+    __syncwarp();
+    if (in && before == 0) mine[d] = (uint16_t)(have + __popc(same));
+    __syncwarp();
+    place[j] = have + before;
+  }
+  __syncthreads();
+  // per digit: the warps' starts among each other and the tile's count; a thread has consecutive digits
+  constexpr int kDigits = (kMaxBins + WARPS * 32 - 1) / (WARPS * 32);
+  const int per = (bins + WARPS * 32 - 1) / (WARPS * 32);
+  uint32_t cnt[kDigits], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kDigits; ++q) {
+    const int d = tid * per + q;
+    cnt[q] = 0;
+    if (q < per && d < bins) {
+      uint32_t c[WARPS];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) c[w] = wh[(w << bits) + d];
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        wh[(w << bits) + d] = (uint16_t)cnt[q];
+        cnt[q] += c[w];
+      }
+    }
+    sum += cnt[q];
+  }
+  uint32_t at = block_exclusive<WARPS * 32>(sum, warp_sums);
+#pragma unroll
+  for (int q = 0; q < kDigits; ++q) {
+    const int d = tid * per + q;
+    if (q < per && d < bins) start[d] = at;
+    at += cnt[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const uint32_t d = (key[j] >> shift) & (bins - 1);
+    place[j] += start[d] + mine[d];
+  }
+}
+
+constexpr int kScatterSmem = kTile * 8 + (kThreads / 32) * kMaxBins * 2 + kMaxBins * 8 + 32 * 4;
+
+template <bool FIRST>
+__global__ void __launch_bounds__(kThreads, 3) sort_scatter_kernel(const SortPass p) {
   pdl_wait();
   pdl_trigger();
   constexpr int kWarps = kThreads / 32;
-  __shared__ uint32_t wh[kWarps][kMaxBins];  // pairs of each digit in each warp, then where they start
-  __shared__ uint32_t start[kMaxBins];       // a digit's first place in the sorted tile
-  __shared__ uint32_t gbase[kMaxBins];       // its first place in the output, less start
-  __shared__ uint32_t warp_sums[kWarps];
-  __shared__ uint32_t sk[kTile], sp[kTile];  // the tile in digit order
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int b = tid; b < kWarps * kMaxBins; b += kThreads) (&wh[0][0])[b] = 0;
-  __syncthreads();
-  // a warp takes 32 * kPerThread consecutive pairs, 32 at a time, so (step, lane) is position order
-  const int64_t base = (int64_t)blockIdx.x * kTile + (int64_t)warp * 32 * kPerThread;
-  uint32_t key[kPerThread], pos[kPerThread], rank[kPerThread];
+  extern __shared__ uint32_t smem[];
+  uint32_t* sk = smem;                                         // [kTile] the tile in digit order
+  uint32_t* sp = sk + kTile;                                   // [kTile]
+  uint32_t* start = sp + kTile;                                // [kMaxBins]
+  uint32_t* gbase = start + kMaxBins;                          // [kMaxBins] a digit's first place in the output, less start
+  uint32_t* warp_sums = gbase + kMaxBins;                      // [32]
+  uint16_t* wh = reinterpret_cast<uint16_t*>(warp_sums + 32);  // [kWarps][kMaxBins]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = 1 << p.bits;
+  const int64_t tile0 = (int64_t)blockIdx.x * kTile;
+  const int left = (int)min((int64_t)kTile, p.n - tile0);
+  uint32_t key[kPerThread], pos[kPerThread], place[kPerThread];
+  const int base = warp * 32 * kPerThread + lane;
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const int64_t i = base + j * 32 + lane;
-    if (i < p.n) {
-      key[j] = key_at(e, p, i);
-      pos[j] = p.key_in != nullptr ? p.pos_in[i] : (uint32_t)i;
+    key[j] = 0;
+    pos[j] = (uint32_t)(tile0 + base + j * 32);
+    if (base + j * 32 < left) {
+      key[j] = p.key_in[tile0 + base + j * 32];
+      if (!FIRST) pos[j] = p.pos_in[tile0 + base + j * 32];
     }
   }
+  // where each digit goes: the digits before it, the same digit in the tiles before
+  const int per = (bins + kThreads - 1) / kThreads;
+  uint32_t tot[kMaxBins / kThreads], sum = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxBins / kThreads; ++q) {
+    const int d = tid * per + q;
+    tot[q] = q < per && d < bins ? p.totals[d] : 0u;
+    sum += tot[q];
+  }
+  uint32_t all = block_exclusive<kThreads>(sum, warp_sums);
+#pragma unroll
+  for (int q = 0; q < kMaxBins / kThreads; ++q) {
+    const int d = tid * per + q;
+    if (q < per && d < bins) gbase[d] = all + p.counts[(int64_t)d * p.tiles + blockIdx.x];
+    all += tot[q];
+  }
+  rank_tile<kWarps, kPerThread>(key, place, left, p.shift, p.bits, wh, start, warp_sums);
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const int64_t i = base + j * 32 + lane;
-    const bool in = i < p.n;
-    const uint32_t d = in ? (key[j] >> p.shift) & (p.bins - 1) : 0xffffffffu;
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    const int before = __popc(same & ((1u << lane) - 1u));
-    uint32_t have = 0;
-    if (in) have = wh[warp][d];
-    __syncwarp();
-    if (in && before == 0) wh[warp][d] = have + __popc(same);
-    __syncwarp();
-    rank[j] = have + before;
-  }
-  __syncthreads();
-  // per digit: the warps' starts, the tile's total
-  uint32_t total = 0;
-  if (tid < p.bins) {
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const uint32_t c = wh[w][tid];
-      wh[w][tid] = total;
-      total += c;
-    }
-  }
-  const uint32_t first = block_exclusive(tid < p.bins ? total : 0u, warp_sums);
-  const uint32_t all = block_exclusive(tid < p.bins ? p.totals[tid] : 0u, warp_sums);
-  if (tid < p.bins) {
-    start[tid] = first;
-    gbase[tid] = all + p.counts[(int64_t)tid * p.tiles + blockIdx.x] - first;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    const int64_t i = base + j * 32 + lane;
-    if (i < p.n) {
-      const uint32_t d = (key[j] >> p.shift) & (p.bins - 1);
-      const uint32_t at = start[d] + wh[warp][d] + rank[j];
-      sk[at] = key[j];
-      sp[at] = pos[j];
+    if (base + j * 32 < left) {
+      sk[place[j]] = key[j];
+      sp[place[j]] = pos[j];
     }
   }
   __syncthreads();
-  const int64_t left = p.n - (int64_t)blockIdx.x * kTile;
-  const int m = left < kTile ? (int)left : kTile;
-  for (int i = tid; i < m; i += kThreads) {
-    const uint32_t k = sk[i];
-    const uint32_t g = gbase[(k >> p.shift) & (p.bins - 1)] + i;
+  for (int i = tid; i < left; i += kThreads) {
+    const uint32_t k = sk[i], d = (k >> p.shift) & (bins - 1);
+    const uint32_t g = gbase[d] + (i - start[d]);
     p.key_out[g] = k;
     p.pos_out[g] = sp[i];
   }
@@ -209,21 +289,43 @@ __global__ void __launch_bounds__(kThreads) sort_scatter_kernel(const EmbedArgs 
 constexpr int kSegTile = 2048;
 constexpr uint32_t kNone = 0xffffffffu;
 
-__device__ __forceinline__ bool is_head(const uint32_t* key, int64_t i, uint32_t rows) {
-  const uint32_t k = key[i];
-  return k < rows && (i == 0 || key[i - 1] != k);
+constexpr int kSegPer = kSegTile / kThreads;
+
+// bit j: pair i0 + j begins a segment. The keys are read 4 at a time; the array reaches kBatch past n.
+__device__ __forceinline__ uint32_t head_bits(const uint32_t* key, int64_t i0, int64_t n, uint32_t rows,
+                                              uint32_t (&k)[kSegPer]) {
+  uint32_t bits = 0;
+  if (i0 >= n) return 0;
+#pragma unroll
+  for (int j = 0; j < kSegPer; j += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(key + i0 + j);
+    k[j] = v.x;
+    k[j + 1] = v.y;
+    k[j + 2] = v.z;
+    k[j + 3] = v.w;
+  }
+  uint32_t before = i0 == 0 ? ~k[0] : key[i0 - 1];
+#pragma unroll
+  for (int j = 0; j < kSegPer; ++j) {
+    if (i0 + j < n && k[j] < rows && k[j] != before) bits |= 1u << j;
+    before = k[j];
+  }
+  return bits;
 }
 
 __global__ void __launch_bounds__(kThreads) head_count_kernel(const uint32_t* __restrict__ key, int64_t n,
                                                               uint32_t rows, uint32_t* __restrict__ heads) {
   pdl_wait();
   pdl_trigger();
-  int c = 0;
-  for (int j = threadIdx.x; j < kSegTile; j += kThreads) {
-    const int64_t i = (int64_t)blockIdx.x * kSegTile + j;
-    c += __syncthreads_count(i < n && is_head(key, i, rows));
-  }
-  if (threadIdx.x == 0) heads[blockIdx.x] = (uint32_t)c;
+  __shared__ uint32_t sum;
+  if (threadIdx.x == 0) sum = 0;
+  __syncthreads();
+  uint32_t k[kSegPer];
+  const int c = __popc(head_bits(key, ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kSegPer, n, rows, k));
+  const int w = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&sum, (uint32_t)w);
+  __syncthreads();
+  if (threadIdx.x == 0) heads[blockIdx.x] = sum;
 }
 
 // ids, and the sparse form's grad_rows (-1 past the count) and count
@@ -234,30 +336,41 @@ __global__ void __launch_bounds__(kThreads)
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t sum_s[2];
-  __shared__ uint32_t warp_sums[kThreads / 32];
+  __shared__ uint32_t warp_sums[32];
   if (threadIdx.x < 2) sum_s[threadIdx.x] = 0;
   __syncthreads();
+  const int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kSegPer;
+  uint32_t k[kSegPer];
+  const uint32_t bits = head_bits(key, i0, n, rows, k);
   uint32_t before = 0, all = 0;
   for (int t = threadIdx.x; t < tiles; t += kThreads) {
     const uint32_t h = heads[t];
     all += h;
     if (t < (int)blockIdx.x) before += h;
   }
-  atomicAdd(&sum_s[0], before);
-  atomicAdd(&sum_s[1], all);
-  __syncthreads();
-  uint32_t u = sum_s[0];
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if ((threadIdx.x & 31) == 0) {
+    atomicAdd(&sum_s[0], before);
+    atomicAdd(&sum_s[1], all);
+  }
+  const uint32_t off = block_exclusive<kThreads>(__popc(bits), warp_sums);
+  uint32_t u = sum_s[0] + off;
   const uint32_t total = sum_s[1];
+  uint32_t id[kSegPer];
+#pragma unroll
+  for (int j = 0; j < kSegPer; ++j) {
+    if (bits >> j & 1) grad_rows[u++] = k[j];
+    id[j] = i0 < n && k[j] < rows ? u - 1 : kNone;
+  }
+  if (i0 < n) {
+#pragma unroll
+    for (int j = 0; j < kSegPer; j += 4)
+      *reinterpret_cast<uint4*>(ids + i0 + j) = make_uint4(id[j], id[j + 1], id[j + 2], id[j + 3]);
+  }
   for (int j = threadIdx.x; j < kSegTile; j += kThreads) {
     const int64_t i = (int64_t)blockIdx.x * kSegTile + j;
-    const bool h = i < n && is_head(key, i, rows);
-    const uint32_t off = block_exclusive(h ? 1u : 0u, warp_sums);
-    if (h) grad_rows[u + off] = key[i];
-    if (i < n) {
-      ids[i] = key[i] < rows ? u + off - (h ? 0u : 1u) : kNone;
-      if (i >= (int64_t)total) grad_rows[i] = -1;
-    }
-    u += __syncthreads_count(h);
+    if (i < n && i >= (int64_t)total) grad_rows[i] = -1;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *count = total;
 }
@@ -272,7 +385,7 @@ __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallPer = 8;
 constexpr int kSmall = kSmallThreads * kSmallPer;
-constexpr int kSmallSmem = kSmall * 4 + kSmall * 2 + (kSmallThreads / 32) * kMaxBins * 2 + kMaxBins * 4 + 64 * 4;
+constexpr int kSmallSmem = kSmall * 4 + kSmall * 2 + (kSmallThreads / 32) * kMaxBins * 2 + kMaxBins * 4 + 32 * 4;
 
 __global__ void __launch_bounds__(kSmallThreads)
     sort_small_kernel(const EmbedArgs e, const int n, const int passes, const int width, uint32_t* __restrict__ key_out,
@@ -283,64 +396,28 @@ __global__ void __launch_bounds__(kSmallThreads)
   constexpr int kWarps = kSmallThreads / 32;
   extern __shared__ uint32_t smem[];
   uint32_t* sk = smem;                                         // [kSmall] keys
-  uint32_t* start = sk + kSmall;                               // [kMaxBins] first place of each digit
-  uint32_t* warp_sums = start + kMaxBins;                      // [64]
-  uint16_t* sp = reinterpret_cast<uint16_t*>(warp_sums + 64);  // [kSmall] positions
-  uint16_t* wh = sp + kSmall;                                  // [kWarps][kMaxBins] counts, then starts
+  uint32_t* start = sk + kSmall;                               // [kMaxBins]
+  uint32_t* warp_sums = start + kMaxBins;                      // [32]
+  uint16_t* sp = reinterpret_cast<uint16_t*>(warp_sums + 32);  // [kSmall] positions
+  uint16_t* wh = sp + kSmall;                                  // [kWarps][1 << width]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rows = (uint32_t)e.rows;
-  uint32_t key[kSmallPer];
+  uint32_t key[kSmallPer], place[kSmallPer];
   uint16_t pos[kSmallPer];
-  const int base = warp * 32 * kSmallPer + lane;  // (warp, step, lane) is position order
+  const int base = warp * 32 * kSmallPer + lane;
 #pragma unroll
   for (int j = 0; j < kSmallPer; ++j) {
     const int i = base + j * 32;
-    key[j] = rows;
     pos[j] = (uint16_t)i;
-    if (i < n) {
-      const int t = i / e.n_cols;
-      const int64_t r = e.idx[t * e.idx_stride + (i - t * e.n_cols)];
-      if (r >= 0 && r < e.rows) key[j] = (uint32_t)r;
-    }
+    key[j] = i < n ? key_of_id(e, i) : rows;
   }
   for (int q = 0; q < passes; ++q) {
-    const int shift = q * width, bins = 1 << width;
-    for (int b = tid; b < kWarps * kMaxBins / 2; b += kSmallThreads) reinterpret_cast<uint32_t*>(wh)[b] = 0;
-    __syncthreads();
-    uint16_t rank[kSmallPer];
-#pragma unroll
-    for (int j = 0; j < kSmallPer; ++j) {
-      const bool in = base + j * 32 < n;
-      const uint32_t d = in ? (key[j] >> shift) & (bins - 1) : 0xffffffffu;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      uint32_t have = 0;
-      if (in) have = wh[warp * kMaxBins + d];
-      __syncwarp();
-      if (in && before == 0) wh[warp * kMaxBins + d] = (uint16_t)(have + __popc(same));
-      __syncwarp();
-      rank[j] = (uint16_t)(have + before);
-    }
-    __syncthreads();
-    // per digit: exclusive sums over the warps
-    uint32_t total = 0;
-    if (tid < bins) {
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t c = wh[w * kMaxBins + tid];
-        wh[w * kMaxBins + tid] = (uint16_t)total;
-        total += c;
-      }
-    }
-    const uint32_t first = block_exclusive(tid < bins ? total : 0u, warp_sums);
-    if (tid < bins) start[tid] = first;
-    __syncthreads();
+    rank_tile<kWarps, kSmallPer>(key, place, n, q * width, width, wh, start, warp_sums);
 #pragma unroll
     for (int j = 0; j < kSmallPer; ++j) {
       if (base + j * 32 < n) {
-        const uint32_t d = (key[j] >> shift) & (bins - 1);
-        const uint32_t at = start[d] + wh[warp * kMaxBins + d] + rank[j];
-        sk[at] = key[j];
-        sp[at] = pos[j];
+        sk[place[j]] = key[j];
+        sp[place[j]] = pos[j];
       }
     }
     __syncthreads();
@@ -359,7 +436,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     const int i = i0 + j;
     if (i < n && sk[i] < rows && (i == 0 || sk[i - 1] != sk[i])) heads++;
   }
-  uint32_t u = block_exclusive(heads, warp_sums);
+  uint32_t u = block_exclusive<kSmallThreads>(heads, warp_sums);
   if (tid == kSmallThreads - 1) start[0] = u + heads;
   for (int j = 0; j < kSmallPer; ++j) {
     const int i = i0 + j;
@@ -767,7 +844,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
     const int tiles = (int)ceil_div(n, kTile);
     for (int q = 0; q < passes; ++q) {
       SortPass p;
-      p.key_in = q == 0 ? nullptr : u32(l.key[q & 1]);
+      p.key_in = u32(l.key[q & 1]);
       p.pos_in = q == 0 ? nullptr : u32(l.pos[q & 1]);
       p.key_out = u32(l.key[(q + 1) & 1]);
       p.pos_out = u32(l.pos[(q + 1) & 1]);
@@ -776,12 +853,17 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       p.n = n;
       p.tiles = tiles;
       p.shift = q * width;
-      p.bins = 1 << std::min(width, 32 - q * width);
-      e = launch_pdl(sort_count_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+      p.bits = std::min(width, 32 - q * width);
+      auto count = q == 0 ? sort_count_kernel<true> : sort_count_kernel<false>;
+      e = launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
       if (e != cudaSuccess) return e;
-      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div(p.bins, kThreads / 32)), dim3(kThreads), 0, s, p);
+      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, kThreads / 32)), dim3(kThreads), 0,
+                     s, p);
       if (e != cudaSuccess) return e;
-      e = launch_pdl(sort_scatter_kernel, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+      auto scatter = q == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
+      e = cudaFuncSetAttribute(scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, kScatterSmem);
+      if (e != cudaSuccess) return e;
+      e = launch_pdl(scatter, dim3(tiles), dim3(kThreads), kScatterSmem, s, p);
       if (e != cudaSuccess) return e;
     }
     key = u32(l.key[passes & 1]);
