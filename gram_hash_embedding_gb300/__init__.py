@@ -181,14 +181,24 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# the current stream's handle without a Stream object around it (0.4 us a call instead of 2.9)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream_handle() -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
+
+
 def _launch_stream(stream, temps=()) -> int:
     """The stream handle a call launches on. The wrapper's own temporaries (a start_pos array built
     from an int, outputs it allocates) are made on the current stream; when the caller names another
     stream, that stream first waits for the current one, and each temporary is marked as in use on it
     so the caching allocator does not hand its memory out again before the library's kernel is done."""
-    cur = torch.cuda.current_stream()
     if stream is None:
-        return cur.cuda_stream
+        return _current_stream_handle()
+    cur = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if handle == cur.cuda_stream:
@@ -769,6 +779,8 @@ def sharded_lookup(idx: torch.Tensor, W_shard: torch.Tensor, S_shard: torch.Tens
 
 
 # ----------------------------------------------------------------------------- training operators
+# A training step makes many small calls, so these wrappers check a call's tensors in one pass each and
+# allocate no more than the call returns: Python's share of a small call is what it costs.
 def _float_type(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -777,25 +789,50 @@ def _float_type(t: torch.Tensor, name: str) -> int:
     return _TYPE_OF_DTYPE[t.dtype]
 
 
+def _pointers(specs) -> list:
+    """The device pointers of (tensor, dtype, elements, name) specifications, all of them contiguous CUDA
+    tensors of that type and size; otherwise the error that _size or _dev raises."""
+    try:
+        ptrs = [t.data_ptr() for t, dtype, n, _ in specs
+                if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous()]
+    except AttributeError:
+        ptrs = ()
+    if len(ptrs) != len(specs):
+        for t, _, n, name in specs:
+            _size(t, n, name)
+        for t, dtype, _, name in specs:
+            _dev(t, dtype, name)
+    return ptrs
+
+
+def _scratch(workspace, need: int, device) -> tuple:
+    """(the tensor to keep alive, pointer, bytes) of a caller's workspace, or of one made for this call."""
+    if workspace is not None:
+        return (workspace, *_workspace(workspace, need, device, []))
+    ws = torch.empty(need if need > 256 else 256, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), ws.numel()
+
+
 def _embed_ids(idx: torch.Tensor):
     """Row ids of a lookup: int64 [T, C] with unit stride along C, or any contiguous shape (then one
     column): (pointer, row stride, T, C)."""
-    if not isinstance(idx, torch.Tensor) or not idx.is_cuda or idx.dtype != torch.int64:
+    if not isinstance(idx, torch.Tensor) or not idx.is_cuda or idx.dtype is not torch.int64:
         raise TypeError("idx must be an int64 CUDA tensor")
-    if idx.dim() == 2 and idx.shape[1] > 0 and not idx.is_contiguous():
-        return _hash_ids(idx)
+    shape = idx.shape
+    if len(shape) == 2 and shape[1] > 0:
+        return (idx.data_ptr(), shape[1], shape[0], shape[1]) if idx.is_contiguous() else _hash_ids(idx)
     if not idx.is_contiguous():
         raise ValueError(f"idx must be contiguous, or [T, C] with unit stride along C, got strides {idx.stride()}")
-    return (idx.data_ptr(),) + ((idx.shape[1], *idx.shape) if idx.dim() == 2 and idx.shape[1] > 0
-                                else (1, idx.numel(), 1))
+    return idx.data_ptr(), 1, idx.numel(), 1
 
 
 def _rows_of(t: torch.Tensor, name: str):
     """A table [rows, dim] with unit stride along dim: (pointer, rows, dim, row stride)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [rows, dim] with unit stride along dim, got shape {tuple(t.shape)} "
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, dim] with unit stride along dim, got shape {tuple(shape)} "
                          f"strides {t.stride()}")
-    rows, dim = t.shape
+    rows, dim = shape
     stride = t.stride(0) if rows > 1 else dim
     if stride < dim:
         raise ValueError(f"{name}: rows overlap")
@@ -811,16 +848,16 @@ def engram_embed(idx: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: to
     wt = _float_type(W, "W")
     wp, rows, dim, stride = _rows_of(W, "W")
     ip, istride, T, C = _embed_ids(idx)
-    temps = []
     if out is None:
-        out = torch.empty(tuple(idx.shape) + (dim,), dtype=out_dtype or W.dtype, device=idx.device)
-        temps.append(out)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
-    _size(out, T * C * dim, "out")
-    ot = _float_type(out, "out")
-    _check(_lib().engram_embed(ip, istride, T, C, wp, rows, dim, stride, wt, float(scale), _dev(out, out.dtype, "out"),
-                               ot, _launch_stream(stream, temps)), "engram_embed")
+        out = torch.empty((*idx.shape, dim), dtype=out_dtype or W.dtype, device=idx.device)
+        ot, op = _float_type(out, "out"), out.data_ptr()
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+        _size(out, T * C * dim, "out")
+        ot, op = _float_type(out, "out"), _dev(out, out.dtype, "out")
+    _check(_lib().engram_embed(ip, istride, T, C, wp, rows, dim, stride, wt, float(scale), op, ot,
+                               _launch_stream(stream, (out,))), "engram_embed")
     return out
 
 
@@ -859,25 +896,26 @@ def engram_embed_grad(idx: torch.Tensor, dout: torch.Tensor, rows: int, scale: f
     ip, istride, T, C = _embed_ids(idx)
     dt = _float_type(dout, "dout")
     dp, dstride, dim = _embed_dout(dout, T, C)
-    n, dev, temps = T * C, idx.device, []
+    n, dev = T * C, idx.device
+    temps = []
     if grad_rows is None:
         grad_rows = torch.empty(n, dtype=torch.int64, device=dev)
         temps.append(grad_rows)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int64, device=dev)
+        temps.append(count)
+    rp, cp = _pointers(((grad_rows, torch.int64, n, "grad_rows"), (count, torch.int64, 1, "count")))
     if grad is None:
         grad = torch.empty((n, dim), dtype=grad_dtype or torch.float32, device=dev)
         temps.append(grad)
     elif grad_dtype is not None and grad.dtype != grad_dtype:
         raise TypeError(f"grad is {grad.dtype}, not {grad_dtype}")
-    if count is None:
-        count = torch.empty(1, dtype=torch.int64, device=dev)
-        temps.append(count)
-    _size(grad_rows, n, "grad_rows")
+    gt = _float_type(grad, "grad")
     _size(grad, n * dim, "grad")
-    _size(count, 1, "count")
-    ws, nbytes = _workspace(workspace, engram_embed_grad_workspace(n, rows, dim), dev, temps)
-    _check(_lib().engram_embed_grad(ip, istride, T, C, dp, dstride, dt, int(rows), dim, float(scale),
-                                    _dev(grad_rows, torch.int64, "grad_rows"), _dev(grad, grad.dtype, "grad"),
-                                    _float_type(grad, "grad"), _dev(count, torch.int64, "count"), ws, nbytes,
+    keep, ws, nbytes = _scratch(workspace, _lib().engram_embed_grad_workspace(n, int(rows), dim), dev)
+    temps.append(keep)
+    _check(_lib().engram_embed_grad(ip, istride, T, C, dp, dstride, dt, int(rows), dim, float(scale), rp,
+                                    _dev(grad, grad.dtype, "grad"), gt, cp, ws, nbytes,
                                     _launch_stream(stream, temps)), "engram_embed_grad")
     return grad_rows, grad, count
 
@@ -894,10 +932,9 @@ def engram_embed_grad_dense(idx: torch.Tensor, dout: torch.Tensor, grad: torch.T
     dp, dstride, ddim = _embed_dout(dout, T, C)
     if ddim != dim:
         raise ValueError(f"dout has rows of {ddim} values, grad of {dim}")
-    temps = []
-    ws, nbytes = _workspace(workspace, engram_embed_grad_workspace(T * C, rows, dim), idx.device, temps)
+    keep, ws, nbytes = _scratch(workspace, _lib().engram_embed_grad_workspace(T * C, rows, dim), idx.device)
     _check(_lib().engram_embed_grad_dense(ip, istride, T, C, dp, dstride, dt, rows, dim, float(scale), gp, gstride, gt,
-                                          int(bool(accumulate)), ws, nbytes, _launch_stream(stream, temps)),
+                                          int(bool(accumulate)), ws, nbytes, _launch_stream(stream, (keep,))),
            "engram_embed_grad_dense")
     return grad
 
@@ -915,8 +952,9 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
     """The gradient of engram_gate (same x, kv, weights, mask, eps) for dout, the gradient of its output.
     Returns (or fills) dx bf16 like x (may be dout), dkv bf16 like kv, and dq_weight, dk_weight float32
     [hc, dim], summed over the tokens in a fixed order. A masked token passes dout through."""
-    hc, dim = x.shape[-2], x.shape[-1]
+    hc, dim = x.shape[-2:]
     T = x.numel() // (hc * dim)
+    bf, f32, dev = torch.bfloat16, torch.float32, x.device
     temps = []
     if dx is None:
         dx = torch.empty_like(x)
@@ -925,22 +963,22 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
         dkv = torch.empty_like(kv)
         temps.append(dkv)
     if dq_weight is None:
-        dq_weight = torch.empty((hc, dim), dtype=torch.float32, device=x.device)
+        dq_weight = torch.empty((hc, dim), dtype=f32, device=dev)
         temps.append(dq_weight)
     if dk_weight is None:
-        dk_weight = torch.empty((hc, dim), dtype=torch.float32, device=x.device)
+        dk_weight = torch.empty((hc, dim), dtype=f32, device=dev)
         temps.append(dk_weight)
-    for name, t, n in (("kv", kv, T * (hc + 1) * dim), ("dkv", dkv, T * (hc + 1) * dim), ("dout", dout, T * hc * dim),
-                       ("dx", dx, T * hc * dim), ("q_weight", q_weight, hc * dim), ("k_weight", k_weight, hc * dim),
-                       ("dq_weight", dq_weight, hc * dim), ("dk_weight", dk_weight, hc * dim), ("mask", mask, T)):
-        _size(t, n, name)
-    bf, f32 = torch.bfloat16, torch.float32
-    m = None if mask is None else _dev(_as_u8(mask), torch.uint8, "mask")
-    ptr = [_dev(x, bf, "x"), _dev(kv, bf, "kv"), _dev(q_weight, bf, "q_weight"), _dev(k_weight, bf, "k_weight"),
-           _dev(dout, bf, "dout"), m, T, hc, dim, float(eps), _dev(dx, bf, "dx"), _dev(dkv, bf, "dkv"),
-           _dev(dq_weight, f32, "dq_weight"), _dev(dk_weight, f32, "dk_weight")]
-    ws, nbytes = _workspace(workspace, engram_gate_grad_workspace(T, hc, dim), x.device, temps)
-    _check(_lib().engram_gate_grad(*ptr, ws, nbytes, _launch_stream(stream, temps)), "engram_gate_grad")
+    specs = [(x, bf, T * hc * dim, "x"), (kv, bf, T * (hc + 1) * dim, "kv"), (q_weight, bf, hc * dim, "q_weight"),
+             (k_weight, bf, hc * dim, "k_weight"), (dout, bf, T * hc * dim, "dout"), (dx, bf, T * hc * dim, "dx"),
+             (dkv, bf, T * (hc + 1) * dim, "dkv"), (dq_weight, f32, hc * dim, "dq_weight"),
+             (dk_weight, f32, hc * dim, "dk_weight")]
+    if mask is not None:
+        specs.append((_as_u8(mask), torch.uint8, T, "mask"))
+    p = _pointers(specs)
+    keep, ws, nbytes = _scratch(workspace, _lib().engram_gate_grad_workspace(T, hc, dim), dev)
+    temps.append(keep)
+    _check(_lib().engram_gate_grad(*p[:5], p[9] if mask is not None else None, T, hc, dim, float(eps), *p[5:9], ws,
+                                   nbytes, _launch_stream(stream, temps)), "engram_gate_grad")
     return dx, dkv, dq_weight, dk_weight
 
 
@@ -1006,13 +1044,17 @@ def _norm_call(grads, norm_type, counts, norm, workspace, stream, out=None, max_
     arr, n = _tensor_list(grads, out, counts)
     ap = arr.buffer_info()[0]
     dev = grads[0].device if n else (norm.device if norm is not None else torch.device("cuda"))
-    temps = []
-    if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        temps.append(norm)
-    _size(norm, 1, "norm")
-    ws, nbytes = _workspace(workspace, engram_grad_norm_workspace(n), dev, temps)
-    args = (_dev(norm, torch.float32, "norm"), ws, nbytes, _launch_stream(stream, temps))
+    need = _lib().engram_grad_norm_workspace(n)
+    if norm is None and workspace is None:  # one allocation: the norm, then the workspace
+        keep = torch.empty(64 + (need + 3) // 4, dtype=torch.float32, device=dev)
+        norm, p = keep[0], keep.data_ptr()
+        args = (p, p + 256, need)
+    else:
+        if norm is None:
+            norm = torch.empty((), dtype=torch.float32, device=dev)
+        keep, ws, nbytes = _scratch(workspace, need, dev)
+        args = (*_pointers(((norm, torch.float32, 1, "norm"),)), ws, nbytes)
+    args += (_launch_stream(stream, (keep, norm)),)
     if max_norm is None:
         _check(_lib().engram_grad_norm(ap, n, _NORM_OF[norm_type], *args), "engram_grad_norm")
     else:

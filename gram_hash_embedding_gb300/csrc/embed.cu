@@ -74,12 +74,14 @@ __device__ __forceinline__ uint32_t key_of_id(const EmbedArgs& e, uint32_t i) {
   return r >= 0 && r < e.rows ? (uint32_t)r : (uint32_t)e.rows;
 }
 
-// lanes of the warp with the same `bits`-bit digit (a ballot per bit)
-__device__ __forceinline__ unsigned same_digit(uint32_t d, int bits, unsigned in) {
+// lanes of the warp with the same digit (a ballot per bit, also for bits that every digit has 0)
+__device__ __forceinline__ unsigned same_digit(uint32_t d, unsigned in) {
   unsigned m = in;
-  for (int b = 0; b < bits; ++b) {
-    const unsigned v = __ballot_sync(0xffffffffu, (d >> b) & 1);
-    m &= (d >> b) & 1 ? v : ~v;
+#pragma unroll
+  for (int b = 0; b < kMaxBits; ++b) {
+    const bool set = d & (1u << b);
+    const unsigned v = __ballot_sync(0xffffffffu, set);
+    m &= set ? v : ~v;
   }
   return m;
 }
@@ -176,7 +178,7 @@ __device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], uint32_t (
   for (int j = 0; j < PER; ++j) {
     const bool in = base + j * 32 < left;
     const uint32_t d = (key[j] >> shift) & (bins - 1);
-    const unsigned same = same_digit(d, bits, __ballot_sync(0xffffffffu, in));
+    const unsigned same = same_digit(d, __ballot_sync(0xffffffffu, in));
     const int before = __popc(same & ((1u << lane) - 1u));
     uint32_t have = 0;
     if (in) have = mine[d];
@@ -381,81 +383,49 @@ __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
   if (threadIdx.x == 0) *count = 0;
 }
 
-// Calls of up to kSmall ids: the whole sort and the numbering in one CTA, the pairs in shared memory.
-constexpr int kSmallThreads = 1024;
-constexpr int kSmallPer = 8;
-constexpr int kSmall = kSmallThreads * kSmallPer;
-constexpr int kSmallSmem = kSmall * 4 + kSmall * 2 + (kSmallThreads / 32) * kMaxBins * 2 + kMaxBins * 4 + 32 * 4;
+// Calls of up to kSmall ids: a pair's place is counted, not sorted for. It is the number of smaller keys plus the
+// number of equal ones before it, n^2 comparisons that all SMs share: 6,144 pairs take 38 million, a few
+// microseconds, where a radix sort in one CTA took 40. A CTA places 32 pairs, a lane each; its 8 warps take an
+// eighth of the keys each.
+constexpr int kSmall = 8192;
+constexpr int kPlaced = 32;  // pairs placed by a CTA
 
-__global__ void __launch_bounds__(kSmallThreads)
-    sort_small_kernel(const EmbedArgs e, const int n, const int passes, const int width, uint32_t* __restrict__ key_out,
-                      uint32_t* __restrict__ pos_out, uint32_t* __restrict__ ids, int64_t* __restrict__ grad_rows,
-                      int64_t* __restrict__ count) {
+__global__ void __launch_bounds__(kThreads) place_small_kernel(const EmbedArgs e, const int n,
+                                                               uint32_t* __restrict__ key_out,
+                                                               uint32_t* __restrict__ pos_out) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kWarps = kSmallThreads / 32;
-  extern __shared__ uint32_t smem[];
-  uint32_t* sk = smem;                                         // [kSmall] keys
-  uint32_t* start = sk + kSmall;                               // [kMaxBins]
-  uint32_t* warp_sums = start + kMaxBins;                      // [32]
-  uint16_t* sp = reinterpret_cast<uint16_t*>(warp_sums + 32);  // [kSmall] positions
-  uint16_t* wh = sp + kSmall;                                  // [kWarps][1 << width]
+  constexpr int kWarps = kThreads / 32;
+  __shared__ __align__(16) uint32_t sk[kSmall];
+  __shared__ int part[kWarps][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rows = (uint32_t)e.rows;
-  uint32_t key[kSmallPer], place[kSmallPer];
-  uint16_t pos[kSmallPer];
-  const int base = warp * 32 * kSmallPer + lane;
-#pragma unroll
-  for (int j = 0; j < kSmallPer; ++j) {
-    const int i = base + j * 32;
-    pos[j] = (uint16_t)i;
-    key[j] = i < n ? key_of_id(e, i) : rows;
-  }
-  for (int q = 0; q < passes; ++q) {
-    rank_tile<kWarps, kSmallPer>(key, place, n, q * width, width, wh, start, warp_sums);
-#pragma unroll
-    for (int j = 0; j < kSmallPer; ++j) {
-      if (base + j * 32 < n) {
-        sk[place[j]] = key[j];
-        sp[place[j]] = pos[j];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kSmallPer; ++j) {
-      if (base + j * 32 < n) {
-        key[j] = sk[base + j * 32];
-        pos[j] = sp[base + j * 32];
-      }
-    }
-  }
-  // a thread's kSmallPer consecutive pairs of the sorted order
-  const int i0 = tid * kSmallPer;
-  uint32_t heads = 0;
-  for (int j = 0; j < kSmallPer; ++j) {
-    const int i = i0 + j;
-    if (i < n && sk[i] < rows && (i == 0 || sk[i - 1] != sk[i])) heads++;
-  }
-  uint32_t u = block_exclusive<kSmallThreads>(heads, warp_sums);
-  if (tid == kSmallThreads - 1) start[0] = u + heads;
-  for (int j = 0; j < kSmallPer; ++j) {
-    const int i = i0 + j;
-    if (i >= n) break;
-    const uint32_t k = sk[i];
-    key_out[i] = k;
-    pos_out[i] = sp[i];
-    if (grad_rows != nullptr) {
-      const bool h = k < rows && (i == 0 || sk[i - 1] != k);
-      if (h) grad_rows[u++] = k;
-      ids[i] = k < rows ? u - 1 : kNone;
-    }
-  }
+  const int vecs = (n + 3) / 4;  // the last one is filled up with a key above every other
+#pragma unroll 8
+  for (int i = tid; i < vecs * 4; i += kThreads) sk[i] = i < n ? key_of_id(e, i) : 0xffffffffu;
   __syncthreads();
-  if (grad_rows != nullptr) {
-    for (int i = tid; i < n; i += kSmallThreads)
-      if (i >= (int)start[0]) grad_rows[i] = -1;
-    if (tid == 0) *count = start[0];
-  }
+  const int i0 = blockIdx.x * kPlaced, i = i0 + lane;
+  const uint32_t mine = sk[min(i, n - 1)];
+  const uint4* sv = reinterpret_cast<const uint4*>(sk);
+  int c = 0;
+  // keys below `limit` in vectors [v0, v1)
+  auto count = [&](int v0, int v1, uint32_t limit) {
+#pragma unroll 4
+    for (int v = v0; v < v1; ++v) {
+      const uint4 k = sv[v];
+      c += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+    }
+  };
+  const int a = vecs * warp / kWarps, b = vecs * (warp + 1) / kWarps;
+  const int m0 = i0 / 4, m1 = m0 + kPlaced / 4;  // the vectors of the CTA's own pairs
+  count(a, min(b, m0), mine + 1);                // before them equal keys count too (keys are at most 2^32 - 2)
+  for (int j = max(a, m0) * 4; j < min(b, m1) * 4; ++j) c += sk[j] < mine || (sk[j] == mine && j < i);
+  count(max(a, m1), b, mine);
+  part[warp][lane] = c;
+  __syncthreads();
+  if (warp != 0 || i >= n) return;
+  for (int w = 1; w < kWarps; ++w) c += part[w][lane];
+  key_out[c] = mine;
+  pos_out[c] = (uint32_t)i;
 }
 
 // ------------------------------------------------------------------------------------ segment sums
@@ -471,6 +441,8 @@ struct SumArgs {
   const uint32_t* ids;
   const uint32_t* pos;
   uint32_t limit;  // ids from here on are no rows
+  int32_t number;  // sparse form of a small call: ids are keys, and this kernel numbers the segments and writes
+                   // grad_rows and count
   int64_t n;
   int32_t glog, per_unit, chunks;
   int64_t tiles;
@@ -478,6 +450,7 @@ struct SumArgs {
   float* trail;  // [tiles][dim4]: the part of a segment that goes on in the next tile
   int32_t dim4;  // dim rounded up to 4
   uint8_t* flags;  // [tiles] kOpen, kCloses, kThrough
+  uint32_t* open_row;  // [tiles] with kOpen: the row of grad that the segment belongs to
   // dense form without accumulation: CTAs from tiles * chunks on write the rows that no id names
   int32_t zero_rows;  // rows per such CTA
 };
@@ -556,8 +529,37 @@ __global__ void __launch_bounds__(kThreads) segment_sum_kernel(const EmbedGradAr
   const bool packed = a.dout_stride == (int64_t)a.e.n_cols * a.e.dim;
 
   float acc[V];
-  uint32_t cur = kNone;  // the running segment
+  uint32_t cur = kNone;  // the running segment's id
+  uint32_t slot = 0;     // number: its number, or that of the one before the unit's first head
   bool leading = i0 > 0 && i0 < i1 && s.ids[i0 - 1] == s.ids[i0];
+  if (s.number) {
+    __shared__ uint32_t sums[2], warp_sums[32];
+    if (threadIdx.x < 2) sums[threadIdx.x] = 0;
+    __syncthreads();
+    const int64_t tile0 = tile * units * s.per_unit;
+    uint32_t before = 0, all = 0, k8[kSegPer];
+    for (int64_t i = threadIdx.x * kSegPer; i < s.n; i += kThreads * kSegPer) {
+      const uint32_t bits = head_bits(s.ids, i, s.n, s.limit, k8);
+      all += __popc(bits);
+      if (i < tile0) before += __popc(bits);  // tile0 is a multiple of kSegPer
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
+    if ((threadIdx.x & 31) == 0) {
+      atomicAdd(&sums[0], before);
+      atomicAdd(&sums[1], all);
+    }
+    uint32_t own = 0;
+    if (gl == 0)
+      for (int64_t i = i0; i < i1; i += kSegPer) own += __popc(head_bits(s.ids, i, s.n, s.limit, k8));
+    const uint32_t off = block_exclusive<kThreads>(own, warp_sums);
+    slot = sums[0] + __shfl_sync(0xffffffffu, off, threadIdx.x & 31 & ~(G - 1)) - 1;
+    if (chunk == 0) {
+      for (int j = threadIdx.x; j < units * s.per_unit; j += kThreads)
+        if (tile0 + j < s.n && tile0 + j >= sums[1]) a.grad_rows[tile0 + j] = -1;
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = sums[1];
+    }
+  }
   int flag = 0;
   auto put_lead = [&]() {
 #pragma unroll
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kThreads) segment_sum_kernel(const EmbedGradAr
       flag |= kCloses;
       leading = false;
     } else if (on) {
-      finish_row<GT, V>(a, cur, k, acc);
+      finish_row<GT, V>(a, s.number ? slot : cur, k, acc);
     }
   };
   for (int64_t i = i0; i < i1; i += kBatch) {
@@ -599,6 +601,11 @@ __global__ void __launch_bounds__(kThreads) segment_sum_kernel(const EmbedGradAr
       raw[j].widen(f);
       if (id[j] != cur) {
         if (cur != kNone) close();
+        // a new segment; a leading run began in an earlier unit
+        if (s.number && id[j] != kNone && !(leading && cur == kNone)) {
+          ++slot;
+          if (chunk == 0 && gl == 0) a.grad_rows[slot] = id[j];
+        }
         cur = id[j];
 #pragma unroll
         for (int q = 0; q < V; ++q) acc[q] = f[q];
@@ -634,8 +641,12 @@ __global__ void __launch_bounds__(kThreads) segment_sum_kernel(const EmbedGradAr
       for (int j = 0; j < V; ++j) acc[j] += l[j];
       if (flag_s[v] & kCloses) break;
     }
-    if (v == units) part(s.trail);
-    else if (on) finish_row<GT, V>(a, cur, k, acc);
+    if (v == units) {
+      part(s.trail);
+      if (chunk == 0 && gl == 0) s.open_row[tile] = s.number ? slot : cur;
+    } else if (on) {
+      finish_row<GT, V>(a, s.number ? slot : cur, k, acc);
+    }
   }
   if (unit == 0 && (flag & (kCloses | kThrough))) {
     const float* l0 = lead_of(0);
@@ -712,8 +723,7 @@ __global__ void __launch_bounds__(kThreads) segment_join_kernel(const EmbedGradA
     sum.z += v.z;
     sum.w += v.w;
   }
-  const int64_t per_tile = (int64_t)(kThreads >> s.glog) * s.per_unit;
-  const uint32_t row = s.ids[(b + 1) * per_tile - 1];
+  const uint32_t row = s.open_row[b];
   const float f[4] = {sum.x, sum.y, sum.z, sum.w};
   for (int j = 0; j < 4 && k + j < a.e.dim; ++j) {
     float v = f[j];
@@ -757,7 +767,7 @@ Cut cut_of(int64_t n, int32_t dim, int v) {
 }
 
 struct Layout {  // byte offsets into the workspace
-  uint64_t key[2], pos[2], ids, counts, totals, heads, lead, trail, flags, end;
+  uint64_t key[2], pos[2], ids, counts, totals, heads, lead, trail, flags, open_row, end;
 };
 Layout layout_of(int64_t n, int32_t dim) {
   Layout l;
@@ -780,6 +790,7 @@ Layout layout_of(int64_t n, int32_t dim) {
   l.lead = take(tiles * dim4 * 4);
   l.trail = take(tiles * dim4 * 4);
   l.flags = take(tiles);
+  l.open_row = take(tiles * 4);
   l.end = at;
   return l;
 }
@@ -833,10 +844,8 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
   const int passes = (bits + kMaxBits - 1) / kMaxBits, width = (bits + passes - 1) / passes;
   const uint32_t *key, *pos, *ids;
   if (n <= kSmall) {
-    e = cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(sort_small_kernel, dim3(1), dim3(kSmallThreads), kSmallSmem, s, a.e, (int)n, passes, width,
-                   u32(l.key[0]), u32(l.pos[0]), u32(l.ids), a.grad_rows, a.count);
+    e = launch_pdl(place_small_kernel, dim3((unsigned)ceil_div(n, kPlaced)), dim3(kThreads), 0, s, a.e, (int)n,
+                   u32(l.key[0]), u32(l.pos[0]));
     if (e != cudaSuccess) return e;
     key = u32(l.key[0]);
     pos = u32(l.pos[0]);
@@ -878,13 +887,15 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       if (e != cudaSuccess) return e;
     }
   }
-  ids = sparse ? u32(l.ids) : key;
+  const bool number = sparse && n <= kSmall;
+  ids = sparse && !number ? u32(l.ids) : key;
   const bool v8 = wide(a.dout, a.dout_stride, a.e.dim, a.dout_type) && wide(a.grad, a.grad_stride, a.e.dim, a.grad_type);
   const Cut c = cut_of(n, a.e.dim, v8 ? 8 : 1);
   SumArgs m;
   m.ids = ids;
   m.pos = pos;
-  m.limit = sparse ? kNone : (uint32_t)a.e.rows;
+  m.limit = sparse && !number ? kNone : (uint32_t)a.e.rows;
+  m.number = number;
   m.n = n;
   m.glog = c.glog;
   m.per_unit = c.per_unit;
@@ -894,6 +905,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
   m.trail = reinterpret_cast<float*>(ws + l.trail);
   m.dim4 = (int32_t)ceil_div(a.e.dim, 4) * 4;
   m.flags = ws + l.flags;
+  m.open_row = u32(l.open_row);
   const int64_t row_bytes = (int64_t)a.e.dim * type_bytes(a.grad_type);
   m.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads, (128 << 10) / row_bytes));
   const int64_t grid = c.tiles * c.chunks + (zero ? ceil_div(a.e.rows, m.zero_rows) : 0);

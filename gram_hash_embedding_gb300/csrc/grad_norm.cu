@@ -24,11 +24,13 @@ constexpr int kThreads = 256;
 constexpr int kFew = 32;           // tensors of a launch with the short argument
 constexpr int kPerLaunch = 512;    // tensors of a launch with the long one (22 KB of the 32 KB allowed)
 constexpr int kMaxGrid = 152 * 8;
-constexpr int kVecs = 8;           // vectors of 8 values a thread has per chunk, at kThreads threads
-constexpr int64_t kChunk = (int64_t)kThreads * kVecs * 8;  // values per work item
+constexpr int kVecs = 8;           // vectors of 8 values a thread has per chunk
+constexpr int64_t kChunk = (int64_t)kThreads * kVecs * 8;  // values per work item: a CTA takes it
 constexpr int kCluster = 8;        // CTAs of the one-launch form
 constexpr int kClusterThreads = 512;
-constexpr uint32_t kClusterChunks = 64;  // the most chunks it takes
+constexpr int64_t kWarpChunk = 32 * kVecs * 8;  // values per work item there: a warp takes it, so that the many
+                                                // small tensors of a small model are read all at once
+constexpr uint32_t kClusterChunks = 512;  // the most work items it takes
 
 struct Item {
   const void* data;
@@ -69,18 +71,19 @@ struct Span8 {
   int64_t one0, n_one;  // single values [one0, one0 + n_one)
   int before;        // and [0, before)
 };
+template <int64_t CHUNK>
 __device__ __forceinline__ Span8 span_of(const Item& it, int64_t used, int64_t q) {
   Span8 s;
   s.before = 0;
   if (!it.wide) {
     s.i0 = 0;
     s.m = 0;
-    s.one0 = q * kChunk;
-    s.n_one = max((int64_t)0, min(kChunk, used - s.one0));
+    s.one0 = q * CHUNK;
+    s.n_one = max((int64_t)0, min(CHUNK, used - s.one0));
     return s;
   }
-  s.i0 = q * kChunk + it.head;
-  const int64_t i1 = min(s.i0 + kChunk, used);
+  s.i0 = q * CHUNK + it.head;
+  const int64_t i1 = min(s.i0 + CHUNK, used);
   s.m = i1 > s.i0 ? (int)((i1 - s.i0) >> 3) : 0;
   s.one0 = s.i0 + (int64_t)s.m * 8;
   s.n_one = max((int64_t)0, i1 - s.one0);
@@ -90,7 +93,8 @@ __device__ __forceinline__ Span8 span_of(const Item& it, int64_t used, int64_t q
 
 // the chunk's sum of squares (or its largest magnitude) over one thread's values
 template <int TYPE, int THREADS>
-__device__ __forceinline__ double chunk_norm(const typename Elem<TYPE>::type* p, const Span8 c, const bool is_max) {
+__device__ __forceinline__ double chunk_norm(const typename Elem<TYPE>::type* p, const Span8 c, const bool is_max,
+                                             const int tid) {
   float s[8] = {};
   uint32_t top = 0;  // a magnitude's bits order like the magnitude, NaN above infinity
   auto one = [&](int64_t i) {
@@ -101,7 +105,7 @@ __device__ __forceinline__ double chunk_norm(const typename Elem<TYPE>::type* p,
   const typename Elem<TYPE>::type* v0 = p + c.i0;
   constexpr int kFly = TYPE == ENGRAM_TYPE_F32 ? 2 : 4;  // vectors in flight
 #pragma unroll 1
-  for (int v = threadIdx.x; v < c.m; v += kFly * THREADS) {
+  for (int v = tid; v < c.m; v += kFly * THREADS) {
     Raw<TYPE, 8> raw[kFly];
 #pragma unroll
     for (int j = 0; j < kFly; ++j) {
@@ -120,8 +124,8 @@ __device__ __forceinline__ double chunk_norm(const typename Elem<TYPE>::type* p,
     }
   }
 #pragma unroll 1
-  for (int64_t i = threadIdx.x; i < c.n_one; i += THREADS) one(c.one0 + i);
-  if ((int)threadIdx.x < c.before) one(threadIdx.x);
+  for (int64_t i = tid; i < c.n_one; i += THREADS) one(c.one0 + i);
+  if (tid < c.before) one(tid);
   if (is_max) return (double)__uint_as_float(top);
   return (double)(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
 }
@@ -135,10 +139,10 @@ __device__ __forceinline__ void store_as(void* o, int out_type, int64_t i, const
 
 template <int TYPE, int THREADS>
 __device__ __forceinline__ void chunk_clip(const typename Elem<TYPE>::type* p, void* o, const int out_type,
-                                           const Span8 c, const float coef) {
+                                           const Span8 c, const float coef, const int tid) {
   constexpr int kFly = TYPE == ENGRAM_TYPE_F32 ? 2 : 4;
 #pragma unroll 1
-  for (int v = threadIdx.x; v < c.m; v += kFly * THREADS) {
+  for (int v = tid; v < c.m; v += kFly * THREADS) {
     Raw<TYPE, 8> raw[kFly];
 #pragma unroll
     for (int j = 0; j < kFly; ++j)
@@ -159,31 +163,32 @@ __device__ __forceinline__ void chunk_clip(const typename Elem<TYPE>::type* p, v
     store_as<1>(o, out_type, i, &f);
   };
 #pragma unroll 1
-  for (int64_t i = threadIdx.x; i < c.n_one; i += THREADS) one(c.one0 + i);
-  if ((int)threadIdx.x < c.before) one(threadIdx.x);
+  for (int64_t i = tid; i < c.n_one; i += THREADS) one(c.one0 + i);
+  if (tid < c.before) one(tid);
 }
 
+// THREADS threads (a CTA or a warp), this one number `tid` of them, on chunk q of a tensor
 template <int THREADS>
-__device__ __forceinline__ double any_norm(const Item& it, int64_t q, bool is_max) {
-  const Span8 c = span_of(it, values_in_use(it), q);
+__device__ __forceinline__ double any_norm(const Item& it, int64_t q, bool is_max, int tid) {
+  const Span8 c = span_of<(int64_t)THREADS * kVecs * 8>(it, values_in_use(it), q);
   switch (it.type) {
-    case ENGRAM_TYPE_F32: return chunk_norm<ENGRAM_TYPE_F32, THREADS>(in_of<ENGRAM_TYPE_F32>(it), c, is_max);
-    case ENGRAM_TYPE_BF16: return chunk_norm<ENGRAM_TYPE_BF16, THREADS>(in_of<ENGRAM_TYPE_BF16>(it), c, is_max);
-    default: return chunk_norm<ENGRAM_TYPE_F16, THREADS>(in_of<ENGRAM_TYPE_F16>(it), c, is_max);
+    case ENGRAM_TYPE_F32: return chunk_norm<ENGRAM_TYPE_F32, THREADS>(in_of<ENGRAM_TYPE_F32>(it), c, is_max, tid);
+    case ENGRAM_TYPE_BF16: return chunk_norm<ENGRAM_TYPE_BF16, THREADS>(in_of<ENGRAM_TYPE_BF16>(it), c, is_max, tid);
+    default: return chunk_norm<ENGRAM_TYPE_F16, THREADS>(in_of<ENGRAM_TYPE_F16>(it), c, is_max, tid);
   }
 }
 
 template <int THREADS>
-__device__ __forceinline__ void any_clip(const Item& it, int64_t q, float coef) {
+__device__ __forceinline__ void any_clip(const Item& it, int64_t q, float coef, int tid) {
   if (coef == 1.0f && it.out == it.data) return;
-  const Span8 c = span_of(it, values_in_use(it), q);
+  const Span8 c = span_of<(int64_t)THREADS * kVecs * 8>(it, values_in_use(it), q);
   const int ot = it.out_type;
   switch (it.type) {
-    case ENGRAM_TYPE_F32: chunk_clip<ENGRAM_TYPE_F32, THREADS>(in_of<ENGRAM_TYPE_F32>(it), it.out, ot, c, coef); break;
+    case ENGRAM_TYPE_F32: chunk_clip<ENGRAM_TYPE_F32, THREADS>(in_of<ENGRAM_TYPE_F32>(it), it.out, ot, c, coef, tid); break;
     case ENGRAM_TYPE_BF16:
-      chunk_clip<ENGRAM_TYPE_BF16, THREADS>(in_of<ENGRAM_TYPE_BF16>(it), it.out, ot, c, coef);
+      chunk_clip<ENGRAM_TYPE_BF16, THREADS>(in_of<ENGRAM_TYPE_BF16>(it), it.out, ot, c, coef, tid);
       break;
-    default: chunk_clip<ENGRAM_TYPE_F16, THREADS>(in_of<ENGRAM_TYPE_F16>(it), it.out, ot, c, coef);
+    default: chunk_clip<ENGRAM_TYPE_F16, THREADS>(in_of<ENGRAM_TYPE_F16>(it), it.out, ot, c, coef, tid);
   }
 }
 
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_partial_kernel(const __grid_
   int j = blockIdx.x < all ? tensor_of(b, blockIdx.x) : 0;
   for (uint32_t c = blockIdx.x; c < all; c += gridDim.x) {
     while (b.first[j + 1] <= c) ++j;
-    sum = join(sum, any_norm<kThreads>(b.item[j], c - b.first[j], is_max), is_max);
+    sum = join(sum, any_norm<kThreads>(b.item[j], c - b.first[j], is_max, threadIdx.x), is_max);
   }
   const double r = block_join<kThreads>(sum, is_max, ws);
   if (threadIdx.x == 0) part[blockIdx.x] = r;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant
   for (uint32_t i = blockIdx.x; i < all; i += gridDim.x) {
     const uint32_t c = all - 1 - i;
     while (b.first[j] > c) --j;
-    any_clip<kThreads>(b.item[j], c - b.first[j], coef);
+    any_clip<kThreads>(b.item[j], c - b.first[j], coef, threadIdx.x);
   }
 }
 
@@ -301,11 +306,15 @@ __global__ void __launch_bounds__(kClusterThreads)
   __shared__ double ws[kClusterThreads / 32];
   __shared__ double sums[kCluster];
   const uint32_t rank = cluster_rank(), all = b.first[b.n];
+  // warps across the CTAs first, so that few items spread over all of them
+  constexpr uint32_t kAll = kCluster * kClusterThreads / 32;
+  const uint32_t c0 = (threadIdx.x >> 5) * kCluster + rank;
+  const int lane = threadIdx.x & 31;
   double sum = 0.0;
-  int j = 0;
-  for (uint32_t c = rank; c < all; c += kCluster) {
+  int j = c0 < all ? tensor_of(b, c0) : 0;
+  for (uint32_t c = c0; c < all; c += kAll) {
     while (b.first[j + 1] <= c) ++j;
-    sum = join(sum, any_norm<kClusterThreads>(b.item[j], c - b.first[j], is_max), is_max);
+    sum = join(sum, any_norm<32>(b.item[j], c - b.first[j], is_max, lane), is_max);
   }
   const double mine = block_join<kClusterThreads>(sum, is_max, ws);
   cluster_barrier();  // every CTA has started before another writes into its shared memory
@@ -317,10 +326,10 @@ __global__ void __launch_bounds__(kClusterThreads)
   if (rank == 0 && threadIdx.x == 0) *norm = total;
   if (!clip) return;
   const float coef = clip_factor(total, max_norm);
-  j = 0;
-  for (uint32_t c = rank; c < all; c += kCluster) {
+  j = c0 < all ? tensor_of(b, c0) : 0;
+  for (uint32_t c = c0; c < all; c += kAll) {
     while (b.first[j + 1] <= c) ++j;
-    any_clip<kClusterThreads>(b.item[j], c - b.first[j], coef);
+    any_clip<32>(b.item[j], c - b.first[j], coef, lane);
   }
 }
 
@@ -337,7 +346,7 @@ int head_of(const engram_tensor& x, bool clip) {
 
 // the batch starting at tensor t0; returns the next tensor
 template <int N>
-int32_t fill_batch(const engram_tensor* t, int32_t n, int32_t t0, bool clip, Batch<N>* b) {
+int32_t fill_batch(const engram_tensor* t, int32_t n, int32_t t0, bool clip, int64_t chunk, Batch<N>* b) {
   int32_t k = 0;
   uint64_t chunks = 0;  // at most N * 2^36 / kChunk = 2^31
   for (; t0 + k < n && k < N; ++k) {
@@ -348,7 +357,7 @@ int32_t fill_batch(const engram_tensor* t, int32_t n, int32_t t0, bool clip, Bat
                       x.rows_used != nullptr ? x.row_len : 1, (int8_t)x.type, (int8_t)(apart ? x.out_type : x.type),
                       (int8_t)(head < 0 ? 0 : head), (int8_t)(head >= 0)};
     b->first[k] = (uint32_t)chunks;
-    chunks += (uint64_t)((x.n + kChunk - 1) / kChunk);
+    chunks += (uint64_t)((x.n + chunk - 1) / chunk);
   }
   b->first[k] = (uint32_t)chunks;
   b->n = k;
@@ -366,7 +375,7 @@ cudaError_t launch_lists(const engram_tensor* tensors, int32_t n_tensors, int is
   int n_part = 0;
   Batch<N> b;
   for (int32_t t = 0; t < n_tensors;) {
-    t = fill_batch(tensors, n_tensors, t, clip, &b);
+    t = fill_batch(tensors, n_tensors, t, clip, kChunk, &b);
     const unsigned g = grid_of(b);
     const cudaError_t e = launch_pdl(norm_partial_kernel<N>, dim3(g), dim3(kThreads), 0, s, b, is_max, part + n_part);
     if (e != cudaSuccess) return e;
@@ -375,7 +384,7 @@ cudaError_t launch_lists(const engram_tensor* tensors, int32_t n_tensors, int is
   if (!clip)
     return launch_pdl(norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, (const double*)part, n_part, is_max, norm);
   for (int32_t t = (n_tensors - 1) / N * N; t >= 0; t -= N) {
-    fill_batch(tensors, n_tensors, t, clip, &b);
+    fill_batch(tensors, n_tensors, t, clip, kChunk, &b);
     const cudaError_t e = launch_pdl(clip_kernel<N>, dim3(grid_of(b)), dim3(kThreads), 0, s, b, is_max,
                                      (const double*)part, n_part, max_norm, norm);
     if (e != cudaSuccess) return e;
@@ -395,10 +404,12 @@ cudaError_t launch_grad_norm(const engram_tensor* tensors, int32_t n_tensors, in
   const int is_max = norm_type == ENGRAM_NORM_MAX;
   double* part = static_cast<double*>(workspace);
   if (n_tensors > kFew) return launch_lists<kPerLaunch>(tensors, n_tensors, is_max, clip, max_norm, norm, part, s);
-  Batch<kFew> b;
-  fill_batch(tensors, n_tensors, 0, clip, &b);
-  if (b.first[b.n] > kClusterChunks)
+  uint64_t chunks = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) chunks += (uint64_t)((tensors[i].n + kWarpChunk - 1) / kWarpChunk);
+  if (chunks > kClusterChunks)
     return launch_lists<kFew>(tensors, n_tensors, is_max, clip, max_norm, norm, part, s);
+  Batch<kFew> b;
+  fill_batch(tensors, n_tensors, 0, clip, kWarpChunk, &b);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
