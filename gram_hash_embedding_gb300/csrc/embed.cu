@@ -19,27 +19,55 @@ namespace {
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------------------------------- lookup
-template <int WT, int OT, int V>
+// A CTA writes kThreads * kFly consecutive vectors of the output, kFly of them a thread and all of their rows in
+// flight at once. N: the type that numbers vectors (32 bits where they fit: 64-bit divisions cost more than
+// the copy). The output goes out with an evict-first policy: rows that ids repeat stay in L2 longer.
+// 65,536 x 24 bf16 rows of 128 values (half of the ids repeat): 92 us, 0.94 of the copy bandwidth counting each
+// distinct row once; 1, 2 and 8 vectors a thread 143, 106 and 129 us; with 64-bit divisions and one vector 123 us.
+constexpr int kFly = 4;
+
+template <int WT, int OT, int V, typename N>
 __global__ void __launch_bounds__(kThreads)
     embed_kernel(const EmbedArgs a, const typename Elem<WT>::type* __restrict__ W, const int64_t row_stride,
-                 typename Elem<OT>::type* __restrict__ out) {
+                 typename Elem<OT>::type* __restrict__ out, const N units) {
   pdl_wait();
   pdl_trigger();
-  const int per_row = a.dim / V;
-  const int64_t units = a.T * a.n_cols * per_row;
-  for (int64_t u = (int64_t)blockIdx.x * kThreads + threadIdx.x; u < units; u += (int64_t)gridDim.x * kThreads) {
-    const int64_t e = u / per_row;
-    const int k = (int)(u - e * per_row) * V;
-    const int64_t t = e / a.n_cols;
-    const int64_t r = a.idx[t * a.idx_stride + (e - t * a.n_cols)];
-    Raw<WT, V> raw;
-    raw.zero();
-    if (r >= 0 && r < a.rows) raw.load(W + r * row_stride + k);
-    float f[V];
-    raw.widen(f);
+  const uint32_t per_row = a.dim / V;
+  const N u0 = (N)blockIdx.x * (kThreads * kFly) + threadIdx.x;
+  int64_t r[kFly];
+  uint32_t k[kFly];
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = (r >= 0 && r < a.rows) ? f[i] * a.scale : 0.f;
-    store_vals<OT, V>(out + e * a.dim + k, f);
+  for (int j = 0; j < kFly; ++j) {
+    const N u = u0 + j * kThreads;
+    r[j] = -1;
+    if (u < units) {
+      const N e = u / per_row;
+      k[j] = (uint32_t)(u - e * per_row) * V;
+      int64_t at = (int64_t)e;
+      if (a.idx_stride != a.n_cols) {
+        const N t = e / (uint32_t)a.n_cols;
+        at = (int64_t)t * a.idx_stride + (int64_t)(e - t * (uint32_t)a.n_cols);
+      }
+      r[j] = a.idx[at];
+    }
+  }
+  Raw<WT, V> raw[kFly];
+#pragma unroll
+  for (int j = 0; j < kFly; ++j) {
+    raw[j].zero();
+    if (r[j] >= 0 && r[j] < a.rows) raw[j].load(W + r[j] * row_stride + k[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kFly; ++j) {
+    const N u = u0 + j * kThreads;
+    if (u < units) {
+      const bool ok = r[j] >= 0 && r[j] < a.rows;
+      float f[V];
+      raw[j].widen(f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = ok ? f[i] * a.scale : 0.f;
+      store_vals<OT, V, true>(out + (int64_t)u * V, f);
+    }
   }
 }
 
@@ -50,8 +78,9 @@ __global__ void __launch_bounds__(kThreads)
 // also writes the keys, so that the ids are read once.
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int kPerThread = 16;
-constexpr int kTile = kThreads * kPerThread;  // pairs per tile (one CTA)
+constexpr int kSortThreads = 512;
+constexpr int kPerThread = 12;
+constexpr int kTile = kSortThreads * kPerThread;  // pairs per tile (one CTA)
 
 struct SortPass {
   uint32_t* key_in;        // written by the first pass's count
@@ -74,43 +103,31 @@ __device__ __forceinline__ uint32_t key_of_id(const EmbedArgs& e, uint32_t i) {
   return r >= 0 && r < e.rows ? (uint32_t)r : (uint32_t)e.rows;
 }
 
-// lanes of the warp with the same digit (a ballot per bit, also for bits that every digit has 0)
-__device__ __forceinline__ unsigned same_digit(uint32_t d, unsigned in) {
-  unsigned m = in;
-#pragma unroll
-  for (int b = 0; b < kMaxBits; ++b) {
-    const bool set = d & (1u << b);
-    const unsigned v = __ballot_sync(0xffffffffu, set);
-    m &= set ? v : ~v;
-  }
-  return m;
-}
-
 template <bool FIRST>
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const EmbedArgs e, const SortPass p) {
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const EmbedArgs e, const SortPass p) {
   pdl_wait();
   pdl_trigger();
   __shared__ uint32_t hist[kMaxBins];
   const int bins = 1 << p.bits;
-  for (int b = threadIdx.x; b < bins; b += kThreads) hist[b] = 0;
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
   __syncthreads();
   const uint32_t base = blockIdx.x * (uint32_t)kTile, n = (uint32_t)p.n;
   uint32_t key[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const uint32_t i = base + j * kThreads + threadIdx.x;
+    const uint32_t i = base + j * kSortThreads + threadIdx.x;
     if (i < n) key[j] = FIRST ? key_of_id(e, i) : p.key_in[i];
   }
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
-    const uint32_t i = base + j * kThreads + threadIdx.x;
+    const uint32_t i = base + j * kSortThreads + threadIdx.x;
     if (i < n) {
       if (FIRST) p.key_in[i] = key[j];
       atomicAdd(&hist[(key[j] >> p.shift) & (bins - 1)], 1u);
     }
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kThreads) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
 }
 
 // one warp per digit: counts[b][tile] becomes the pairs of digit b in the tiles before
@@ -162,85 +179,28 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   return s + x - v;
 }
 
-// The places of a CTA's pairs in its sorted tile: WARPS warps of 32 * PER consecutive pairs, taken 32 at a time,
-// so (warp, step, lane) is their order. wh: [WARPS][1 << bits]; start: [1 << bits], on return
-// the first place of each digit.
-template <int WARPS, int PER>
-__device__ __forceinline__ void rank_tile(const uint32_t (&key)[PER], uint32_t (&place)[PER], int left, int shift,
-                                          int bits, uint16_t* wh, uint32_t* start, uint32_t* warp_sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = 1 << bits;
-  uint32_t* wz = reinterpret_cast<uint32_t*>(wh);
-  for (int b = tid; b < (WARPS << bits) / 2; b += WARPS * 32) wz[b] = 0;
-  __syncthreads();
-  uint16_t* mine = wh + (warp << bits);
-  const int base = warp * 32 * PER + lane;
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const bool in = base + j * 32 < left;
-    const uint32_t d = (key[j] >> shift) & (bins - 1);
-    const unsigned same = same_digit(d, __ballot_sync(0xffffffffu, in));
-    const int before = __popc(same & ((1u << lane) - 1u));
-    uint32_t have = 0;
-    if (in) have = mine[d];
-    __syncwarp();
-    if (in && before == 0) mine[d] = (uint16_t)(have + __popc(same));
-    __syncwarp();
-    place[j] = have + before;
-  }
-  __syncthreads();
-  // per digit: the warps' starts among each other and the tile's count; a thread has consecutive digits
-  constexpr int kDigits = (kMaxBins + WARPS * 32 - 1) / (WARPS * 32);
-  const int per = (bins + WARPS * 32 - 1) / (WARPS * 32);
-  uint32_t cnt[kDigits], sum = 0;
-#pragma unroll
-  for (int q = 0; q < kDigits; ++q) {
-    const int d = tid * per + q;
-    cnt[q] = 0;
-    if (q < per && d < bins) {
-      uint32_t c[WARPS];
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) c[w] = wh[(w << bits) + d];
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        wh[(w << bits) + d] = (uint16_t)cnt[q];
-        cnt[q] += c[w];
-      }
-    }
-    sum += cnt[q];
-  }
-  uint32_t at = block_exclusive<WARPS * 32>(sum, warp_sums);
-#pragma unroll
-  for (int q = 0; q < kDigits; ++q) {
-    const int d = tid * per + q;
-    if (q < per && d < bins) start[d] = at;
-    at += cnt[q];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const uint32_t d = (key[j] >> shift) & (bins - 1);
-    place[j] += start[d] + mine[d];
-  }
-}
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = kMaxBins / kSortThreads;  // digits of a thread: two, which share a word of the warps' counts
+static_assert(kDigits == 2 && kTile < 65536, "the counts of two digits are one word of two 16-bit halves");
+constexpr int kScatterSmem = kTile * 8 + kSortWarps * kMaxBins * 2 + kMaxBins * 4 + 32 * 4;
 
-constexpr int kScatterSmem = kTile * 8 + (kThreads / 32) * kMaxBins * 2 + kMaxBins * 8 + 32 * 4;
-
+// The stable scatter of a tile: places inside the sorted tile first (the pairs' order is (warp, step, lane), a warp
+// taking 32 * kPerThread consecutive pairs 32 at a time), an exchange through shared memory, then runs of equal digits
+// go out together. The warps' counts are 16-bit, all digits of all warps, whatever the pass's width.
 template <bool FIRST>
-__global__ void __launch_bounds__(kThreads, 3) sort_scatter_kernel(const SortPass p) {
+__global__ void __launch_bounds__(kSortThreads, 2) sort_scatter_kernel(const SortPass p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kWarps = kThreads / 32;
   extern __shared__ uint32_t smem[];
-  uint32_t* sk = smem;                                         // [kTile] the tile in digit order
-  uint32_t* sp = sk + kTile;                                   // [kTile]
-  uint32_t* start = sp + kTile;                                // [kMaxBins]
-  uint32_t* gbase = start + kMaxBins;                          // [kMaxBins] a digit's first place in the output, less start
-  uint32_t* warp_sums = gbase + kMaxBins;                      // [32]
-  uint16_t* wh = reinterpret_cast<uint16_t*>(warp_sums + 32);  // [kWarps][kMaxBins]
+  uint32_t* sk = smem;                    // [kTile] the tile in digit order
+  uint32_t* sp = sk + kTile;              // [kTile]
+  uint32_t* wh = sp + kTile;              // [kSortWarps][kMaxBins / 2] two 16-bit counts a word, then places
+  uint32_t* go = wh + kSortWarps * kMaxBins / 2;  // [kMaxBins] a digit's first place in the output less that in the tile
+  uint32_t* warp_sums = go + kMaxBins;            // [32]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = 1 << p.bits;
   const int64_t tile0 = (int64_t)blockIdx.x * kTile;
   const int left = (int)min((int64_t)kTile, p.n - tile0);
-  uint32_t key[kPerThread], pos[kPerThread], place[kPerThread];
+  uint32_t key[kPerThread], pos[kPerThread];
   const int base = warp * 32 * kPerThread + lane;
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
@@ -251,34 +211,81 @@ __global__ void __launch_bounds__(kThreads, 3) sort_scatter_kernel(const SortPas
       if (!FIRST) pos[j] = p.pos_in[tile0 + base + j * 32];
     }
   }
-  // where each digit goes: the digits before it, the same digit in the tiles before
-  const int per = (bins + kThreads - 1) / kThreads;
-  uint32_t tot[kMaxBins / kThreads], sum = 0;
+  for (int b = tid; b < kSortWarps * kMaxBins / 8; b += kSortThreads)
+    reinterpret_cast<uint4*>(wh)[b] = make_uint4(0u, 0u, 0u, 0u);
+  // where each of the thread's digits goes: the digits before it, the same digit in the tiles before
+  uint32_t tot[kDigits], there[kDigits];
 #pragma unroll
-  for (int q = 0; q < kMaxBins / kThreads; ++q) {
-    const int d = tid * per + q;
-    tot[q] = q < per && d < bins ? p.totals[d] : 0u;
-    sum += tot[q];
+  for (int q = 0; q < kDigits; ++q) {
+    const int d = tid * kDigits + q;
+    tot[q] = d < bins ? p.totals[d] : 0u;
+    there[q] = d < bins ? p.counts[(int64_t)d * p.tiles + blockIdx.x] : 0u;
   }
-  uint32_t all = block_exclusive<kThreads>(sum, warp_sums);
+  const uint32_t all = block_exclusive<kSortThreads>(tot[0] + tot[1], warp_sums);
+  there[0] += all;
+  there[1] += all + tot[0];
+  // lanes of the warp with the same digit: a ballot per bit (also for bits that every digit has 0), all steps together
+  unsigned same[kPerThread];
 #pragma unroll
-  for (int q = 0; q < kMaxBins / kThreads; ++q) {
-    const int d = tid * per + q;
-    if (q < per && d < bins) gbase[d] = all + p.counts[(int64_t)d * p.tiles + blockIdx.x];
-    all += tot[q];
+  for (int j = 0; j < kPerThread; ++j) same[j] = __ballot_sync(0xffffffffu, base + j * 32 < left);
+#pragma unroll
+  for (int b = 0; b < kMaxBits; ++b) {
+    const uint32_t bit = b < p.bits ? 1u << (p.shift + b) : 0u;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+      const bool set = key[j] & bit;
+      const unsigned v = __ballot_sync(0xffffffffu, set);
+      same[j] &= set ? v : ~v;
+    }
   }
-  rank_tile<kWarps, kPerThread>(key, place, left, p.shift, p.bits, wh, start, warp_sums);
+  uint16_t* mine = reinterpret_cast<uint16_t*>(wh + warp * kMaxBins / 2);
+  uint32_t rank[kPerThread / 2];  // two 16-bit ranks a word
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    const bool in = base + j * 32 < left;
+    const uint32_t d = (key[j] >> p.shift) & (bins - 1);
+    const int before = __popc(same[j] & ((1u << lane) - 1u));
+    uint32_t have = 0;
+    if (in) have = mine[d];
+    __syncwarp();
+    if (in && before == 0) mine[d] = (uint16_t)(have + __popc(same[j]));
+    __syncwarp();
+    if (j % 2 == 0) rank[j / 2] = have + before;
+    else rank[j / 2] |= (have + before) << 16;
+  }
+  __syncthreads();
+  // the warps' counts of the thread's two digits become places: digits before, warps before
+  uint32_t c[kSortWarps], sum = 0;
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    c[w] = wh[w * kMaxBins / 2 + tid];
+    sum += c[w];  // no carry: a half is at most kTile
+  }
+  const uint32_t n0 = sum & 0xffffu, n1 = sum >> 16;
+  const uint32_t at = block_exclusive<kSortThreads>(n0 + n1, warp_sums);
+  uint32_t run = at | (at + n0) << 16;
+#pragma unroll
+  for (int w = 0; w < kSortWarps; ++w) {
+    wh[w * kMaxBins / 2 + tid] = run;
+    run += c[w];
+  }
+  go[tid * kDigits] = there[0] - at;
+  go[tid * kDigits + 1] = there[1] - (at + n0);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
     if (base + j * 32 < left) {
-      sk[place[j]] = key[j];
-      sp[place[j]] = pos[j];
+      const uint32_t d = (key[j] >> p.shift) & (bins - 1);
+      const uint32_t place = mine[d] + (rank[j / 2] >> (16 * (j % 2)) & 0xffffu);
+      sk[place] = key[j];
+      sp[place] = pos[j];
     }
   }
   __syncthreads();
-  for (int i = tid; i < left; i += kThreads) {
-    const uint32_t k = sk[i], d = (k >> p.shift) & (bins - 1);
-    const uint32_t g = gbase[d] + (i - start[d]);
+#pragma unroll 4
+  for (int i = tid; i < left; i += kSortThreads) {
+    const uint32_t k = sk[i];
+    const uint32_t g = go[(k >> p.shift) & (bins - 1)] + i;
     p.key_out[g] = k;
     p.pos_out[g] = sp[i];
   }
@@ -337,8 +344,9 @@ __global__ void __launch_bounds__(kThreads)
                     int64_t* __restrict__ count) {
   pdl_wait();
   pdl_trigger();
-  __shared__ uint32_t sum_s[2];
+  __shared__ uint32_t sum_s[2], n_rows;
   __shared__ uint32_t warp_sums[32];
+  __shared__ uint32_t rows_s[kSegTile];  // the rows that begin here, for whole-line stores
   if (threadIdx.x < 2) sum_s[threadIdx.x] = 0;
   __syncthreads();
   const int64_t i0 = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kSegPer;
@@ -356,20 +364,22 @@ __global__ void __launch_bounds__(kThreads)
     atomicAdd(&sum_s[0], before);
     atomicAdd(&sum_s[1], all);
   }
-  const uint32_t off = block_exclusive<kThreads>(__popc(bits), warp_sums);
-  uint32_t u = sum_s[0] + off;
-  const uint32_t total = sum_s[1];
+  uint32_t off = block_exclusive<kThreads>(__popc(bits), warp_sums);
+  const uint32_t u0 = sum_s[0], total = sum_s[1];
   uint32_t id[kSegPer];
 #pragma unroll
   for (int j = 0; j < kSegPer; ++j) {
-    if (bits >> j & 1) grad_rows[u++] = k[j];
-    id[j] = i0 < n && k[j] < rows ? u - 1 : kNone;
+    if (bits >> j & 1) rows_s[off++] = k[j];
+    id[j] = i0 < n && k[j] < rows ? u0 + off - 1 : kNone;
   }
+  if (threadIdx.x == kThreads - 1) n_rows = off;
   if (i0 < n) {
 #pragma unroll
     for (int j = 0; j < kSegPer; j += 4)
       *reinterpret_cast<uint4*>(ids + i0 + j) = make_uint4(id[j], id[j + 1], id[j + 2], id[j + 3]);
   }
+  __syncthreads();
+  for (int j = threadIdx.x; j < (int)n_rows; j += kThreads) grad_rows[u0 + j] = rows_s[j];
   for (int j = threadIdx.x; j < kSegTile; j += kThreads) {
     const int64_t i = (int64_t)blockIdx.x * kSegTile + j;
     if (i < n && i >= (int64_t)total) grad_rows[i] = -1;
@@ -806,16 +816,21 @@ cudaError_t launch_embed(const EmbedArgs& a, const void* W, int64_t row_stride, 
                          int32_t out_type, cudaStream_t s) {
   const bool v8 = wide(W, row_stride, a.dim, w_type) && wide(out, a.dim, a.dim, out_type);
   const int64_t units = a.T * a.n_cols * (a.dim / (v8 ? 8 : 1));
-  const int64_t grid = std::min<int64_t>(ceil_div(units, kThreads), 152 * 64);
+  const int64_t grid = ceil_div(units, kThreads * kFly);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const bool few = units < (int64_t)UINT32_MAX - kThreads * kFly;
   return with_type(w_type, [&](auto wt) {
     return with_type(out_type, [&](auto ot) {
       using WE = typename Elem<wt()>::type;
       using OE = typename Elem<ot()>::type;
+      auto go = [&](auto kern, auto n) {
+        return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (const WE*)W, row_stride, (OE*)out, n);
+      };
       if (v8)
-        return launch_pdl(embed_kernel<wt(), ot(), 8>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (const WE*)W,
-                          row_stride, (OE*)out);
-      return launch_pdl(embed_kernel<wt(), ot(), 1>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (const WE*)W,
-                        row_stride, (OE*)out);
+        return few ? go(embed_kernel<wt(), ot(), 8, uint32_t>, (uint32_t)units)
+                   : go(embed_kernel<wt(), ot(), 8, uint64_t>, (uint64_t)units);
+      return few ? go(embed_kernel<wt(), ot(), 1, uint32_t>, (uint32_t)units)
+                 : go(embed_kernel<wt(), ot(), 1, uint64_t>, (uint64_t)units);
     });
   });
 }
@@ -864,7 +879,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       p.shift = q * width;
       p.bits = std::min(width, 32 - q * width);
       auto count = q == 0 ? sort_count_kernel<true> : sort_count_kernel<false>;
-      e = launch_pdl(count, dim3(tiles), dim3(kThreads), 0, s, a.e, p);
+      e = launch_pdl(count, dim3(tiles), dim3(kSortThreads), 0, s, a.e, p);
       if (e != cudaSuccess) return e;
       e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, kThreads / 32)), dim3(kThreads), 0,
                      s, p);
@@ -872,7 +887,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       auto scatter = q == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
       e = cudaFuncSetAttribute(scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, kScatterSmem);
       if (e != cudaSuccess) return e;
-      e = launch_pdl(scatter, dim3(tiles), dim3(kThreads), kScatterSmem, s, p);
+      e = launch_pdl(scatter, dim3(tiles), dim3(kSortThreads), kScatterSmem, s, p);
       if (e != cudaSuccess) return e;
     }
     key = u32(l.key[passes & 1]);

@@ -110,23 +110,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// V values rounded once (to nearest even) to the stored type
-template <int TYPE, int V>
+// V values rounded once (to nearest even) to the stored type. ONCE: with an evict-first policy, for what is
+// written and not read again by the same call
+template <int TYPE, int V, bool ONCE = false>
 __device__ __forceinline__ void store_vals(typename Elem<TYPE>::type* p, const float* f) {
   if constexpr (V == 1) {
     Elem<TYPE>::store(p, f[0]);
   } else if constexpr (TYPE == ENGRAM_TYPE_F32) {
     if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
-                   "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
-                   : "memory");
+      if constexpr (ONCE)
+        asm volatile("st.global.L2::evict_first.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]),
+                     "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+      else
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]),
+                     "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
     } else {
       reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
       reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
   } else {
-    *reinterpret_cast<uint4*>(p) =
+    const uint4 v =
         make_uint4(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]), pack2<TYPE>(f[4], f[5]), pack2<TYPE>(f[6], f[7]));
+    if constexpr (ONCE) __stcs(reinterpret_cast<uint4*>(p), v);
+    else *reinterpret_cast<uint4*>(p) = v;
   }
 }
 
