@@ -771,10 +771,10 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
   return engram::gate_grad_workspace(T, hc, dim);
 }
 
-int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
+static int gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
                      const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
                      uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
-                     uint64_t workspace_bytes, engram_stream_t stream) {
+                     uint64_t workspace_bytes, engram_stream_t stream, int64_t withhold) {
   if (T < 0) return ENGRAM_ERR_INVALID;
   if (!gate_grad_shape_ok(T, hc, dim)) return ENGRAM_ERR_UNSUPPORTED;
   if (q_weight == nullptr || k_weight == nullptr || dq_weight == nullptr || dk_weight == nullptr ||
@@ -789,9 +789,28 @@ int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_we
   }
   const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
   const uint64_t w = (uint64_t)hc * dim * 4;
-  return launched(launch_rc(engram::launch_gate_grad(a, workspace, (cudaStream_t)stream)), (cudaStream_t)stream,
+  return launched(launch_rc(engram::launch_gate_grad(a, workspace, (cudaStream_t)stream, withhold)),
+                  (cudaStream_t)stream,
                   {span(dx, (uint64_t)T * hc * dim * 2), span(dkv, (uint64_t)T * (hc + 1) * dim * 2),
                    span(dq_weight, w), span(dk_weight, w), span(workspace, T > 0 ? workspace_bytes : 0)});
+}
+
+int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
+                     const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
+                     uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
+                     uint64_t workspace_bytes, engram_stream_t stream) {
+  return gate_grad(x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight, workspace,
+                   workspace_bytes, stream, -1);
+}
+
+int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight,
+                              const uint16_t* k_weight, const uint16_t* dout, const uint8_t* mask, int64_t T,
+                              int32_t hc, int32_t dim, float eps, uint16_t* dx, uint16_t* dkv, float* dq_weight,
+                              float* dk_weight, void* workspace, uint64_t workspace_bytes, int64_t token,
+                              engram_stream_t stream) {
+  if (token < 0) return ENGRAM_ERR_INVALID;
+  return gate_grad(x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight, workspace,
+                   workspace_bytes, stream, token);
 }
 
 namespace {

@@ -127,11 +127,11 @@ __device__ __forceinline__ void send(float* p, uint32_t bar, uint32_t rank, floa
 // the most threads of a CTA, one per vector of 8 columns: what the registers allow
 constexpr int max_threads(int hc) { return hc <= 2 ? 640 : 320; }
 
-// HC copies, S stages
+// HC copies, S stages; withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
 template <int HC, int S>
 __global__ void __launch_bounds__(max_threads(HC))
     gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int cs,
-                     float* __restrict__ part, unsigned int* __restrict__ status) {
+                     float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
   pdl_wait();
   pdl_trigger();
   constexpr int kArrays = 3 * HC + 1;   // rows of a token: h, keys and douts of the copies, the value
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(max_threads(HC))
       float* to = red + ((buf * cs + rank) * nw + warp) * N + lane / (32 / N);
       if (lane % (32 / N) == 0) {
         if (cs == 1) *to = mine;
-        else
+        else if (t != withhold || rank != 0)
           for (int r = 0; r < cs; ++r) send(to, bar0 + 8 * buf, r, mine);
       }
       if (cs == 1) __syncthreads();
@@ -401,7 +401,8 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
 }
 
 template <int HC, int S>
-cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, cudaStream_t s) {
+cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, int64_t withhold,
+                         cudaStream_t s) {
   auto kern = gate_grad_kernel<HC, S>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
@@ -433,7 +434,7 @@ cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, in
   *parts = (int)clusters;
   cfg.gridDim = dim3((unsigned)(clusters * sh.cs));
   return cudaLaunchKernelEx(&cfg, kern, a, 1.0f / (float)a.dim, (float)(1.0 / sqrt((double)a.dim)), sh.nv, sh.cs, part,
-                            status);
+                            status, withhold);
 }
 
 }  // namespace
@@ -442,18 +443,18 @@ uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
   return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
 }
 
-cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s, int64_t withhold) {
   float* part = static_cast<float*>(workspace);
   int parts = 0;
   if (a.T > 0) {
     const Shape sh = shape_of(a.T, a.hc, a.dim);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.hc) {
-      case 1: e = launch_shape<1, 3>(a, sh, part, &parts, s); break;
-      case 2: e = launch_shape<2, 3>(a, sh, part, &parts, s); break;
-      case 4: e = launch_shape<4, 3>(a, sh, part, &parts, s); break;
+      case 1: e = launch_shape<1, 3>(a, sh, part, &parts, withhold, s); break;
+      case 2: e = launch_shape<2, 3>(a, sh, part, &parts, withhold, s); break;
+      case 4: e = launch_shape<4, 3>(a, sh, part, &parts, withhold, s); break;
       case 8:
-        e = sh.stages == 3 ? launch_shape<8, 3>(a, sh, part, &parts, s) : launch_shape<8, 2>(a, sh, part, &parts, s);
+        e = sh.stages == 3 ? launch_shape<8, 3>(a, sh, part, &parts, withhold, s) : launch_shape<8, 2>(a, sh, part, &parts, withhold, s);
         break;
     }
     if (e != cudaSuccess) return e;

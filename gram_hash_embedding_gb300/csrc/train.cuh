@@ -188,7 +188,8 @@ struct GateGradArgs {
   float *dq, *dk;
 };
 uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
-cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s);
+// withhold >= 0: the test hook of engram_gate_grad_withhold
+cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s, int64_t withhold = -1);
 
 // ------------------------------------------------------------------------- gradient norm and clipping
 uint64_t grad_norm_workspace(int32_t n_tensors);

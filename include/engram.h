@@ -68,9 +68,10 @@ typedef struct engram_state engram_state;
 #define ENGRAM_STATUS_CHECK 16u    /* checked builds only (compiled with -DENGRAM_CHECKED=1): a hash or fused kernel
                                       skipped a memory access outside the call's buffers. A library bug, never a
                                       data error; release builds do not test for it */
-#define ENGRAM_STATUS_TIMEOUT 32u  /* a tensor-core kernel (engram_project, engram_project_gate) gave up a wait that
-                                      did not complete within a second: its outputs are undefined. A library or
-                                      device fault, never a data error; read with engram_device_status */
+#define ENGRAM_STATUS_TIMEOUT 32u  /* a tensor-core kernel (engram_project, engram_project_gate) or the gate's gradient
+                                      gave up a wait that did not complete within a second: its outputs are undefined.
+                                      A library or device fault, never a data error; read with
+                                      engram_device_status */
 
 /* Storage types of the scale tensors. The engram-first/lookup page leaves `scale_dtype` open and
  * widens the scale with `.float()`; each type below widens to fp32 exactly before the one fp32
@@ -521,16 +522,30 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
  *   dout       device bf16 [T][hc][dim]
  *   dx         device bf16 [T][hc][dim], written; may be the same buffer as dout
  *   dkv        device bf16 [T][(hc+1)*dim], written
- *   dq_weight, dk_weight  device fp32 [hc][dim], written (+0 for T == 0)
+ *   dq_weight, dk_weight  device fp32 [hc][dim], written (0 for T == 0)
  *   workspace  engram_gate_grad_workspace(T, hc, dim) bytes, 256-byte aligned, owned by the caller; calls
  *              that use one workspace must not overlap on the GPU (may be NULL for T == 0)
  * Every pointer but mask 16-byte aligned. The sums over tokens run in a fixed order: the same inputs give
- * the same bits. Errors: _INVALID, _UNSUPPORTED (hc, dim, T >= 2^31), _CUDA.
+ * the same bits. A wait that does not end raises ENGRAM_STATUS_TIMEOUT (engram_device_status) after one second
+ * instead of hanging. Errors: _INVALID, _UNSUPPORTED (hc, dim, T >= 2^31), _CUDA.
  */
 int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
                      const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
                      uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
                      uint64_t workspace_bytes, engram_stream_t stream);
+
+/*
+ * Test hook of engram_gate_grad's failure path (no counterpart in the pages): the same call, except that the
+ * sums of token `token` (one whose mask is open) are not exchanged in full where a token is shared by several
+ * CTAs. Their waits run out after one second, the kernel raises ENGRAM_STATUS_TIMEOUT (engram_device_status), starts
+ * no more copies, waits for those in flight and ends instead of hanging; the outputs are undefined and the
+ * context stays usable. Errors: as engram_gate_grad, and _INVALID for token < 0.
+ */
+int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight,
+                              const uint16_t* k_weight, const uint16_t* dout, const uint8_t* mask, int64_t T,
+                              int32_t hc, int32_t dim, float eps, uint16_t* dx, uint16_t* dkv, float* dq_weight,
+                              float* dk_weight, void* workspace, uint64_t workspace_bytes, int64_t token,
+                              engram_stream_t stream);
 
 /* One gradient of engram_grad_norm / engram_grad_clip. */
 typedef struct engram_tensor {

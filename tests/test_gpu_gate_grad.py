@@ -201,3 +201,32 @@ def test_gate_grad_matches_the_forward_by_differences():
         # third-order terms of a step of 1/16 of the inputs' size, and bf16 results: 2^-8 of each term
         tol = 2.0 ** -8 * np.abs(change * (dx if which == "x" else dkv)).sum() + 0.02 * abs(diff)
         assert abs(diff - pred) <= tol, (which, diff, pred, tol)
+
+
+@pytest.mark.parametrize("T,hc,dim", [(4, 4, 5120), (400, 4, 5120)])
+def test_gate_grad_withheld_sums_end_with_the_timeout_flag(T, hc, dim):
+    """A token's sums that never arrive: the waits run out, the call ends within seconds with the flag
+    raised, and the same context then computes a correct gradient."""
+    import ctypes
+    import time
+
+    L = geng._lib()
+    P, I32 = ctypes.c_void_p, ctypes.c_int32
+    L.engram_gate_grad_withhold.argtypes = [P, P, P, P, P, P, ctypes.c_int64, I32, I32, ctypes.c_float, P, P, P, P, P,
+                                            ctypes.c_uint64, ctypes.c_int64, P]
+    args = _inputs(np.random.default_rng(3), T, hc, dim, masked=0.0)
+    dev = [a.cuda() for a in args[:5]]
+    out = [torch.empty_like(dev[0]), torch.empty_like(dev[1])] + [torch.empty((hc, dim), device="cuda") for _ in range(2)]
+    ws = torch.empty(geng.engram_gate_grad_workspace(T, hc, dim), dtype=torch.uint8, device="cuda")
+    assert geng.engram_device_status() == 0  # a clean start (reads and clears)
+    call = lambda token: L.engram_gate_grad_withhold(*[a.data_ptr() for a in dev], None, T, hc, dim, EPS,
+                                                     *[o.data_ptr() for o in out], ws.data_ptr(), ws.numel(), token,
+                                                     torch.cuda.current_stream().cuda_stream)
+    assert call(-1) == geng.ERR_INVALID
+    t0 = time.time()
+    assert call(1) == geng.OK
+    torch.cuda.synchronize()
+    assert time.time() - t0 < 30.0
+    assert geng.engram_device_status() & geng.STATUS_TIMEOUT
+    _check(args, _run(args), "after the timeout")
+    assert geng.engram_device_status() == 0
