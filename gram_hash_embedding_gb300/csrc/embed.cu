@@ -76,6 +76,10 @@ __global__ void __launch_bounds__(kThreads)
 // tile, a scan over the tiles of each digit, and a stable scatter. Keys are row ids as 32-bit values,
 // with `rows` itself standing for every id outside the table, so those sort to the end. The first count
 // also writes the keys, so that the ids are read once.
+// 1.57 million ids of a table of 384 million rows (29 bits, 3 passes): 75 us of the call's 208. A pass is 4 us of
+// counting (7 in the first), 4 of scanning and 14 of scattering, which no memory bounds (25 MB out of L2): the ranks'
+// ballots and the exchange do. Tiles of 512 threads x 12 pairs measured best (whole call: 8 pairs 231, 16 pairs 254,
+// 256 threads x 16 pairs 248 us); 8-bit passes with __match_any_sync instead of ballots 15 us more.
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;
@@ -87,7 +91,7 @@ struct SortPass {
   const uint32_t* pos_in;  // null in the first pass: the positions are 0, 1, 2, ...
   uint32_t* key_out;
   uint32_t* pos_out;
-  uint32_t* counts;  // [bins][tiles]
+  uint32_t* counts;  // [tiles][bins]
   uint32_t* totals;  // [bins]
   int64_t n;
   int32_t tiles, shift, bits;
@@ -112,51 +116,73 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const EmbedArg
   for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
   __syncthreads();
   const uint32_t base = blockIdx.x * (uint32_t)kTile, n = (uint32_t)p.n;
-  uint32_t key[kPerThread];
+  // a thread has runs of 4 pairs
+  static_assert(kPerThread % 4 == 0, "a tile is whole runs");
+  uint32_t key[kPerThread] = {};
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    const uint32_t i = base + j * kSortThreads + threadIdx.x;
-    if (i < n) key[j] = FIRST ? key_of_id(e, i) : p.key_in[i];
+  for (int j = 0; j < kPerThread; j += 4) {
+    const uint32_t i = base + (j / 4 * kSortThreads + threadIdx.x) * 4;
+    if (FIRST) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + q < n) key[j + q] = key_of_id(e, i + q);
+    } else if (i < n) {  // the arrays reach past n
+      const uint4 v = *reinterpret_cast<const uint4*>(p.key_in + i);
+      key[j] = v.x;
+      key[j + 1] = v.y;
+      key[j + 2] = v.z;
+      key[j + 3] = v.w;
+    }
   }
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
-    const uint32_t i = base + j * kSortThreads + threadIdx.x;
-    if (i < n) {
-      if (FIRST) p.key_in[i] = key[j];
-      atomicAdd(&hist[(key[j] >> p.shift) & (bins - 1)], 1u);
-    }
+  for (int j = 0; j < kPerThread; j += 4) {
+    const uint32_t i = base + (j / 4 * kSortThreads + threadIdx.x) * 4;
+    if (FIRST && i < n) *reinterpret_cast<uint4*>(p.key_in + i) = make_uint4(key[j], key[j + 1], key[j + 2], key[j + 3]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i + q < n) atomicAdd(&hist[(key[j + q] >> p.shift) & (bins - 1)], 1u);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) p.counts[((int64_t)blockIdx.x << p.bits) + b] = hist[b];
 }
 
-// one warp per digit: counts[b][tile] becomes the pairs of digit b in the tiles before
-__global__ void __launch_bounds__(kThreads) sort_scan_kernel(const SortPass p) {
+// counts[tile][digit] becomes the pairs of the digit in the tiles before. A CTA takes 32 digits, a lane each, and
+// a warp a 32nd of the tiles.
+constexpr int kScanThreads = 1024;
+__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(const SortPass p) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= 1 << p.bits) return;
-  uint32_t* c = p.counts + (int64_t)b * p.tiles;
-  uint32_t run = 0;
-  constexpr int kAhead = 4;
-  for (int t0 = 0; t0 < p.tiles; t0 += 32 * kAhead) {
-    uint32_t v[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) v[j] = t0 + 32 * j + lane < p.tiles ? c[t0 + 32 * j + lane] : 0u;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int t = t0 + 32 * j + lane;
-      uint32_t x = v[j];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (t < p.tiles) c[t] = run + x - v[j];
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
+  __shared__ uint32_t part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, bins = 1 << p.bits;
+  const int d = blockIdx.x * 32 + lane, per = (p.tiles + 31) / 32;
+  const int t0 = warp * per, t1 = min(p.tiles, t0 + per);
+  uint32_t* c = p.counts + d;
+  uint32_t sum = 0;
+  if (d < bins) {
+#pragma unroll 8
+    for (int t = t0; t < t1; ++t) sum += c[(int64_t)t << p.bits];
   }
-  if (lane == 0) p.totals[b] = run;
+  part[warp][lane] = sum;
+  __syncthreads();
+  // warp w scans digit w's parts
+  const uint32_t v = part[lane][warp];
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  part[lane][warp] = x - v;
+  if (lane == 31 && blockIdx.x * 32 + warp < bins) p.totals[blockIdx.x * 32 + warp] = x;
+  __syncthreads();
+  if (d >= bins) return;
+  uint32_t run = part[warp][lane];
+#pragma unroll 8
+  for (int t = t0; t < t1; ++t) {
+    const uint32_t n = c[(int64_t)t << p.bits];
+    c[(int64_t)t << p.bits] = run;
+    run += n;
+  }
 }
 
 // exclusive scan over the block of one value per thread; warp_sums: 32 words
@@ -219,7 +245,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_scatter_kernel(const Sor
   for (int q = 0; q < kDigits; ++q) {
     const int d = tid * kDigits + q;
     tot[q] = d < bins ? p.totals[d] : 0u;
-    there[q] = d < bins ? p.counts[(int64_t)d * p.tiles + blockIdx.x] : 0u;
+    there[q] = d < bins ? p.counts[((int64_t)blockIdx.x << p.bits) + d] : 0u;
   }
   const uint32_t all = block_exclusive<kSortThreads>(tot[0] + tot[1], warp_sums);
   there[0] += all;
@@ -395,7 +421,7 @@ __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
 
 // Calls of up to kSmall ids: a pair's place is counted, not sorted for. It is the number of smaller keys plus the
 // number of equal ones before it, n^2 comparisons that all SMs share: 6,144 pairs take 38 million, a few
-// microseconds, where a radix sort in one CTA took 40. A CTA places 32 pairs, a lane each; its 8 warps take an
+// microseconds (15 from a cold start), where a radix sort in one CTA took 40 to 50. A CTA places 32 pairs, a lane each; its 8 warps take an
 // eighth of the keys each.
 constexpr int kSmall = 8192;
 constexpr int kPlaced = 32;  // pairs placed by a CTA
@@ -439,6 +465,9 @@ __global__ void __launch_bounds__(kThreads) place_small_kernel(const EmbedArgs e
 }
 
 // ------------------------------------------------------------------------------------ segment sums
+// Bound by memory: every gradient row is read once, every distinct row written once. 1.57 million bf16 rows of 128 values,
+// 0.82 million distinct, fp32 sums: 133 us, 0.82 GB at 6.2 TB/s (0.92 of the copy bandwidth). The sums before this form, a
+// warp per distinct row, took the call 1,658 us: the row that ids name most often was one warp's work.
 // The sorted pairs are cut into units of `per_unit` consecutive ones, whatever segments they belong to,
 // so a row named a million times and a million rows named once cost the same. A group of 2^glog lanes
 // takes one unit and V columns a lane, with kBatch rows of dout in flight; it writes the segments that
@@ -761,7 +790,7 @@ struct Cut {
   int glog, per_unit, chunks;
   int64_t tiles;
 };
-constexpr int64_t kWantCtas = 1216;  // 8 CTAs on each of the 152 SMs
+constexpr int64_t kWantCtas = 1216;  // 8 CTAs on each of the 152 SMs; units of 64 and 16 pairs at most: 224 us each, of 32: 218
 Cut cut_of(int64_t n, int32_t dim, int v) {
   Cut c;
   const int lanes = (dim + v - 1) / v;
@@ -770,7 +799,7 @@ Cut cut_of(int64_t n, int32_t dim, int v) {
   c.chunks = (int)ceil_div(lanes, 1 << c.glog);
   const int units = kThreads >> c.glog;
   // the longest units that still give every SM work; a unit of one batch where there is too little
-  c.per_unit = 64;
+  c.per_unit = 32;
   while (c.per_unit > kBatch && ceil_div(n, (int64_t)units * c.per_unit) * c.chunks < kWantCtas) c.per_unit >>= 1;
   c.tiles = ceil_div(n, (int64_t)units * c.per_unit);
   return c;
@@ -881,8 +910,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       auto count = q == 0 ? sort_count_kernel<true> : sort_count_kernel<false>;
       e = launch_pdl(count, dim3(tiles), dim3(kSortThreads), 0, s, a.e, p);
       if (e != cudaSuccess) return e;
-      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, kThreads / 32)), dim3(kThreads), 0,
-                     s, p);
+      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, 32)), dim3(kScanThreads), 0, s, p);
       if (e != cudaSuccess) return e;
       auto scatter = q == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
       e = cudaFuncSetAttribute(scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, kScatterSmem);
