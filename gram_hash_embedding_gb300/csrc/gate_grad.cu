@@ -7,7 +7,7 @@
 //   dkey   = c * w * h - (e / B) * key
 //   dvalue = sum_i gate_i * u_i
 //   dq     = k_weight * sum_t c * h * key,  dk = q_weight * the same sum
-// in fp32, everything recomputed from the forward's inputs. A masked token's gate is the constant 0:
+// in fp32 (sum(h * w * key) in twice that where it is almost 0), everything recomputed from the forward's inputs. A masked token's gate is the constant 0:
 // dh = u, dkey = dvalue = 0 and no part in dq and dk, whatever its key and value hold.
 //
 // Design: bound by memory (a token reads (3 hc + 1) dim and writes (2 hc + 1) dim bf16 values, once), but
@@ -40,9 +40,10 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kMaxSmem = 226 << 10;
+constexpr uint64_t kSettleNs = 100000;  // after a wait has run out: far longer than a store to another SM takes
 
 struct CopyGrad {
-  float gate, c, ea, eb;  // gate, c, e / A, e / B
+  float gate, c, ea, eb, m;  // gate, c, e / A, e / B, |dot|
 };
 
 // The scalars of one residual copy from its four sums
@@ -53,6 +54,7 @@ __device__ __forceinline__ CopyGrad copy_grad(float sh, float sk, float sd, floa
   const float dot = sd * r;
   const float m = fabsf(dot), ri = rsqrtf(fmaxf(m, 1e-6f));  // 1 / |z|
   CopyGrad g;
+  g.m = m;
   // from exp(-|z|), so that neither the gate nor 1 - gate cancels: gate (1 - gate) = x / (1 + x)^2
   const float x = expf(-fmaxf(m, 1e-6f) * ri), y = __frcp_rn(1.0f + x);
   g.gate = dot < 0.f ? x * y : y;
@@ -86,6 +88,7 @@ __device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
 }
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
 
 // one row's part of a token into shared memory, counted in bytes on `bar`
 __device__ __forceinline__ void copy_row(uint4* dst, const uint16_t* src, uint32_t bytes, uint32_t bar) {
@@ -115,6 +118,59 @@ __device__ __forceinline__ float warp_reduce_scatter(float (&s)[N], int lane) {
   return r;
 }
 
+// A sum and what its roundings lost, so far: twice the precision of fp32. Where sum(h w key) cancels to almost
+// nothing, the gate's slope (1 / sqrt of it) magnifies its error, and a few such tokens set the error of the weights'
+// gradients: up to 1e-3 of them at widths of some hundred columns. So a token with a copy of |dot| < kSmallDot has
+// that sum formed once more in this way (for every token it cost 687 instead of 538 us at 16,384 tokens of
+// 4 x 5,120).
+constexpr float kSmallDot = 0.03125f;
+struct Sum2 {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Sum2 add2(const Sum2& a, const Sum2& b) {
+  Sum2 r;
+  r.hi = __fadd_rn(a.hi, b.hi);
+  const float z = __fsub_rn(r.hi, a.hi);
+  r.lo = __fadd_rn(__fadd_rn(a.lo, b.lo), __fadd_rn(__fsub_rn(a.hi, __fsub_rn(r.hi, z)), __fsub_rn(b.hi, z)));
+  return r;
+}
+
+// one thread's part of sum(h w key): h * key and q_weight * k_weight are exact (bf16 factors), their product comes in
+// two parts, and both are summed
+__device__ __forceinline__ Sum2 dot_part(const Vec8& h, const Vec8& k, const Vec8& w) {
+  float2 hi = {}, lo = {};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 hk = __fmul2_rn(h.p[e], k.p[e]), term = __fmul2_rn(hk, w.p[e]);
+    const float2 sum = __fadd2_rn(hi, term), z = __fadd2_rn(sum, minus(hi));
+    lo = __fadd2_rn(lo, __ffma2_rn(hk, w.p[e], minus(term)));
+    lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(hi, minus(__fadd2_rn(sum, minus(z)))), __fadd2_rn(term, minus(z))));
+    hi = sum;
+  }
+  return add2(Sum2{hi.x, lo.x}, Sum2{hi.y, lo.y});
+}
+
+// warp_reduce_scatter for N sums of that kind
+template <int N>
+__device__ __forceinline__ Sum2 warp_reduce_scatter2(Sum2 (&s)[N], int lane) {
+#pragma unroll
+  for (int w = N / 2, off = 16; w >= 1; w /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const Sum2 give = up ? s[j] : s[j + w];
+      const Sum2 keep = up ? s[j + w] : s[j];
+      s[j] = add2(keep, Sum2{__shfl_xor_sync(0xffffffffu, give.hi, off), __shfl_xor_sync(0xffffffffu, give.lo, off)});
+    }
+  }
+  Sum2 r = s[0];
+#pragma unroll
+  for (int off = 16 / N; off >= 1; off /= 2)
+    r = add2(r, Sum2{__shfl_xor_sync(0xffffffffu, r.hi, off), __shfl_xor_sync(0xffffffffu, r.lo, off)});
+  return r;
+}
+
 // Write v to the same shared variable of CTA `rank` and count its 4 bytes on that CTA's mbarrier. Unlike a
 // cluster barrier's release this waits for none of the thread's global stores.
 __device__ __forceinline__ void send(float* p, uint32_t bar, uint32_t rank, float v) {
@@ -139,7 +195,8 @@ __global__ void __launch_bounds__(max_threads(HC))
   constexpr bool kKeepW = HC <= 4;      // the weights stay in registers; 8 copies read them again (L1, L2)
   extern __shared__ uint4 smem[];
   __shared__ float4 scal[2][HC];
-  __shared__ volatile int dead;  // a wait has run out: nothing more is fetched, the results are not to be used
+  __shared__ int again[2];
+  __shared__ volatile int dead;  // a wait has run out: nothing more is fetched or sent, the results are not to be used
   __shared__ __align__(8) uint64_t bars[2 + S];  // of red's two halves: the bytes of a token's sums; of the stages
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
   const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
@@ -238,26 +295,28 @@ __global__ void __launch_bounds__(max_threads(HC))
           for (int e = 0; e < 4; ++e) {
             q[0] = __ffma2_rn(h.p[e], h.p[e], q[0]);
             q[1] = __ffma2_rn(k.p[e], k.p[e], q[1]);
-            q[2] = __ffma2_rn(__fmul2_rn(h.p[e], w.p[e]), k.p[e], q[2]);
+            q[2] = __ffma2_rn(__fmul2_rn(h.p[e], k.p[e]), w.p[e], q[2]);
             q[3] = __ffma2_rn(u.p[e], v.p[e], q[3]);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: what the slots hold
+          for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: another vector's
         }
       }
       const float mine = warp_reduce_scatter<N>(s, lane);
       float* to = red + ((buf * cs + rank) * nw + warp) * N + lane / (32 / N);
       if (lane % (32 / N) == 0) {
         if (cs == 1) *to = mine;
-        else if (t != withhold || rank != 0)
+        else if (!dead && (t != withhold || rank != 0))
           for (int r = 0; r < cs; ++r) send(to, bar0 + 8 * buf, r, mine);
       }
       if (cs == 1) __syncthreads();
-      // red[buf] is written again two tokens on: whoever does has the sums of the token between from every CTA,
-      // each sent past the barrier below that follows the reads here
+      // red[buf] is written again two exchanges on: whoever does has the sums of the exchange between from every
+      // CTA, each sent past the barrier below that follows the reads here
+      float f[4];  // (the scalar warp's) the sums of copy lane % HC
       if (warp == nw - 1) {
         if (cs > 1) {
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * N * 4));
+          // once dead, the barrier's phase may be open still: another arrival would be one too many
+          if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * N * 4));
           wait(buf);
         }
         // lane l: every (32 / N)-th of the warps' parts of sum l % N (no division here: with one per part this
@@ -269,14 +328,55 @@ __global__ void __launch_bounds__(max_threads(HC))
         for (int j = lane / N; j < parts_of_token; j += 32 / N) sum += from[j * N];
 #pragma unroll
         for (int off = N; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        float f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = __shfl_sync(0xffffffffu, sum, 4 * (lane % HC) + e);
         const CopyGrad g = copy_grad(f[0], f[1], f[2], f[3], rd, a.eps, inv_sqrt_dim);
         if (lane < HC) scal[buf][lane] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+        // the same sums in the same order in every CTA of the cluster, so the same answer
+        const bool any = __any_sync(0xffffffffu, g.m < kSmallDot);
+        if (lane == 0) again[buf] = any;
       }
       __syncthreads();
       refill();
+      if (again[buf]) {  // sum(h w key) once more, in twice the precision
+        buf ^= 1;
+        Sum2 d[HC];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), w = weights(i);
+          d[i] = Sum2{0.f, 0.f};
+          if (on) d[i] = dot_part(h, k, w);
+        }
+        const Sum2 mine2 = warp_reduce_scatter2<HC>(d, lane);
+        float* to2 = red + ((buf * cs + rank) * nw + warp) * N + 2 * (lane / (32 / HC));
+        if (lane % (32 / HC) == 0) {
+          if (cs == 1) {
+            to2[0] = mine2.hi;
+            to2[1] = mine2.lo;
+          } else if (!dead) {
+            for (int r = 0; r < cs; ++r) {
+              send(to2, bar0 + 8 * buf, r, mine2.hi);
+              send(to2 + 1, bar0 + 8 * buf, r, mine2.lo);
+            }
+          }
+        }
+        if (cs == 1) __syncthreads();
+        if (warp == nw - 1) {
+          if (cs > 1) {
+            if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * 2 * HC * 4));
+            wait(buf);
+          }
+          const float* from = red + buf * cs * nw * N + 2 * (lane % HC);
+          Sum2 sum = {0.f, 0.f};
+          for (int j = lane / HC; j < cs * nw; j += 32 / HC) sum = add2(sum, Sum2{from[j * N], from[j * N + 1]});
+#pragma unroll
+          for (int off = HC; off < 32; off *= 2)
+            sum = add2(sum, Sum2{__shfl_xor_sync(0xffffffffu, sum.hi, off), __shfl_xor_sync(0xffffffffu, sum.lo, off)});
+          const CopyGrad g = copy_grad(f[0], f[1], sum.hi + sum.lo, f[3], rd, a.eps, inv_sqrt_dim);
+          if (lane < HC) scal[buf][lane] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+        }
+        __syncthreads();
+      }
       if (on) {
         Vec8 dv = {};
 #pragma unroll
@@ -287,11 +387,11 @@ __global__ void __launch_bounds__(max_threads(HC))
           Vec8 dh, dk;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 ch = __fmul2_rn(both(g.y), h.p[e]), ck = __fmul2_rn(both(g.y), k.p[e]);
-            dh.p[e] = __ffma2_rn(w.p[e], ck, __ffma2_rn(both(g.z), h.p[e], u.p[e]));
-            dk.p[e] = __ffma2_rn(w.p[e], ch, __fmul2_rn(both(g.w), k.p[e]));
+            const float2 cw = __fmul2_rn(both(g.y), w.p[e]);
+            dh.p[e] = __ffma2_rn(cw, k.p[e], __ffma2_rn(both(g.z), h.p[e], u.p[e]));
+            dk.p[e] = __ffma2_rn(cw, h.p[e], __fmul2_rn(both(g.w), k.p[e]));
             dv.p[e] = __ffma2_rn(both(g.x), u.p[e], dv.p[e]);
-            dw[i].p[e] = __ffma2_rn(ch, k.p[e], dw[i].p[e]);
+            dw[i].p[e] = __ffma2_rn(both(g.y), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
           }
           st8(dxt + i * a.dim, dh);
           st8(dkt + i * a.dim, dk);
@@ -324,10 +424,14 @@ __global__ void __launch_bounds__(max_threads(HC))
       *reinterpret_cast<float4*>(to + 4) = make_float4(d[2].x, d[2].y, d[3].x, d[3].y);
     }
   }
-  if (tid == 0 && dead)  // copies may still be on their way into this CTA's memory
-    for (int st = 0; st < S; ++st)
-      if (cluster + (int64_t)st * nc < a.T) tc::mbar_wait(bar0 + 16 + 8 * st, (last >> st) & 1, nullptr);
-  if (cs > 1) tc::cluster_sync();  // and other CTAs' sums
+  if (dead) {  // copies may still be on their way into this CTA's memory, and sums into another's
+    if (tid == 0)
+      for (int st = 0; st < S; ++st)
+        if (cluster + (int64_t)st * nc < a.T) tc::mbar_wait(bar0 + 16 + 8 * st, (last >> st) & 1, nullptr);
+    const uint64_t t0 = tc::global_timer_ns();
+    while (tc::global_timer_ns() - t0 < kSettleNs) {}
+  }
+  if (cs > 1) tc::cluster_sync();  // no CTA leaves while another may send to it
 }
 
 // The weights' gradients from the clusters' parts: a CTA takes 128 columns, its 8 warps take every 8th part

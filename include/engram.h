@@ -516,7 +516,8 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
  *   dkv key i    = ddot * (r * w * h - dot / (B * dim) * key_i)
  *   dkv value    = sum over i of gate_i * u_i
  *   dq_weight[i] = k_weight[i] * sum over t of ddot * r * h * key_i;   dk_weight[i]: with q_weight[i]
- * in fp32. A token whose mask is 0 has a constant gate: dx = dout bit for bit, its dkv is +0 and it takes no
+ * in fp32; sum(h * w * key_i) is formed in twice that precision for tokens with a copy of |dot| < 1/32, where the
+ * slope 0.5 / sqrt(|dot|) magnifies its error. A token whose mask is 0 has a constant gate: dx = dout bit for bit, its dkv is +0 and it takes no
  * part in the weights' gradients, whatever its x, key and value hold.
  *   x, kv, q_weight, k_weight, mask, hc, eps  as engram_gate; dim a multiple of 8, <= ENGRAM_MAX_GATE_GRAD_DIM
  *   dout       device bf16 [T][hc][dim]

@@ -49,7 +49,7 @@ def _inputs(rng, T, hc, dim, masked=0.2):
     return [_bf(a) for a in (x, kv.reshape(T, -1), q, k, dout)] + [torch.from_numpy(mask)]
 
 
-def _check(args, got, what):
+def _check(args, got, what, small=False):
     x, kv, q, k, dout = (_f64(a) for a in args[:5])
     mask = args[5].cpu().numpy()
     T, hc, dim = x.shape
@@ -60,6 +60,8 @@ def _check(args, got, what):
     A, B = (x * x).mean(-1, keepdims=True) + EPS, (key * key).mean(-1, keepdims=True) + EPS
     r, w, m = 1 / np.sqrt(A * B * dim), q * k, np.abs(dot)
     dot_err = r * s * np.abs(x * w * key).sum(-1, keepdims=True) + m * (s + 4 * u)
+    if small:  # the sum in twice the precision: what is left is the mean squares' error and single roundings
+        dot_err = m * (2 * s + 16 * u)
     clear = (np.abs(m - 1e-6) > 2 * dot_err) & ((m > 4 * dot_err) | (m == 0)) | ~mask[:, None, None]
     assert clear.all(), f"{what}: the test's own inputs are too near the clamp"
     root = np.sqrt(np.maximum(m, 1e-6))
@@ -137,6 +139,27 @@ def test_gate_grad_masks():
     for a, b in zip(got[:2], exp[:2]):
         assert torch.equal(a.cpu()[~bad], b.cpu()[~bad])
     assert torch.equal(got[2], exp[2]) and torch.equal(got[3], exp[3])
+
+
+@pytest.mark.parametrize("T,hc,dim", [(600, 1, 64), (300, 4, 1024), (200, 2, 5120), (64, 8, 640), (90, 4, 5120)])
+def test_gate_grad_small_dots(T, hc, dim):
+    """Keys almost orthogonal to h: sum(h w key) cancels and 1 / sqrt(dot) magnifies what an fp32 sum of it
+    would be off by. The kernel forms such sums in twice the precision, so dot is held to the error of the
+    mean squares alone. Tokens with a copy of |dot| outside [1e-5, 0.03] are masked out."""
+    rng = np.random.default_rng(T + dim)
+    args = _inputs(rng, T, hc, dim, masked=0.0)
+    x, q, k = _f64(args[0]), _f64(args[2]), _f64(args[3])
+    kv = rng.standard_normal((T, hc + 1, dim))
+    key = kv[:, :hc]
+    key -= (x * q * k * key).sum(-1, keepdims=True) / (x * x * q * k * q * k).sum(-1, keepdims=True) * (x * q * k)
+    kv[:, :hc] = key + rng.uniform(-1, 1, (T, hc, 1)) * 0.002 * dim ** -0.5 * x
+    args[1] = _bf(kv.reshape(T, -1))
+    dot = np.abs(R.gate_grad(x, _f64(args[1]), q, k, _f64(args[4]), np.ones(T, bool), EPS)[5][..., 0])
+    args[5] = torch.from_numpy(((dot > 1e-5) & (dot < 0.03)).all(1))
+    assert args[5].float().mean() > 0.5
+    got = _run(args)
+    _check(args, got, "small dots", small=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, _run(args)))
 
 
 def test_gate_grad_clamped_and_zero_rows():
