@@ -514,9 +514,18 @@ __device__ __forceinline__ void finish_row(const EmbedGradArgs& a, uint32_t row,
   store_vals<GT, V>(g, acc);
 }
 
+// Rows [r0, r0 + m) that no id names, in words of the widest type that their addresses and width allow
+template <typename Word>
+__device__ __forceinline__ void zero_words(uint8_t* row0, int64_t stride, int m, int per_row, const uint8_t* named) {
+  for (int i = threadIdx.x; i < m * per_row; i += kThreads) {
+    const int r = i / per_row;
+    if (!named[r]) reinterpret_cast<Word*>(row0 + r * stride)[i - r * per_row] = Word{};
+  }
+}
+
 template <int GT>
 __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const SumArgs& s, int64_t block) {
-  // rows without ids: row r has one exactly if the first sorted id >= r is r
+  // row r has an id exactly if the first sorted id >= r is r
   __shared__ uint8_t named[kThreads];
   const int64_t r0 = block * s.zero_rows;
   const int m = (int)min((int64_t)s.zero_rows, a.e.rows - r0);
@@ -530,20 +539,15 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, const SumArgs&
     named[threadIdx.x] = lo < s.n && s.ids[lo] == r;
   }
   __syncthreads();
-  using G = typename Elem<GT>::type;
-  G* g = static_cast<G*>(a.grad);
-  constexpr int kPer = 16 / sizeof(G);
-  const bool wide = (reinterpret_cast<uintptr_t>(g) % 16 == 0) && a.grad_stride % kPer == 0 && a.e.dim % kPer == 0;
-  for (int r = 0; r < m; ++r) {
-    if (named[r]) continue;
-    G* row = g + (r0 + r) * a.grad_stride;
-    if (wide) {
-      for (int k = threadIdx.x; k < a.e.dim / kPer; k += kThreads)
-        reinterpret_cast<uint4*>(row)[k] = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      for (int k = threadIdx.x; k < a.e.dim; k += kThreads) Elem<GT>::store(row + k, 0.f);
-    }
-  }
+  constexpr int kSize = sizeof(typename Elem<GT>::type);
+  const int64_t stride = a.grad_stride * kSize;
+  uint8_t* row0 = static_cast<uint8_t*>(a.grad) + r0 * stride;
+  const int bytes = a.e.dim * kSize;
+  const uint64_t any = reinterpret_cast<uintptr_t>(row0) | (uint64_t)stride | (uint64_t)bytes;
+  if (any % 16 == 0) zero_words<uint4>(row0, stride, m, bytes / 16, named);
+  else if (any % 8 == 0) zero_words<uint2>(row0, stride, m, bytes / 8, named);
+  else if (any % 4 == 0) zero_words<uint32_t>(row0, stride, m, bytes / 4, named);
+  else zero_words<uint16_t>(row0, stride, m, bytes / 2, named);
 }
 
 template <int DT, int GT, int V>
@@ -825,7 +829,7 @@ Layout layout_of(int64_t n, int32_t dim) {
   l.counts = take((uint64_t)ceil_div(n, kTile) * kMaxBins * 4);
   l.totals = take(kMaxBins * 4);
   l.heads = take((uint64_t)ceil_div(n, kSegTile) * 4);
-  const uint64_t tiles = (uint64_t)std::max(cut_of(n, dim, 1).tiles, cut_of(n, dim, 8).tiles);
+  const uint64_t tiles = (uint64_t)std::max({cut_of(n, dim, 1).tiles, cut_of(n, dim, 4).tiles, cut_of(n, dim, 8).tiles});
   const uint64_t dim4 = (uint64_t)ceil_div(dim, 4) * 4;
   l.lead = take(tiles * dim4 * 4);
   l.trail = take(tiles * dim4 * 4);
@@ -835,32 +839,42 @@ Layout layout_of(int64_t n, int32_t dim) {
   return l;
 }
 
-inline bool wide(const void* p, int64_t stride, int32_t dim, int32_t type) {
-  const int per = 16 / type_bytes(type);
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % per == 0 && dim % 8 == 0;
+// values that one access of a row may take: 8, 4 or 1
+inline int vec_of(const void* p, int64_t stride, int32_t dim, int32_t type) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const int size = type_bytes(type);
+  if (at % 16 == 0 && stride * size % 16 == 0 && dim % 8 == 0) return 8;
+  return at % (4 * size) == 0 && stride % 4 == 0 && dim % 4 == 0 ? 4 : 1;
+}
+
+// calls f(integral_constant<V>)
+template <typename F>
+cudaError_t with_vec(int v, F&& f) {
+  if (v == 8) return f(std::integral_constant<int, 8>{});
+  if (v == 4) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
 
 cudaError_t launch_embed(const EmbedArgs& a, const void* W, int64_t row_stride, int32_t w_type, void* out,
                          int32_t out_type, cudaStream_t s) {
-  const bool v8 = wide(W, row_stride, a.dim, w_type) && wide(out, a.dim, a.dim, out_type);
-  const int64_t units = a.T * a.n_cols * (a.dim / (v8 ? 8 : 1));
+  const int vec = std::min(vec_of(W, row_stride, a.dim, w_type), vec_of(out, a.dim, a.dim, out_type));
+  const int64_t units = a.T * a.n_cols * (a.dim / vec);
   const int64_t grid = ceil_div(units, kThreads * kFly);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   const bool few = units < (int64_t)UINT32_MAX - kThreads * kFly;
   return with_type(w_type, [&](auto wt) {
     return with_type(out_type, [&](auto ot) {
-      using WE = typename Elem<wt()>::type;
-      using OE = typename Elem<ot()>::type;
-      auto go = [&](auto kern, auto n) {
-        return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (const WE*)W, row_stride, (OE*)out, n);
-      };
-      if (v8)
-        return few ? go(embed_kernel<wt(), ot(), 8, uint32_t>, (uint32_t)units)
-                   : go(embed_kernel<wt(), ot(), 8, uint64_t>, (uint64_t)units);
-      return few ? go(embed_kernel<wt(), ot(), 1, uint32_t>, (uint32_t)units)
-                 : go(embed_kernel<wt(), ot(), 1, uint64_t>, (uint64_t)units);
+      return with_vec(vec, [&](auto v) {
+        using WE = typename Elem<wt()>::type;
+        using OE = typename Elem<ot()>::type;
+        auto go = [&](auto kern, auto n) {
+          return launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), 0, s, a, (const WE*)W, row_stride, (OE*)out, n);
+        };
+        return few ? go(embed_kernel<wt(), ot(), v(), uint32_t>, (uint32_t)units)
+                   : go(embed_kernel<wt(), ot(), v(), uint64_t>, (uint64_t)units);
+      });
     });
   });
 }
@@ -933,8 +947,9 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
   }
   const bool number = sparse && n <= kSmall;
   ids = sparse && !number ? u32(l.ids) : key;
-  const bool v8 = wide(a.dout, a.dout_stride, a.e.dim, a.dout_type) && wide(a.grad, a.grad_stride, a.e.dim, a.grad_type);
-  const Cut c = cut_of(n, a.e.dim, v8 ? 8 : 1);
+  const int vec = std::min(vec_of(a.dout, a.dout_stride, a.e.dim, a.dout_type),
+                           vec_of(a.grad, a.grad_stride, a.e.dim, a.grad_type));
+  const Cut c = cut_of(n, a.e.dim, vec);
   SumArgs m;
   m.ids = ids;
   m.pos = pos;
@@ -951,14 +966,16 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
   m.flags = ws + l.flags;
   m.open_row = u32(l.open_row);
   const int64_t row_bytes = (int64_t)a.e.dim * type_bytes(a.grad_type);
-  m.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads, (128 << 10) / row_bytes));
+  // 128 KB a CTA, less where that would leave SMs without one
+  const int64_t zero_bytes = std::max<int64_t>(4 << 10, std::min<int64_t>(128 << 10, a.e.rows * row_bytes / kWantCtas));
+  m.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads, zero_bytes / row_bytes));
   const int64_t grid = c.tiles * c.chunks + (zero ? ceil_div(a.e.rows, m.zero_rows) : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return with_type(a.grad_type, [&](auto gt) {
     cudaError_t r = with_type(a.dout_type, [&](auto dt) {
-      if (v8)
-        return launch_pdl(segment_sum_kernel<dt(), gt(), 8>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, m);
-      return launch_pdl(segment_sum_kernel<dt(), gt(), 1>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, m);
+      return with_vec(vec, [&](auto v) {
+        return launch_pdl(segment_sum_kernel<dt(), gt(), v()>, dim3((unsigned)grid), dim3(kThreads), 0, s, a, m);
+      });
     });
     if (r != cudaSuccess || c.tiles == 1) return r;
     return launch_pdl(segment_join_kernel<gt()>, dim3((unsigned)c.tiles, (unsigned)ceil_div(a.e.dim, kJoinCols)),

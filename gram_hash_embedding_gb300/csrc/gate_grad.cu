@@ -434,38 +434,46 @@ __global__ void __launch_bounds__(max_threads(HC))
   if (cs > 1) tc::cluster_sync();  // no CTA leaves while another may send to it
 }
 
-// The weights' gradients from the clusters' parts: a CTA takes 128 columns, its 8 warps take every 8th part
-// each, and the warps' sums are added in order.
-constexpr int kFinishThreads = 256;
-__global__ void __launch_bounds__(kFinishThreads) gate_weight_finish_kernel(const GateGradArgs a,
-                                                                            const float* __restrict__ part, int parts) {
+// The weights' gradients from the clusters' parts: LANES lanes take 4 columns each, the CTA's THREADS / LANES groups of
+// them take every so many-th part, and the groups' sums are added in order. Few parts (the large widths): 128
+// columns a CTA, 8 groups. Many (narrow rows, whose CTAs are small and many): 32 columns, 128 groups; with 8
+// groups 3,040 parts took 33 us.
+template <int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS) gate_weight_finish_kernel(const GateGradArgs a,
+                                                                     const float* __restrict__ part, int parts) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kWarps = kFinishThreads / 32;
-  __shared__ float4 sum_s[kWarps][32];
-  const int n = a.hc * a.dim, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j = (blockIdx.x * 32 + lane) * 4;
+  constexpr int kGroups = THREADS / LANES;
+  __shared__ float4 sum_s[kGroups][LANES];
+  const int n = a.hc * a.dim, lane = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const int j = (blockIdx.x * LANES + lane) * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (j < n) {
-#pragma unroll 8
-    for (int z = warp; z < parts; z += kWarps) {
-      const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)z * n + j);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
-  }
-  sum_s[warp][lane] = s;
-  __syncthreads();
-  if (warp != 0 || j >= n) return;
-  for (int w = 1; w < kWarps; ++w) {
-    const float4 v = sum_s[w][lane];
+  auto add = [&](const float4 v) {
     s.x += v.x;
     s.y += v.y;
     s.z += v.z;
     s.w += v.w;
+  };
+  if (j < n) {
+#pragma unroll 8
+    for (int z = group; z < parts; z += kGroups) add(*reinterpret_cast<const float4*>(part + (int64_t)z * n + j));
   }
+  sum_s[group][lane] = s;
+  __syncthreads();
+  // 8 groups at a time, twice where there are many
+#pragma unroll
+  for (int left = kGroups; left > 1;) {
+    const int next = left > 8 ? left / 8 : 1, each = left / next;
+    if (group < next) {
+      s = sum_s[group * each][lane];
+      for (int g = 1; g < each; ++g) add(sum_s[group * each + g][lane]);
+    }
+    __syncthreads();
+    if (group < next) sum_s[group][lane] = s;
+    __syncthreads();
+    left = next;
+  }
+  if (group != 0 || j >= n) return;
   const uint2 q = *reinterpret_cast<const uint2*>(a.qw + j), k = *reinterpret_cast<const uint2*>(a.kw + j);
   auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
   auto hi = [](uint32_t v) { return __uint_as_float(v & 0xffff0000u); };
@@ -563,8 +571,12 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_
     }
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(gate_weight_finish_kernel, dim3((a.hc * a.dim + 127) / 128), dim3(kFinishThreads), 0, s, a,
-                    (const float*)part, parts);
+  const int n = a.hc * a.dim;
+  if (parts > 256)
+    return launch_pdl(gate_weight_finish_kernel<8, 1024>, dim3((n + 31) / 32), dim3(1024), 0, s, a, (const float*)part,
+                      parts);
+  return launch_pdl(gate_weight_finish_kernel<32, 256>, dim3((n + 127) / 128), dim3(256), 0, s, a, (const float*)part,
+                    parts);
 }
 
 }  // namespace engram

@@ -35,10 +35,11 @@ struct Elem<ENGRAM_TYPE_F16> {
   static __device__ __forceinline__ void store(__half* p, float v) { *p = __float2half_rn(v); }
 };
 
-// V consecutive values: V = 8 with one access of 16 bytes for the 16-bit types and of 32 for fp32 (two
-// of 16 where the address is on no 32-byte boundary: a warp's halves of sectors cost the pass
-// that writes 2.1 GB of clipped fp32 values 930 us instead of 575), V = 1 for rows whose width or alignment allows no wide access. Raw<>
-// keeps them as loaded, so that many loads can be in flight before the first is widened.
+// V consecutive values: V = 8 with one access of 16 bytes for the 16-bit types and of 32 for fp32 (two of 16 where
+// the address is on no 32-byte boundary: a warp's halves of sectors cost the pass that writes 2.1 GB of clipped
+// fp32 values 930 us instead of 575); V = 4 with half of that (rows of 100 values, say); V = 1 for rows whose width or
+// alignment allows neither. Raw<> keeps them as loaded, so that many loads can be in flight before the first
+// is widened.
 template <int TYPE, int V>
 struct Raw;
 template <int TYPE>
@@ -88,6 +89,29 @@ struct Raw<TYPE, 8> {
     }
   }
 };
+template <>
+struct Raw<ENGRAM_TYPE_F32, 4> {
+  float4 a;
+  __device__ __forceinline__ void load(const float* p) { a = *reinterpret_cast<const float4*>(p); }
+  __device__ __forceinline__ void zero() { a = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void widen(float* f) const {
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = a.z;
+    f[3] = a.w;
+  }
+};
+template <int TYPE>
+struct Raw<TYPE, 4> {
+  uint2 a;
+  __device__ __forceinline__ void load(const typename Elem<TYPE>::type* p) { a = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void zero() { a = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void widen(float* f) const {
+    const typename Elem<TYPE>::type* e = reinterpret_cast<const typename Elem<TYPE>::type*>(&a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = Elem<TYPE>::load(e + i);
+  }
+};
 template <int TYPE>
 struct Raw<TYPE, 1> {
   typename Elem<TYPE>::type a;
@@ -116,6 +140,10 @@ template <int TYPE, int V, bool ONCE = false>
 __device__ __forceinline__ void store_vals(typename Elem<TYPE>::type* p, const float* f) {
   if constexpr (V == 1) {
     Elem<TYPE>::store(p, f[0]);
+  } else if constexpr (V == 4 && TYPE == ENGRAM_TYPE_F32) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else if constexpr (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<TYPE>(f[0], f[1]), pack2<TYPE>(f[2], f[3]));
   } else if constexpr (TYPE == ENGRAM_TYPE_F32) {
     if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
       if constexpr (ONCE)
