@@ -44,6 +44,7 @@ __all__ = [
     "engram_lookup_project_workspace", "engram_lookup_project_gate", "engram_lookup_project_gate_workspace",
     "engram_embed", "engram_embed_grad", "engram_embed_grad_dense", "engram_embed_grad_workspace", "engram_gate_grad",
     "engram_gate_grad_workspace", "engram_grad_norm", "engram_grad_clip", "engram_grad_norm_workspace",
+    "PreparedGradClip",
     "TYPE_F32", "TYPE_BF16", "TYPE_F16", "NORM_L2", "NORM_MAX",
 ]
 
@@ -1017,18 +1018,19 @@ def _tensor_list(grads, out, counts):
     words[3::6] = sizes
     words[4::6] = [t << 32 for t in types]
     if out is not None:
-        at = [i for i in range(n) if out[i] is not None]
-        given = [out[i] for i in at]
-        types, ptrs, osizes = _list_part(given, "out")
-        for i, t, p, m in zip(at, types, ptrs, osizes):
-            if m != sizes[i]:
-                raise ValueError(f"out[{i}] has {m} elements, expected {sizes[i]}")
-            words[6 * i + 1] = p
-            words[6 * i + 5] = t
+        at = range(n) if all([o is not None for o in out]) else [i for i in range(n) if out[i] is not None]
+        types, ptrs, osizes = _list_part(out if len(at) == n else [out[i] for i in at], "out")
+        if osizes != (sizes if len(at) == n else [sizes[i] for i in at]):
+            i = next(i for i, m in zip(at, osizes) if m != sizes[i])
+            raise ValueError(f"out[{i}] has {out[i].numel()} elements, expected {sizes[i]}")
+        if len(at) == n:
+            words[1::6], words[5::6] = ptrs, types
+        else:
+            for i, p, t in zip(at, ptrs, types):
+                words[6 * i + 1], words[6 * i + 5] = p, t
     if counts is not None:
-        for i, c in enumerate(counts):
-            if c is None:
-                continue
+        for i in [i for i, c in enumerate(counts) if c is not None]:
+            c = counts[i]
             _size(c, 1, "counts")
             if grads[i].dim() < 2 or sizes[i] == 0:
                 raise ValueError("a gradient with a count must be [n, dim]")
@@ -1077,6 +1079,38 @@ def engram_grad_clip(grads, max_norm: float, norm_type: float = 2.0, out=None, c
     it was before clipping). In place, or into `out`: per gradient a tensor of the same size in any of the
     three types, or None for in place. Rows past a gradient's count are neither read nor written."""
     return _norm_call(grads, norm_type, counts, norm, workspace, stream, out, max_norm)
+
+
+class PreparedGradClip:
+    """A call of engram_grad_norm (max_norm None) or engram_grad_clip whose tensors are checked and marshalled once,
+    for training loops that refill the same gradient buffers: the look at every tensor is most of an
+    unprepared call's time where a model has hundreds. Calling it only enqueues the kernels and returns the norm (one
+    device scalar, written by every call). It runs on the stream given here, or else on the stream current
+    at each call (so it also works inside a CUDA-graph capture). The object keeps the tensors alive."""
+
+    def __init__(self, grads, max_norm: float | None = None, norm_type: float = 2.0, out=None, counts=None,
+                 norm: torch.Tensor | None = None, stream=None):
+        if norm_type not in _NORM_OF:
+            raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+        grads = list(grads)
+        self._arr, n = _tensor_list(grads, out if max_norm is not None else None, counts)
+        dev = grads[0].device if n else torch.device("cuda")
+        self.norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm
+        _size(self.norm, 1, "norm")
+        L = _lib()
+        ws, wp, nbytes = _scratch(None, L.engram_grad_norm_workspace(n), dev)
+        self._keep = (grads, out, counts, ws)
+        self._stream = None if stream is None else _stream(stream)
+        head = (self._arr.buffer_info()[0], n, _NORM_OF[norm_type])
+        tail = (_dev(self.norm, torch.float32, "norm"), wp, nbytes)
+        self._fn = L.engram_grad_norm if max_norm is None else L.engram_grad_clip
+        self._args = head + tail if max_norm is None else head + (float(max_norm),) + tail
+
+    def __call__(self) -> torch.Tensor:
+        rc = self._fn(*self._args, self._stream if self._stream is not None else _current_stream_handle())
+        if rc != OK:
+            raise EngramError(rc, "prepared engram_grad_clip")
+        return self.norm
 
 
 class PreparedHashLookup:

@@ -24,7 +24,8 @@
 // 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 537 us, 3.55 GB at
 // 6.6 TB/s (0.99 of the copy bandwidth). Tried: copies
 // of 16 bytes by each thread into its own slots instead of bulk copies 735 us; a cluster barrier and IEEE
-// roots and divisions in every warp 796 us; two groups of threads with two copies each 683 us; clusters
+// roots and divisions in every warp 796 us; two groups of threads with two copies each 683 us (with 8 copies two
+// groups of four are kept: 4,096 tokens of 8 x 5,120 take 374 us instead of 700, floor 263); clusters
 // of 4, two to an SM, 690 us where all of them fit and 1,217 us where 2 of 76 had to wait.
 #include <algorithm>
 #include <cstdint>
@@ -180,19 +181,23 @@ __device__ __forceinline__ void send(float* p, uint32_t bar, uint32_t rank, floa
                : "memory");
 }
 
-// the most threads of a CTA, one per vector of 8 columns: what the registers allow
-constexpr int max_threads(int hc) { return hc <= 2 ? 640 : 320; }
+// the most threads of a CTA: what the registers allow
+constexpr int max_threads(int hc, int cg) { return hc <= 2 ? 640 : (cg == 1 ? 320 : 384); }
 
-// HC copies, S stages; withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
-template <int HC, int S>
-__global__ void __launch_bounds__(max_threads(HC))
+// HC copies, S stages. CG groups of threads take HC / CG copies each of the same columns: 8 copies in one thread leave too
+// few threads on an SM (the stages' shared memory is per column) and no registers for the weights.
+// withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
+template <int HC, int CG, int S>
+__global__ void __launch_bounds__(max_threads(HC, CG))
     gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int cs,
                      float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
   pdl_wait();
   pdl_trigger();
   constexpr int kArrays = 3 * HC + 1;   // rows of a token: h, keys and douts of the copies, the value
   constexpr int N = 4 * HC;             // sums of a token
-  constexpr bool kKeepW = HC <= 4;      // the weights stay in registers; 8 copies read them again (L1, L2)
+  constexpr int HPT = HC / CG;          // copies of a thread
+  constexpr int M = 4 * HPT;            // sums of a warp
+  constexpr bool kKeepW = HPT <= 4;     // the weights stay in registers; 8 copies read them again (L1, L2)
   extern __shared__ uint4 smem[];
   __shared__ float4 scal[2][HC];
   __shared__ int again[2];
@@ -201,12 +206,16 @@ __global__ void __launch_bounds__(max_threads(HC))
   const int tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nthr >> 5;
   const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
   const uint32_t rank = blockIdx.x % cs;
-  float* red = reinterpret_cast<float*>(smem + (size_t)S * kArrays * nv);  // [2][cs][nw][N]
+  const int per_group = nthr / CG, group = CG == 1 ? 0 : tid / per_group, gt = tid - group * per_group;
+  const int g0 = group * HPT, wg = nw / CG;  // its first copy, and the warps of a group
+  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)S * kArrays * nv);  // [CG - 1][2][per_group]
+  float* red = reinterpret_cast<float*>(dvp + (CG - 1) * 2 * per_group);     // [2][CG][cs][wg][M]
   const int cnt = min(nv, (a.dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
-  const bool on = tid < cnt;
-  const int me = min(tid, cnt - 1);  // threads past the row read its last vector and use nothing of it
+  const bool on = gt < cnt;
+  const int me = min(gt, cnt - 1);  // threads past the row read its last vector and use nothing of it
   const int64_t row0 = 8 * (int64_t)rank * nv;   // its first column
-  const int64_t col = row0 + 8 * tid;
+  const int64_t col = row0 + 8 * gt;
+  const int64_t gcol = (int64_t)g0 * a.dim + col;  // the thread's place in its first copy
   const uint32_t bar0 = tc::smem_u32(bars);
   auto slot = [&](int st, int j) -> const uint4& { return smem[(st * kArrays + j) * nv + me]; };
   // one thread starts a token's copies
@@ -234,23 +243,23 @@ __global__ void __launch_bounds__(max_threads(HC))
   auto load_weights = [&](int i) {
     Vec8 w = {};
     if (on) {
-      const Vec8 q = widen8(__ldg(reinterpret_cast<const uint4*>(a.qw + col + (int64_t)i * a.dim)));
-      const Vec8 k = widen8(__ldg(reinterpret_cast<const uint4*>(a.kw + col + (int64_t)i * a.dim)));
+      const Vec8 q = widen8(__ldg(reinterpret_cast<const uint4*>(a.qw + gcol + (int64_t)i * a.dim)));
+      const Vec8 k = widen8(__ldg(reinterpret_cast<const uint4*>(a.kw + gcol + (int64_t)i * a.dim)));
 #pragma unroll
       for (int e = 0; e < 4; ++e) w.p[e] = __fmul2_rn(q.p[e], k.p[e]);
     }
     return w;
   };
-  Vec8 w_kept[kKeepW ? HC : 1];
+  Vec8 w_kept[kKeepW ? HPT : 1];
   if constexpr (kKeepW) {
 #pragma unroll
-    for (int i = 0; i < HC; ++i) w_kept[i] = load_weights(i);
+    for (int i = 0; i < HPT; ++i) w_kept[i] = load_weights(i);
   }
   auto weights = [&](int i) {
     if constexpr (kKeepW) return w_kept[i];
     else return load_weights(i);
   };
-  Vec8 dw[HC] = {};
+  Vec8 dw[HPT] = {};
   if (tid == 0) {
     dead = 0;
     for (int i = 0; i < 2 + S; ++i) tc::mbar_init(bar0 + 8 * i, 1);
@@ -280,15 +289,15 @@ __global__ void __launch_bounds__(max_threads(HC))
     auto refill = [&]() {
       if (tid == 0) fetch(t + (int64_t)(S - 1) * nc, st == 0 ? S - 1 : st - 1, (open >> (S - 1)) & 1);
     };
-    uint16_t* dxt = a.dx + t * HC * a.dim + col;
-    uint16_t* dkt = a.dkv + t * (HC + 1) * a.dim + col;
+    uint16_t* dxt = a.dx + t * HC * a.dim + gcol;
+    uint16_t* dkt = a.dkv + t * (HC + 1) * a.dim + gcol;
     if (open & 1) {
-      float s[N];
+      float s[M];
       {
         const Vec8 v = widen8(slot(st, 3 * HC));
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), u = widen8(slot(st, 2 * HC + i));
+        for (int i = 0; i < HPT; ++i) {
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), u = widen8(slot(st, 2 * HC + g0 + i));
           const Vec8 w = weights(i);
           float2 q[4] = {};
 #pragma unroll
@@ -302,9 +311,9 @@ __global__ void __launch_bounds__(max_threads(HC))
           for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: another vector's
         }
       }
-      const float mine = warp_reduce_scatter<N>(s, lane);
-      float* to = red + ((buf * cs + rank) * nw + warp) * N + lane / (32 / N);
-      if (lane % (32 / N) == 0) {
+      const float mine = warp_reduce_scatter<M>(s, lane);
+      float* to = red + (((buf * CG + group) * cs + rank) * wg + (warp - group * wg)) * M + lane / (32 / M);
+      if (lane % (32 / M) == 0) {
         if (cs == 1) *to = mine;
         else if (!dead && (t != withhold || rank != 0))
           for (int r = 0; r < cs; ++r) send(to, bar0 + 8 * buf, r, mine);
@@ -316,16 +325,16 @@ __global__ void __launch_bounds__(max_threads(HC))
       if (warp == nw - 1) {
         if (cs > 1) {
           // once dead, the barrier's phase may be open still: another arrival would be one too many
-          if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * N * 4));
+          if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * M * 4));
           wait(buf);
         }
-        // lane l: every (32 / N)-th of the warps' parts of sum l % N (no division here: with one per part this
-        // warp held the others up and the call took 696 us instead of 537)
-        const float* from = red + buf * cs * nw * N + lane % N;
-        const int parts_of_token = cs * nw;
+        // lane l: every (32 / N)-th part of sum l % N by the warps of its copy's group, which lie together (a division
+        // per part here held the other warps up: the call took 696 us instead of 537)
+        const int parts_of_group = cs * wg;
+        const float* from = red + (buf * CG + lane % N / M) * parts_of_group * M + lane % M;
         float sum = 0.f;
 #pragma unroll 5
-        for (int j = lane / N; j < parts_of_token; j += 32 / N) sum += from[j * N];
+        for (int j = lane / N; j < parts_of_group; j += 32 / N) sum += from[j * M];
 #pragma unroll
         for (int off = N; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
 #pragma unroll
@@ -340,16 +349,16 @@ __global__ void __launch_bounds__(max_threads(HC))
       refill();
       if (again[buf]) {  // sum(h w key) once more, in twice the precision
         buf ^= 1;
-        Sum2 d[HC];
+        Sum2 d[HPT];
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), w = weights(i);
+        for (int i = 0; i < HPT; ++i) {
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), w = weights(i);
           d[i] = Sum2{0.f, 0.f};
           if (on) d[i] = dot_part(h, k, w);
         }
-        const Sum2 mine2 = warp_reduce_scatter2<HC>(d, lane);
-        float* to2 = red + ((buf * cs + rank) * nw + warp) * N + 2 * (lane / (32 / HC));
-        if (lane % (32 / HC) == 0) {
+        const Sum2 mine2 = warp_reduce_scatter2<HPT>(d, lane);
+        float* to2 = red + (((buf * CG + group) * cs + rank) * wg + (warp - group * wg)) * M + 2 * (lane / (32 / HPT));
+        if (lane % (32 / HPT) == 0) {
           if (cs == 1) {
             to2[0] = mine2.hi;
             to2[1] = mine2.lo;
@@ -363,12 +372,13 @@ __global__ void __launch_bounds__(max_threads(HC))
         if (cs == 1) __syncthreads();
         if (warp == nw - 1) {
           if (cs > 1) {
-            if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * 2 * HC * 4));
+            if (lane == 0 && !dead) tc::mbar_arrive_expect_tx(bar0 + 8 * buf, (uint32_t)(cs * nw * 2 * HPT * 4));
             wait(buf);
           }
-          const float* from = red + buf * cs * nw * N + 2 * (lane % HC);
+          const int parts_of_group = cs * wg;
+          const float* from = red + (buf * CG + lane % HC / HPT) * parts_of_group * M + 2 * (lane % HPT);
           Sum2 sum = {0.f, 0.f};
-          for (int j = lane / HC; j < cs * nw; j += 32 / HC) sum = add2(sum, Sum2{from[j * N], from[j * N + 1]});
+          for (int j = lane / HC; j < parts_of_group; j += 32 / HC) sum = add2(sum, Sum2{from[j * M], from[j * M + 1]});
 #pragma unroll
           for (int off = HC; off < 32; off *= 2)
             sum = add2(sum, Sum2{__shfl_xor_sync(0xffffffffu, sum.hi, off), __shfl_xor_sync(0xffffffffu, sum.lo, off)});
@@ -377,12 +387,12 @@ __global__ void __launch_bounds__(max_threads(HC))
         }
         __syncthreads();
       }
+      Vec8 dv = {};
       if (on) {
-        Vec8 dv = {};
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          const float4 g = scal[buf][i];  // gate, c, -e / A, -e / B
-          const Vec8 h = widen8(slot(st, i)), k = widen8(slot(st, HC + i)), u = widen8(slot(st, 2 * HC + i));
+        for (int i = 0; i < HPT; ++i) {
+          const float4 g = scal[buf][g0 + i];  // gate, c, -e / A, -e / B
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), u = widen8(slot(st, 2 * HC + g0 + i));
           const Vec8 w = weights(i);
           Vec8 dh, dk;
 #pragma unroll
@@ -396,6 +406,25 @@ __global__ void __launch_bounds__(max_threads(HC))
           st8(dxt + i * a.dim, dh);
           st8(dkt + i * a.dim, dk);
         }
+        if (group > 0) {
+          dvp[(2 * group - 2) * per_group + gt] = make_float4(dv.p[0].x, dv.p[0].y, dv.p[1].x, dv.p[1].y);
+          dvp[(2 * group - 1) * per_group + gt] = make_float4(dv.p[2].x, dv.p[2].y, dv.p[3].x, dv.p[3].y);
+        }
+      }
+      if constexpr (CG > 1) {  // the other groups go on; group 0 waits for their parts of the value's gradient, which the
+                               // barrier of the next token's sums keeps until it has read them
+        if (group > 0) asm volatile("bar.arrive 1, %0;" ::"r"(nthr) : "memory");
+        else asm volatile("bar.sync 1, %0;" ::"r"(nthr) : "memory");
+      }
+      if (group == 0 && on) {
+#pragma unroll
+        for (int g = 0; g < CG - 1; ++g) {
+          const float4 lo = dvp[2 * g * per_group + gt], hi = dvp[(2 * g + 1) * per_group + gt];
+          dv.p[0] = __fadd2_rn(dv.p[0], make_float2(lo.x, lo.y));
+          dv.p[1] = __fadd2_rn(dv.p[1], make_float2(lo.z, lo.w));
+          dv.p[2] = __fadd2_rn(dv.p[2], make_float2(hi.x, hi.y));
+          dv.p[3] = __fadd2_rn(dv.p[3], make_float2(hi.z, hi.w));
+        }
         st8(a.dkv + (t * (HC + 1) + HC) * a.dim + col, dv);
       }
       buf ^= 1;
@@ -405,11 +434,11 @@ __global__ void __launch_bounds__(max_threads(HC))
       if (on) {
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int i = 0; i < HC; ++i) {
-          *reinterpret_cast<uint4*>(dxt + i * a.dim) = slot(st, 2 * HC + i);
+        for (int i = 0; i < HPT; ++i) {
+          *reinterpret_cast<uint4*>(dxt + i * a.dim) = slot(st, 2 * HC + g0 + i);
           *reinterpret_cast<uint4*>(dkt + i * a.dim) = z;
         }
-        *reinterpret_cast<uint4*>(a.dkv + (t * (HC + 1) + HC) * a.dim + col) = z;
+        if (group == 0) *reinterpret_cast<uint4*>(a.dkv + (t * (HC + 1) + HC) * a.dim + col) = z;
       }
     }
     open = open >> 1 | next << (S - 1);
@@ -417,8 +446,8 @@ __global__ void __launch_bounds__(max_threads(HC))
   }
   if (on) {
 #pragma unroll
-    for (int i = 0; i < HC; ++i) {
-      float* to = part + (int64_t)cluster * HC * a.dim + col + (int64_t)i * a.dim;
+    for (int i = 0; i < HPT; ++i) {
+      float* to = part + (int64_t)cluster * HC * a.dim + gcol + (int64_t)i * a.dim;
       const float2* d = dw[i].p;
       *reinterpret_cast<float4*>(to) = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
       *reinterpret_cast<float4*>(to + 4) = make_float4(d[2].x, d[2].y, d[3].x, d[3].y);
@@ -484,38 +513,42 @@ __global__ void __launch_bounds__(THREADS) gate_weight_finish_kernel(const GateG
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 
 struct Shape {
-  int cs, nv, threads, stages;  // CTAs per cluster, vectors and threads per CTA
+  int cs, cg, nv, threads, stages;  // CTAs per cluster, groups of copies, vectors and threads per CTA
   int64_t smem, clusters;
 };
 
-// The smallest cluster whose CTAs hold their columns in registers and three stages of shared memory (8
-// copies of more than 10,000 columns or so: two); more CTAs a token when there are too few tokens for every
-// SM. Few clusters rather than many when every cluster would see few tokens: each leaves hc * dim partial
-// sums behind.
+// The smallest cluster whose CTAs hold their columns in registers and three stages of shared memory (8 copies: in two
+// groups of threads; of more than 12,000 columns or so: in one, and two stages); more CTAs a token when there are too
+// few tokens for every SM. Few clusters rather than many when every cluster would see few tokens: each
+// leaves hc * dim partial sums behind.
 Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   Shape s;
   const int nvec = dim / 8;
-  auto set = [&](int cs, int stages) {
+  auto set = [&](int cs, int cg, int stages) {
     s.cs = cs;
+    s.cg = cg;
     s.stages = stages;
     s.nv = (nvec + cs - 1) / cs;
-    s.threads = (s.nv + 31) / 32 * 32;
-    s.smem = (int64_t)stages * (3 * hc + 1) * s.nv * 16 + 2ll * cs * (s.threads / 32) * 4 * hc * 4;
-    return s.threads <= max_threads(hc) && s.smem <= kMaxSmem;
+    const int per_group = (s.nv + 31) / 32 * 32;
+    s.threads = per_group * cg;
+    s.smem = (int64_t)stages * (3 * hc + 1) * s.nv * 16 + (cg - 1) * per_group * 32ll +
+             2ll * cs * (s.threads / 32) * 4 * (hc / cg) * 4;
+    return s.threads <= max_threads(hc, cg) && s.smem <= kMaxSmem;
   };
+  const int cg = hc == 8 ? 2 : 1;
   int cs = 1;
-  while (cs < 8 && !set(cs, 3)) cs *= 2;
+  while (cs < 8 && !set(cs, cg, 3)) cs *= 2;
   while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
-  if (!set(cs, 3)) set(cs, 2);
-  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(kMaxSmem / s.smem, max_threads(hc) / s.threads));
+  if (!set(cs, cg, 3)) set(cs, 1, 2);
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(kMaxSmem / s.smem, max_threads(hc, s.cg) / s.threads));
   s.clusters = std::min({T, std::max<int64_t>(1, kSms * resident / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
   return s;
 }
 
-template <int HC, int S>
+template <int HC, int CG, int S>
 cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, int64_t withhold,
                          cudaStream_t s) {
-  auto kern = gate_grad_kernel<HC, S>;
+  auto kern = gate_grad_kernel<HC, CG, S>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -562,11 +595,12 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_
     const Shape sh = shape_of(a.T, a.hc, a.dim);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.hc) {
-      case 1: e = launch_shape<1, 3>(a, sh, part, &parts, withhold, s); break;
-      case 2: e = launch_shape<2, 3>(a, sh, part, &parts, withhold, s); break;
-      case 4: e = launch_shape<4, 3>(a, sh, part, &parts, withhold, s); break;
+      case 1: e = launch_shape<1, 1, 3>(a, sh, part, &parts, withhold, s); break;
+      case 2: e = launch_shape<2, 1, 3>(a, sh, part, &parts, withhold, s); break;
+      case 4: e = launch_shape<4, 1, 3>(a, sh, part, &parts, withhold, s); break;
       case 8:
-        e = sh.stages == 3 ? launch_shape<8, 3>(a, sh, part, &parts, withhold, s) : launch_shape<8, 2>(a, sh, part, &parts, withhold, s);
+        e = sh.cg == 2 ? launch_shape<8, 2, 3>(a, sh, part, &parts, withhold, s)
+                       : launch_shape<8, 1, 2>(a, sh, part, &parts, withhold, s);
         break;
     }
     if (e != cudaSuccess) return e;

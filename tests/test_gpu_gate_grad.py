@@ -253,3 +253,19 @@ def test_gate_grad_withheld_sums_end_with_the_timeout_flag(T, hc, dim):
     assert geng.engram_device_status() & geng.STATUS_TIMEOUT
     _check(args, _run(args), "after the timeout")
     assert geng.engram_device_status() == 0
+
+
+def test_gate_grad_offsets_beyond_32_bits():
+    """More than 2^31 values of x: all tokens masked but the last few, which have to come out right."""
+    hc, dim = 4, 5120
+    T, k = (1 << 31) // (hc * dim) + 50, 5
+    args = _inputs(np.random.default_rng(4), k, hc, dim, masked=0.0)
+    x, kv, dout = (torch.zeros((T, *a.shape[1:]), dtype=torch.bfloat16, device="cuda") for a in (args[0], args[1], args[4]))
+    for big, a in ((x, args[0]), (kv, args[1]), (dout, args[4])):
+        big[-k:] = a.cuda()
+    dout[:-k, 1, 7] = 3.0
+    mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+    mask[-k:] = True
+    dx, dkv, dq, dk = geng.engram_gate_grad(x, kv, args[2].cuda(), args[3].cuda(), dout, mask)
+    _check(args, (dx[-k:], dkv[-k:], dq, dk), "last tokens")
+    assert torch.equal(dx[:-k], dout[:-k]) and not dkv[:-k].any()

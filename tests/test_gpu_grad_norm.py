@@ -160,3 +160,42 @@ def test_no_tensors_streams_and_graphs():
         assert abs(float(norm) - exp) <= 2.0 ** -16 * exp
         for o, d in zip(outs, dev):
             assert torch.equal(o.cpu(), _clipped(d.cpu(), float(norm), 2.0, o.dtype))
+
+
+def test_prepared_call():
+    """Marshalled once, called on refilled buffers and inside a graph: the same bits as the plain calls."""
+    rng = np.random.default_rng(7)
+    sizes = [5000, 1, 70_001, 33] * 15
+    dev = [t.cuda() for t in _grads(rng, sizes, ["bf16", "f32", "f16", "f32"] * 15)]
+    dev.append(torch.from_numpy(rng.standard_normal((400, 16)).astype(np.float32)).cuda())
+    counts = [None] * len(sizes) + [torch.tensor([123], device="cuda")]
+    outs = [torch.zeros(t.shape, device="cuda") for t in dev]
+    exp = [torch.zeros(t.shape, device="cuda") for t in dev]
+    clip = geng.PreparedGradClip(dev, 1.0, out=outs, counts=counts)
+    norm = geng.PreparedGradClip(dev, norm_type=float("inf"), counts=counts)
+    clip()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        clip()
+    for scale, call in ((1.0, clip), (0.25, clip), (4.0, g.replay)):
+        for t in dev:
+            t.mul_(scale)
+        call()
+        want = geng.engram_grad_clip(dev, 1.0, out=exp, counts=counts)
+        assert torch.equal(clip.norm, want) and all(torch.equal(a, b) for a, b in zip(outs, exp))
+        assert torch.equal(norm(), geng.engram_grad_norm(dev, float("inf"), counts))
+    with pytest.raises(ValueError, match="norm_type"):
+        geng.PreparedGradClip(dev, 1.0, norm_type=1)
+    with pytest.raises(geng.EngramError):
+        geng.PreparedGradClip(dev, -1.0)()
+
+
+def test_more_than_32_bits_of_values():
+    n = (1 << 31) + 70_001
+    t = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    t[-1], t[5], t[(1 << 31) + 3] = 2.0, 3.0, 6.0
+    assert float(geng.engram_grad_norm([t])) == 7.0
+    assert float(geng.engram_grad_norm([t], norm_type=float("inf"))) == 6.0
+    geng.engram_grad_clip([t], 3.5)
+    assert (t[-1], t[5], t[(1 << 31) + 3]) == (1.0, 1.5, 3.0) and int(t.count_nonzero()) == 3
