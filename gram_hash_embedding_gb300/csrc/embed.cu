@@ -79,12 +79,18 @@ __global__ void __launch_bounds__(kThreads)
 // 1.57 million ids of a table of 384 million rows (29 bits, 3 passes): 75 us of the call's 208. A pass is 4 us of
 // counting (7 in the first), 4 of scanning and 14 of scattering, which no memory bounds (25 MB out of L2): the ranks'
 // ballots and the exchange do. Tiles of 512 threads x 12 pairs measured best (whole call: 8 pairs 231, 16 pairs 254,
-// 256 threads x 16 pairs 248 us); 8-bit passes with __match_any_sync instead of ballots 15 us more.
+// 256 threads x 16 pairs 248 us), of 4 pairs for calls of few ids (20,000: 31 us on the GPU instead of 43; the same at 390,000); 8-bit passes with __match_any_sync instead of ballots 15 us more.
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;
-constexpr int kPerThread = 12;
-constexpr int kTile = kSortThreads * kPerThread;  // pairs per tile (one CTA)
+// Pairs a thread has of a tile (one CTA's pairs): 12, and 4 for calls that would leave most SMs without a tile
+constexpr int kPairs = 12, kPairsFew = 4;
+constexpr int64_t kFewIds = 400000;
+constexpr int pairs_of(int64_t n) { return n <= kFewIds ? kPairsFew : kPairs; }
+
+// With few tiles a pass has no scan of its own: every CTA of the scatter adds up the tiles' counts itself, which costs
+// less than a launch
+constexpr int kFewTiles = 32;
 
 struct SortPass {
   uint32_t* key_in;        // written by the first pass's count
@@ -107,7 +113,7 @@ __device__ __forceinline__ uint32_t key_of_id(const EmbedArgs& e, uint32_t i) {
   return r >= 0 && r < e.rows ? (uint32_t)r : (uint32_t)e.rows;
 }
 
-template <bool FIRST>
+template <bool FIRST, int kPerThread>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const EmbedArgs e, const SortPass p) {
   pdl_wait();
   pdl_trigger();
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const EmbedArg
   const int bins = 1 << p.bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[b] = 0;
   __syncthreads();
-  const uint32_t base = blockIdx.x * (uint32_t)kTile, n = (uint32_t)p.n;
+  const uint32_t base = blockIdx.x * (uint32_t)(kSortThreads * kPerThread), n = (uint32_t)p.n;
   // a thread has runs of 4 pairs
   static_assert(kPerThread % 4 == 0, "a tile is whole runs");
   uint32_t key[kPerThread] = {};
@@ -207,14 +213,17 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
 
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = kMaxBins / kSortThreads;  // digits of a thread: two, which share a word of the warps' counts
-static_assert(kDigits == 2 && kTile < 65536, "the counts of two digits are one word of two 16-bit halves");
-constexpr int kScatterSmem = kTile * 8 + kSortWarps * kMaxBins * 2 + kMaxBins * 4 + 32 * 4;
+static_assert(kDigits == 2 && kSortThreads * kPairs < 65536, "the counts of two digits are one word of two 16-bit halves");
+constexpr int scatter_smem(int pairs) {
+  return kSortThreads * pairs * 8 + kSortWarps * kMaxBins * 2 + kMaxBins * 4 + 32 * 4;
+}
 
 // The stable scatter of a tile: places inside the sorted tile first (the pairs' order is (warp, step, lane), a warp
 // taking 32 * kPerThread consecutive pairs 32 at a time), an exchange through shared memory, then runs of equal digits
 // go out together. The warps' counts are 16-bit, all digits of all warps, whatever the pass's width.
-template <bool FIRST>
+template <bool FIRST, int kPerThread>
 __global__ void __launch_bounds__(kSortThreads, 2) sort_scatter_kernel(const SortPass p) {
+  constexpr int kTile = kSortThreads * kPerThread;
   pdl_wait();
   pdl_trigger();
   extern __shared__ uint32_t smem[];
@@ -242,10 +251,28 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_scatter_kernel(const Sor
   // where each of the thread's digits goes: the digits before it, the same digit in the tiles before
   uint32_t tot[kDigits], there[kDigits];
 #pragma unroll
-  for (int q = 0; q < kDigits; ++q) {
-    const int d = tid * kDigits + q;
-    tot[q] = d < bins ? p.totals[d] : 0u;
-    there[q] = d < bins ? p.counts[((int64_t)blockIdx.x << p.bits) + d] : 0u;
+  for (int q = 0; q < kDigits; ++q) tot[q] = there[q] = 0;
+  if (tid * kDigits < bins) {  // the counts of a thread's two digits are one access
+    const uint2* c = reinterpret_cast<const uint2*>(p.counts) + tid;
+    const int64_t row = bins / kDigits;
+    if (p.tiles <= kFewTiles) {
+#pragma unroll 8
+      for (int t = 0; t < p.tiles; ++t) {
+        const uint2 v = c[t * row];
+        tot[0] += v.x;
+        tot[1] += v.y;
+        if (t < (int)blockIdx.x) {
+          there[0] += v.x;
+          there[1] += v.y;
+        }
+      }
+    } else {
+      const uint2 n = reinterpret_cast<const uint2*>(p.totals)[tid], v = c[blockIdx.x * row];
+      tot[0] = n.x;
+      tot[1] = n.y;
+      there[0] = v.x;
+      there[1] = v.y;
+    }
   }
   const uint32_t all = block_exclusive<kSortThreads>(tot[0] + tot[1], warp_sums);
   there[0] += all;
@@ -363,7 +390,9 @@ __global__ void __launch_bounds__(kThreads) head_count_kernel(const uint32_t* __
   if (threadIdx.x == 0) heads[blockIdx.x] = sum;
 }
 
-// ids, and the sparse form's grad_rows (-1 past the count) and count
+// ids, and the sparse form's grad_rows (-1 past the count) and count. heads null: every CTA counts the heads of all
+// tiles itself, which for a few tiles costs less than a launch.
+constexpr int kFewSegTiles = 16;
 __global__ void __launch_bounds__(kThreads)
     segments_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t rows, const uint32_t* __restrict__ heads,
                     int32_t tiles, uint32_t* __restrict__ ids, int64_t* __restrict__ grad_rows,
@@ -379,10 +408,19 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t k[kSegPer];
   const uint32_t bits = head_bits(key, i0, n, rows, k);
   uint32_t before = 0, all = 0;
-  for (int t = threadIdx.x; t < tiles; t += kThreads) {
-    const uint32_t h = heads[t];
-    all += h;
-    if (t < (int)blockIdx.x) before += h;
+  if (heads != nullptr) {
+    for (int t = threadIdx.x; t < tiles; t += kThreads) {
+      const uint32_t h = heads[t];
+      all += h;
+      if (t < (int)blockIdx.x) before += h;
+    }
+  } else {
+    uint32_t other[kSegPer];
+    for (int t = 0; t < tiles; ++t) {
+      const uint32_t h = __popc(head_bits(key, ((int64_t)t * kThreads + threadIdx.x) * kSegPer, n, rows, other));
+      all += h;
+      if (t < (int)blockIdx.x) before += h;
+    }
   }
   before = __reduce_add_sync(0xffffffffu, before);
   all = __reduce_add_sync(0xffffffffu, all);
@@ -421,9 +459,9 @@ __global__ void __launch_bounds__(32) no_segments_kernel(int64_t* count) {
 
 // Calls of up to kSmall ids: a pair's place is counted, not sorted for. It is the number of smaller keys plus the
 // number of equal ones before it, n^2 comparisons that all SMs share: 6,144 pairs take 38 million, a few
-// microseconds (15 from a cold start), where a radix sort in one CTA took 40 to 50. At 8,192 the whole call takes 23 us,
-// through the radix passes 41; at 16,384 counting would take 57 us against 41 to 47. A CTA places 32 pairs, a lane
-// each; its 8 warps take an eighth of the keys each.
+// microseconds (15 from a cold start), where a radix sort in one CTA took 40 to 50. At 8,192 the whole call takes 25 us,
+// through the radix passes 37 to 40; at 16,384 counting would take 57 us against 37 to 41. A CTA places 32 pairs, a
+// lane each; its 8 warps take an eighth of the keys each.
 constexpr int kSmall = 8192;
 constexpr int kPlaced = 32;  // pairs placed by a CTA
 
@@ -826,7 +864,7 @@ Layout layout_of(int64_t n, int32_t dim) {
     l.pos[i] = take((uint64_t)(n + kBatch) * 4);
   }
   l.ids = take((uint64_t)(n + kBatch) * 4);
-  l.counts = take((uint64_t)ceil_div(n, kTile) * kMaxBins * 4);
+  l.counts = take((uint64_t)ceil_div(n, kSortThreads * pairs_of(n)) * kMaxBins * 4);
   l.totals = take(kMaxBins * 4);
   l.heads = take((uint64_t)ceil_div(n, kSegTile) * 4);
   const uint64_t tiles = (uint64_t)std::max({cut_of(n, dim, 1).tiles, cut_of(n, dim, 4).tiles, cut_of(n, dim, 8).tiles});
@@ -909,7 +947,8 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
     key = u32(l.key[0]);
     pos = u32(l.pos[0]);
   } else {
-    const int tiles = (int)ceil_div(n, kTile);
+    const int pairs = pairs_of(n), tiles = (int)ceil_div(n, kSortThreads * pairs);
+    const bool few = pairs == kPairsFew;
     for (int q = 0; q < passes; ++q) {
       SortPass p;
       p.key_in = u32(l.key[q & 1]);
@@ -922,26 +961,32 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
       p.tiles = tiles;
       p.shift = q * width;
       p.bits = std::min(width, 32 - q * width);
-      auto count = q == 0 ? sort_count_kernel<true> : sort_count_kernel<false>;
+      auto count = few ? (q == 0 ? sort_count_kernel<true, kPairsFew> : sort_count_kernel<false, kPairsFew>)
+                       : (q == 0 ? sort_count_kernel<true, kPairs> : sort_count_kernel<false, kPairs>);
       e = launch_pdl(count, dim3(tiles), dim3(kSortThreads), 0, s, a.e, p);
       if (e != cudaSuccess) return e;
-      e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, 32)), dim3(kScanThreads), 0, s, p);
+      if (tiles > kFewTiles)
+        e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, 32)), dim3(kScanThreads), 0, s, p);
       if (e != cudaSuccess) return e;
-      auto scatter = q == 0 ? sort_scatter_kernel<true> : sort_scatter_kernel<false>;
-      e = cudaFuncSetAttribute(scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, kScatterSmem);
+      auto scatter = few ? (q == 0 ? sort_scatter_kernel<true, kPairsFew> : sort_scatter_kernel<false, kPairsFew>)
+                         : (q == 0 ? sort_scatter_kernel<true, kPairs> : sort_scatter_kernel<false, kPairs>);
+      e = cudaFuncSetAttribute(scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, scatter_smem(pairs));
       if (e != cudaSuccess) return e;
-      e = launch_pdl(scatter, dim3(tiles), dim3(kSortThreads), kScatterSmem, s, p);
+      e = launch_pdl(scatter, dim3(tiles), dim3(kSortThreads), scatter_smem(pairs), s, p);
       if (e != cudaSuccess) return e;
     }
     key = u32(l.key[passes & 1]);
     pos = u32(l.pos[passes & 1]);
     if (sparse) {
       const int seg_tiles = (int)ceil_div(n, kSegTile);
-      e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
-                     u32(l.heads));
-      if (e != cudaSuccess) return e;
+      uint32_t* heads = nullptr;
+      if (seg_tiles > kFewSegTiles) {
+        heads = u32(l.heads);
+        e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows, heads);
+        if (e != cudaSuccess) return e;
+      }
       e = launch_pdl(segments_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
-                     (const uint32_t*)u32(l.heads), seg_tiles, u32(l.ids), a.grad_rows, a.count);
+                     (const uint32_t*)heads, seg_tiles, u32(l.ids), a.grad_rows, a.count);
       if (e != cudaSuccess) return e;
     }
   }
