@@ -973,8 +973,8 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
              (k_weight, bf, hc * dim, "k_weight"), (dout, bf, T * hc * dim, "dout"), (dx, bf, T * hc * dim, "dx"),
              (dkv, bf, T * (hc + 1) * dim, "dkv"), (dq_weight, f32, hc * dim, "dq_weight"),
              (dk_weight, f32, hc * dim, "dk_weight")]
-    if mask is not None:
-        specs.append((_as_u8(mask), torch.uint8, T, "mask"))
+    if mask is not None:  # a bool tensor's bytes, without a view of it
+        specs.append((mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T, "mask"))
     p = _pointers(specs)
     keep, ws, nbytes = _scratch(workspace, _lib().engram_gate_grad_workspace(T, hc, dim), dev)
     temps.append(keep)
