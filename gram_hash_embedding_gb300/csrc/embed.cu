@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(kThreads)
 // 1.57 million ids of a table of 384 million rows (29 bits, 3 passes): 75 us of the call's 208. A pass is 4 us of
 // counting (7 in the first), 4 of scanning and 14 of scattering, which no memory bounds (25 MB out of L2): the ranks'
 // ballots and the exchange do. Tiles of 512 threads x 12 pairs measured best (whole call: 8 pairs 231, 16 pairs 254,
-// 256 threads x 16 pairs 248 us), of 4 pairs for calls of few ids (20,000: 31 us on the GPU instead of 43; the same at 390,000); 8-bit passes with __match_any_sync instead of ballots 15 us more.
+// 256 threads x 16 pairs 248 us), of 4 pairs for calls of few ids (20,000: 31 us on the GPU instead of 43; the same at
+// 390,000); 8-bit passes with __match_any_sync instead of ballots 15 us more.
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;

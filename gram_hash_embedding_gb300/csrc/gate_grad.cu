@@ -193,7 +193,12 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
                      float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kArrays = 3 * HC + 1;   // rows of a token: h, keys and douts of the copies, the value
+  constexpr int kArrays = 3 * HC + 1;   // rows of a token: h and dout of the copies, their keys, the value
+  // A CTA with whole rows brings each tensor's rows of a token, which lie together, by one copy: three for 3 HC + 1
+  // (9,557 tokens of 8 x 464: 80 -> 68 us; 16,384 of 1 x 5,120: 228 -> 225 us). The one group of threads for 8 copies
+  // has rows too wide for one CTA and keeps the order that spills least (16,384 columns: 450 us for 483 us).
+  constexpr bool kWhole = HC < 8 || CG == 2;
+  constexpr int kU = kWhole ? HC : 2 * HC, kK = kWhole ? 2 * HC : HC;  // a stage's rows of dout and of the keys
   constexpr int N = 4 * HC;             // sums of a token
   constexpr int HPT = HC / CG;          // copies of a thread
   constexpr int M = 4 * HPT;            // sums of a warp
@@ -227,13 +232,21 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
     uint4* to = smem + (size_t)st * kArrays * nv;
     tc::mbar_arrive_expect_tx(bar, bytes * (open ? kArrays : HC));
     const uint16_t* u = a.dout + t * HC * a.dim + row0;
-    for (int i = 0; i < HC; ++i) copy_row(to + (2 * HC + i) * nv, u + (int64_t)i * a.dim, bytes, bar);
+    const uint16_t* h = a.x + t * HC * a.dim + row0;
+    const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
+    if (kWhole && cs == 1) {
+      copy_row(to + kU * nv, u, bytes * HC, bar);
+      if (open) {
+        copy_row(to, h, bytes * HC, bar);
+        copy_row(to + kK * nv, k, bytes * (HC + 1), bar);
+      }
+      return;
+    }
+    for (int i = 0; i < HC; ++i) copy_row(to + (kU + i) * nv, u + (int64_t)i * a.dim, bytes, bar);
     if (open) {
-      const uint16_t* h = a.x + t * HC * a.dim + row0;
-      const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
       for (int i = 0; i < HC; ++i) {
         copy_row(to + i * nv, h + (int64_t)i * a.dim, bytes, bar);
-        copy_row(to + (HC + i) * nv, k + (int64_t)i * a.dim, bytes, bar);
+        copy_row(to + (kK + i) * nv, k + (int64_t)i * a.dim, bytes, bar);
       }
       copy_row(to + 3 * HC * nv, k + (int64_t)HC * a.dim, bytes, bar);
     }
@@ -297,7 +310,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
         const Vec8 v = widen8(slot(st, 3 * HC));
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), u = widen8(slot(st, 2 * HC + g0 + i));
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           float2 q[4] = {};
 #pragma unroll
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
         Sum2 d[HPT];
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), w = weights(i);
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), w = weights(i);
           d[i] = Sum2{0.f, 0.f};
           if (on) d[i] = dot_part(h, k, w);
         }
@@ -392,7 +405,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
           const float4 g = scal[buf][g0 + i];  // gate, c, -e / A, -e / B
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, HC + g0 + i)), u = widen8(slot(st, 2 * HC + g0 + i));
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           Vec8 dh, dk;
 #pragma unroll
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          *reinterpret_cast<uint4*>(dxt + i * a.dim) = slot(st, 2 * HC + g0 + i);
+          *reinterpret_cast<uint4*>(dxt + i * a.dim) = slot(st, kU + g0 + i);
           *reinterpret_cast<uint4*>(dkt + i * a.dim) = z;
         }
         if (group == 0) *reinterpret_cast<uint4*>(a.dkv + (t * (HC + 1) + HC) * a.dim + col) = z;
