@@ -525,6 +525,9 @@ __global__ void __launch_bounds__(THREADS) gate_weight_finish_kernel(const GateG
 
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 
+// the threads that an SM's registers hold
+constexpr int resident_threads(int hc) { return hc == 1 ? 896 : hc == 2 ? 736 : hc == 4 ? 480 : 384; }
+
 struct Shape {
   int cs, cg, nv, threads, stages;  // CTAs per cluster, groups of copies, vectors and threads per CTA
   int64_t smem, clusters;
@@ -553,7 +556,8 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   while (cs < 8 && !set(cs, cg, 3)) cs *= 2;
   while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
   if (!set(cs, cg, 3)) set(cs, 1, 2);
-  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>(kMaxSmem / s.smem, max_threads(hc, s.cg) / s.threads));
+  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024),
+                                                                  resident_threads(hc) / s.threads));
   s.clusters = std::min({T, std::max<int64_t>(1, kSms * resident / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
   return s;
 }
@@ -576,7 +580,8 @@ cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, in
   cfg.dynamicSmemBytes = sh.smem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  // CTAs that hold whole rows launch without the attribute: as clusters of one, 8 at most were resident on an SM
+  cfg.numAttrs = sh.cs > 1 ? 2 : 1;
   // no more clusters than can be resident: one that had to wait would run its share of the tokens alone
   cfg.gridDim = dim3((unsigned)(sh.clusters * sh.cs));
   int64_t clusters = sh.clusters;
@@ -585,6 +590,11 @@ cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, in
     e = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg);
     if (e != cudaSuccess) return e;
     clusters = std::max<int64_t>(1, std::min<int64_t>(clusters, resident));
+  } else if (clusters > kSms) {
+    int resident = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, sh.threads, sh.smem);
+    if (e != cudaSuccess) return e;
+    clusters = std::min<int64_t>(clusters, std::max<int64_t>(1, resident) * kSms);
   }
   unsigned int* status = nullptr;
   e = device_status_word(&status);
