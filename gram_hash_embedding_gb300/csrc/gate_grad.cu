@@ -7,8 +7,9 @@
 //   dkey   = c * w * h - (e / B) * key
 //   dvalue = sum_i gate_i * u_i
 //   dq     = k_weight * sum_t c * h * key,  dk = q_weight * the same sum
-// in fp32 (sum(h * w * key) in twice that where it is almost 0), everything recomputed from the forward's inputs. A masked token's gate is the constant 0:
-// dh = u, dkey = dvalue = 0 and no part in dq and dk, whatever its key and value hold.
+// in fp32 (sum(h * w * key) in twice that where it is almost 0), everything recomputed from the forward's inputs. A
+// masked token's gate is the constant 0: dh = u, dkey = dvalue = 0 and no part in dq and dk, whatever its key and value
+// hold.
 //
 // Design: bound by memory (a token reads (3 hc + 1) dim and writes (2 hc + 1) dim bf16 values, once), but
 // every output needs sums over the whole row first, and the weights' gradients are sums over all tokens
@@ -533,10 +534,10 @@ struct Shape {
   int64_t smem, clusters;
 };
 
-// The smallest cluster whose CTAs hold their columns in registers and three stages of shared memory (8 copies: in two
-// groups of threads; of more than 12,000 columns or so: in one, and two stages); more CTAs a token when there are too
-// few tokens for every SM. Few clusters rather than many when every cluster would see few tokens: each
-// leaves hc * dim partial sums behind.
+// The smallest cluster (with one exception below) whose CTAs hold their columns in registers and three stages of
+// shared memory (8 copies: in two groups of threads; of more than 12,000 columns or so: in one, and two stages); more
+// CTAs a token when there are too few tokens for every SM. Few clusters rather than many when every cluster would see
+// few tokens: each leaves hc * dim partial sums behind.
 Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   Shape s;
   const int nvec = dim / 8;
@@ -555,10 +556,21 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   int cs = 1;
   while (cs < 8 && !set(cs, cg, 3)) cs *= 2;
   while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
-  if (!set(cs, cg, 3)) set(cs, 1, 2);
-  const int64_t resident = std::max<int64_t>(1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024),
-                                                                  resident_threads(hc) / s.threads));
-  s.clusters = std::min({T, std::max<int64_t>(1, kSms * resident / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
+  // CTAs resident on an SM, by shared memory and registers
+  auto resident = [&]() {
+    return std::max<int64_t>(1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / s.threads));
+  };
+  if (!set(cs, cg, 3)) {
+    set(cs, 1, 2);
+  } else if (cs < 8) {
+    // one more halving where it brings half as many columns again onto an SM: more tokens' chains at a time (8,192 of
+    // 4 x 3,616: 251 -> 215 us; 20,000 of 1 x 3,800: 248 -> 194). Where it brings as many as before it costs up to a
+    // quarter (8,192 of 8 x 1,024: 139 -> 165).
+    const int64_t columns = s.nv * resident();
+    set(cs * 2, cg, 3);
+    if (s.nv * resident() * 5 < columns * 7) set(cs, cg, 3);
+  }
+  s.clusters = std::min({T, std::max<int64_t>(1, kSms * resident() / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
   return s;
 }
 
