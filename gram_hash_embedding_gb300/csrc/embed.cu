@@ -89,9 +89,14 @@ constexpr int kPairs = 12, kPairsFew = 4;
 constexpr int64_t kFewIds = 400000;
 constexpr int pairs_of(int64_t n) { return n <= kFewIds ? kPairsFew : kPairs; }
 
-// With few tiles a pass has no scan of its own: every CTA of the scatter adds up the tiles' counts itself, which costs
-// less than a launch
+// With few counts a pass has no scan of its own: every CTA of the scatter adds up the tiles' counts itself, which costs
+// less than a launch (348,000 ids of a table of 2,520 rows, 170 tiles of 64 counts: 49 us instead of 52; but 581,000 of
+// 2.7 million rows, 95 tiles of 256 counts, 93 us for 75: all CTAs ask L2 for the same lines)
 constexpr int kFewTiles = 32;
+constexpr int64_t kFewCounts = 12 << 10;
+__host__ __device__ inline bool few_counts(int tiles, int bits) {
+  return tiles <= kFewTiles || ((int64_t)tiles << bits) <= kFewCounts;
+}
 
 struct SortPass {
   uint32_t* key_in;        // written by the first pass's count
@@ -253,37 +258,54 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_scatter_kernel(const Sor
   uint32_t tot[kDigits], there[kDigits];
 #pragma unroll
   for (int q = 0; q < kDigits; ++q) tot[q] = there[q] = 0;
-  if (tid * kDigits < bins) {  // the counts of a thread's two digits are one access
-    const uint2* c = reinterpret_cast<const uint2*>(p.counts) + tid;
-    const int64_t row = bins / kDigits;
-    if (p.tiles <= kFewTiles) {
+  const int row = bins / kDigits;  // a tile's counts, in words of two digits
+  const uint2* c2 = reinterpret_cast<const uint2*>(p.counts);
+  if (few_counts(p.tiles, p.bits)) {
+    // the digits of word tid % row, of every groups-th tile; the parts meet in shared memory, in the tile's place
+    const int group = tid / row, groups = min(16, kSortThreads / row);
+    const uint2* c = c2 + (tid - group * row);
 #pragma unroll 8
-      for (int t = 0; t < p.tiles; ++t) {
-        const uint2 v = c[t * row];
-        tot[0] += v.x;
-        tot[1] += v.y;
-        if (t < (int)blockIdx.x) {
-          there[0] += v.x;
-          there[1] += v.y;
+    for (int t = group < groups ? group : p.tiles; t < p.tiles; t += groups) {
+      const uint2 v = c[t * row];
+      tot[0] += v.x;
+      tot[1] += v.y;
+      if (t < (int)blockIdx.x) {
+        there[0] += v.x;
+        there[1] += v.y;
+      }
+    }
+    if (groups > 1) {
+      uint4* parts = reinterpret_cast<uint4*>(smem);
+      parts[tid] = make_uint4(tot[0], tot[1], there[0], there[1]);
+      __syncthreads();
+      tot[0] = tot[1] = there[0] = there[1] = 0;
+      if (tid < row) {
+        for (int g = 0; g < groups; ++g) {
+          const uint4 v = parts[g * row + tid];
+          tot[0] += v.x;
+          tot[1] += v.y;
+          there[0] += v.z;
+          there[1] += v.w;
         }
       }
-    } else {
-      const uint2 n = reinterpret_cast<const uint2*>(p.totals)[tid], v = c[blockIdx.x * row];
-      tot[0] = n.x;
-      tot[1] = n.y;
-      there[0] = v.x;
-      there[1] = v.y;
     }
+  } else if (tid < row) {
+    const uint2 n = reinterpret_cast<const uint2*>(p.totals)[tid], v = c2[(int64_t)blockIdx.x * row + tid];
+    tot[0] = n.x;
+    tot[1] = n.y;
+    there[0] = v.x;
+    there[1] = v.y;
   }
   const uint32_t all = block_exclusive<kSortThreads>(tot[0] + tot[1], warp_sums);
   there[0] += all;
   there[1] += all + tot[0];
-  // lanes of the warp with the same digit: a ballot per bit (also for bits that every digit has 0), all steps together
+  // lanes of the warp with the same digit: a ballot per bit (of 6 at least), all steps together
   unsigned same[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) same[j] = __ballot_sync(0xffffffffu, base + j * 32 < left);
 #pragma unroll
   for (int b = 0; b < kMaxBits; ++b) {
+    if (b >= 6 && b >= p.bits) break;
     const uint32_t bit = b < p.bits ? 1u << (p.shift + b) : 0u;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
@@ -966,7 +988,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
                        : (q == 0 ? sort_count_kernel<true, kPairs> : sort_count_kernel<false, kPairs>);
       e = launch_pdl(count, dim3(tiles), dim3(kSortThreads), 0, s, a.e, p);
       if (e != cudaSuccess) return e;
-      if (tiles > kFewTiles)
+      if (!few_counts(tiles, p.bits))
         e = launch_pdl(sort_scan_kernel, dim3((unsigned)ceil_div((int64_t)1 << p.bits, 32)), dim3(kScanThreads), 0, s, p);
       if (e != cudaSuccess) return e;
       auto scatter = few ? (q == 0 ? sort_scatter_kernel<true, kPairsFew> : sort_scatter_kernel<false, kPairsFew>)
