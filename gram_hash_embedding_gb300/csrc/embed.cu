@@ -856,7 +856,11 @@ struct Cut {
   int glog, per_unit, chunks;
   int64_t tiles;
 };
-constexpr int64_t kWantCtas = 1216;  // 8 CTAs on each of the 152 SMs; units of 64 and 16 pairs at most: 224 us each, of 32: 218
+// One CTA on each of the 152 SMs: longer units leave fewer parts to join and wait for ids less often (1.1 million ids of
+// 1,342 rows of 64 bf16: 98 us of the call with 8 CTAs an SM wanted, 90 with 1, 2, 3 or 4; 498,000 fp32 rows: 82, 71).
+// Units of 64 and 16 pairs at most for 1.57 million ids of 128: 215 and 224 us, of 32: 210.
+constexpr int64_t kWantCtas = 152;
+constexpr int64_t kZeroCtas = 1216;  // of zeros: 8 on each SM
 Cut cut_of(int64_t n, int32_t dim, int v) {
   Cut c;
   const int lanes = (dim + v - 1) / v;
@@ -1035,7 +1039,7 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
   m.open_row = u32(l.open_row);
   const int64_t row_bytes = (int64_t)a.e.dim * type_bytes(a.grad_type);
   // 128 KB a CTA, less where that would leave SMs without one
-  const int64_t zero_bytes = std::max<int64_t>(4 << 10, std::min<int64_t>(128 << 10, a.e.rows * row_bytes / kWantCtas));
+  const int64_t zero_bytes = std::max<int64_t>(4 << 10, std::min<int64_t>(128 << 10, a.e.rows * row_bytes / kZeroCtas));
   m.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads, zero_bytes / row_bytes));
   const int64_t grid = c.tiles * c.chunks + (zero ? ceil_div(a.e.rows, m.zero_rows) : 0);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
