@@ -79,14 +79,15 @@ __global__ void __launch_bounds__(kThreads)
 // 1.57 million ids of a table of 384 million rows (29 bits, 3 passes): 75 us of the call's 208. A pass is 4 us of
 // counting (7 in the first), 4 of scanning and 14 of scattering, which no memory bounds (25 MB out of L2): the ranks'
 // ballots and the exchange do. Tiles of 512 threads x 12 pairs measured best (whole call: 8 pairs 231, 16 pairs 254,
-// 256 threads x 16 pairs 248 us), of 4 pairs for calls of few ids (20,000: 31 us on the GPU instead of 43; the same at
-// 390,000); 8-bit passes with __match_any_sync instead of ballots 15 us more.
+// 256 threads x 16 pairs 248 us), of 4 pairs while that makes two tiles an SM at most (20,000 ids: 31 us on the GPU
+// instead of 43; 600,000: 69 us a call instead of 71; but 700,000: 76 instead of 74); 8-bit passes with
+// __match_any_sync instead of ballots 15 us more.
 constexpr int kMaxBits = 10;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortThreads = 512;
-// Pairs a thread has of a tile (one CTA's pairs): 12, and 4 for calls that would leave most SMs without a tile
+// Pairs a thread has of a tile (one CTA's pairs): 12, and 4 for calls of few ids
 constexpr int kPairs = 12, kPairsFew = 4;
-constexpr int64_t kFewIds = 400000;
+constexpr int64_t kFewIds = 2 * 152 * kSortThreads * kPairsFew;
 constexpr int pairs_of(int64_t n) { return n <= kFewIds ? kPairsFew : kPairs; }
 
 // With few counts a pass has no scan of its own: every CTA of the scatter adds up the tiles' counts itself, which costs
