@@ -22,11 +22,11 @@
 // forms the token's scalars. That chain is what limits the rate, so it is kept short: approximate reciprocal
 // roots, no integer division. The cluster is as small as registers and shared memory allow (2 CTAs at dim
 // 5120 and 4 copies: one cluster on each pair of SMs).
-// 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 537 us, 3.55 GB at
-// 6.6 TB/s (0.99 of the copy bandwidth). Tried: copies
+// 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 535 to 556 us, 3.55 GB at
+// 6.6 TB/s (0.95 to 0.99 of the copy bandwidth). Tried: copies
 // of 16 bytes by each thread into its own slots instead of bulk copies 735 us; a cluster barrier and IEEE
 // roots and divisions in every warp 796 us; two groups of threads with two copies each 683 us (with 8 copies two
-// groups of four are kept: 4,096 tokens of 8 x 5,120 take 374 us instead of 700, floor 263); clusters
+// groups of four are kept: 4,096 tokens of 8 x 5,120 take 381 us instead of 700, floor 263); clusters
 // of 4, two to an SM, 690 us where all of them fit and 1,217 us where 2 of 76 had to wait.
 #include <algorithm>
 #include <cstdint>

@@ -139,6 +139,13 @@ def test_embed_grad_rows(T, C, dim, rows, kind, dt, gt):
     assert torch.equal(again[1][:k].view(torch.int8), got[1][:k].view(torch.int8))
 
 
+# tables of few rows (digits of few bits), and calls on both sides of 622,592 ids, where the sort's tiles grow
+@pytest.mark.parametrize("T,C,dim,rows,kind", [(348_000, 1, 8, 2520, "uniform"), (622_592, 1, 4, 50, "runs"), (622_593, 1, 4, 1342, "uniform"),
+                                               (30_000, 24, 8, 1, "uniform"), (207_600, 3, 4, 2_700_000, "heavy")])
+def test_embed_grad_rows_many_ids(T, C, dim, rows, kind):
+    test_embed_grad_rows(T, C, dim, rows, kind, "bf16", "f32")
+
+
 @pytest.mark.parametrize("T,C,dim,rows,kind", [s for s in SHAPES if s[3] <= 200_000])
 @pytest.mark.parametrize("dt,gt,acc", [("bf16", "f32", False), ("f32", "bf16", False), ("bf16", "f32", True),
                                        ("f16", "f16", True)])

@@ -255,6 +255,17 @@ def test_gate_grad_withheld_sums_end_with_the_timeout_flag(T, hc, dim):
     assert geng.engram_device_status() == 0
 
 
+# many CTAs to an SM (narrow rows), and rows cut in two where that brings more columns onto an SM
+@pytest.mark.parametrize("T,hc,dim", [(9000, 1, 64), (5003, 1, 216), (6000, 4, 168), (4001, 2, 512), (2500, 8, 464),
+                                      (400, 4, 1536), (333, 1, 3800), (170, 8, 1600), (310, 2, 3200), (157, 4, 3616)])
+def test_gate_grad_many_tokens(T, hc, dim):
+    args = _inputs(np.random.default_rng(T + hc * dim), T, hc, dim)
+    got = _run(args)
+    _check(args, got, f"T={T} hc={hc} dim={dim}")
+    again = _run(args)
+    assert all(torch.equal(a.view(torch.int8), b.view(torch.int8)) for a, b in zip(got, again))
+
+
 def test_gate_grad_offsets_beyond_32_bits():
     """More than 2^31 values of x: all tokens masked but the last few, which have to come out right."""
     hc, dim = 4, 5120
