@@ -414,9 +414,10 @@ __global__ void __launch_bounds__(kThreads) head_count_kernel(const uint32_t* __
   if (threadIdx.x == 0) heads[blockIdx.x] = sum;
 }
 
-// ids, and the sparse form's grad_rows (-1 past the count) and count. heads null: every CTA counts the heads of all
-// tiles itself, which for a few tiles costs less than a launch.
-constexpr int kFewSegTiles = 16;
+// ids, and the sparse form's grad_rows (-1 past the count) and count. Calls of up to kNumbered ids need neither of these
+// two kernels: there every CTA of the sums counts the heads of all ids itself, which costs less than two launches
+// (9,000 ids: 38 us a call instead of 40; 32,000: 45 instead of 48; but 65,000: 67 instead of 55).
+constexpr int64_t kNumbered = 32768;
 __global__ void __launch_bounds__(kThreads)
     segments_kernel(const uint32_t* __restrict__ key, int64_t n, uint32_t rows, const uint32_t* __restrict__ heads,
                     int32_t tiles, uint32_t* __restrict__ ids, int64_t* __restrict__ grad_rows,
@@ -432,19 +433,10 @@ __global__ void __launch_bounds__(kThreads)
   uint32_t k[kSegPer];
   const uint32_t bits = head_bits(key, i0, n, rows, k);
   uint32_t before = 0, all = 0;
-  if (heads != nullptr) {
-    for (int t = threadIdx.x; t < tiles; t += kThreads) {
-      const uint32_t h = heads[t];
-      all += h;
-      if (t < (int)blockIdx.x) before += h;
-    }
-  } else {
-    uint32_t other[kSegPer];
-    for (int t = 0; t < tiles; ++t) {
-      const uint32_t h = __popc(head_bits(key, ((int64_t)t * kThreads + threadIdx.x) * kSegPer, n, rows, other));
-      all += h;
-      if (t < (int)blockIdx.x) before += h;
-    }
+  for (int t = threadIdx.x; t < tiles; t += kThreads) {
+    const uint32_t h = heads[t];
+    all += h;
+    if (t < (int)blockIdx.x) before += h;
   }
   before = __reduce_add_sync(0xffffffffu, before);
   all = __reduce_add_sync(0xffffffffu, all);
@@ -543,7 +535,7 @@ struct SumArgs {
   const uint32_t* ids;
   const uint32_t* pos;
   uint32_t limit;  // ids from here on are no rows
-  int32_t number;  // sparse form of a small call: ids are keys, and this kernel numbers the segments and writes
+  int32_t number;  // sparse form of up to kNumbered ids: ids are keys, and this kernel numbers the segments and writes
                    // grad_rows and count
   int64_t n;
   int32_t glog, per_unit, chunks;
@@ -1005,20 +997,17 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
     }
     key = u32(l.key[passes & 1]);
     pos = u32(l.pos[passes & 1]);
-    if (sparse) {
+    if (sparse && n > kNumbered) {
       const int seg_tiles = (int)ceil_div(n, kSegTile);
-      uint32_t* heads = nullptr;
-      if (seg_tiles > kFewSegTiles) {
-        heads = u32(l.heads);
-        e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows, heads);
-        if (e != cudaSuccess) return e;
-      }
+      uint32_t* heads = u32(l.heads);
+      e = launch_pdl(head_count_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows, heads);
+      if (e != cudaSuccess) return e;
       e = launch_pdl(segments_kernel, dim3(seg_tiles), dim3(kThreads), 0, s, key, n, (uint32_t)a.e.rows,
                      (const uint32_t*)heads, seg_tiles, u32(l.ids), a.grad_rows, a.count);
       if (e != cudaSuccess) return e;
     }
   }
-  const bool number = sparse && n <= kSmall;
+  const bool number = sparse && n <= kNumbered;
   ids = sparse && !number ? u32(l.ids) : key;
   const int vec = std::min(vec_of(a.dout, a.dout_stride, a.e.dim, a.dout_type),
                            vec_of(a.grad, a.grad_stride, a.e.dim, a.grad_type));

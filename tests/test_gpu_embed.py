@@ -139,8 +139,10 @@ def test_embed_grad_rows(T, C, dim, rows, kind, dt, gt):
     assert torch.equal(again[1][:k].view(torch.int8), got[1][:k].view(torch.int8))
 
 
-# tables of few rows (digits of few bits), and calls on both sides of 622,592 ids, where the sort's tiles grow
-@pytest.mark.parametrize("T,C,dim,rows,kind", [(348_000, 1, 8, 2520, "uniform"), (622_592, 1, 4, 50, "runs"), (622_593, 1, 4, 1342, "uniform"),
+# tables of few rows (digits of few bits), and calls on both sides of 32,768 ids, up to which the sums number the
+# segments, and of 622,592, where the sort's tiles grow
+@pytest.mark.parametrize("T,C,dim,rows,kind", [(8193, 1, 520, 3000, "heavy"), (20_000, 1, 264, 3000, "one"), (10_000, 1, 1032, 500, "none"),
+                                               (32_768, 1, 8, 9000, "runs"), (32_769, 1, 8, 9000, "uniform"), (348_000, 1, 8, 2520, "uniform"), (622_592, 1, 4, 50, "runs"), (622_593, 1, 4, 1342, "uniform"),
                                                (30_000, 24, 8, 1, "uniform"), (207_600, 3, 4, 2_700_000, "heavy")])
 def test_embed_grad_rows_many_ids(T, C, dim, rows, kind):
     test_embed_grad_rows(T, C, dim, rows, kind, "bf16", "f32")
