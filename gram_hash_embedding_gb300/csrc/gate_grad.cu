@@ -22,11 +22,11 @@
 // forms the token's scalars. That chain is what limits the rate, so it is kept short: approximate reciprocal
 // roots, no integer division. The cluster is as small as registers and shared memory allow (2 CTAs at dim
 // 5120 and 4 copies: one cluster on each pair of SMs).
-// 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 535 to 556 us, 3.55 GB at
-// 6.6 TB/s (0.95 to 0.99 of the copy bandwidth). Tried: copies
+// 16,384 tokens, dim 5120, 4 copies, a tenth of the tokens masked (they read only dout): 542 to 547 us, 3.55 GB at
+// 6.5 TB/s (0.97 of the copy bandwidth). Tried: copies
 // of 16 bytes by each thread into its own slots instead of bulk copies 735 us; a cluster barrier and IEEE
 // roots and divisions in every warp 796 us; two groups of threads with two copies each 683 us (with 8 copies two
-// groups of four are kept: 4,096 tokens of 8 x 5,120 take 381 us instead of 700, floor 263); clusters
+// groups of four are kept: 4,096 tokens of 8 x 5,120 take 374 us instead of 700, floor 263); clusters
 // of 4, two to an SM, 690 us where all of them fit and 1,217 us where 2 of 76 had to wait.
 #include <algorithm>
 #include <cstdint>
@@ -187,19 +187,19 @@ constexpr int max_threads(int hc, int cg) { return hc <= 2 ? 640 : (cg == 1 ? 32
 
 // HC copies, S stages. CG groups of threads take HC / CG copies each of the same columns: 8 copies in one thread leave too
 // few threads on an SM (the stages' shared memory is per column) and no registers for the weights.
+// WHOLE: a CTA has whole rows. It brings each tensor's rows of a token, which lie together, by one copy: three for
+// 3 HC + 1 (9,557 tokens of 8 x 464: 80 -> 68 us), and has no cluster's code. One kernel for both kinds took 8,192 tokens
+// of 4 x 2,048 136 us instead of 122 and, two CTAs a token, 16,384 of 4 x 5,120 556 instead of 545.
 // withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
-template <int HC, int CG, int S>
+template <int HC, int CG, int S, bool WHOLE>
 __global__ void __launch_bounds__(max_threads(HC, CG))
-    gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int cs,
+    gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
                      float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
   pdl_wait();
   pdl_trigger();
   constexpr int kArrays = 3 * HC + 1;   // rows of a token: h and dout of the copies, their keys, the value
-  // A CTA with whole rows brings each tensor's rows of a token, which lie together, by one copy: three for 3 HC + 1
-  // (9,557 tokens of 8 x 464: 80 -> 68 us; 16,384 of 1 x 5,120: 228 -> 225 us). The one group of threads for 8 copies
-  // has rows too wide for one CTA and keeps the order that spills least (16,384 columns: 450 us for 483 us).
-  constexpr bool kWhole = HC < 8 || CG == 2;
-  constexpr int kU = kWhole ? HC : 2 * HC, kK = kWhole ? 2 * HC : HC;  // a stage's rows of dout and of the keys
+  const int cs = WHOLE ? 1 : ctas;      // CTAs of the cluster
+  constexpr int kU = WHOLE ? HC : 2 * HC, kK = WHOLE ? 2 * HC : HC;  // a stage's rows of dout and of the keys
   constexpr int N = 4 * HC;             // sums of a token
   constexpr int HPT = HC / CG;          // copies of a thread
   constexpr int M = 4 * HPT;            // sums of a warp
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
     const uint16_t* u = a.dout + t * HC * a.dim + row0;
     const uint16_t* h = a.x + t * HC * a.dim + row0;
     const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
-    if (kWhole && cs == 1) {
+    if (WHOLE) {
       copy_row(to + kU * nv, u, bytes * HC, bar);
       if (open) {
         copy_row(to, h, bytes * HC, bar);
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(THREADS) gate_weight_finish_kernel(const GateG
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 
 // the threads that an SM's registers hold
-constexpr int resident_threads(int hc) { return hc == 1 ? 896 : hc == 2 ? 736 : hc == 4 ? 480 : 384; }
+constexpr int resident_threads(int hc) { return hc == 1 ? 896 : hc == 2 ? 736 : 384; }
 
 struct Shape {
   int cs, cg, nv, threads, stages;  // CTAs per cluster, groups of copies, vectors and threads per CTA
@@ -574,10 +574,10 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   return s;
 }
 
-template <int HC, int CG, int S>
+template <int HC, int CG, int S, bool WHOLE>
 cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, int64_t withhold,
                          cudaStream_t s) {
-  auto kern = gate_grad_kernel<HC, CG, S>;
+  auto kern = gate_grad_kernel<HC, CG, S, WHOLE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -629,13 +629,22 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_
   if (a.T > 0) {
     const Shape sh = shape_of(a.T, a.hc, a.dim);
     cudaError_t e = cudaErrorInvalidValue;
+    auto launch = [&](auto hc, auto cg, auto stages) {
+      constexpr int HC = decltype(hc)::value, CG = decltype(cg)::value, S = decltype(stages)::value;
+      if constexpr (S == 3)  // with two stages rows are too wide for one CTA
+        if (sh.cs == 1) return launch_shape<HC, CG, S, true>(a, sh, part, &parts, withhold, s);
+      return launch_shape<HC, CG, S, false>(a, sh, part, &parts, withhold, s);
+    };
+    using std::integral_constant;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 3> three;
     switch (a.hc) {
-      case 1: e = launch_shape<1, 1, 3>(a, sh, part, &parts, withhold, s); break;
-      case 2: e = launch_shape<2, 1, 3>(a, sh, part, &parts, withhold, s); break;
-      case 4: e = launch_shape<4, 1, 3>(a, sh, part, &parts, withhold, s); break;
+      case 1: e = launch(one, one, three); break;
+      case 2: e = launch(two, one, three); break;
+      case 4: e = launch(integral_constant<int, 4>{}, one, three); break;
       case 8:
-        e = sh.cg == 2 ? launch_shape<8, 2, 3>(a, sh, part, &parts, withhold, s)
-                       : launch_shape<8, 1, 2>(a, sh, part, &parts, withhold, s);
+        e = sh.cg == 2 ? launch(integral_constant<int, 8>{}, two, three) : launch(integral_constant<int, 8>{}, one, two);
         break;
     }
     if (e != cudaSuccess) return e;
