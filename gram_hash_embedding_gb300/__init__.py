@@ -1086,7 +1086,11 @@ class PreparedGradClip:
     for training loops that refill the same gradient buffers: the look at every tensor is most of an
     unprepared call's time where a model has hundreds. Calling it only enqueues the kernels and returns the norm (one
     device scalar, written by every call). It runs on the stream given here, or else on the stream current
-    at each call (so it also works inside a CUDA-graph capture). The object keeps the tensors alive."""
+    at each call (so it also works inside a CUDA-graph capture). The object keeps the tensors alive.
+
+    Its calls share one norm and one workspace, so they must not overlap on the GPU: a caller who uses several
+    streams orders them, and orders the work that fills the gradients before a call on another stream. A
+    graph that captured a call needs the object for as long as it is replayed."""
 
     def __init__(self, grads, max_norm: float | None = None, norm_type: float = 2.0, out=None, counts=None,
                  norm: torch.Tensor | None = None, stream=None):
@@ -1100,14 +1104,41 @@ class PreparedGradClip:
         L = _lib()
         ws, wp, nbytes = _scratch(None, L.engram_grad_norm_workspace(n), dev)
         self._keep = (grads, out, counts, ws)
-        self._stream = None if stream is None else _stream(stream)
         head = (self._arr.buffer_info()[0], n, _NORM_OF[norm_type])
         tail = (_dev(self.norm, torch.float32, "norm"), wp, nbytes)
         self._fn = L.engram_grad_norm if max_norm is None else L.engram_grad_clip
         self._args = head + tail if max_norm is None else head + (float(max_norm),) + tail
+        # The memory made here belongs to the current stream, whose earlier work may still use it
+        self._own = (ws,) if norm is not None else (ws, self.norm)
+        self._ordered = {_current_stream_handle()}  # streams on which a call may use it
+        self._made = None
+        if not torch.cuda.is_current_stream_capturing():
+            self._made = torch.cuda.Event()
+            self._made.record()
+        self._given, self._stream = stream, None if stream is None else _stream(stream)
+
+    def _order(self) -> None:
+        """The first call on a stream other than the constructing one: what that stream had in hand when this
+        object was made ends first, and the memory made here is not handed out again before the calls
+        on the new stream have ended. A capture cannot wait for work outside it (torch.cuda.graph waits
+        for the device before it captures)."""
+        if self._made is None or torch.cuda.is_current_stream_capturing():
+            return
+        stream = self._given
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(self._stream)
+        stream.wait_event(self._made)
+        for t in self._own:
+            t.record_stream(stream)
+        self._ordered.add(stream.cuda_stream)
 
     def __call__(self) -> torch.Tensor:
-        rc = self._fn(*self._args, self._stream if self._stream is not None else _current_stream_handle())
+        handle = self._stream if self._stream is not None else _current_stream_handle()
+        if handle not in self._ordered:
+            self._order()
+        rc = self._fn(*self._args, handle)
         if rc != OK:
             raise EngramError(rc, "prepared engram_grad_clip")
         return self.norm

@@ -199,3 +199,36 @@ def test_more_than_32_bits_of_values():
     assert float(geng.engram_grad_norm([t], norm_type=float("inf"))) == 6.0
     geng.engram_grad_clip([t], 3.5)
     assert (t[-1], t[5], t[(1 << 31) + 3]) == (1.0, 1.5, 3.0) and int(t.count_nonzero()) == 3
+
+
+def test_prepared_call_on_another_stream():
+    """Built behind work of its stream that still writes into the memory it gets, called on another stream at
+    once; and dropped while its call is still waiting there: its memory is not handed out before."""
+    rng = np.random.default_rng(17)
+    host = _grads(rng, [70_001, 33, 500_000], ["bf16", "f32", "f32"])
+    for given in (False, True):
+        dev = [t.cuda() for t in host]
+        outs = [torch.empty(t.shape, device="cuda") for t in host]
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        before = [torch.empty((), device="cuda"), torch.empty(geng.engram_grad_norm_workspace(3), dtype=torch.uint8, device="cuda")]
+        torch.cuda._sleep(100_000_000)
+        for t in before:
+            t.fill_(77)
+        del before, t
+        clip = geng.PreparedGradClip(dev, 1.0, out=outs, stream=side if given else None)
+        with torch.cuda.stream(side):
+            norm = clip()
+        torch.cuda.synchronize()
+        exp = _norm64(host)
+        assert abs(float(norm) - exp) <= 2.0 ** -16 * exp
+        for o, t in zip(outs, host):
+            assert torch.equal(o.cpu(), _clipped(t, float(norm), 1.0, o.dtype))
+        at = clip.norm.data_ptr()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+            clip()
+        del clip, norm
+        other = [torch.empty((), device="cuda") for _ in range(64)]
+        assert all(t.data_ptr() != at for t in other)
+        torch.cuda.synchronize()

@@ -1,0 +1,107 @@
+"""The training operators' binding on the CPU: what it makes of its arguments and which streams it orders. The
+tensors only claim to be on the device and the calls of the library are recorded, not made."""
+import pytest
+import torch
+
+import gram_hash_embedding_gb300 as geng
+
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it is a CUDA tensor and notes the streams it is marked as used on."""
+
+    is_cuda = True
+
+    def record_stream(self, stream):
+        self.__dict__.setdefault("streams", []).append(stream.cuda_stream)
+
+
+def on_device(*shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(OnDevice)
+
+
+class Stream:
+    def __init__(self, handle, log):
+        self.cuda_stream, self.log = handle, log
+
+    def wait_event(self, event):
+        self.log.append(("wait", self.cuda_stream, event.of))
+
+
+@pytest.fixture
+def device(monkeypatch):
+    """torch.cuda's streams, as far as a prepared call uses them; `log` has what happened in order."""
+    geng.build()
+
+    class Device:
+        log, capturing = [], False
+
+        def use(self, handle):
+            self.current = Stream(handle, self.log)
+
+    d = Device()
+    d.log = []
+    d.use(10)
+
+    class Event:
+        def record(self):
+            self.of = d.current.cuda_stream
+            d.log.append(("record", self.of))
+
+    monkeypatch.setattr(torch.cuda, "Event", Event)
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: d.current)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: d.capturing)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: Stream(handle, d.log))
+    monkeypatch.setattr(geng, "_current_stream_handle", lambda: d.current.cuda_stream)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **k).as_subclass(OnDevice))
+
+    class Lib:
+        real = geng._lib()
+        engram_grad_norm_workspace = staticmethod(real.engram_grad_norm_workspace)
+
+        @staticmethod
+        def engram_grad_clip(*args):
+            d.log.append(("call", args[-1]))
+            return geng.OK
+        engram_grad_norm = engram_grad_clip
+
+    monkeypatch.setattr(geng, "_lib", Lib)
+    return d
+
+
+def _marked(clip):
+    """of the norm and the workspace: the streams they are marked as used on"""
+    return [t.__dict__.get("streams", []) for t in (clip.norm, clip._keep[-1])]
+
+
+@pytest.mark.parametrize("given", [None, "object", "handle"])
+def test_prepared_clip_orders_its_memory(device, given):
+    """Its norm and workspace may still be in use by the constructing stream, and their calls on another
+    stream may outlast the object: the other stream waits once, and both tensors are marked as used on it."""
+    stream = {None: None, "object": Stream(20, device.log), "handle": 20}[given]
+    clip = geng.PreparedGradClip([on_device(5)], 1.0, stream=stream)
+    if given is None:
+        clip()
+        assert device.log[-1] == ("call", 10) and _marked(clip) == [[], []]  # the constructing stream needs neither
+        device.use(20)
+    for _ in range(2):
+        clip()
+    waits = [e for e in device.log if e[0] == "wait"]
+    assert waits == [("wait", 20, 10)] and _marked(clip) == [[20], [20]]
+    assert device.log.index(waits[0]) < device.log.index(("call", 20)) and device.log[-1] == ("call", 20)
+    if given is None:
+        device.use(30)
+        device.capturing = True
+        clip()  # a capture cannot wait for what is outside it
+        device.capturing = False
+        assert device.log[-1] == ("call", 30) and len([e for e in device.log if e[0] == "wait"]) == 1
+        clip()
+        assert device.log[-2:] == [("wait", 30, 10), ("call", 30)]
+
+
+def test_prepared_clip_leaves_a_given_norm_alone(device):
+    norm = on_device()
+    clip = geng.PreparedGradClip([on_device(5)], 1.0, norm=norm)
+    device.use(20)
+    assert clip() is norm and _marked(clip) == [[], [20]]
