@@ -1096,7 +1096,9 @@ class PreparedGradClip:
                  norm: torch.Tensor | None = None, stream=None):
         if norm_type not in _NORM_OF:
             raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+        # copies: what the caller does with its lists later frees none of the tensors
         grads = list(grads)
+        out, counts = None if out is None else list(out), None if counts is None else list(counts)
         self._arr, n = _tensor_list(grads, out if max_norm is not None else None, counts)
         dev = grads[0].device if n else torch.device("cuda")
         self.norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else norm

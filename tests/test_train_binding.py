@@ -1,5 +1,8 @@
 """The training operators' binding on the CPU: what it makes of its arguments and which streams it orders. The
 tensors only claim to be on the device and the calls of the library are recorded, not made."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -105,3 +108,20 @@ def test_prepared_clip_leaves_a_given_norm_alone(device):
     clip = geng.PreparedGradClip([on_device(5)], 1.0, norm=norm)
     device.use(20)
     assert clip() is norm and _marked(clip) == [[], [20]]
+
+
+def test_prepared_clip_keeps_its_tensors(device):
+    """Their addresses are marshalled, so they stay whatever the caller does with the lists that were passed."""
+    grads, outs = [on_device(5, 2), on_device(3)], [on_device(5, 2), on_device(3)]
+    counts = [on_device(1, dtype=torch.int64), None]
+    kept = [weakref.ref(t) for t in grads + outs + counts[:1]]
+    clip = geng.PreparedGradClip(grads, 1.0, out=outs, counts=counts)
+    grads.clear()
+    outs.clear()
+    counts[0] = None
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    clip()
+    del clip
+    gc.collect()
+    assert all(r() is None for r in kept)
