@@ -1171,7 +1171,8 @@ class PreparedHashLookup:
         _size(mask, rows_out, "mask")
         _size(start_pos, B, "start_pos")
         _size(cache_rows, B, "cache_rows")
-        self._keep = (ids, start_pos, W, S, out, mask, hashes, cu_seqlens, cache_rows)  # the buffers stay alive
+        # the buffers stay alive, whatever the caller does with its lists
+        self._keep = (ids, start_pos, list(W), list(S), list(out), mask, hashes, cu_seqlens, cache_rows)
         self._W = (_P * n)(*[_dev(w.view(torch.uint8), torch.uint8, "W") for w in W])
         sdt = lay["scale_dtype"]
         self._S = (_P * n)(*[_dev_scales(x, sdt) for x in S])

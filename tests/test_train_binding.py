@@ -125,3 +125,21 @@ def test_prepared_clip_keeps_its_tensors(device):
     del clip
     gc.collect()
     assert all(r() is None for r in kept)
+
+
+def test_prepared_lookup_keeps_its_tensors(device, monkeypatch):
+    """The same for the prepared hash + lookup."""
+    monkeypatch.setattr(geng, "engram_state_layout", lambda state: dict(
+        n_layers=2, max_ngram=2, n_heads=1, head_dim=16, block=16, scale_dtype=geng.SCALE_F32))
+    monkeypatch.setattr(geng._lib, "engram_hash_lookup", staticmethod(lambda *args: geng.OK), raising=False)
+    ids, start = on_device(1, 4, dtype=torch.int64), on_device(1, dtype=torch.int32)
+    W = [on_device(7, 16, dtype=torch.uint8) for _ in range(2)]
+    S = [on_device(7, 1) for _ in range(2)]
+    out = [on_device(4, 16, dtype=torch.bfloat16) for _ in range(2)]
+    kept = [weakref.ref(t) for t in W + S + out]
+    call = geng.PreparedHashLookup(1, ids, start, W, S, out)
+    for ts in (W, S, out):
+        ts.clear()
+    gc.collect()
+    assert all(r() is not None for r in kept)
+    call()
