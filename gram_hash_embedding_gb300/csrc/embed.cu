@@ -868,7 +868,15 @@ Cut cut_of(int64_t n, int32_t dim, int v) {
   return c;
 }
 
-struct Layout {  // byte offsets into the workspace
+// The most tiles of any call of up to n ids, for a workspace that serves them all: units shorter than 32 pairs were chosen
+// because units twice as long would leave fewer than kWantCtas CTAs.
+int64_t most_tiles(int64_t n, int32_t dim, int v) {
+  const Cut c = cut_of(n, dim, v);
+  const int64_t shortest = ceil_div(n, (int64_t)(kThreads >> c.glog) * kBatch);
+  return std::max(c.tiles, std::min(shortest, 2 * (ceil_div(kWantCtas, c.chunks) - 1)));
+}
+
+struct Layout {  // byte offsets into the workspace; no offset and no size falls as n grows
   uint64_t key[2], pos[2], ids, counts, totals, heads, lead, trail, flags, open_row, end;
 };
 Layout layout_of(int64_t n, int32_t dim) {
@@ -884,10 +892,12 @@ Layout layout_of(int64_t n, int32_t dim) {
     l.pos[i] = take((uint64_t)(n + kBatch) * 4);
   }
   l.ids = take((uint64_t)(n + kBatch) * 4);
-  l.counts = take((uint64_t)ceil_div(n, kSortThreads * pairs_of(n)) * kMaxBins * 4);
+  const int64_t sort_tiles = std::max(ceil_div(std::min(n, kFewIds), kSortThreads * kPairsFew),
+                                      n > kFewIds ? ceil_div(n, kSortThreads * kPairs) : 0);
+  l.counts = take((uint64_t)sort_tiles * kMaxBins * 4);
   l.totals = take(kMaxBins * 4);
   l.heads = take((uint64_t)ceil_div(n, kSegTile) * 4);
-  const uint64_t tiles = (uint64_t)std::max({cut_of(n, dim, 1).tiles, cut_of(n, dim, 4).tiles, cut_of(n, dim, 8).tiles});
+  const uint64_t tiles = (uint64_t)std::max({most_tiles(n, dim, 1), most_tiles(n, dim, 4), most_tiles(n, dim, 8)});
   const uint64_t dim4 = (uint64_t)ceil_div(dim, 4) * 4;
   l.lead = take(tiles * dim4 * 4);
   l.trail = take(tiles * dim4 * 4);

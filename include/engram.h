@@ -470,7 +470,7 @@ int engram_embed(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_co
                  engram_stream_t stream);
 
 /* Bytes of device workspace that either form of engram_embed's gradient needs for n = T * n_cols ids
- * (a multiple of 256; 0 for n <= 0). */
+ * (a multiple of 256; 0 for n <= 0). It never falls as n grows: memory for the largest call serves every smaller one. */
 uint64_t engram_embed_grad_workspace(int64_t n, int64_t rows, int32_t dim);
 
 /*
@@ -504,7 +504,7 @@ int engram_embed_grad_dense(const int64_t* idx, int64_t idx_stride, int64_t T, i
                             uint64_t workspace_bytes, engram_stream_t stream);
 
 /* Bytes of device workspace that engram_gate_grad needs (a multiple of 256; 0 for T <= 0 or an
- * unsupported hc or dim). */
+ * unsupported hc or dim). It never falls as T grows. */
 uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
 
 /*

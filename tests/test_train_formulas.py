@@ -186,3 +186,24 @@ def test_binding_refuses_before_any_pointer():
         geng.engram_gate_grad(x, kv[:, 64:], w, w, x)
     with pytest.raises(ValueError, match="mask has"):
         geng.engram_gate_grad(x, kv, w, w, x, mask=torch.ones(4, dtype=torch.bool))
+
+
+def test_workspaces_never_shrink(lib):
+    """A workspace made for the largest call serves every smaller one: its size never falls as the ids, tokens
+    or tensors grow, across every change of tiles, units and clusters."""
+    rng = np.random.default_rng(0)
+    edges = [1, 100, 1216, 2432, 4864, 8192, 9728, 19456, 32768, 38912, 77824, 155648, 311296, 622592, 1245184, 1867776]
+    ns = sorted({max(1, n + d) for n in edges for d in (-1, 0, 1, 2)} | set(range(1, 700)) |
+                {int(n) for n in np.exp(rng.uniform(0, np.log(2 ** 31 - 1), 4000))} | set(range(50, 200_000, 61)))
+    for dim in (1, 3, 4, 7, 8, 12, 16, 20, 36, 64, 100, 128, 256, 260, 264, 512, 1000, 1024, 1027, 2048, 5120, 20_000, 65536):
+        sizes = [lib.engram_embed_grad_workspace(n, 10 ** 6, dim) for n in ns]
+        fall = [(a, b) for a, b, x, y in zip(ns, ns[1:], sizes, sizes[1:]) if y < x]
+        assert not fall, f"dim {dim}: smaller for {fall[0][1]} ids than for {fall[0][0]}"
+    Ts = list(range(1, 700)) + list(range(700, 40_000, 37))
+    for hc in (1, 2, 4, 8):
+        for dim in (8, 64, 168, 464, 512, 1024, 1032, 2048, 2056, 3616, 3800, 5120, 10248, 12000, 16384):
+            sizes = [lib.engram_gate_grad_workspace(T, hc, dim) for T in Ts]
+            fall = [(a, b) for a, b, x, y in zip(Ts, Ts[1:], sizes, sizes[1:]) if y < x]
+            assert not fall, f"{hc} x {dim}: smaller for {fall[0][1]} tokens than for {fall[0][0]}"
+    sizes = [lib.engram_grad_norm_workspace(n) for n in range(3000)]
+    assert sizes == sorted(sizes)
