@@ -3,8 +3,8 @@
 //   out[t][c]  = round(scale * W[idx[t][c]])                    (+0 where idx is outside [0, rows))
 //   G[r]       = scale * sum over (t, c) with idx[t][c] == r of dout[t][c]
 //
-// The gradient's sums run in fp32 in an order that depends on the ids alone (ascending position), so
-// the same call gives the same bits. The ids are sorted (a stable radix sort of (row id, position)
+// The gradient's sums run in fp32 in an order that depends on the ids, their number and dim alone, so the same ids and
+// gradients give the same bits, also at other addresses and strides. The ids are sorted (a stable radix sort of (row id, position)
 // pairs), equal ids become one segment, and every segment is summed and written once.
 #include <algorithm>
 #include <cstdint>
@@ -844,11 +844,15 @@ __global__ void __launch_bounds__(kThreads)
 inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// How the sums are cut up: 2^glog lanes a unit, per_unit pairs a unit, chunks of columns, tiles of units
+// How the sums are cut up: 2^glog lanes a unit, per_unit pairs a unit, chunks of columns, tiles of units. Which pairs meet
+// in a unit and in a tile decides the order of the sums, so it follows from n and dim alone: from the widest access that
+// rows of dim values allow, whatever access a call's types, addresses and strides allow (v values; a narrower one takes
+// more chunks of as many lanes).
 struct Cut {
   int glog, per_unit, chunks;
   int64_t tiles;
 };
+constexpr int widest(int32_t dim) { return dim % 8 == 0 ? 8 : dim % 4 == 0 ? 4 : 1; }
 // One CTA on each of the 152 SMs: longer units leave fewer parts to join and wait for ids less often (1.1 million ids of
 // 1,342 rows of 64 bf16: 98 us of the call with 8 CTAs an SM wanted, 90 with 1, 2, 3 or 4; 498,000 fp32 rows: 82, 71).
 // Units of 64 and 16 pairs at most for 1.57 million ids of 128: 215 and 224 us, of 32: 210.
@@ -856,22 +860,22 @@ constexpr int64_t kWantCtas = 152;
 constexpr int64_t kZeroCtas = 1216;  // of zeros: 8 on each SM
 Cut cut_of(int64_t n, int32_t dim, int v) {
   Cut c;
-  const int lanes = (dim + v - 1) / v;
+  const int lanes = (int)ceil_div(dim, widest(dim));
   c.glog = 0;
   while (c.glog < 5 && (1 << c.glog) < lanes) ++c.glog;
-  c.chunks = (int)ceil_div(lanes, 1 << c.glog);
-  const int units = kThreads >> c.glog;
+  const int units = kThreads >> c.glog, chunks = (int)ceil_div(lanes, 1 << c.glog);
   // the longest units that still give every SM work; a unit of one batch where there is too little
   c.per_unit = 32;
-  while (c.per_unit > kBatch && ceil_div(n, (int64_t)units * c.per_unit) * c.chunks < kWantCtas) c.per_unit >>= 1;
+  while (c.per_unit > kBatch && ceil_div(n, (int64_t)units * c.per_unit) * chunks < kWantCtas) c.per_unit >>= 1;
   c.tiles = ceil_div(n, (int64_t)units * c.per_unit);
+  c.chunks = (int)ceil_div(ceil_div(dim, v), 1 << c.glog);
   return c;
 }
 
 // The most tiles of any call of up to n ids, for a workspace that serves them all: units shorter than 32 pairs were chosen
 // because units twice as long would leave fewer than kWantCtas CTAs.
-int64_t most_tiles(int64_t n, int32_t dim, int v) {
-  const Cut c = cut_of(n, dim, v);
+int64_t most_tiles(int64_t n, int32_t dim) {
+  const Cut c = cut_of(n, dim, widest(dim));
   const int64_t shortest = ceil_div(n, (int64_t)(kThreads >> c.glog) * kBatch);
   return std::max(c.tiles, std::min(shortest, 2 * (ceil_div(kWantCtas, c.chunks) - 1)));
 }
@@ -897,7 +901,7 @@ Layout layout_of(int64_t n, int32_t dim) {
   l.counts = take((uint64_t)sort_tiles * kMaxBins * 4);
   l.totals = take(kMaxBins * 4);
   l.heads = take((uint64_t)ceil_div(n, kSegTile) * 4);
-  const uint64_t tiles = (uint64_t)std::max({most_tiles(n, dim, 1), most_tiles(n, dim, 4), most_tiles(n, dim, 8)});
+  const uint64_t tiles = (uint64_t)most_tiles(n, dim);
   const uint64_t dim4 = (uint64_t)ceil_div(dim, 4) * 4;
   l.lead = take(tiles * dim4 * 4);
   l.trail = take(tiles * dim4 * 4);

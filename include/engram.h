@@ -476,8 +476,8 @@ uint64_t engram_embed_grad_workspace(int64_t n, int64_t rows, int32_t dim);
 /*
  * The gradient of engram_embed by sorted row ids:
  *   G[r] = scale * sum over (t, c) with idx[t * idx_stride + c] == r of dout[t * dout_stride + c * dim ..]
- * Ids outside [0, rows) take no part. The sums are fp32 in an order that depends on the ids alone, so the
- * same inputs give the same bits; the result is rounded once to grad_type.
+ * Ids outside [0, rows) take no part. The sums are fp32 in an order that depends on the ids, their number
+ * and dim alone, so the same ids and gradients give the same bits, at any addresses and strides; the result is rounded once to grad_type.
  *
  * engram_embed_grad, the sparse form: only the rows that occur, for tables whose dense gradient would not fit.
  *   dout        device: token t's n_cols gradients of dim values of dout_type at dout + t * dout_stride

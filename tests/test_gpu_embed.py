@@ -277,3 +277,30 @@ def test_embed_grad_in_a_graph():
         g.replay()
         torch.cuda.synchronize()
         _check_rows(idx, dout, rows, 1.0, out, "f32", kind)
+
+
+@pytest.mark.parametrize("n,dim,kind", [(40_000, 128, "heavy"), (40_000, 64, "one"), (9000, 264, "runs"), (700, 128, "heavy"),
+                                        (12_000, 100, "heavy"), (700_000, 16, "one"), (3000, 2048, "one")])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_embed_grad_bits_do_not_depend_on_addresses(n, dim, kind, dt):
+    """The same ids and gradients in aligned buffers, in views that allow only 4 or 1 values an access and in
+    rows a stride apart: the same bits, in both forms, which agree with each other too."""
+    rng = np.random.default_rng(n + dim)
+    rows = 3000
+    idx = torch.from_numpy(_ids(rng, n, 1, rows, kind)).cuda()
+    dout = _vals(rng, (n, dim), dt).cuda()
+    first = None
+    for off, gap in ((0, 0), (4, 0), (1, 0), (0, 1), (8, 24)):
+        d = torch.empty(n * (dim + gap) + 8, device="cuda", dtype=DT[dt])[off:off + n * (dim + gap)].view(n, dim + gap)[:, :dim]
+        d.copy_(dout)
+        grad = torch.empty(n * dim + 8, device="cuda")[off:off + n * dim].view(n, dim)
+        grad_rows, grad, count = geng.engram_embed_grad(idx, d, rows, grad=grad)
+        k = int(count)
+        got = grad[:k].clone()
+        table = torch.empty(rows * (dim + gap) + 8, device="cuda")[off:off + rows * (dim + gap)].view(rows, dim + gap)[:, :dim]
+        geng.engram_embed_grad_dense(idx, d, table)
+        assert torch.equal(table[grad_rows[:k]].view(torch.int32), got.view(torch.int32)), (off, gap)
+        if first is None:
+            first = got
+            assert torch.isfinite(first).all() and k > 0
+        assert torch.equal(got.view(torch.int32), first.view(torch.int32)), (off, gap)
