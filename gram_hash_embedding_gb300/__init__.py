@@ -1032,10 +1032,10 @@ def _tensor_list(grads, out, counts):
         for i in [i for i, c in enumerate(counts) if c is not None]:
             c = counts[i]
             _size(c, 1, "counts")
-            if grads[i].dim() < 2 or sizes[i] == 0:
+            if grads[i].dim() < 2:
                 raise ValueError("a gradient with a count must be [n, dim]")
             words[6 * i + 2] = _dev(c, torch.int64, "counts")
-            words[6 * i + 4] |= sizes[i] // grads[i].shape[0]
+            words[6 * i + 4] |= grads[i].shape[1:].numel() or 1  # no values: any length will do
     return array.array("q", words), n
 
 

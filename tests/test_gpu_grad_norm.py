@@ -232,3 +232,15 @@ def test_prepared_call_on_another_stream():
         other = [torch.empty((), device="cuda") for _ in range(64)]
         assert all(t.data_ptr() != at for t in other)
         torch.cuda.synchronize()
+
+
+def test_empty_batch_through_the_chain():
+    """An empty batch's sparse gradient with its count, clipped beside another tensor."""
+    none = torch.empty((0, 3), dtype=torch.int64, device="cuda")
+    _, grad, count = geng.engram_embed_grad(none, torch.empty((0, 3, 16), device="cuda"), 9)
+    other = torch.full((100,), 2.0, device="cuda")
+    exp = _clipped(other.cpu(), 20.0, 1.0)
+    assert float(geng.engram_grad_norm([grad, other], counts=[count, None])) == 20.0
+    assert float(geng.engram_grad_clip([grad, other], 1.0, counts=[count, None])) == 20.0
+    assert torch.equal(other.cpu(), exp)
+    assert float(geng.engram_grad_norm([grad], counts=[count])) == 0.0

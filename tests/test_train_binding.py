@@ -143,3 +143,14 @@ def test_prepared_lookup_keeps_its_tensors(device, monkeypatch):
     gc.collect()
     assert all(r() is not None for r in kept)
     call()
+
+
+def test_empty_gradient_with_a_count():
+    """What engram_embed_grad returns for an empty batch, grad [0, dim] and a count, goes into the norm and the
+    clip like any other; an empty gradient without rows is still refused."""
+    count = on_device(1, dtype=torch.int64)
+    arr, n = geng._tensor_list([on_device(0, 128), on_device(3)], None, [count, None])
+    assert n == 2 and list(arr[3::6]) == [0, 3]
+    assert arr[2] == count.data_ptr() and arr[4] & 0xffffffff == 128
+    with pytest.raises(ValueError, match="must be"):
+        geng._tensor_list([on_device(0)], None, [count])
