@@ -867,13 +867,23 @@ def engram_embed_grad_workspace(n: int, rows: int, dim: int) -> int:
     return int(_lib().engram_embed_grad_workspace(int(n), int(rows), int(dim)))
 
 
-def _embed_dout(dout: torch.Tensor, T: int, C: int):
+def _row_width(values: torch.Size, ids: torch.Size) -> int:
+    """Values per id of a gradient of that shape (0: it does not hold one row for each id). In an empty batch the
+    zeros of both shapes cancel, so that its rows are as wide as those of a full one."""
+    n, m = ids.numel(), values.numel()
+    if n == 0:
+        if sum(s == 0 for s in values) != sum(s == 0 for s in ids):
+            return 0
+        n, m = (torch.Size([s or 1 for s in shape]).numel() for shape in (ids, values))
+    return 0 if m % n else m // n
+
+
+def _embed_dout(dout: torch.Tensor, ids: torch.Size, T: int, C: int):
     """The gradient of a lookup's output: contiguous, or [T, C * dim] / [T, C, dim] whose tokens are a
     stride apart: (pointer, token stride, dim)."""
-    n = T * C
-    if dout.dim() == 0 or (n and dout.numel() % n):
-        raise ValueError(f"dout {tuple(dout.shape)} does not hold one row for each of {n} ids")
-    dim = dout.numel() // n if n else dout.shape[-1]
+    dim = _row_width(dout.shape, ids)
+    if dim == 0:
+        raise ValueError(f"dout {tuple(dout.shape)} does not hold one row for each of {T * C} ids")
     if dout.is_contiguous():
         return dout.data_ptr(), C * dim, dim
     inner = dout.dim() == 2 and dout.shape == (T, C * dim) and (dout.shape[1] == 1 or dout.stride(1) == 1)
@@ -896,7 +906,7 @@ def engram_embed_grad(idx: torch.Tensor, dout: torch.Tensor, rows: int, scale: f
     int64 [1], n = idx.numel(). The sums are fp32 in an order fixed by the ids."""
     ip, istride, T, C = _embed_ids(idx)
     dt = _float_type(dout, "dout")
-    dp, dstride, dim = _embed_dout(dout, T, C)
+    dp, dstride, dim = _embed_dout(dout, idx.shape, T, C)
     n, dev = T * C, idx.device
     temps = []
     if grad_rows is None:
@@ -930,7 +940,7 @@ def engram_embed_grad_dense(idx: torch.Tensor, dout: torch.Tensor, grad: torch.T
     ip, istride, T, C = _embed_ids(idx)
     dt, gt = _float_type(dout, "dout"), _float_type(grad, "grad")
     gp, rows, dim, gstride = _rows_of(grad, "grad")
-    dp, dstride, ddim = _embed_dout(dout, T, C)
+    dp, dstride, ddim = _embed_dout(dout, idx.shape, T, C)
     if ddim != dim:
         raise ValueError(f"dout has rows of {ddim} values, grad of {dim}")
     keep, ws, nbytes = _scratch(workspace, _lib().engram_embed_grad_workspace(T * C, rows, dim), idx.device)

@@ -304,3 +304,15 @@ def test_embed_grad_bits_do_not_depend_on_addresses(n, dim, kind, dt):
             first = got
             assert torch.isfinite(first).all() and k > 0
         assert torch.equal(got.view(torch.int32), first.view(torch.int32)), (off, gap)
+
+
+def test_embed_grad_empty_flat():
+    """An empty batch whose gradients are laid out [T, C * dim]."""
+    none = torch.empty((0, 3), dtype=torch.int64, device="cuda")
+    rows, grad, count = geng.engram_embed_grad(none, torch.empty((0, 48), device="cuda"), 9)
+    assert rows.shape == (0,) and grad.shape == (0, 16) and int(count) == 0
+    g = torch.full((9, 16), 5.0, device="cuda")
+    geng.engram_embed_grad_dense(none, torch.empty((0, 48), device="cuda"), g, accumulate=True)
+    assert (g == 5.0).all()
+    geng.engram_embed_grad_dense(none, torch.empty((0, 48), device="cuda"), g)
+    assert (g == 0.0).all()

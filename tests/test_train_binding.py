@@ -154,3 +154,32 @@ def test_empty_gradient_with_a_count():
     assert arr[2] == count.data_ptr() and arr[4] & 0xffffffff == 128
     with pytest.raises(ValueError, match="must be"):
         geng._tensor_list([on_device(0)], None, [count])
+
+
+def _both_forms(device, monkeypatch, idx, dout, dim):
+    """(the sparse form's grad, the width that each form passes to the library) for arguments of these shapes"""
+    seen = []
+    monkeypatch.setattr(geng._lib, "engram_embed_grad_workspace", geng._lib.real.engram_embed_grad_workspace, raising=False)
+    for name in ("engram_embed_grad", "engram_embed_grad_dense"):
+        monkeypatch.setattr(geng._lib, name, staticmethod(lambda *a: seen.append(a[8]) or geng.OK), raising=False)
+    idx, dout = on_device(*idx, dtype=torch.int64), on_device(*dout)
+    grad = geng.engram_embed_grad(idx, dout, 9)[1]
+    geng.engram_embed_grad_dense(idx, dout, on_device(9, dim))
+    return grad, seen
+
+
+@pytest.mark.parametrize("idx,dout,dim", [((0, 3), (0, 48), 16), ((0, 3), (0, 3, 16), 16), ((0,), (0, 16), 16), ((0, 5, 7), (0, 5, 7, 8), 8),
+                                          ((0, 5, 7), (0, 280), 8), ((4, 0), (4, 0, 16), 16), ((0,), (0,), 1), ((0, 1), (0, 16), 16)])
+def test_empty_batch_has_the_width_of_a_full_one(device, monkeypatch, idx, dout, dim):
+    """The same layouts with and without tokens: rows as wide, in both forms of the gradient."""
+    full = [tuple(2 if n == 0 else n for n in shape) for shape in (idx, dout)]
+    for shapes in ((idx, dout), full):
+        grad, seen = _both_forms(device, monkeypatch, *shapes, dim)
+        assert grad.shape[1] == dim and seen == [dim, dim], shapes
+
+
+@pytest.mark.parametrize("idx,dout", [((0, 3), (0, 47)), ((0, 3), (0,)), ((2, 3), (0, 48)), ((0, 3), (2, 48)), ((0, 3), (0, 0)), ((0,), ()),
+                                      ((2, 3), (2, 47))])
+def test_gradients_that_do_not_fit_their_ids(device, monkeypatch, idx, dout):
+    with pytest.raises(ValueError, match="does not hold one row"):
+        _both_forms(device, monkeypatch, idx, dout, 16)
