@@ -1088,6 +1088,8 @@ def engram_grad_clip(grads, max_norm: float, norm_type: float = 2.0, out=None, c
     """Multiply the gradients by min(1, max_norm / (norm + 1e-6)), norm as engram_grad_norm (returned, as
     it was before clipping). In place, or into `out`: per gradient a tensor of the same size in any of the
     three types, or None for in place. Rows past a gradient's count are neither read nor written."""
+    if max_norm is None:
+        raise TypeError("max_norm must be a number (engram_grad_norm computes the norm alone)")
     return _norm_call(grads, norm_type, counts, norm, workspace, stream, out, max_norm)
 
 

@@ -183,3 +183,14 @@ def test_empty_batch_has_the_width_of_a_full_one(device, monkeypatch, idx, dout,
 def test_gradients_that_do_not_fit_their_ids(device, monkeypatch, idx, dout):
     with pytest.raises(ValueError, match="does not hold one row"):
         _both_forms(device, monkeypatch, idx, dout, 16)
+
+
+def test_clip_without_a_bound_is_refused(device):
+    """engram_grad_clip with max_norm None is no call for the norm alone (PreparedGradClip's None is)."""
+    with pytest.raises(TypeError, match="max_norm"):
+        geng.engram_grad_clip([on_device(5)], None)
+    assert device.log == []
+    geng.engram_grad_clip([on_device(5)], 1.0)
+    geng.engram_grad_norm([on_device(5)])
+    geng.PreparedGradClip([on_device(5)], None)()
+    assert [e[0] for e in device.log if e[0] == "call"] == ["call"] * 3
