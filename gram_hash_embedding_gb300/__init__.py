@@ -1045,7 +1045,10 @@ def _tensor_list(grads, out, counts):
             if grads[i].dim() < 2:
                 raise ValueError("a gradient with a count must be [n, dim]")
             words[6 * i + 2] = _dev(c, torch.int64, "counts")
-            words[6 * i + 4] |= grads[i].shape[1:].numel() or 1  # no values: any length will do
+            length = grads[i].shape[1:].numel() or 1  # no values: any length will do
+            if length > 0x7fffffff:
+                raise ValueError(f"a gradient with a count may have rows of 2^31 - 1 values, got {length}")
+            words[6 * i + 4] |= length
     return array.array("q", words), n
 
 

@@ -194,3 +194,14 @@ def test_clip_without_a_bound_is_refused(device):
     geng.engram_grad_norm([on_device(5)])
     geng.PreparedGradClip([on_device(5)], None)()
     assert [e[0] for e in device.log if e[0] == "call"] == ["call"] * 3
+
+
+@pytest.mark.parametrize("shape", [(2, 2 ** 32), (1, 2 ** 32 + 5), (2, 2 ** 31), (3, 2 ** 20, 2 ** 12)])
+def test_counted_rows_too_long_for_the_library(shape):
+    """A row length is a 32-bit field beside the tensor's type; a longer one would run into it."""
+    long_rows = torch.empty(shape, device="meta", dtype=torch.bfloat16).as_subclass(OnDevice)
+    count = on_device(1, dtype=torch.int64)
+    with pytest.raises(ValueError, match="rows of"):
+        geng._tensor_list([long_rows], None, [count])
+    assert geng._tensor_list([long_rows], None, [None])[1] == 1  # without a count it is a flat list of values
+    assert geng._tensor_list([torch.empty((2, 2 ** 31 - 1), device="meta").as_subclass(OnDevice)], None, [count])[1] == 1
