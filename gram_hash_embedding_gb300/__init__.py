@@ -814,6 +814,13 @@ def _scratch(workspace, need: int, device) -> tuple:
     return ws, ws.data_ptr(), ws.numel()
 
 
+def _narrow(size: int, name: str) -> int:
+    """A size that the library takes as 32 bits (ctypes would pass on its low bits)."""
+    if size > 0x7fffffff:
+        raise ValueError(f"{name} is {size}, beyond 2^31 - 1")
+    return size
+
+
 def _embed_ids(idx: torch.Tensor):
     """Row ids of a lookup: int64 [T, C] with unit stride along C, or any contiguous shape (then one
     column): (pointer, row stride, T, C)."""
@@ -821,6 +828,7 @@ def _embed_ids(idx: torch.Tensor):
         raise TypeError("idx must be an int64 CUDA tensor")
     shape = idx.shape
     if len(shape) == 2 and shape[1] > 0:
+        _narrow(shape[1], "the ids per token")
         return (idx.data_ptr(), shape[1], shape[0], shape[1]) if idx.is_contiguous() else _hash_ids(idx)
     if not idx.is_contiguous():
         raise ValueError(f"idx must be contiguous, or [T, C] with unit stride along C, got strides {idx.stride()}")
@@ -837,7 +845,7 @@ def _rows_of(t: torch.Tensor, name: str):
     stride = t.stride(0) if rows > 1 else dim
     if stride < dim:
         raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), rows, dim, stride
+    return t.data_ptr(), rows, _narrow(dim, f"the width of {name}"), stride
 
 
 def engram_embed(idx: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
@@ -881,7 +889,7 @@ def _row_width(values: torch.Size, ids: torch.Size) -> int:
 def _embed_dout(dout: torch.Tensor, ids: torch.Size, T: int, C: int):
     """The gradient of a lookup's output: contiguous, or [T, C * dim] / [T, C, dim] whose tokens are a
     stride apart: (pointer, token stride, dim)."""
-    dim = _row_width(dout.shape, ids)
+    dim = _narrow(_row_width(dout.shape, ids), "the width of dout")
     if dim == 0:
         raise ValueError(f"dout {tuple(dout.shape)} does not hold one row for each of {T * C} ids")
     if dout.is_contiguous():
@@ -964,6 +972,7 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
     Returns (or fills) dx bf16 like x (may be dout), dkv bf16 like kv, and dq_weight, dk_weight float32
     [hc, dim], summed over the tokens in a fixed order. A masked token passes dout through."""
     hc, dim = x.shape[-2:]
+    _narrow(max(hc, dim), "hc or dim")
     T = x.numel() // (hc * dim)
     bf, f32, dev = torch.bfloat16, torch.float32, x.device
     temps = []
@@ -1045,10 +1054,8 @@ def _tensor_list(grads, out, counts):
             if grads[i].dim() < 2:
                 raise ValueError("a gradient with a count must be [n, dim]")
             words[6 * i + 2] = _dev(c, torch.int64, "counts")
-            length = grads[i].shape[1:].numel() or 1  # no values: any length will do
-            if length > 0x7fffffff:
-                raise ValueError(f"a gradient with a count may have rows of 2^31 - 1 values, got {length}")
-            words[6 * i + 4] |= length
+            # no values: any length will do
+            words[6 * i + 4] |= _narrow(grads[i].shape[1:].numel() or 1, "the length of rows of a gradient with a count")
     return array.array("q", words), n
 
 

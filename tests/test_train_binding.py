@@ -205,3 +205,19 @@ def test_counted_rows_too_long_for_the_library(shape):
         geng._tensor_list([long_rows], None, [count])
     assert geng._tensor_list([long_rows], None, [None])[1] == 1  # without a count it is a flat list of values
     assert geng._tensor_list([torch.empty((2, 2 ** 31 - 1), device="meta").as_subclass(OnDevice)], None, [count])[1] == 1
+
+
+def test_sizes_beyond_the_librarys_fields(device):
+    """Widths, columns and copies are 32-bit arguments; a larger one is refused, not cut to its low bits."""
+    meta = lambda *shape, dtype=torch.float32: torch.empty_strided(
+        shape, [torch.Size(shape[i + 1:]).numel() for i in range(len(shape))], device="meta", dtype=dtype).as_subclass(OnDevice)
+    idx, wide = on_device(1, 1, dtype=torch.int64), 2 ** 32 + 8
+    many = meta(1, wide, dtype=torch.int64)
+    for call in (lambda: geng.engram_embed(idx, meta(1, wide), out=meta(1, 1, wide)),
+                 lambda: geng.engram_embed(many, on_device(1, 8), out=meta(1, wide, 8)),
+                 lambda: geng.engram_embed_grad(idx, meta(1, wide), 1, grad=meta(1, wide)),
+                 lambda: geng.engram_embed_grad_dense(idx, meta(1, wide), meta(1, wide)),
+                 lambda: geng.engram_gate_grad(*[meta(1, 1, wide, dtype=torch.bfloat16)] + [meta(1, 2 * wide, dtype=torch.bfloat16)] +
+                                               [meta(1, wide, dtype=torch.bfloat16)] * 2 + [meta(1, 1, wide, dtype=torch.bfloat16)])):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
