@@ -54,13 +54,14 @@ __device__ __forceinline__ CopyGrad copy_grad(float sh, float sk, float sd, floa
   const float ra = rsqrtf(sh * rd + eps), rb = rsqrtf(sk * rd + eps);
   const float r = ra * rb * inv_sqrt_dim;
   const float dot = sd * r;
-  const float m = fabsf(dot), ri = rsqrtf(fmaxf(m, 1e-6f));  // 1 / |z|
+  // a NaN dot stays one and makes the gate and all of the copy's gradients NaN (fmaxf would take the bound for it)
+  const float m = fabsf(dot), bounded = m < 1e-6f ? 1e-6f : m, ri = rsqrtf(bounded);  // 1 / |z|
   CopyGrad g;
   g.m = m;
   // from exp(-|z|), so that neither the gate nor 1 - gate cancels: gate (1 - gate) = x / (1 + x)^2
-  const float x = expf(-fmaxf(m, 1e-6f) * ri), y = __frcp_rn(1.0f + x);
+  const float x = expf(-bounded * ri), y = __frcp_rn(1.0f + x);
   g.gate = dot < 0.f ? x * y : y;
-  const float ddot = m >= 1e-6f ? su * (x * y * y) * (0.5f * ri) : 0.f;
+  const float ddot = m < 1e-6f ? 0.f : su * (x * y * y) * (0.5f * ri);
   const float e = ddot * dot * rd;
   g.c = ddot * r;
   g.ea = e * ra * ra;

@@ -517,8 +517,10 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
  *   dkv value    = sum over i of gate_i * u_i
  *   dq_weight[i] = k_weight[i] * sum over t of ddot * r * h * key_i;   dk_weight[i]: with q_weight[i]
  * in fp32; sum(h * w * key_i) is formed in twice that precision for tokens with a copy of |dot| < 1/32, where the
- * slope 0.5 / sqrt(|dot|) magnifies its error. A token whose mask is 0 has a constant gate: dx = dout bit for bit, its dkv is +0 and it takes no
- * part in the weights' gradients, whatever its x, key and value hold.
+ * slope 0.5 / sqrt(|dot|) magnifies its error. A token whose mask is 0 has a constant gate: dx = dout bit for bit,
+ * its dkv is +0 and it takes no part in the weights' gradients, whatever its x, key and value hold. In an open
+ * token a NaN dot (a NaN or an infinity in x or a key) makes that copy's dx and key gradient, the value's gradient and
+ * the copy's weight gradients NaN (engram_gate itself takes |dot| = 1e-6 for a NaN and mixes half of the value in).
  *   x, kv, q_weight, k_weight, mask, hc, eps  as engram_gate; dim a multiple of 8, <= ENGRAM_MAX_GATE_GRAD_DIM
  *   dout       device bf16 [T][hc][dim]
  *   dx         device bf16 [T][hc][dim], written; may be the same buffer as dout

@@ -280,3 +280,29 @@ def test_gate_grad_offsets_beyond_32_bits():
     dx, dkv, dq, dk = geng.engram_gate_grad(x, kv, args[2].cuda(), args[3].cuda(), dout, mask)
     _check(args, (dx[-k:], dkv[-k:], dq, dk), "last tokens")
     assert torch.equal(dx[:-k], dout[:-k]) and not dkv[:-k].any()
+
+
+@pytest.mark.parametrize("T,hc,dim", [(40, 4, 1024), (40, 8, 640), (30, 4, 5120), (33, 1, 64)])
+def test_gate_grad_nan_and_infinity_in_open_tokens(T, hc, dim):
+    """A NaN or an infinity in an open token's x, key, value or dout: NaN wherever the formula has it (a NaN dot
+    makes the gate NaN, and with it the value's gradient), nothing of it in other tokens."""
+    clean = _inputs(np.random.default_rng(T + dim), T, hc, dim, masked=0.0)
+    args = [a.clone() for a in clean]
+    kv = args[1].view(T, hc + 1, dim)
+    i = hc - 1
+    args[0][3, i, 5] = float("nan")
+    kv[7, 0, dim - 1] = float("nan")
+    args[0][11, 0, 9] = float("inf")
+    kv[13, i, 0] = -float("inf")
+    kv[17, hc, 6] = float("nan")
+    args[4][19, i, 7] = float("nan")
+    bad = [3, 7, 11, 13, 17, 19]
+    got, exp = _run(args), _run(clean)
+    with np.errstate(all="ignore"):
+        want = R.gate_grad(*(_f64(a) for a in args[:5]), args[5].numpy(), EPS)
+    for name, g, w in zip(("dx", "dkv", "dq_weight", "dk_weight"), got, want):
+        assert np.array_equal(np.isnan(_f64(g)), np.isnan(w)), name
+    assert all(torch.isnan(got[1].view(T, hc + 1, dim)[t, hc]).all() for t in (3, 7, 11, 13))  # the value's gradient
+    good = np.setdiff1d(np.arange(T), bad)
+    for g, e in zip(got[:2], exp[:2]):
+        assert torch.equal(g[good], e[good])
