@@ -316,3 +316,54 @@ def test_embed_grad_empty_flat():
     assert (g == 5.0).all()
     geng.engram_embed_grad_dense(none, torch.empty((0, 48), device="cuda"), g)
     assert (g == 0.0).all()
+
+
+# ------------------------------------------------------------- rows that are never written, NaN sums
+# The comparison above (_close) takes a NaN for a hit. These cases compare so that a NaN misses.
+def _close_strict(g, exp, mag, times, gt, what, old=0.0):
+    u = 2.0 ** -24
+    tol = (times[:, None] + 2) * u * mag + u * np.abs(old) + ROUND[gt] * (np.abs(exp) + np.abs(old)) + (2.0 ** -24 if gt == "f16" else 0.0) + 1e-40
+    bad = ~(np.abs(g - exp) <= tol)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} off; first {np.argwhere(bad)[0]}: {g[bad][0]} for {exp[bad][0]}"
+
+
+STRICT = SHAPES + [(8193, 1, 520, 3000, "heavy"), (20_000, 1, 264, 3000, "one"), (32_768, 1, 8, 9000, "runs"), (32_769, 1, 8, 9000, "uniform"),
+                   (622_593, 1, 4, 1342, "uniform"), (30_000, 24, 8, 1, "uniform"), (207_600, 3, 4, 2_700_000, "heavy")]
+
+
+@pytest.mark.parametrize("T,C,dim,rows,kind", STRICT)
+@pytest.mark.parametrize("dt,gt", [("bf16", "f32"), ("f32", "bf16"), ("f16", "f16")])
+def test_embed_grad_writes_every_row(T, C, dim, rows, kind, dt, gt):
+    """Both forms into buffers of NaN, and the dense form added to what a buffer holds."""
+    rng = np.random.default_rng(T + dim + 2)
+    idx = _ids(rng, T, C, rows, kind)
+    dout = _vals(rng, (T, C, dim), dt)
+    ids, exp, mag, times = R.embed_grad(idx, _f64(dout), rows, 0.75)
+    di, dd = torch.from_numpy(idx).cuda(), dout.cuda()
+    grad = torch.full((T * C, dim), float("nan"), device="cuda", dtype=DT[gt])
+    grad_rows, grad, count = geng.engram_embed_grad(di, dd, rows, scale=0.75, grad=grad)
+    k = int(count)
+    assert k == ids.size and np.array_equal(grad_rows.cpu().numpy()[:k], ids)
+    _close_strict(_f64(grad[:k]), exp, mag, times, gt, "sparse")
+    assert torch.isnan(grad[k:]).all()
+    if rows > 3_000_000:  # a dense table of those would be large
+        return
+    table = geng.engram_embed_grad_dense(di, dd, torch.full((rows, dim), float("nan"), device="cuda", dtype=DT[gt]), scale=0.75)
+    _close_strict(_f64(table)[ids], exp, mag, times, gt, "dense")
+    rest = np.ones(rows, bool)
+    rest[ids] = False
+    assert (table.cpu()[torch.from_numpy(rest)].float().view(torch.int32) == 0).all()
+    old = _vals(rng, (rows, dim), gt)
+    table = geng.engram_embed_grad_dense(di, dd, old.cuda(), scale=0.75, accumulate=True)
+    o = _f64(old)[ids]
+    _close_strict(_f64(table)[ids], exp + o, mag, times, gt, "added", old=o)
+    assert torch.equal(table.cpu()[torch.from_numpy(rest)], old[torch.from_numpy(rest)])
+
+
+def test_strict_comparison_sees_a_row_that_is_never_written():
+    exp, times = np.ones((3, 4)), np.ones(3)
+    _close_strict(exp.copy(), exp, exp, times, "f32", "")
+    g = exp.copy()
+    g[1] = np.nan
+    with pytest.raises(AssertionError):
+        _close_strict(g, exp, exp, times, "f32", "")
