@@ -306,3 +306,46 @@ def test_gate_grad_nan_and_infinity_in_open_tokens(T, hc, dim):
     good = np.setdiff1d(np.arange(T), bad)
     for g, e in zip(got[:2], exp[:2]):
         assert torch.equal(g[good], e[good])
+
+
+@pytest.mark.parametrize("T,hc,dim", [(64, 2, 1024), (48, 4, 512), (24, 8, 640), (16, 4, 5120)])
+def test_gate_grad_is_the_gradient_of_the_forward_kernel(T, hc, dim):
+    """Central differences of sum(dout * engram_gate(...)) against engram_gate_grad, for x, the keys, the value and
+    both weights, each along the signs of what its gradient adds through the gate, so that nothing cancels. dout
+    leans on the value, which makes that part large. The bound: 8 standard deviations of the sum of the outputs'
+    bf16 roundings (independent, uniform over an ulp), twice the difference's own truncation (the formula's
+    difference less the formula's gradient, in 64 bits), and 2^-8 of every term for the gradient's rounding to
+    bf16. All of it has to stay below a tenth of the part looked at, and a gradient without that part, or with its
+    sign changed, has to be seen."""
+    rng = np.random.default_rng(T + dim)
+    x, kv = rng.standard_normal((T, hc, dim)), rng.standard_normal((T, hc + 1, dim))
+    kv[:, :hc] += np.where(rng.random((T, hc, 1)) < 0.3, -1.0, 1.0) * 5 * dim ** -0.5 * x  # |dot| of about 5
+    q, k = rng.uniform(0.5, 1.5, (hc, dim)), rng.uniform(0.5, 1.5, (hc, dim))
+    dout = np.where(rng.random((T, hc, 1)) < 0.5, -1, 1) * kv[:, hc:] + 0.25 * rng.standard_normal((T, hc, dim))
+    mask = rng.random(T) >= 0.1
+    args = [_bf(a) for a in (x, kv.reshape(T, -1), q, k, dout)] + [torch.from_numpy(mask)]
+    D = _f64(args[4])
+    got, want = _run(args), R.gate_grad(*(_f64(a) for a in args[:5]), mask, EPS)
+    key_part = np.zeros((T, hc + 1, dim))
+    key_part[:, :hc] = 1.0
+    key_part = key_part.reshape(T, -1)
+    ulp = lambda o: 2.0 ** (np.floor(np.log2(np.abs(o) + 1e-30)) - 7)
+    gpu = lambda ins: _f64(geng.engram_gate(*[a.cuda() for a in ins], mask=args[5].cuda(), eps=EPS))
+    formula = lambda ins: R.gate(*[_f64(a) for a in ins], mask, EPS)
+    for name, j, part, step in (("x", 0, want[0] - D, 2.0 ** -7), ("keys", 1, want[1] * key_part, 2.0 ** -7),
+                                ("value", 1, want[1] * (1 - key_part), 2.0 ** -4), ("q_weight", 2, want[2], 2.0 ** -6),
+                                ("k_weight", 3, want[3], 2.0 ** -6)):
+        move = torch.from_numpy(np.sign(part) * step).float()
+        hi, lo = list(args[:4]), list(args[:4])
+        hi[j], lo[j] = (args[j].float() + move).to(torch.bfloat16), (args[j].float() - move).to(torch.bfloat16)
+        change = 0.5 * (_f64(hi[j]) - _f64(lo[j]))
+        diff = 0.5 * ((gpu(hi) - gpu(lo)) * D).sum()
+        fhi, flo = formula(hi), formula(lo)
+        trunc = abs(0.5 * ((fhi - flo) * D).sum() - (change * want[j]).sum())
+        noise = np.sqrt(((0.5 * D) ** 2 * (ulp(fhi) ** 2 + ulp(flo) ** 2) / 12).sum())
+        g = _f64(got[j])
+        tol = 8 * noise + 2 * trunc + 2.0 ** -8 * np.abs(change * g).sum()
+        pred, through = (change * g).sum(), (change * part).sum()
+        assert tol < 0.1 * through, (name, tol, through)
+        assert abs(diff - pred) <= tol, (name, diff, pred, tol)
+        assert abs(diff - (pred - through)) > tol and abs(diff - (pred - 2 * through)) > tol, name
