@@ -25,9 +25,8 @@
 // hash ids into a workspace one tile group ahead of the loads (see "lookup ahead" below); the loader
 // waits, once per group, until that group's rows are written.
 // Tiles are visited in groups of 16 tile rows, column block outer, so the tiles in flight share a few
-// A and B blocks, which stay in L2. Built with ENGRAM_PROJ_CLUSTER=1 or 4 the same kernel runs one
-// CTA per tile (M = 128 MMAs) or two pairs side by side that share A by TMA multicast; both measured
-// no faster.
+// A and B blocks, which stay in L2. Built with ENGRAM_PROJ_CLUSTER=1 the same kernel runs one CTA per
+// tile (M = 128 MMAs), which measured no faster.
 //
 // Every wait is bounded (tc_ptx.cuh): a wait that runs out raises ENGRAM_STATUS_TIMEOUT in the
 // library's device status word, the CTA stops issuing work, waits for its copies and MMAs in
@@ -91,18 +90,14 @@ constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;  // one epilogue warp's 32 rows
 // CS = 2: a cluster of two CTAs (a pair) computes a 256 x 256 tile with M = 256 pair MMAs issued by
 // the leader; each CTA loads its own 128 rows of A and its half (128 rows) of B, 32 KB per atom, so
 // each SM reads 2/3 of the bytes per MMA from L2 that a lone CTA does.
-// CS = 4: two pairs side by side along N compute a 256 x 512 tile and share A: each CTA loads 64 of
-// its 128 A rows and multicasts them to the CTA at the same place in the other pair, so L2 serves
-// 3/4 of the bytes per MMA of a pair. Four-CTA clusters fill 144 of the 152 SMs.
 // BN: tile columns (256, or 128 for calls with few row tiles); the ring keeps the bytes of
 // ENGRAM_PROJ_PAIR_STAGES stages of the 256-column form, so narrower tiles get more stages.
 template <int CS, int BN = kBN>
 struct Cfg {
-  static constexpr bool kPairs = CS >= 2;
+  static constexpr bool kPairs = CS == 2;
   static constexpr int kAccCols = BN;                          // fp32 accumulator columns per tile
   static constexpr int kTmemCols = 2 * BN;                     // two accumulators
   static constexpr int kBRows = kPairs ? BN / 2 : BN;          // rows of the B tile this CTA loads
-  static constexpr int kARows = CS == 4 ? kBM / 2 : kBM;        // rows of A this CTA loads per stage
   static constexpr uint32_t kBBytes = kBRows * kBK * 2;
   static constexpr uint32_t kBAtomBytes = kBRows * kAtomK * 2;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
@@ -110,7 +105,6 @@ struct Cfg {
                                         : 4 / kKAtoms;
   static constexpr uint32_t kTxBytes = kPairs ? 2 * kStageBytes : kStageBytes;  // per stage, both CTAs of a pair
   static constexpr int kTileM = kPairs ? 2 * kBM : kBM;        // rows of one cluster tile
-  static constexpr int kNBlocks = CS == 4 ? 2 : 1;             // 256-column blocks of one cluster tile
   static constexpr int kGroup = (kPairs ? 1 : 2) * ENGRAM_PROJ_GROUP;  // tile rows per group (256-row units)
   static constexpr uint32_t kIdesc = tc::idesc_bf16_f32(kTileM, BN);
   // shared memory: the stage ring (1024-byte aligned), then barriers and two words
@@ -135,8 +129,7 @@ struct ProjParams {
   int32_t num_kb;   // ceil(K / kBK)
   int32_t n_mtile;  // ceil(T / cluster tile rows)
   int32_t bn;       // tile columns: 256, or 128 (project_tile_cols)
-  int32_t n_nblk;   // ceil(N / bn)
-  int32_t n_ntile;  // ceil(n_nblk / 256-column blocks per cluster tile)
+  int32_t n_ntile;  // ceil(N / bn)
   int64_t n_tiles;
   // EPI_STORE: out [T][N] bf16
   uint16_t* out;
@@ -482,24 +475,20 @@ __global__ void __launch_bounds__(LA ? kThreadsLookup : kThreads, 1)
   auto acc_empty = [&](uint32_t a) { return bar(2 * C::kStages + 2 + (int)a); };
   const uint32_t drain = bar(2 * C::kStages + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // place in the cluster: pair pr (of CS / 2), position q in the pair; q = 0 leads (issues the pair's
-  // MMAs; its full and acc_empty barriers count for both CTAs of the pair)
+  // position q in the pair; q = 0 leads (issues the pair's MMAs; its full and acc_empty barriers count
+  // for both CTAs of the pair)
   const uint32_t rank = CS > 1 ? tc::cluster_ctarank() : 0u;
   const uint32_t q = PAIR ? (rank & 1u) : 0u;
-  const uint32_t pr = CS == 4 ? (rank >> 1) : 0u;
   const uint32_t lead = rank & ~1u;
   const bool leader = q == 0;
   const int64_t unit = (int64_t)(blockIdx.x / CS);  // cluster index
   const int64_t n_units = (int64_t)(gridDim.x / CS);
-  // the loads and MMAs of a stage must have been read by every pair that writes into this CTA's copy
-  // of it: with CS = 4 the other pair multicasts half of A into it
-  constexpr uint32_t kEmptyArrivals = CS == 4 ? 2 : 1;
   constexpr uint16_t kAllCtas = (uint16_t)((1u << CS) - 1u);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      tc::mbar_init(full(s), 1);                // the leader's arrive + the bytes of its pair's loads
-      tc::mbar_init(empty(s), kEmptyArrivals);  // a commit of every pair's leader
+      tc::mbar_init(full(s), 1);   // the leader's arrive + the bytes of its pair's loads
+      tc::mbar_init(empty(s), 1);  // a commit of the pair's leader
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(acc_full(a), 1);
@@ -551,9 +540,8 @@ __global__ void __launch_bounds__(LA ? kThreadsLookup : kThreads, 1)
           ready_group = g;
         }
       }
-      const int32_t nb = nt * C::kNBlocks + (int32_t)pr;
-      const int32_t arow0 = mt * C::kTileM + (int32_t)q * kBM + (int32_t)pr * C::kARows;
-      const int32_t brow0 = nb * BN + (int32_t)q * C::kBRows;
+      const int32_t arow0 = mt * C::kTileM + (int32_t)q * kBM;
+      const int32_t brow0 = nt * BN + (int32_t)q * C::kBRows;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!tc::mbar_wait(empty(stage), phase ^ 1u, abort)) {
           raise_timeout(abort);
@@ -567,11 +555,7 @@ __global__ void __launch_bounds__(LA ? kThreadsLookup : kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kKAtoms; ++j) {
             const int x = kb * kBK + j * kAtomK;
-            if (CS == 4)  // this CTA's half of its A block, to itself and its counterpart in the other pair
-              tc::tma_load_2d_pair_multicast(a_dst + j * kAAtomBytes + pr * (C::kARows * kAtomK * 2), &tmA, fb, x,
-                                             arow0, (uint16_t)((1u << q) | (1u << (q + 2))));
-            else
-              tc::tma_load_2d_pair(a_dst + j * kAAtomBytes, &tmA, fb, x, arow0);
+            tc::tma_load_2d_pair(a_dst + j * kAAtomBytes, &tmA, fb, x, arow0);
             tc::tma_load_2d_pair(a_dst + kABytes + j * C::kBAtomBytes, &tmB, fb, x, brow0);
           }
         } else {
@@ -673,7 +657,7 @@ __global__ void __launch_bounds__(LA ? kThreadsLookup : kThreads, 1)
       if (EPI != EPI_GATE || t >= p.n_tiles) return;
       int32_t pm, pn;
       tile_coords(p, C::kGroup, t, pm, pn);
-      const int col = (pn * C::kNBlocks + (int)pr) * BN;
+      const int col = pn * BN;
       if (col >= p.N) return;
       const uint16_t* hr = h_row(p, ((int64_t)pm * (C::kTileM / kBM) + q) * kBM + r, col);
       if (hr != nullptr) tc::prefetch_l2_bulk(hr, BN * 2);
@@ -688,7 +672,7 @@ __global__ void __launch_bounds__(LA ? kThreadsLookup : kThreads, 1)
       const int64_t mb = (int64_t)mt * (C::kTileM / kBM) + q;  // this CTA's block of 128 rows
       const int64_t row = mb * kBM + r;
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * C::kAccCols;
-      const int col0 = (nt * C::kNBlocks + (int)pr) * BN;  // a pair past the last column block stores nothing
+      const int col0 = nt * BN;
       const uint32_t stage_base = base + C::kEpiOff + (uint32_t)quarter * 2u * kEpiChunkBytes;
       const int32_t y0 = (int32_t)(mb * kBM) + quarter * 32;  // TMA stores skip rows past T
       if (EPI == EPI_STORE) {
@@ -785,11 +769,9 @@ bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uin
 #ifndef ENGRAM_PROJ_CLUSTER
 #define ENGRAM_PROJ_CLUSTER 2
 #endif
-// CTAs per cluster: 1, 2 (a pair) or 4 (two pairs sharing A). Sustained at the block shape on one box
-// (power-limited, alternating rounds) pairs took 5.91 ms and four-CTA clusters 5.94 ms: the multicast
-// saves L2 traffic but leaves 8 SMs idle, so pairs are the default.
+// CTAs per cluster: 1 or 2 (a pair)
 constexpr int kCS = ENGRAM_PROJ_CLUSTER;
-static_assert(kCS == 1 || kCS == 2 || kCS == 4, "cluster of 1, 2 or 4 CTAs");
+static_assert(kCS == 1 || kCS == 2, "cluster of 1 or 2 CTAs");
 
 ProjParams base_params(int64_t T, int32_t K, int32_t N) {
   ProjParams p = {};
@@ -799,8 +781,7 @@ ProjParams base_params(int64_t T, int32_t K, int32_t N) {
   p.num_kb = (K + kBK - 1) / kBK;
   p.n_mtile = (int32_t)((T + Cfg<kCS>::kTileM - 1) / Cfg<kCS>::kTileM);
   p.bn = (int32_t)project_tile_cols(T);
-  p.n_nblk = (N + p.bn - 1) / p.bn;
-  p.n_ntile = (p.n_nblk + Cfg<kCS>::kNBlocks - 1) / Cfg<kCS>::kNBlocks;
+  p.n_ntile = (N + p.bn - 1) / p.bn;
   p.n_tiles = (int64_t)p.n_mtile * p.n_ntile;
   p.withhold = -1;
   return p;
@@ -815,7 +796,7 @@ cudaError_t launch_proj_bn(const uint16_t* emb, const uint16_t* w, const ProjPar
   // the output tensor: out [T][N], or the value rows [T][dim] of the gate epilogue
   const uint16_t* optr = EPI == EPI_STORE ? p.out : p.value;
   const uint64_t ocols = EPI == EPI_STORE ? (uint64_t)p.N : (uint64_t)p.dim;
-  if (!make_map(&ta, emb, (uint64_t)p.T, (uint64_t)p.K, (uint32_t)C::kARows) ||
+  if (!make_map(&ta, emb, (uint64_t)p.T, (uint64_t)p.K, kBM) ||
       !make_map(&tb, w, (uint64_t)p.N, (uint64_t)p.K, (uint32_t)C::kBRows) ||
       !make_map(&to, optr, (uint64_t)p.T, ocols, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;

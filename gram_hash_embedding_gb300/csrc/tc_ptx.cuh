@@ -245,17 +245,7 @@ __device__ __forceinline__ void commit_pair_multicast(uint32_t bar, uint16_t cta
                ::"r"(bar), "h"(cta_mask)
                : "memory");
 }
-// 2-D tiled load multicast to the CTAs of `cta_mask` (the same shared-memory offset in each); the
-// completion of each copy is counted on the mbarrier at offset `bar` of the leader of the
-// destination CTA's pair (`bar` a shared::cluster address of a pair leader)
-__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const void* tmap, uint32_t bar, int32_t x,
-                                                           int32_t y, uint16_t cta_mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "h"(cta_mask)
-      : "memory");
-}
+
 // ------------------------------------------------------------------------------------------ TMA stores
 // make this thread's generic-proxy shared-memory writes visible to the bulk copy engine
 // order this thread's generic-proxy global writes before later async-proxy (TMA) reads of them
