@@ -781,7 +781,8 @@ def sharded_lookup(idx: torch.Tensor, W_shard: torch.Tensor, S_shard: torch.Tens
 
 # ----------------------------------------------------------------------------- training operators
 # A training step makes many small calls, so these wrappers check a call's tensors in one pass each and
-# allocate no more than the call returns: Python's share of a small call is what it costs.
+# allocate no more than the call returns: Python's share of a small call is what it costs. They record nothing for
+# torch.autograd; the caller wires the backward pass.
 def _float_type(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -871,7 +872,7 @@ def engram_embed(idx: torch.Tensor, W: torch.Tensor, scale: float = 1.0, out: to
 
 
 def engram_embed_grad_workspace(n: int, rows: int, dim: int) -> int:
-    """Bytes of workspace that engram_embed_grad and engram_embed_grad_dense need for n ids."""
+    """Bytes of workspace that engram_embed_grad and engram_embed_grad_dense need for n ids (never fewer for more ids)."""
     return int(_lib().engram_embed_grad_workspace(int(n), int(rows), int(dim)))
 
 
@@ -911,7 +912,7 @@ def engram_embed_grad(idx: torch.Tensor, dout: torch.Tensor, rows: int, scale: f
     engram_embed; dout: the gradient of its output, float32, bfloat16 or float16 (tokens may be a stride
     apart). Returns (or fills) grad_rows int64 [n] (the distinct ids ascending, then -1), grad [n, dim]
     (grad[u] belongs to grad_rows[u]; float32 unless given; rows from count on are not written) and count
-    int64 [1], n = idx.numel(). The sums are fp32 in an order fixed by the ids."""
+    int64 [1], n = idx.numel(). The sums are fp32 in an order fixed by the ids, their number and dim."""
     ip, istride, T, C = _embed_ids(idx)
     dt = _float_type(dout, "dout")
     dp, dstride, dim = _embed_dout(dout, idx.shape, T, C)

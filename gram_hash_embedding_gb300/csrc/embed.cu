@@ -847,7 +847,8 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // How the sums are cut up: 2^glog lanes a unit, per_unit pairs a unit, chunks of columns, tiles of units. Which pairs meet
 // in a unit and in a tile decides the order of the sums, so it follows from n and dim alone: from the widest access that
 // rows of dim values allow, whatever access a call's types, addresses and strides allow (v values; a narrower one takes
-// more chunks of as many lanes).
+// more chunks of as many lanes: 1.57 million bf16 rows of 128 at odd addresses 388 us a call, 374 with a cut of their own,
+// 199 where they are aligned).
 struct Cut {
   int glog, per_unit, chunks;
   int64_t tiles;

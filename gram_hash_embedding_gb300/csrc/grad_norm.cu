@@ -1,8 +1,8 @@
 // The global norm of a list of gradients, and clipping (sm_103a):
 //   norm = sqrt(sum over all tensors of g^2)   or   max |g|
 //   out  = round(g * min(1, max_norm / (norm + 1e-6)))
-// A value's square and a thread's sums over one chunk are fp32; everything from there on is 64-bit, in a
-// fixed order, so the same call gives the same bits.
+// A value's square and a thread's sums over one chunk are fp32; everything from there on is 64-bit, in an order
+// that follows from the tensors' sizes and where they lie in their 16-byte words, so the same call gives the same bits.
 //
 // Design: bound by memory, one read for the norm and a read and a write for the clip. The tensors'
 // descriptions travel as the launch's argument (no copy to the device, nothing kept between calls), and

@@ -461,7 +461,7 @@ int engram_shard_unpack(const uint16_t* rows, const int64_t* positions, int64_t 
  *   W           device [rows] rows of dim values of w_type, row_stride values apart (row_stride >= dim)
  *   out         device [T][n_cols][dim] of out_type, written
  * Any dim >= 1 and any alignment to the type's width; rows on 16-byte boundaries with dim a multiple of 8
- * move in 16-byte accesses, others value by value. T == 0 is a no-op. Errors: _INVALID (null or misaligned
+ * move 8 values an access, rows on boundaries of 4 values with dim a multiple of 4 move 4, others one. T == 0 is a no-op. Errors: _INVALID (null or misaligned
  * pointer, negative size, a stride below its row, an unknown type, scale not finite), _UNSUPPORTED (dim >
  * ENGRAM_MAX_EMBED_DIM, T * n_cols >= 2^31, rows >= 2^32 - 1), _CUDA.
  */
@@ -569,8 +569,9 @@ uint64_t engram_grad_norm_workspace(int32_t n_tensors);
  * The global norm over a list of gradients, and clipping by it:
  *   norm = sqrt(sum over all values g^2) (ENGRAM_NORM_L2) or max |g| (ENGRAM_NORM_MAX); 0 for no values
  *   engram_grad_clip: out = round(g * min(1, max_norm / (norm + 1e-6)))
- * A value's square is formed in fp32 (|g| above 1.8e19 makes the norm infinite); blocks' sums are joined in
- * 64 bits in a fixed order. A NaN anywhere makes the norm NaN and every clipped value NaN; an infinite norm
+ * A value's square is formed in fp32 (|g| above 1.8e19 makes the norm infinite, a square below 1e-45 is 0); blocks'
+ * sums are joined in 64 bits in an order that follows from the tensors' sizes and their places (and for a clip
+ * outs') within 16 bytes. A NaN anywhere makes the norm NaN and every clipped value NaN; an infinite norm
  * makes the factor 0, so finite values become 0 and infinite ones NaN. Values past *rows_used are neither
  * counted nor written.
  *   tensors    host array of n_tensors descriptions, read during the call only. The tensors of one call
