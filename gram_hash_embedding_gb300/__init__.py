@@ -17,6 +17,10 @@ row-sharded lookup's two ends (:func:`engram_shard_pack`,
 Training the front end: :func:`engram_embed` (trainable rows) with its gradient
 :func:`engram_embed_grad` / :func:`engram_embed_grad_dense`,
 :func:`engram_gate_grad`, :func:`engram_grad_norm` and :func:`engram_grad_clip`.
+Low-bit forms of the block's operands: 4-bit tables and projection (:func:`engram_quantize4`,
+:func:`engram_dequantize4`, :func:`engram_lookup4`, :func:`engram_lookup4_operand`,
+:func:`engram_project4`) and 8-bit checkpoints (:func:`engram_quantize8`,
+:func:`engram_dequantize8`, :func:`engram_gate_grad8`).
 
 Method: the "DeepSeek V4.1" pages -- blocks/stack-hashes page (the n-gram hash
 ``forward``, ``Engram.forward``) and engram-first/lookup page
@@ -44,7 +48,9 @@ __all__ = [
     "engram_lookup_project_workspace", "engram_lookup_project_gate", "engram_lookup_project_gate_workspace",
     "engram_embed", "engram_embed_grad", "engram_embed_grad_dense", "engram_embed_grad_workspace", "engram_gate_grad",
     "engram_gate_grad_workspace", "engram_grad_norm", "engram_grad_clip", "engram_grad_norm_workspace",
-    "PreparedGradClip",
+    "PreparedGradClip", "engram_quantize4", "engram_dequantize4", "engram_lookup4", "engram_lookup4_operand",
+    "engram_project4", "engram_tiled_scales", "engram_quantize8", "engram_dequantize8", "engram_gate_grad8",
+    "engram_gate_grad8_workspace",
     "TYPE_F32", "TYPE_BF16", "TYPE_F16", "NORM_L2", "NORM_MAX",
 ]
 
@@ -153,6 +159,19 @@ def _lib():
         L.engram_grad_norm_workspace.restype = ctypes.c_uint64
         L.engram_grad_norm.argtypes = [_P, _I32, _I32, _P, _P, ctypes.c_uint64, _P]
         L.engram_grad_clip.argtypes = [_P, _I32, _I32, _F, _P, _P, ctypes.c_uint64, _P]
+        L.engram_tiled_scales.argtypes = [_I64, _I32, _I32]
+        L.engram_tiled_scales.restype = ctypes.c_uint64
+        L.engram_quantize4.argtypes = [_P, _I64, _I32, _I64, _I32, _I32, _F, _I32, _P, _P, _P]
+        L.engram_dequantize4.argtypes = [_P, _P, _I64, _I32, _I32, _F, _I32, _P, _I32, _P]
+        L.engram_quantize8.argtypes = [_P, _I64, _I32, _I64, _I32, _I32, _I32, _P, _P, _P]
+        L.engram_dequantize8.argtypes = [_P, _P, _I64, _I32, _I32, _I32, _P, _I32, _P]
+        L.engram_lookup4.argtypes = [_P, _I64, _I64, _I32, _P, _P, _I64, _I32, _I32, _F, _P, _P]
+        L.engram_lookup4_operand.argtypes = [_P, _I64, _I64, _I32, _P, _P, _I64, _I32, _I32, _P, _P, _P]
+        L.engram_project4.argtypes = [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _F, _P, _P]
+        L.engram_gate_grad8_workspace.argtypes = [_I64, _I32, _I32]
+        L.engram_gate_grad8_workspace.restype = ctypes.c_uint64
+        L.engram_gate_grad8.argtypes = [_P, _P, _P, _P, _I32, _P, _P, _P, _P, _I64, _I32, _I32, _F, _P, _P, _P, _P, _P,
+                                        ctypes.c_uint64, _P]
         L.engram_strerror.argtypes = [ctypes.c_int]
         L.engram_set_l2_fetch_granularity.argtypes = [_I32, ctypes.POINTER(_I32)]
         L.engram_strerror.restype = ctypes.c_char_p
@@ -161,7 +180,9 @@ def _lib():
                      "engram_hash_varlen", "engram_hash_lookup_varlen", "engram_gate", "engram_project",
                      "engram_project_gate", "engram_device_status", "engram_shard_pack", "engram_shard_unpack",
                      "engram_lookup_project", "engram_lookup_project_gate", "engram_embed", "engram_embed_grad",
-                     "engram_embed_grad_dense", "engram_gate_grad", "engram_grad_norm", "engram_grad_clip"):
+                     "engram_embed_grad_dense", "engram_gate_grad", "engram_grad_norm", "engram_grad_clip",
+                     "engram_quantize4", "engram_dequantize4", "engram_quantize8", "engram_dequantize8",
+                     "engram_lookup4", "engram_lookup4_operand", "engram_project4", "engram_gate_grad8"):
             getattr(L, name).restype = ctypes.c_int
         _lib_handle = L
     return _lib_handle
@@ -1000,6 +1021,294 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
     temps.append(keep)
     _check(_lib().engram_gate_grad(*p[:5], p[9] if mask is not None else None, T, hc, dim, float(eps), *p[5:9], ws,
                                    nbytes, _launch_stream(stream, temps)), "engram_gate_grad")
+    return dx, dkv, dq_weight, dk_weight
+
+
+# ----------------------------------------------------------------------------- low-bit operators
+_E8M0 = getattr(torch, "float8_e8m0fnu", torch.uint8)
+_SCALE4_DTYPE = {32: _E8M0, 16: torch.float8_e4m3fn}  # by the block's length
+_SCALE8_DTYPE = {SCALE_F32: torch.float32, SCALE_BF16: torch.bfloat16, SCALE_E8M0: _E8M0}
+
+
+def _bytes(t: torch.Tensor, n: int, name: str, dtypes=(torch.uint8,)) -> int:
+    """The pointer of a contiguous CUDA tensor of n one-byte values of uint8 or one of `dtypes`."""
+    if not isinstance(t, torch.Tensor) or (t.dtype is not torch.uint8 and t.dtype not in dtypes):
+        raise TypeError(f"{name} must be uint8{''.join(f' or {d}' for d in dtypes if d is not torch.uint8)}, got "
+                        f"{getattr(t, 'dtype', type(t).__name__)}")
+    _size(t, n, name)
+    return _dev(t, t.dtype, name)
+
+
+def _block4(block: int) -> int:
+    if block not in _SCALE4_DTYPE:
+        raise ValueError(f"block must be 32 (UE8M0 scales) or 16 (E4M3 scales), got {block}")
+    return block
+
+
+def _block8(block: int) -> int:
+    if block not in (32, 64, 128):
+        raise ValueError(f"block must be 32, 64 or 128, got {block}")
+    return block
+
+
+def _rows_view(x: torch.Tensor, name: str):
+    """x [..., cols] as rows: (pointer, rows, cols, row stride); contiguous, or [rows, cols] with rows a stride apart."""
+    if x.dim() < 1 or x.shape[-1] == 0:
+        raise ValueError(f"{name} must be [..., cols], got {tuple(x.shape)}")
+    cols = _narrow(x.shape[-1], f"the width of {name}")
+    rows = x.numel() // cols
+    if x.is_contiguous():
+        return x.data_ptr(), rows, cols, cols
+    if x.dim() != 2 or (cols > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < cols):
+        raise ValueError(f"{name} must be contiguous, or [rows, cols] with only its rows a stride apart, got shape "
+                         f"{tuple(x.shape)} strides {x.stride()}")
+    return x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols
+
+
+def engram_tiled_scales(rows: int, cols: int, block: int) -> int:
+    """Bytes of the tiled scales of 4-bit values [rows, cols] (0 for no rows or a size that is refused)."""
+    return int(_lib().engram_tiled_scales(int(rows), int(cols), int(block)))
+
+
+def _tiled_shape(rows: int, cols: int, block: int) -> tuple:
+    return -(-rows // 128), -(-cols // (4 * block)), 512
+
+
+def _scales4_size(rows: int, cols: int, block: int, tiled: bool) -> int:
+    if tiled:
+        a, b, c = _tiled_shape(rows, cols, block)
+        return a * b * c
+    return rows * (cols // block)
+
+
+def engram_quantize4(x: torch.Tensor, block: int = 32, scale: float = 1.0, tiled: bool = False,
+                     codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """Block-scaled 4-bit codes of x [..., cols] (float32, bfloat16 or float16; contiguous, or 2-D with its rows a
+    multiple of 8 values apart): E2M1 codes uint8 [..., cols / 2] and a scale for each `block` columns, a power of two
+    (32: float8_e8m0fnu) or an E4M3 number (16: float8_e4m3fn). code * block scale * scale stands for x; `scale` is a
+    power of two. The scales are [..., cols / block], or with `tiled` in the order engram_project4 reads them
+    ([rows / 128, groups of four scales, 512], rounded up; rows past the last are not written). Returns (or fills) codes, scales."""
+    _block4(block)
+    xt = _float_type(x, "x")
+    xp, rows, cols, stride = _rows_view(x, "x")
+    temps = []
+    if cols % (32 if tiled else block):
+        raise ValueError(f"x has {cols} columns, not a multiple of {32 if tiled else block}")
+    if codes is None:
+        codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
+        temps.append(codes)
+    if scales is None:
+        shape = _tiled_shape(rows, cols, block) if tiled else (*x.shape[:-1], cols // block)
+        scales = torch.empty(shape, dtype=_SCALE4_DTYPE[block], device=x.device)
+        temps.append(scales)
+    cp = _bytes(codes, rows * (cols // 2), "codes")
+    sp = _bytes(scales, _scales4_size(rows, cols, block, tiled), "scales", (_SCALE4_DTYPE[block],))
+    _check(_lib().engram_quantize4(xp, rows, cols, stride, xt, block, float(scale), int(bool(tiled)), cp, sp,
+                                   _launch_stream(stream, temps)), "engram_quantize4")
+    return codes, scales
+
+
+def engram_dequantize4(codes: torch.Tensor, scales: torch.Tensor, block: int, scale: float = 1.0, tiled: bool = False,
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, stream=None):
+    """The values of engram_quantize4's codes uint8 [..., cols / 2] and scales, times `scale`: returns (or fills)
+    [..., cols] of out_dtype (bfloat16 unless given; float32, float16)."""
+    _block4(block)
+    cols = 2 * codes.shape[-1]
+    rows = codes.numel() // codes.shape[-1] if codes.shape[-1] else 0
+    if cols % (32 if tiled else block):
+        raise ValueError(f"codes stand for {cols} columns, not a multiple of {32 if tiled else block}")
+    temps = []
+    if out is None:
+        out = torch.empty((*codes.shape[:-1], cols), dtype=out_dtype, device=codes.device)
+        temps.append(out)
+    _size(out, rows * cols, "out")
+    ot = _float_type(out, "out")
+    cp = _bytes(codes, rows * (cols // 2), "codes")
+    sp = _bytes(scales, _scales4_size(rows, cols, block, tiled), "scales", (_SCALE4_DTYPE[block],))
+    _check(_lib().engram_dequantize4(cp, sp, rows, cols, block, float(scale), int(bool(tiled)),
+                                     _dev(out, out.dtype, "out"), ot, _launch_stream(stream, temps)),
+           "engram_dequantize4")
+    return out
+
+
+def _table4(Q: torch.Tensor, S: torch.Tensor, block: int):
+    _block4(block)
+    if Q.dim() != 2:
+        raise ValueError(f"Q must be [rows, dim / 2], got {tuple(Q.shape)}")
+    rows, dim = Q.shape[0], 2 * Q.shape[1]
+    if dim == 0 or dim % block:
+        raise ValueError(f"rows of {dim} values are not whole blocks of {block}")
+    return _bytes(Q, rows * (dim // 2), "Q"), _bytes(S, rows * (dim // block), "S", (_SCALE4_DTYPE[block],)), rows, \
+        _narrow(dim, "the width of Q")
+
+
+def engram_lookup4(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, block: int, scale: float = 1.0,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rows of a 4-bit table (engram_quantize4's codes Q [rows, dim / 2] and row-by-row scales S): idx int64 [T, C]
+    (unit stride along C) or any contiguous shape. Returns (or fills) bf16 idx.shape + (dim,) = the rows' values times
+    `scale`, +0 rows where idx is outside the table."""
+    qp, sp, rows, dim = _table4(Q, S, block)
+    ip, istride, T, C = _embed_ids(idx)
+    temps = []
+    if out is None:
+        out = torch.empty((*idx.shape, dim), dtype=torch.bfloat16, device=idx.device)
+        temps.append(out)
+    _size(out, T * C * dim, "out")
+    _check(_lib().engram_lookup4(ip, istride, T, C, qp, sp, rows, dim, block, float(scale),
+                                 _dev(out, torch.bfloat16, "out"), _launch_stream(stream, temps)), "engram_lookup4")
+    return out
+
+
+def engram_lookup4_operand(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, block: int,
+                           codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """The rows of a 4-bit table as they stand, as the first operand of engram_project4: idx int64 [T, C] (unit stride
+    along C), Q and S as engram_lookup4. Returns (or fills) codes uint8 [T, C * dim / 2] and tiled scales."""
+    qp, sp, rows, dim = _table4(Q, S, block)
+    ip, istride, T, C = _hash_ids(idx)
+    K = _narrow(C * dim, "the operand's width")
+    if K == 0 or K % 32:
+        raise ValueError(f"{C} rows of {dim} values are not a multiple of 32")
+    temps = []
+    if codes is None:
+        codes = torch.empty((T, K // 2), dtype=torch.uint8, device=idx.device)
+        temps.append(codes)
+    if scales is None:
+        scales = torch.empty(_tiled_shape(T, K, block), dtype=_SCALE4_DTYPE[block], device=idx.device)
+        temps.append(scales)
+    cp = _bytes(codes, T * (K // 2), "codes")
+    op = _bytes(scales, _scales4_size(T, K, block, True), "scales", (_SCALE4_DTYPE[block],))
+    _check(_lib().engram_lookup4_operand(ip, istride, T, C, qp, sp, rows, dim, block, cp, op,
+                                         _launch_stream(stream, temps)), "engram_lookup4_operand")
+    return codes, scales
+
+
+def engram_project4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, block: int,
+                    scale: float = 1.0, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The `wkv` projection with both operands in 4 bits on the tensor cores: a uint8 [..., K / 2] (T rows) and
+    w uint8 [N, K / 2] with tiled scales, as engram_quantize4(..., tiled=True) (or engram_lookup4_operand for a) makes
+    them. Returns (or fills) bf16 [..., N] = bf16(scale * a @ w^T), fp32 accumulation; `scale` is the product of the
+    operands' factors."""
+    _block4(block)
+    half = a.shape[-1]
+    K = _narrow(2 * half, "K")
+    if half == 0 or K % 32:
+        raise ValueError(f"K is {K}, not a multiple of 32")
+    if w.dim() != 2 or w.shape[1] != half:
+        raise ValueError(f"w must be [N, {half}], got {tuple(w.shape)}")
+    T, N = a.numel() // half, _narrow(w.shape[0], "N")
+    temps = []
+    if out is None:
+        out = torch.empty((*a.shape[:-1], N), dtype=torch.bfloat16, device=a.device)
+        temps.append(out)
+    _size(out, T * N, "out")
+    sd = (_SCALE4_DTYPE[block],)
+    args = (_bytes(a, T * half, "a"), _bytes(a_scales, _scales4_size(T, K, block, True), "a_scales", sd),
+            _bytes(w, N * half, "w"), _bytes(w_scales, _scales4_size(N, K, block, True), "w_scales", sd))
+    _check(_lib().engram_project4(*args, T, K, N, block, float(scale), _dev(out, torch.bfloat16, "out"),
+                                  _launch_stream(stream, temps)), "engram_project4")
+    return out
+
+
+def engram_quantize8(x: torch.Tensor, block: int = 128, scale_dtype: int = SCALE_E8M0,
+                     codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """8-bit codes of x [..., cols] (float32, bfloat16 or float16; contiguous, or 2-D with its rows a multiple of 8
+    values apart; cols a multiple of 8): E4M3 codes uint8 [..., cols] and for each `block` columns (32, 64 or 128; the
+    last block of a row may be shorter) the smallest power of two whose 448-fold holds them, [..., ceil(cols / block)]
+    of scale_dtype (SCALE_F32, SCALE_BF16 or SCALE_E8M0). A checkpoint for engram_gate_grad8, or a table for
+    engram_lookup. Returns (or fills) codes, scales."""
+    _block8(block)
+    if scale_dtype not in _SCALE8_DTYPE:
+        raise ValueError(f"scale_dtype must be SCALE_F32, SCALE_BF16 or SCALE_E8M0, got {scale_dtype}")
+    xt = _float_type(x, "x")
+    xp, rows, cols, stride = _rows_view(x, "x")
+    if cols % 8:
+        raise ValueError(f"x has {cols} columns, not a multiple of 8")
+    n, temps = -(-cols // block), []
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        temps.append(codes)
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], n), dtype=_SCALE8_DTYPE[scale_dtype], device=x.device)
+        temps.append(scales)
+    _size(scales, rows * n, "scales")
+    cp = _bytes(codes, rows * cols, "codes", (torch.float8_e4m3fn,))
+    _check(_lib().engram_quantize8(xp, rows, cols, stride, xt, block, scale_dtype, cp,
+                                   _dev_scales(scales, scale_dtype, "scales"), _launch_stream(stream, temps)),
+           "engram_quantize8")
+    return codes, scales
+
+
+def engram_dequantize8(codes: torch.Tensor, scales: torch.Tensor, block: int, out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16, scale_dtype: int | None = None, stream=None):
+    """The values of engram_quantize8's codes [..., cols] and scales: returns (or fills) [..., cols] of out_dtype."""
+    _block8(block)
+    sdt = _scale_dtype_of(scales, scale_dtype)
+    if sdt not in _SCALE8_DTYPE:
+        raise ValueError("scales must be float32, bfloat16 or float8_e8m0fnu")
+    cols = _narrow(codes.shape[-1], "the width of codes")
+    if cols == 0 or cols % 8:
+        raise ValueError(f"codes have {cols} columns, not a multiple of 8")
+    rows, temps = codes.numel() // cols, []
+    if out is None:
+        out = torch.empty(codes.shape, dtype=out_dtype, device=codes.device)
+        temps.append(out)
+    _size(out, rows * cols, "out")
+    _size(scales, rows * -(-cols // block), "scales")
+    ot = _float_type(out, "out")
+    cp = _bytes(codes, rows * cols, "codes", (torch.float8_e4m3fn,))
+    _check(_lib().engram_dequantize8(cp, _dev_scales(scales, sdt, "scales"), rows, cols, block, sdt,
+                                     _dev(out, out.dtype, "out"), ot, _launch_stream(stream, temps)),
+           "engram_dequantize8")
+    return out
+
+
+def engram_gate_grad8_workspace(T: int, hc: int, dim: int) -> int:
+    """Bytes of workspace engram_gate_grad8 needs (0 for T == 0 or an unsupported hc / dim)."""
+    return int(_lib().engram_gate_grad8_workspace(int(T), int(hc), int(dim)))
+
+
+def engram_gate_grad8(x: torch.Tensor, x_scales: torch.Tensor, kv: torch.Tensor, kv_scales: torch.Tensor,
+                      q_weight: torch.Tensor, k_weight: torch.Tensor, dout: torch.Tensor, block: int = 128,
+                      mask: torch.Tensor | None = None, eps: float = 1e-20, dx: torch.Tensor | None = None,
+                      dkv: torch.Tensor | None = None, dq_weight: torch.Tensor | None = None,
+                      dk_weight: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """engram_gate_grad from checkpoints in 8 bits: x [..., hc, dim] and kv [..., (hc + 1) * dim] (or [..., hc + 1, dim])
+    as engram_quantize8 gives them for rows of dim values (codes uint8 or float8_e4m3fn, scales uint8 or float8_e8m0fnu
+    with ceil(dim / block) a row). dim a multiple of 16. Returns (or fills) the gradient for the values they stand for,
+    as engram_gate_grad: dx bf16 like x, dkv bf16 [..., (hc + 1) * dim], dq_weight and dk_weight float32 [hc, dim]."""
+    _block8(block)
+    hc, dim = x.shape[-2:]
+    _narrow(max(hc, dim), "hc or dim")
+    if hc == 0 or dim == 0:
+        raise ValueError(f"x must be [..., hc, dim], got {tuple(x.shape)}")
+    T, n = x.numel() // (hc * dim), -(-dim // block)
+    bf, f32, dev = torch.bfloat16, torch.float32, x.device
+    temps = []
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=bf, device=dev)
+        temps.append(dx)
+    if dkv is None:
+        dkv = torch.empty((*x.shape[:-2], (hc + 1) * dim), dtype=bf, device=dev)
+        temps.append(dkv)
+    if dq_weight is None:
+        dq_weight = torch.empty((hc, dim), dtype=f32, device=dev)
+        temps.append(dq_weight)
+    if dk_weight is None:
+        dk_weight = torch.empty((hc, dim), dtype=f32, device=dev)
+        temps.append(dk_weight)
+    e4m3, e8m0 = (torch.float8_e4m3fn,), (_E8M0,)
+    inputs = (_bytes(x, T * hc * dim, "x", e4m3), _bytes(x_scales, T * hc * n, "x_scales", e8m0),
+              _bytes(kv, T * (hc + 1) * dim, "kv", e4m3), _bytes(kv_scales, T * (hc + 1) * n, "kv_scales", e8m0))
+    specs = [(q_weight, bf, hc * dim, "q_weight"), (k_weight, bf, hc * dim, "k_weight"),
+             (dout, bf, T * hc * dim, "dout"), (dx, bf, T * hc * dim, "dx"), (dkv, bf, T * (hc + 1) * dim, "dkv"),
+             (dq_weight, f32, hc * dim, "dq_weight"), (dk_weight, f32, hc * dim, "dk_weight")]
+    if mask is not None:
+        specs.append((mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T, "mask"))
+    p = _pointers(specs)
+    keep, ws, nbytes = _scratch(workspace, _lib().engram_gate_grad8_workspace(T, hc, dim), dev)
+    temps.append(keep)
+    _check(_lib().engram_gate_grad8(*inputs, block, *p[:3], p[7] if mask is not None else None, T, hc, dim, float(eps),
+                                    *p[3:7], ws, nbytes, _launch_stream(stream, temps)), "engram_gate_grad8")
     return dx, dkv, dq_weight, dk_weight
 
 

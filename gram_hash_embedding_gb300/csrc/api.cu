@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "engram_internal.cuh"
+#include "lowbit.cuh"
 #include "proj.cuh"
 #include "train.cuh"
 
@@ -771,36 +772,35 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
   return engram::gate_grad_workspace(T, hc, dim);
 }
 
-static int gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
-                     const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
-                     uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
-                     uint64_t workspace_bytes, engram_stream_t stream, int64_t withhold) {
-  if (T < 0) return ENGRAM_ERR_INVALID;
-  if (!gate_grad_shape_ok(T, hc, dim)) return ENGRAM_ERR_UNSUPPORTED;
-  if (q_weight == nullptr || k_weight == nullptr || dq_weight == nullptr || dk_weight == nullptr ||
-      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(dq_weight, 16) || !aligned(dk_weight, 16))
+// the checks that both kinds of inputs share, and the call
+static int gate_grad(const engram::GateGradArgs& a, uint64_t need, void* workspace, uint64_t workspace_bytes,
+                     engram_stream_t stream, int64_t withhold) {
+  if (a.T < 0) return ENGRAM_ERR_INVALID;
+  if (!gate_grad_shape_ok(a.T, a.hc, a.dim)) return ENGRAM_ERR_UNSUPPORTED;
+  if (a.qw == nullptr || a.kw == nullptr || a.dq == nullptr || a.dk == nullptr || !aligned(a.qw, 16) ||
+      !aligned(a.kw, 16) || !aligned(a.dq, 16) || !aligned(a.dk, 16))
     return ENGRAM_ERR_INVALID;
-  if (T > 0) {
-    if (x == nullptr || kv == nullptr || dout == nullptr || dx == nullptr || dkv == nullptr || workspace == nullptr)
+  if (a.T > 0) {
+    if (a.x == nullptr || a.kv == nullptr || a.dout == nullptr || a.dx == nullptr || a.dkv == nullptr ||
+        workspace == nullptr)
       return ENGRAM_ERR_INVALID;
-    if (!aligned(x, 16) || !aligned(kv, 16) || !aligned(dout, 16) || !aligned(dx, 16) || !aligned(dkv, 16) ||
-        !aligned(workspace, 256) || workspace_bytes < engram_gate_grad_workspace(T, hc, dim))
+    if (!aligned(a.x, 16) || !aligned(a.kv, 16) || !aligned(a.dout, 16) || !aligned(a.dx, 16) || !aligned(a.dkv, 16) ||
+        !aligned(workspace, 256) || workspace_bytes < need)
       return ENGRAM_ERR_INVALID;
   }
-  const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
-  const uint64_t w = (uint64_t)hc * dim * 4;
+  const uint64_t w = (uint64_t)a.hc * a.dim * 4;
   return launched(launch_rc(engram::launch_gate_grad(a, workspace, (cudaStream_t)stream, withhold)),
                   (cudaStream_t)stream,
-                  {span(dx, (uint64_t)T * hc * dim * 2), span(dkv, (uint64_t)T * (hc + 1) * dim * 2),
-                   span(dq_weight, w), span(dk_weight, w), span(workspace, T > 0 ? workspace_bytes : 0)});
+                  {span(a.dx, (uint64_t)a.T * a.hc * a.dim * 2), span(a.dkv, (uint64_t)a.T * (a.hc + 1) * a.dim * 2),
+                   span(a.dq, w), span(a.dk, w), span(workspace, a.T > 0 ? workspace_bytes : 0)});
 }
 
 int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
                      const uint16_t* dout, const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps,
                      uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
                      uint64_t workspace_bytes, engram_stream_t stream) {
-  return gate_grad(x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight, workspace,
-                   workspace_bytes, stream, -1);
+  const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
+  return gate_grad(a, engram_gate_grad_workspace(T, hc, dim), workspace, workspace_bytes, stream, -1);
 }
 
 int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight,
@@ -809,8 +809,195 @@ int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint1
                               float* dk_weight, void* workspace, uint64_t workspace_bytes, int64_t token,
                               engram_stream_t stream) {
   if (token < 0) return ENGRAM_ERR_INVALID;
-  return gate_grad(x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight, workspace,
-                   workspace_bytes, stream, token);
+  const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
+  return gate_grad(a, engram_gate_grad_workspace(T, hc, dim), workspace, workspace_bytes, stream, token);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Low-bit operators (quant.cu, lookup4.cu, proj4.cu, and gate_grad.cu from checkpoints)
+namespace {
+inline bool block8_ok(int32_t block) { return block == 32 || block == 64 || block == 128; }
+
+inline bool power_of_two(float v) {
+  int e = 0;
+  return std::isfinite(v) && v > 0.f && std::frexp(v, &e) == 0.5f;
+}
+
+// sizes of [rows][cols] low-bit values; `unit` divides cols
+int check_lowbit(int64_t rows, int32_t cols, int32_t unit) {
+  if (rows < 0) return ENGRAM_ERR_INVALID;
+  if (cols < unit || cols % unit != 0 || cols > (1 << 30) || rows > ((int64_t)1 << 42) / cols)
+    return ENGRAM_ERR_UNSUPPORTED;
+  return ENGRAM_OK;
+}
+
+int check_quantize(const void* x, int64_t rows, int32_t cols, int64_t x_stride, int32_t x_type, const void* codes,
+                   const void* scales, uintptr_t scale_align) {
+  if (!type_ok(x_type) || x_stride < cols || x_stride % 8 != 0) return ENGRAM_ERR_INVALID;
+  if (rows > 0 && (x == nullptr || codes == nullptr || scales == nullptr || !aligned(x, 16) || !aligned(codes, 16) ||
+                   !aligned(scales, scale_align)))
+    return ENGRAM_ERR_INVALID;
+  return ENGRAM_OK;
+}
+
+int check_dequantize(const void* codes, const void* scales, uintptr_t scale_align, int64_t rows, const void* out,
+                     int32_t out_type) {
+  if (!type_ok(out_type)) return ENGRAM_ERR_INVALID;
+  if (rows > 0 && (codes == nullptr || scales == nullptr || out == nullptr || !aligned(codes, 16) ||
+                   !aligned(scales, scale_align) || !aligned(out, 16)))
+    return ENGRAM_ERR_INVALID;
+  return ENGRAM_OK;
+}
+
+inline bool scale8_ok(int32_t t) { return t == ENGRAM_SCALE_F32 || t == ENGRAM_SCALE_BF16 || t == ENGRAM_SCALE_E8M0; }
+
+uint64_t scale4_bytes(int64_t rows, int32_t cols, int32_t block, int32_t tiled) {
+  return tiled ? (uint64_t)engram::tiled_scale_bytes(rows, cols, block) : (uint64_t)rows * (cols / block);
+}
+}  // namespace
+
+uint64_t engram_tiled_scales(int64_t rows, int32_t cols, int32_t block) {
+  if (rows <= 0 || !engram::block4_ok(block) || check_lowbit(rows, cols, 32) != ENGRAM_OK) return 0;
+  return (uint64_t)engram::tiled_scale_bytes(rows, cols, block);
+}
+
+int engram_quantize4(const void* x, int64_t rows, int32_t cols, int64_t x_stride, int32_t x_type, int32_t block,
+                     float scale, int32_t tiled, uint8_t* codes, uint8_t* scales, engram_stream_t stream) {
+  if (!engram::block4_ok(block)) return ENGRAM_ERR_UNSUPPORTED;
+  int rc = check_lowbit(rows, cols, tiled ? 32 : block);
+  if (rc == ENGRAM_OK) rc = check_quantize(x, rows, cols, x_stride, x_type, codes, scales, 16);
+  if (rc != ENGRAM_OK) return rc;
+  if (!power_of_two(scale) || !std::isfinite(1.0f / scale)) return ENGRAM_ERR_INVALID;
+  if (rows == 0) return ENGRAM_OK;
+  const engram::QuantArgs a{x, rows, cols, x_stride, x_type, block, scale, codes, scales, tiled, 0};
+  return launched(launch_rc(engram::launch_quantize4(a, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(codes, (uint64_t)rows * (cols / 2)), span(scales, scale4_bytes(rows, cols, block, tiled))});
+}
+
+int engram_dequantize4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, int32_t block,
+                       float scale, int32_t tiled, void* out, int32_t out_type, engram_stream_t stream) {
+  if (!engram::block4_ok(block)) return ENGRAM_ERR_UNSUPPORTED;
+  int rc = check_lowbit(rows, cols, tiled ? 32 : block);
+  if (rc == ENGRAM_OK) rc = check_dequantize(codes, scales, 16, rows, out, out_type);
+  if (rc != ENGRAM_OK) return rc;
+  if (!std::isfinite(scale)) return ENGRAM_ERR_INVALID;
+  if (rows == 0) return ENGRAM_OK;
+  const engram::DequantArgs a{codes, scales, rows, cols, block, tiled, 0, scale, out, out_type};
+  return launched(launch_rc(engram::launch_dequantize4(a, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(out, (uint64_t)rows * cols * engram::type_bytes(out_type))});
+}
+
+int engram_quantize8(const void* x, int64_t rows, int32_t cols, int64_t x_stride, int32_t x_type, int32_t block,
+                     int32_t scale_dtype, uint8_t* codes, void* scales, engram_stream_t stream) {
+  if (!block8_ok(block) || !scale8_ok(scale_dtype)) return ENGRAM_ERR_UNSUPPORTED;
+  int rc = check_lowbit(rows, cols, 8);
+  if (rc == ENGRAM_OK) rc = check_quantize(x, rows, cols, x_stride, x_type, codes, scales, scale_bytes(scale_dtype));
+  if (rc != ENGRAM_OK) return rc;
+  if (rows == 0) return ENGRAM_OK;
+  const engram::QuantArgs a{x, rows, cols, x_stride, x_type, block, 1.0f, codes, scales, 0, scale_dtype};
+  return launched(launch_rc(engram::launch_quantize8(a, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(codes, (uint64_t)rows * cols),
+                   span(scales, (uint64_t)rows * ((cols + block - 1) / block) * scale_bytes(scale_dtype))});
+}
+
+int engram_dequantize8(const uint8_t* codes, const void* scales, int64_t rows, int32_t cols, int32_t block,
+                       int32_t scale_dtype, void* out, int32_t out_type, engram_stream_t stream) {
+  if (!block8_ok(block) || !scale8_ok(scale_dtype)) return ENGRAM_ERR_UNSUPPORTED;
+  int rc = check_lowbit(rows, cols, 8);
+  if (rc == ENGRAM_OK) rc = check_dequantize(codes, scales, scale_bytes(scale_dtype), rows, out, out_type);
+  if (rc != ENGRAM_OK || rows == 0) return rc;
+  const engram::DequantArgs a{codes, scales, rows, cols, block, 0, scale_dtype, 1.0f, out, out_type};
+  return launched(launch_rc(engram::launch_dequantize8(a, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(out, (uint64_t)rows * cols * engram::type_bytes(out_type))});
+}
+
+namespace {
+int check_lookup4(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const uint8_t* Q, const uint8_t* S,
+                  int64_t table_rows, int32_t dim, int32_t block, float scale) {
+  if (T < 0 || n_cols < 1 || table_rows < 0 || idx_stride < n_cols || !std::isfinite(scale)) return ENGRAM_ERR_INVALID;
+  if (!engram::block4_ok(block) || dim < block || dim % block != 0 || dim > ENGRAM_MAX_EMBED_DIM ||
+      T > INT32_MAX / n_cols)
+    return ENGRAM_ERR_UNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (idx == nullptr || !aligned(idx, 8) || (table_rows > 0 && (Q == nullptr || S == nullptr || !aligned(Q, 16))))
+    return ENGRAM_ERR_INVALID;
+  return ENGRAM_OK;
+}
+}  // namespace
+
+int engram_lookup4(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const uint8_t* Q,
+                   const uint8_t* S, int64_t table_rows, int32_t dim, int32_t block, float scale, uint16_t* out,
+                   engram_stream_t stream) {
+  const int rc = check_lookup4(idx, idx_stride, T, n_cols, Q, S, table_rows, dim, block, scale);
+  if (rc != ENGRAM_OK || T == 0) return rc;
+  if (out == nullptr || !aligned(out, 16)) return ENGRAM_ERR_INVALID;
+  const engram::Lookup4Args a{idx, idx_stride, T, n_cols, Q, S, table_rows, dim, block, scale};
+  return launched(launch_rc(engram::launch_lookup4(a, out, (cudaStream_t)stream)), (cudaStream_t)stream,
+                  {span(out, (uint64_t)T * n_cols * dim * 2)});
+}
+
+int engram_lookup4_operand(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const uint8_t* Q,
+                           const uint8_t* S, int64_t table_rows, int32_t dim, int32_t block, uint8_t* codes,
+                           uint8_t* scales, engram_stream_t stream) {
+  const int rc = check_lookup4(idx, idx_stride, T, n_cols, Q, S, table_rows, dim, block, 1.0f);
+  if (rc != ENGRAM_OK) return rc;
+  const int64_t K = (int64_t)n_cols * dim;
+  if (K % 32 != 0 || K > (1 << 30)) return ENGRAM_ERR_UNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (codes == nullptr || scales == nullptr || !aligned(codes, 16) || !aligned(scales, 16)) return ENGRAM_ERR_INVALID;
+  const engram::Lookup4Args a{idx, idx_stride, T, n_cols, Q, S, table_rows, dim, block, 1.0f};
+  return launched(launch_rc(engram::launch_lookup4_operand(a, codes, scales, (cudaStream_t)stream)),
+                  (cudaStream_t)stream,
+                  {span(codes, (uint64_t)T * (K / 2)), span(scales, scale4_bytes(T, (int32_t)K, block, 1))});
+}
+
+static int project4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int64_t T,
+                    int32_t K, int32_t N, int32_t block, float scale, uint16_t* out, engram_stream_t stream,
+                    int32_t withhold) {
+  if (T < 0 || !std::isfinite(scale)) return ENGRAM_ERR_INVALID;
+  if (!engram::block4_ok(block) || K < 32 || K % 32 != 0 || K > (1 << 30) || N < 8 || N % 8 != 0 ||
+      N > INT32_MAX - 256 || T > INT32_MAX)
+    return ENGRAM_ERR_UNSUPPORTED;
+  // the scales' groups are numbered in 32 bits
+  const int64_t groups = engram::scale_groups(K, block);
+  if ((T + 255) / 128 * groups > INT32_MAX - 8 || ((int64_t)N + 255) / 128 * groups > INT32_MAX - 8)
+    return ENGRAM_ERR_UNSUPPORTED;
+  if (T == 0) return ENGRAM_OK;
+  if (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr || out == nullptr || !aligned(a, 16) ||
+      !aligned(w, 16) || !aligned(a_scales, 128) || !aligned(w_scales, 128) || !aligned(out, 16))
+    return ENGRAM_ERR_INVALID;
+  const engram::Project4Args p{a, a_scales, w, w_scales, T, K, N, block, scale, out};
+  return launched(launch_rc(engram::launch_project4(p, (cudaStream_t)stream, withhold)), (cudaStream_t)stream,
+                  {span(out, (uint64_t)T * N * 2)});
+}
+
+int engram_project4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int64_t T,
+                    int32_t K, int32_t N, int32_t block, float scale, uint16_t* out, engram_stream_t stream) {
+  return project4(a, a_scales, w, w_scales, T, K, N, block, scale, out, stream, -1);
+}
+
+int engram_project4_withhold(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales,
+                             int64_t T, int32_t K, int32_t N, int32_t block, float scale, uint16_t* out, int32_t tile,
+                             engram_stream_t stream) {
+  if (tile < 0) return ENGRAM_ERR_INVALID;
+  return project4(a, a_scales, w, w_scales, T, K, N, block, scale, out, stream, tile);
+}
+
+uint64_t engram_gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim) {
+  if (T <= 0 || !gate_grad_shape_ok(T, hc, dim) || dim % 16 != 0) return 0;
+  return engram::gate_grad_workspace(T, hc, dim, true);
+}
+
+int engram_gate_grad8(const uint8_t* x, const uint8_t* x_scales, const uint8_t* kv, const uint8_t* kv_scales,
+                      int32_t block, const uint16_t* q_weight, const uint16_t* k_weight, const uint16_t* dout,
+                      const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps, uint16_t* dx, uint16_t* dkv,
+                      float* dq_weight, float* dk_weight, void* workspace, uint64_t workspace_bytes,
+                      engram_stream_t stream) {
+  if (!block8_ok(block) || dim % 16 != 0) return ENGRAM_ERR_UNSUPPORTED;
+  if (T > 0 && (x_scales == nullptr || kv_scales == nullptr)) return ENGRAM_ERR_INVALID;
+  const engram::GateGradArgs a{x,  kv, q_weight, k_weight, dout,      mask,      T,        hc,        dim,
+                               eps, dx, dkv,      dq_weight, dk_weight, x_scales, kv_scales, block};
+  return gate_grad(a, engram_gate_grad8_workspace(T, hc, dim), workspace, workspace_bytes, stream, -1);
 }
 
 namespace {

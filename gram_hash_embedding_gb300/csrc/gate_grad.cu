@@ -32,6 +32,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "dequant.cuh"
 #include "engram_internal.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
@@ -93,8 +94,21 @@ __device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
 
+// 8 E4M3 codes of a checkpoint times their block's scale, a power of two: exact
+__device__ __forceinline__ Vec8 widen8(const uint2& v, float s) {
+  const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), lo, hi);
+    r.p[i] = __fmul2_rn(make_float2(lo, hi), make_float2(s, s));
+  }
+  return r;
+}
+
 // one row's part of a token into shared memory, counted in bytes on `bar`
-__device__ __forceinline__ void copy_row(uint4* dst, const uint16_t* src, uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    tc::smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(bar)
@@ -191,8 +205,11 @@ constexpr int max_threads(int hc, int cg) { return hc <= 2 ? 640 : (cg == 1 ? 32
 // WHOLE: a CTA has whole rows. It brings each tensor's rows of a token, which lie together, by one copy: three for
 // 3 HC + 1 (9,557 tokens of 8 x 464: 80 -> 68 us), and has no cluster's code. One kernel for both kinds took 8,192 tokens
 // of 4 x 2,048 136 us instead of 122 and, two CTAs a token, 16,384 of 4 x 5,120 556 instead of 545.
+// Q8: x and kv are checkpoints in 8 bits (engram_gate_grad8): their rows are half as long, a stage holds dout's rows, then
+// theirs, and a thread reads the scales of its columns one token ahead (a byte for each of its rows). The values are
+// widened where bf16 ones are: the same arithmetic on the values that the checkpoints stand for.
 // withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
-template <int HC, int CG, int S, bool WHOLE>
+template <int HC, int CG, int S, bool WHOLE, bool Q8>
 __global__ void __launch_bounds__(max_threads(HC, CG))
     gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
                      float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
@@ -200,7 +217,8 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   pdl_trigger();
   constexpr int kArrays = 3 * HC + 1;   // rows of a token: h and dout of the copies, their keys, the value
   const int cs = WHOLE ? 1 : ctas;      // CTAs of the cluster
-  constexpr int kU = WHOLE ? HC : 2 * HC, kK = WHOLE ? 2 * HC : HC;  // a stage's rows of dout and of the keys
+  // a stage's rows of dout and of the keys
+  constexpr int kU = Q8 ? 0 : WHOLE ? HC : 2 * HC, kK = WHOLE ? 2 * HC : HC;
   constexpr int N = 4 * HC;             // sums of a token
   constexpr int HPT = HC / CG;          // copies of a thread
   constexpr int M = 4 * HPT;            // sums of a warp
@@ -215,7 +233,8 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   const uint32_t rank = blockIdx.x % cs;
   const int per_group = nthr / CG, group = CG == 1 ? 0 : tid / per_group, gt = tid - group * per_group;
   const int g0 = group * HPT, wg = nw / CG;  // its first copy, and the warps of a group
-  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)S * kArrays * nv);  // [CG - 1][2][per_group]
+  const int stage_vecs = Q8 ? (2 * HC + 1) * nv / 2 + HC * nv : kArrays * nv;  // (Q8: nv is even)
+  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)S * stage_vecs);  // [CG - 1][2][per_group]
   float* red = reinterpret_cast<float*>(dvp + (CG - 1) * 2 * per_group);     // [2][CG][cs][wg][M]
   const int cnt = min(nv, (a.dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
   const bool on = gt < cnt;
@@ -224,18 +243,72 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   const int64_t col = row0 + 8 * gt;
   const int64_t gcol = (int64_t)g0 * a.dim + col;  // the thread's place in its first copy
   const uint32_t bar0 = tc::smem_u32(bars);
-  auto slot = [&](int st, int j) -> const uint4& { return smem[(st * kArrays + j) * nv + me]; };
+  auto slot = [&](int st, int j) -> const uint4& { return smem[st * stage_vecs + j * nv + me]; };
+  // the scales of a token's checkpoint at the thread's columns: its copies', their keys', the value's
+  constexpr int kScales = Q8 ? 2 * HPT + 1 : 1;
+  uint32_t sc[kScales], sc_next[kScales];
+  const int64_t n_blocks = Q8 ? (a.dim + a.block - 1) / a.block : 0, my_block = Q8 ? (row0 + 8 * me) / a.block : 0;
+  auto fetch_scales = [&](int64_t t, bool open) {
+    if constexpr (Q8) {
+      if (!open) return;
+      const uint8_t* xs = a.xs + (t * HC + g0) * n_blocks + my_block;
+      const uint8_t* ks = a.kvs + (t * (HC + 1) + g0) * n_blocks + my_block;
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        sc_next[i] = __ldg(xs + i * n_blocks);
+        sc_next[HPT + i] = __ldg(ks + i * n_blocks);
+      }
+      sc_next[2 * HPT] = __ldg(ks + (HC - g0) * n_blocks);
+    }
+  };
+  // a thread's 8 values of copy i (of its group), of that copy's key, and of the value
+  auto packed = [&](int st, int j) {  // row j of the checkpoints' rows
+    return reinterpret_cast<const uint2*>(smem + st * stage_vecs + HC * nv)[j * nv + me];
+  };
+  auto h_of = [&](int st, int i) {
+    if constexpr (Q8) return widen8(packed(st, g0 + i), widen_scale<ENGRAM_SCALE_E8M0>(sc[i]));
+    else return widen8(slot(st, g0 + i));
+  };
+  auto k_of = [&](int st, int i) {
+    if constexpr (Q8) return widen8(packed(st, HC + g0 + i), widen_scale<ENGRAM_SCALE_E8M0>(sc[HPT + i]));
+    else return widen8(slot(st, kK + g0 + i));
+  };
+  auto v_of = [&](int st) {
+    if constexpr (Q8) return widen8(packed(st, 2 * HC), widen_scale<ENGRAM_SCALE_E8M0>(sc[2 * HPT]));
+    else return widen8(slot(st, 3 * HC));
+  };
   // one thread starts a token's copies
   uint32_t last = ~0u;  // (that thread's) bit st: the parity of the stage's last copies
   auto fetch = [&](int64_t t, int st, bool open) {
     if (t >= a.T || dead) return;
     last ^= 1u << st;
     const uint32_t bytes = 16 * cnt, bar = bar0 + 16 + 8 * st;
-    uint4* to = smem + (size_t)st * kArrays * nv;
-    tc::mbar_arrive_expect_tx(bar, bytes * (open ? kArrays : HC));
+    uint4* to = smem + (size_t)st * stage_vecs;
     const uint16_t* u = a.dout + t * HC * a.dim + row0;
-    const uint16_t* h = a.x + t * HC * a.dim + row0;
-    const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
+    if constexpr (Q8) {
+      uint8_t* in = reinterpret_cast<uint8_t*>(to + HC * nv);  // the rows of x, then those of kv
+      const uint32_t part = 8 * cnt;
+      tc::mbar_arrive_expect_tx(bar, bytes * HC + (open ? part * (2 * HC + 1) : 0));
+      const uint8_t* h = static_cast<const uint8_t*>(a.x) + t * HC * a.dim + row0;
+      const uint8_t* k = static_cast<const uint8_t*>(a.kv) + t * (HC + 1) * a.dim + row0;
+      if (WHOLE) {
+        copy_row(to, u, bytes * HC, bar);
+        if (open) {
+          copy_row(in, h, part * HC, bar);
+          copy_row(in + 8 * HC * nv, k, part * (HC + 1), bar);
+        }
+        return;
+      }
+      for (int i = 0; i < HC; ++i) copy_row(to + i * nv, u + (int64_t)i * a.dim, bytes, bar);
+      if (open) {
+        for (int i = 0; i < HC; ++i) copy_row(in + 8 * i * nv, h + (int64_t)i * a.dim, part, bar);
+        for (int i = 0; i <= HC; ++i) copy_row(in + 8 * (HC + i) * nv, k + (int64_t)i * a.dim, part, bar);
+      }
+      return;
+    }
+    tc::mbar_arrive_expect_tx(bar, bytes * (open ? kArrays : HC));
+    const uint16_t* h = static_cast<const uint16_t*>(a.x) + t * HC * a.dim + row0;
+    const uint16_t* k = static_cast<const uint16_t*>(a.kv) + t * (HC + 1) * a.dim + row0;
     if (WHOLE) {
       copy_row(to + kU * nv, u, bytes * HC, bar);
       if (open) {
@@ -288,6 +361,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   for (int j = 0; j < S; ++j) open |= open_at(cluster + (int64_t)j * nc) << j;
   if (tid == 0)
     for (int j = 0; j < S - 1; ++j) fetch(cluster + (int64_t)j * nc, j, (open >> j) & 1);
+  fetch_scales(cluster, open & 1);
   int st = 0, buf = 0;
   uint32_t phase = 0;   // bit b: the parity of bars[b]'s current phase
   auto wait = [&](int b) {
@@ -299,6 +373,11 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   };
   for (int64_t t = cluster; t < a.T; t += nc) {
     const uint32_t next = open_at(t + (int64_t)S * nc);
+    if constexpr (Q8) {
+#pragma unroll
+      for (int i = 0; i < kScales; ++i) sc[i] = sc_next[i];
+      fetch_scales(t + nc, (open >> 1) & 1);
+    }
     wait(2 + st);
     // the stage of the token before is free once every thread has passed this token's first barrier
     auto refill = [&]() {
@@ -309,10 +388,10 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
     if (open & 1) {
       float s[M];
       {
-        const Vec8 v = widen8(slot(st, 3 * HC));
+        const Vec8 v = v_of(st);
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
+          const Vec8 h = h_of(st, i), k = k_of(st, i), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           float2 q[4] = {};
 #pragma unroll
@@ -367,7 +446,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
         Sum2 d[HPT];
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), w = weights(i);
+          const Vec8 h = h_of(st, i), k = k_of(st, i), w = weights(i);
           d[i] = Sum2{0.f, 0.f};
           if (on) d[i] = dot_part(h, k, w);
         }
@@ -407,7 +486,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
           const float4 g = scal[buf][g0 + i];  // gate, c, -e / A, -e / B
-          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
+          const Vec8 h = h_of(st, i), k = k_of(st, i), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           Vec8 dh, dk;
 #pragma unroll
@@ -539,7 +618,7 @@ struct Shape {
 // shared memory (8 copies: in two groups of threads; of more than 12,000 columns or so: in one, and two stages); more
 // CTAs a token when there are too few tokens for every SM. Few clusters rather than many when every cluster would see
 // few tokens: each leaves hc * dim partial sums behind.
-Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
+Shape shape_of(int64_t T, int32_t hc, int32_t dim, bool q8) {
   Shape s;
   const int nvec = dim / 8;
   auto set = [&](int cs, int cg, int stages) {
@@ -547,9 +626,10 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
     s.cg = cg;
     s.stages = stages;
     s.nv = (nvec + cs - 1) / cs;
+    if (q8) s.nv += s.nv & 1;  // rows of 8-byte vectors on 16-byte boundaries
     const int per_group = (s.nv + 31) / 32 * 32;
     s.threads = per_group * cg;
-    s.smem = (int64_t)stages * (3 * hc + 1) * s.nv * 16 + (cg - 1) * per_group * 32ll +
+    s.smem = (int64_t)stages * (q8 ? 32 * hc + 8 : (3 * hc + 1) * 16) * s.nv + (cg - 1) * per_group * 32ll +
              2ll * cs * (s.threads / 32) * 4 * (hc / cg) * 4;
     return s.threads <= max_threads(hc, cg) && s.smem <= kMaxSmem;
   };
@@ -575,10 +655,10 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   return s;
 }
 
-template <int HC, int CG, int S, bool WHOLE>
+template <int HC, int CG, int S, bool WHOLE, bool Q8>
 cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, int64_t withhold,
                          cudaStream_t s) {
-  auto kern = gate_grad_kernel<HC, CG, S, WHOLE>;
+  auto kern = gate_grad_kernel<HC, CG, S, WHOLE, Q8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -620,21 +700,24 @@ cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, in
 
 }  // namespace
 
-uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
-  return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
+uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim, bool q8) {
+  return round256((uint64_t)shape_of(T, hc, dim, q8).clusters * hc * dim * 4);
 }
 
 cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s, int64_t withhold) {
   float* part = static_cast<float*>(workspace);
   int parts = 0;
   if (a.T > 0) {
-    const Shape sh = shape_of(a.T, a.hc, a.dim);
+    const Shape sh = shape_of(a.T, a.hc, a.dim, a.xs != nullptr);
     cudaError_t e = cudaErrorInvalidValue;
     auto launch = [&](auto hc, auto cg, auto stages) {
       constexpr int HC = decltype(hc)::value, CG = decltype(cg)::value, S = decltype(stages)::value;
-      if constexpr (S == 3)  // with two stages rows are too wide for one CTA
-        if (sh.cs == 1) return launch_shape<HC, CG, S, true>(a, sh, part, &parts, withhold, s);
-      return launch_shape<HC, CG, S, false>(a, sh, part, &parts, withhold, s);
+      if constexpr (S == 3) {  // with two stages rows are too wide for one CTA
+        if (sh.cs == 1 && a.xs != nullptr) return launch_shape<HC, CG, S, true, true>(a, sh, part, &parts, withhold, s);
+        if (sh.cs == 1) return launch_shape<HC, CG, S, true, false>(a, sh, part, &parts, withhold, s);
+      }
+      if (a.xs != nullptr) return launch_shape<HC, CG, S, false, true>(a, sh, part, &parts, withhold, s);
+      return launch_shape<HC, CG, S, false, false>(a, sh, part, &parts, withhold, s);
     };
     using std::integral_constant;
     const integral_constant<int, 1> one;

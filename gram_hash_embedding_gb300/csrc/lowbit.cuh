@@ -1,0 +1,136 @@
+// Block-scaled low-bit values and the declarations of the operators on them: quantisation and reading back
+// (quant.cu), rows of 4-bit tables (lookup4.cu), the product of 4-bit operands (proj4.cu).
+//
+// 4-bit codes are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit), the code of an even column in its byte's low
+// half. A block of 32 has a UE8M0 scale (a power of two), a block of 16 an E4M3 scale. 8-bit codes are E4M3 with a
+// power of two for a block of 32, 64 or 128.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "dequant.cuh"
+
+namespace engram {
+
+// kind of block-scaled 4-bit values: the block's length decides
+__host__ __device__ constexpr bool block4_ok(int32_t block) { return block == 32 || block == 16; }
+
+// The scales' order for the tensor cores ("tiled"): 512 bytes hold four consecutive scales of each of 128 rows,
+// at [row % 32][row / 32 % 4][4], which is what the copy into tensor memory reads; the groups of four of a block of 128
+// rows lie one after the other, then the next 128 rows. Groups per row of `cols` values:
+__host__ __device__ constexpr int64_t scale_groups(int64_t cols, int32_t block) { return (cols + 4 * block - 1) / (4 * block); }
+
+// bytes of the tiled scales of `rows` rows
+__host__ __device__ constexpr int64_t tiled_scale_bytes(int64_t rows, int64_t cols, int32_t block) {
+  return (rows + 127) / 128 * scale_groups(cols, block) * 512;
+}
+
+// where row r's scale number k lies
+__device__ __forceinline__ int64_t tiled_scale_at(int64_t r, int64_t k, int64_t groups) {
+  return ((r >> 7) * groups + (k >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (k & 3);
+}
+
+// two fp32 values to a byte of E2M1 codes (nearest, ties to even, |v| > 6 to 6), four pairs to a word
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// 8 E2M1 codes to fp32 times a scale. Every product is exact: a code has two significant bits, a scale at most four.
+__device__ __forceinline__ void widen_e2m1x8(uint32_t w, float s, float* v) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f16x2_to_f32(h[i], v[2 * i], v[2 * i + 1]);
+    v[2 * i] *= s;
+    v[2 * i + 1] *= s;
+  }
+}
+
+// four fp32 values to E4M3 codes (nearest, ties to even, beyond 448 to 448)
+__device__ __forceinline__ uint32_t e4m3x4(const float* v) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
+  return (uint32_t)lo | (uint32_t)hi << 16;
+}
+
+// four E4M3 codes to fp32 times a scale (exact for a power of two, subnormal results aside)
+__device__ __forceinline__ void widen_e4m3x4(uint32_t w, float s, float* v) {
+  f16x2_to_f32(e4m3x2_to_f16x2(w & 0xffffu), v[0], v[1]);
+  f16x2_to_f32(e4m3x2_to_f16x2(w >> 16), v[2], v[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] *= s;
+}
+
+struct QuantArgs {
+  const void* x;       // [rows] rows of cols values, x_stride apart
+  int64_t rows;
+  int32_t cols;
+  int64_t x_stride;
+  int32_t x_type;      // ENGRAM_TYPE_*
+  int32_t block;
+  float scale;         // 4 bits: a power of two; codes stand for x / scale
+  uint8_t* codes;      // [rows][cols / 2] or [rows][cols]
+  void* scales;
+  int32_t tiled;       // 4 bits: scales in the order of the tensor cores
+  int32_t scale_dtype; // 8 bits: storage of the scales
+};
+cudaError_t launch_quantize4(const QuantArgs& a, cudaStream_t s);
+cudaError_t launch_quantize8(const QuantArgs& a, cudaStream_t s);
+
+struct DequantArgs {
+  const uint8_t* codes;
+  const void* scales;
+  int64_t rows;
+  int32_t cols, block, tiled, scale_dtype;
+  float scale;
+  void* out;           // [rows][cols] of out_type
+  int32_t out_type;
+};
+cudaError_t launch_dequantize4(const DequantArgs& a, cudaStream_t s);
+cudaError_t launch_dequantize8(const DequantArgs& a, cudaStream_t s);
+
+struct Lookup4Args {
+  const int64_t* idx;  // token t's row ids at idx[t * idx_stride + c]
+  int64_t idx_stride, T;
+  int32_t n_cols;
+  const uint8_t* Q;    // [table_rows][dim / 2]
+  const uint8_t* S;    // [table_rows][dim / block]
+  int64_t table_rows;
+  int32_t dim, block;
+  float scale;
+};
+cudaError_t launch_lookup4(const Lookup4Args& a, uint16_t* out, cudaStream_t s);
+// the rows as they stand, as an operand of the product: codes [T][n_cols * dim / 2], tiled scales
+cudaError_t launch_lookup4_operand(const Lookup4Args& a, uint8_t* codes, uint8_t* scales, cudaStream_t s);
+
+struct Project4Args {
+  const uint8_t *a, *as;  // [T][K / 2], tiled scales
+  const uint8_t *w, *ws;  // [N][K / 2], tiled scales
+  int64_t T;
+  int32_t K, N, block;
+  float scale;
+  uint16_t* out;          // [T][N] bf16
+};
+// withhold >= 0: the test hook of engram_project4_withhold
+cudaError_t launch_project4(const Project4Args& a, cudaStream_t s, int32_t withhold = -1);
+
+}  // namespace engram

@@ -41,6 +41,7 @@
 #include "engram_internal.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace engram {
 
@@ -750,20 +751,28 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
+bool tensor_map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, uint64_t rows, uint64_t cols,
+                   uint64_t row_bytes, uint32_t box_rows, uint32_t box_cols, CUtensorMapSwizzle swz) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 // [rows][cols] bf16 row-major, moved in boxes of box_rows x box_cols: operands are read with 128-byte
 // swizzling (reads past the matrix, ragged rows or K, are filled with zeros), outputs written from
 // 64-byte swizzled staging chunks (writes past the matrix are dropped)
 bool make_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
               uint32_t box_cols = kAtomK, CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {box_cols, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return tensor_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, rows, cols, cols * 2, box_rows, box_cols, swz);
 }
 
 #ifndef ENGRAM_PROJ_CLUSTER

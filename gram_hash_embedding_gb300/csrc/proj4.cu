@@ -1,0 +1,375 @@
+// The `wkv` projection as a product of block-scaled 4-bit operands on the sm_103a tensor cores:
+//   out[t][n] = bf16_rne(scale * sum_k (a[t][k] * sa[t][k / block]) * (w[n][k] * sw[n][k / block]))
+// a, w E2M1 codes, sa, sw UE8M0 (block of 32) or E4M3 (block of 16) scales, products and sums fp32 in the tensor
+// cores (tcgen05.mma .block_scale, K = 64 an instruction, four times the bf16 rate).
+//
+// Design (GB300): the shape of the bf16 projection (proj.cu): persistent CTA pairs, 256 x BN output tiles by M = 256
+// MMAs of the pair's leader, operands by TMA in 128-byte swizzled rows (256 values of K: one stage), an
+// accumulator in each CTA's tensor memory while the epilogue empties the tile before. What differs:
+// - Scales. A stage's scales come in the tensor cores' order (512 bytes for 128 rows and four scales of each) by TMA, and
+//   are copied from shared into tensor memory by the thread that issues the MMAs (tcgen05.cp): 128 rows of A and all
+//   BN rows of B in each CTA of the pair.
+// - Tensor memory. Two accumulators of 256 columns leave no column for scales, so they overlap: columns [0, 256) and
+//   [192, 448), scales from 448 on. The epilogue reads the 64 shared columns of a tile first and then lets the next
+//   tile's MMAs start.
+// Warp 0 loads, warp 1 issues, warps 2-5 are the epilogue. Every wait is bounded (tc_ptx.cuh): a wait that runs
+// out raises ENGRAM_STATUS_TIMEOUT, the CTA stops issuing, waits for its copies and MMAs in flight and exits.
+#include <cstdint>
+
+#include "engram_internal.cuh"
+#include "lowbit.cuh"
+#include "proj.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.cuh"
+
+namespace engram {
+namespace {
+
+constexpr int kBM = 128;                   // tile rows of one CTA (tokens)
+constexpr int kStageK = 256;               // values of K a stage: one 128-byte swizzle row
+constexpr int kMmaK = 64;                  // values of K an MMA
+constexpr int kMmas = kStageK / kMmaK;     // MMAs a stage
+constexpr int kThreads = 192;              // 6 warps: loader, MMA, 4 epilogue
+constexpr int kGroup = 16;                 // 256-row blocks per tile group
+constexpr uint32_t kABytes = kBM * 128;    // A of a stage
+constexpr uint32_t kChunkBytes = 512;      // scales of 128 rows, four each
+constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;
+constexpr uint32_t kScaleCol = 448;        // first tensor-memory column of the scales
+
+template <bool NV, int BN>
+struct Cfg {
+  static constexpr int kChunks = NV ? 4 : 2;                     // groups of four scales in a stage's K
+  static constexpr int kBBlocks = BN / 128;                      // blocks of 128 rows of B
+  static constexpr uint32_t kBBytes = (BN / 2) * 128;            // this CTA's half of B
+  static constexpr uint32_t kSaBytes = kChunks * kChunkBytes;
+  static constexpr uint32_t kSbBytes = kBBlocks * kSaBytes;
+  static constexpr uint32_t kTileBytes = kABytes + kBBytes;      // 1024-byte multiples
+  static constexpr uint32_t kStageScaleBytes = kSaBytes + kSbBytes;
+  static constexpr uint32_t kTxBytes = 2 * (kTileBytes + kStageScaleBytes);  // both CTAs of the pair
+  static constexpr uint32_t kEpiBytes = 4 * 2 * kEpiChunkBytes;
+  static constexpr int kStages = (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes)) < 8
+                                     ? (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes))
+                                     : 8;
+  static constexpr bool kOverlap = BN == 256;
+  static constexpr uint32_t kAcc1 = kOverlap ? 192 : BN;         // column of the second accumulator
+  static constexpr uint32_t kSaCols = 4 * kChunks, kSbCols = 4 * kBBlocks;  // of a stage; of one group of B
+  static_assert(kScaleCol + kSaCols + kChunks * kSbCols <= 512 && kAcc1 + BN <= kScaleCol, "tensor memory");
+  // shared memory: operand ring, scale ring, output staging, barriers and words
+  static constexpr uint32_t kScaleOff = kStages * kTileBytes;
+  static constexpr uint32_t kEpiOff = kScaleOff + kStages * kStageScaleBytes;
+  static constexpr uint32_t kBarOff = kEpiOff + kEpiBytes;       // full[S], empty[S], acc_full[2], acc_free[2], drain
+  static constexpr uint32_t kNumBars = 2 * kStages + 5;
+  static constexpr uint32_t kTmemSlotOff = kBarOff + 8 * kNumBars;
+  static constexpr uint32_t kAbortOff = kTmemSlotOff + 4;
+  static constexpr uint32_t kSmemBytes = kAbortOff + 4 + 1024;   // + slack to align the ring to 1024 bytes
+  static_assert(kSmemBytes <= 232448 && kStages >= 3, "shared memory");
+};
+
+struct Params {
+  int64_t T;
+  int32_t K, N, num_kb, n_mtile, n_ntile;
+  int64_t n_tiles;
+  int32_t groups;  // groups of four scales in a row
+  float scale;
+  unsigned int* status;
+  int32_t withhold;  // test hook: the tile (of each pair) whose completion is not signalled; -1: none
+};
+
+// tile index -> (tile row, column block): groups of kGroup tile rows, column block outer
+__device__ __forceinline__ void tile_coords(const Params& p, int64_t tile, int32_t& mt, int32_t& nb) {
+  const int64_t per_group = (int64_t)kGroup * p.n_ntile;
+  const int64_t g = tile / per_group;
+  const int32_t r = (int32_t)(tile - g * per_group);
+  const int32_t m0 = (int32_t)(g * kGroup);
+  const int32_t gm = min(kGroup, p.n_mtile - m0);
+  mt = m0 + r % gm;
+  nb = r / gm;
+}
+
+__device__ __forceinline__ void raise_timeout(volatile int* abort, unsigned int* status) {
+  *abort = 1;
+  atomicOr(status, (unsigned)ENGRAM_STATUS_TIMEOUT);
+}
+
+template <bool NV, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    project4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
+                    const __grid_constant__ CUtensorMap tmO, const Params p) {
+  using C = Cfg<NV, BN>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // the same offset in both CTAs
+  uint8_t* gbase = smem_raw + (base - raw);
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + C::kAbortOff);
+  const uint32_t* tmem_slot = reinterpret_cast<const uint32_t*>(gbase + C::kTmemSlotOff);
+  auto bar = [&](int i) { return base + C::kBarOff + 8u * (uint32_t)i; };
+  auto full = [&](uint32_t s) { return bar((int)s); };
+  auto empty = [&](uint32_t s) { return bar(S + (int)s); };
+  auto acc_full = [&](uint32_t a) { return bar(2 * S + (int)a); };
+  auto acc_free = [&](uint32_t a) { return bar(2 * S + 2 + (int)a); };
+  const uint32_t drain = bar(2 * S + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t q = tc::cluster_ctarank();
+  const bool leader = q == 0;
+  const int64_t unit = (int64_t)(blockIdx.x / 2), n_units = (int64_t)(gridDim.x / 2);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(full(s), 1);
+      tc::mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      tc::mbar_init(acc_full(a), 1);
+      tc::mbar_init(acc_free(a), 8);  // one arrival per epilogue warp of the pair
+    }
+    tc::mbar_init(drain, 1);
+    *abort = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_descriptor(&tmA);
+    tc::tma_prefetch_descriptor(&tmB);
+    tc::tma_prefetch_descriptor(&tmSa);
+    tc::tma_prefetch_descriptor(&tmSb);
+    tc::tma_prefetch_descriptor(&tmO);
+  }
+  pdl_wait();
+  tc::cluster_sync();
+  if (warp == 1) {
+    tc::tmem_alloc_pair(base + C::kTmemSlotOff, 512);
+    tc::tmem_relinquish_alloc_permit_pair();
+  }
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- loader (both CTAs)
+    int64_t issued = 0;
+    uint32_t stage = 0, phase = 0;
+    for (int64_t tile = unit; tile < p.n_tiles && !*abort; tile += n_units) {
+      int32_t mt, nt;
+      tile_coords(p, tile, mt, nt);
+      const int32_t arow = (mt * 2 + (int32_t)q) * kBM, brow = nt * BN + (int32_t)q * (BN / 2);
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!tc::mbar_wait(empty(stage), phase ^ 1u, abort)) {
+          raise_timeout(abort, p.status);
+          break;
+        }
+        const uint32_t a_dst = base + stage * C::kTileBytes;
+        const uint32_t s_dst = base + C::kScaleOff + stage * C::kStageScaleBytes;
+        const uint32_t fb = tc::map_to_rank(full(stage), 0);
+        if (leader) tc::mbar_arrive_expect_tx(full(stage), C::kTxBytes);
+        tc::tma_load_2d_pair(a_dst, &tmA, fb, kb * (kStageK / 2), arow);
+        tc::tma_load_2d_pair(a_dst + kABytes, &tmB, fb, kb * (kStageK / 2), brow);
+        // past a row's last group a box reads the next rows' groups, which no MMA uses
+        tc::tma_load_2d_pair(s_dst, &tmSa, fb, 0, (mt * 2 + (int32_t)q) * p.groups + kb * C::kChunks);
+#pragma unroll
+        for (int b = 0; b < C::kBBlocks; ++b)
+          tc::tma_load_2d_pair(s_dst + C::kSaBytes * (1 + b), &tmSb, fb, 0,
+                               (nt * C::kBBlocks + b) * p.groups + kb * C::kChunks);
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // no copy may still be landing when the CTA exits: wait for the MMAs that read the last loads
+    for (int64_t i = issued - (issued < S ? issued : S); i < issued; ++i)
+      if (!tc::mbar_wait(empty((uint32_t)(i % S)), (uint32_t)((i / S) & 1), nullptr))
+        atomicOr(p.status, (unsigned)ENGRAM_STATUS_TIMEOUT);
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ---------------------------------------------------------------- MMA issuer
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    int32_t n = 0;
+    for (int64_t tile = unit; ok && tile < p.n_tiles && !*abort; tile += n_units, ++n) {
+      const uint32_t acc = n & 1;
+      // overlapping accumulators: the tile before must have left the shared columns (and then the one before it is
+      // read in full); separate ones: the tile two before must be read
+      const bool free = C::kOverlap ? n == 0 || tc::mbar_wait(acc_free(acc ^ 1u), ((n - 1) >> 1) & 1, abort)
+                                    : tc::mbar_wait(acc_free(acc), ((n >> 1) & 1) ^ 1u, abort);
+      if (!free) {
+        raise_timeout(abort, p.status);
+        break;
+      }
+      tc::fence_after_thread_sync();
+      const uint32_t d = tmem + acc * C::kAcc1;
+      const uint32_t ta = tmem + kScaleCol, tb = ta + C::kSaCols;
+      for (int kb = 0; kb < p.num_kb; ++kb) {
+        if (!tc::mbar_wait(full(stage), phase, abort)) {
+          raise_timeout(abort, p.status);
+          ok = false;
+          break;
+        }
+        tc::fence_after_thread_sync();
+        const uint32_t a0 = base + stage * C::kTileBytes, b0 = a0 + kABytes;
+        const uint32_t s0 = base + C::kScaleOff + stage * C::kStageScaleBytes;
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          tc::copy_scales<true>(ta + 4 * c, tc::scales_desc(s0 + c * kChunkBytes));
+#pragma unroll
+          for (int b = 0; b < C::kBBlocks; ++b)
+            tc::copy_scales<true>(tb + c * C::kSbCols + 4 * b, tc::scales_desc(s0 + C::kSaBytes * (1 + b) + c * kChunkBytes));
+        }
+        const int left = p.K - kb * kStageK;
+#pragma unroll
+        for (int k = 0; k < kMmas; ++k) {
+          if (k * kMmaK < left) {
+            const int c = NV ? k : k / 2;
+            tc::mma_e2m1<true, NV>(d, tc::sw128_kmajor_desc(a0 + 32 * k), tc::sw128_kmajor_desc(b0 + 32 * k),
+                                   tc::idesc_e2m1(2 * kBM, BN, !NV, NV ? 0u : (uint32_t)(k & 1)), ta + 4 * c,
+                                   tb + c * C::kSbCols, (kb | k) != 0 ? 1u : 0u);
+          }
+        }
+        tc::commit_pair_multicast(empty(stage), 3);
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (n != p.withhold) tc::commit_pair_multicast(acc_full(acc), 3);
+    }
+    tc::commit_pair_multicast(drain, 1);
+    if (!tc::mbar_wait(drain, 0, nullptr)) atomicOr(p.status, (unsigned)ENGRAM_STATUS_TIMEOUT);
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------------- epilogue (both CTAs)
+    const int quarter = warp & 3;  // tensor-memory lanes [32 * quarter, 32 * quarter + 32)
+    const uint32_t staging = base + C::kEpiOff + (uint32_t)quarter * 2u * kEpiChunkBytes;
+    int32_t n = 0, sent = 0;
+    // 32 columns of the warp's 32 rows: scaled, rounded, through a swizzled chunk of shared memory, out by TMA
+    auto put = [&](const float (&v)[32], int col, int32_t row) {
+      const uint32_t chunk = staging + (uint32_t)(sent & 1) * kEpiChunkBytes;
+      ++sent;
+      if (lane == 0) tc::bulk_wait_group_read_1();
+      __syncwarp();
+      const uint32_t to = chunk + (uint32_t)lane * 64u;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float* w = v + 8 * g;
+        tc::st_shared_v4(to + (uint32_t)((g ^ ((lane >> 1) & 3)) * 16),
+                         make_uint4(tc::f32x2_to_bf16x2(w[0] * p.scale, w[1] * p.scale),
+                                    tc::f32x2_to_bf16x2(w[2] * p.scale, w[3] * p.scale),
+                                    tc::f32x2_to_bf16x2(w[4] * p.scale, w[5] * p.scale),
+                                    tc::f32x2_to_bf16x2(w[6] * p.scale, w[7] * p.scale)));
+      }
+      tc::fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        tc::tma_store_2d(&tmO, chunk, col, row);
+        tc::bulk_commit_group();
+      }
+    };
+    for (int64_t tile = unit; tile < p.n_tiles; tile += n_units, ++n) {
+      const uint32_t acc = n & 1;
+      int32_t mt, nt;
+      tile_coords(p, tile, mt, nt);
+      int ok = 1;
+      if (lane == 0) {
+        ok = tc::mbar_wait(acc_full(acc), (n >> 1) & 1, abort) ? 1 : 0;
+        if (!ok) raise_timeout(abort, p.status);
+      }
+      if (__shfl_sync(0xffffffffu, ok, 0) == 0) break;
+      tc::fence_after_thread_sync();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + acc * C::kAcc1;
+      const int32_t row = (mt * 2 + (int32_t)q) * kBM + quarter * 32;  // TMA stores skip rows past T
+      auto release = [&]() {
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_free(acc), 0));
+      };
+      constexpr int kChunksN = BN / 32;
+      // the columns that the next tile's accumulator shares come first: the last 64 of the first, the first of the second
+      const int first = C::kOverlap && acc == 0 ? kChunksN - 2 : 0;
+      float v[32], w[32];
+      tc::tmem_load_32cols(taddr + 32 * first, v);
+      tc::tmem_load_32cols(taddr + 32 * (first + 1), w);
+      if (C::kOverlap) release();
+      put(v, nt * BN + 32 * first, row);
+      put(w, nt * BN + 32 * (first + 1), row);
+#pragma unroll 1
+      for (int i = 2; i < kChunksN; ++i) {
+        const int c = (first + i) % kChunksN;
+        tc::tmem_load_32cols(taddr + 32 * c, v);
+        put(v, nt * BN + 32 * c, row);
+      }
+      if (!C::kOverlap) release();
+    }
+    if (lane == 0) tc::bulk_wait_group_0();
+    __syncwarp();
+  }
+  pdl_trigger();
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::cluster_sync();  // no CTA leaves while the other may still signal its barriers or read its memory
+  if (warp == 1) {
+    __syncwarp();
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <bool NV, int BN>
+cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold) {
+  using C = Cfg<NV, BN>;
+  Params p = {};
+  p.T = a.T;
+  p.K = a.K;
+  p.N = a.N;
+  p.num_kb = (a.K + kStageK - 1) / kStageK;
+  p.n_mtile = (int32_t)((a.T + 2 * kBM - 1) / (2 * kBM));
+  p.n_ntile = (a.N + BN - 1) / BN;
+  p.n_tiles = (int64_t)p.n_mtile * p.n_ntile;
+  p.groups = (int32_t)scale_groups(a.K, a.block);
+  p.scale = a.scale;
+  p.withhold = withhold;
+  cudaError_t e = device_status_word(&p.status);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, i32 = CU_TENSOR_MAP_DATA_TYPE_INT32;
+  const uint64_t kb = (uint64_t)a.K / 2;
+  CUtensorMap ta, tb, tsa, tsb, to;
+  if (!tensor_map_2d(&ta, u8, a.a, (uint64_t)a.T, kb, kb, kBM, 128, sw) ||
+      !tensor_map_2d(&tb, u8, a.w, (uint64_t)a.N, kb, kb, BN / 2, 128, sw) ||
+      !tensor_map_2d(&tsa, i32, a.as, (uint64_t)((a.T + 127) / 128) * p.groups, 128, 512, C::kChunks, 128, none) ||
+      !tensor_map_2d(&tsb, i32, a.ws, (uint64_t)((a.N + 127) / 128) * p.groups, 128, 512, C::kChunks, 128, none) ||
+      !tensor_map_2d(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.T, (uint64_t)a.N, (uint64_t)a.N * 2, 32, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  auto kern = project4_kernel<NV, BN>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = ENGRAM_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3(2);
+  int units = 0;
+  e = cudaOccupancyMaxActiveClusters(&units, kern, &cfg);
+  if (e != cudaSuccess) return e;
+  if (units < 1) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)(2 * (p.n_tiles < units ? p.n_tiles : units)));
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, to, p);
+}
+
+}  // namespace
+
+cudaError_t launch_project4(const Project4Args& a, cudaStream_t s, int32_t withhold) {
+  const int64_t wide = (a.T + 255) / 256 * ((a.N + 255) / 256);
+  if (wide < 76) return a.block == 16 ? launch_pairs<true, 128>(a, s, withhold) : launch_pairs<false, 128>(a, s, withhold);
+  return a.block == 16 ? launch_pairs<true, 256>(a, s, withhold) : launch_pairs<false, 256>(a, s, withhold);
+}
+
+}  // namespace engram

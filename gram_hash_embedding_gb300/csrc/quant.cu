@@ -1,0 +1,251 @@
+// Block-scaled quantisation and reading back (sm_103a): 4-bit E2M1 codes with a scale for 32 or 16 values, 8-bit
+// E4M3 codes with a power of two for 32, 64 or 128.
+//
+//   block of 32 (4 bits) and the 8-bit blocks: scale = the smallest 2^e, e >= -127, with max |v| <= most * 2^e (most = 6
+//   or 448), so no value is cut off; code = nearest(v / scale), ties to even. A power of two: v / scale is exact.
+//   block of 16 (4 bits): scale = nearest E4M3 to max |v| / 6 (448 at most), code = nearest E2M1 to v / scale (6 at
+//   most); a scale that rounds to 0 makes all codes 0.
+//   v = x / the tensor's factor, a power of two (4 bits; 1 for 8 bits). A block with a NaN or an infinity gets the
+//   scale NaN and codes of 0, so it reads back as NaN.
+// Every rounding is decided as in exact arithmetic: quotients that are rounded are either exact or so far from a
+// border between two codes that the fp32 result lies on the same side (below).
+//
+// Bound by memory: each value is read once and half a byte or a byte written. A thread takes 16 values of a row, a
+// block's threads are neighbours and share its maximum by shuffles.
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "engram_internal.cuh"
+#include "lowbit.cuh"
+#include "train.cuh"
+
+namespace engram {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 16;  // values of a thread
+constexpr uint32_t kInf = 0x7f800000u;
+
+// UE8M0 byte of the smallest 2^e with amax <= (1 + frac / 2^23) * 2^(e + exp), as bits of amax; 255 for infinity, NaN
+__device__ __forceinline__ uint32_t pow2_scale(uint32_t amax, uint32_t exp, uint32_t frac) {
+  if (amax >= kInf) return 255u;
+  const int b = (int)(amax >> 23) - (int)exp + ((amax & 0x7fffffu) > frac ? 1 : 0);
+  return (uint32_t)max(b, 0);
+}
+
+// the reciprocal of 2^(b - 127), b in [0, 253]
+__device__ __forceinline__ float pow2_recip(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// E4M3 byte nearest to amax / 6, 0x7f for infinity and NaN. The quotient is rounded to odd (truncated, its last bit
+// set where anything was lost), so that the second rounding, to four bits, falls as the exact quotient's would.
+__device__ __forceinline__ uint32_t e4m3_scale(uint32_t amax) {
+  if (amax >= kInf) return 0x7fu;
+  const float m = __uint_as_float(amax);
+  float q = __fdiv_rz(m, 6.0f);
+  if (__fmaf_rn(q, 6.0f, -m) != 0.f) q = __uint_as_float(__float_as_uint(q) | 1u);
+  const float two[4] = {q, 0.f, 0.f, 0.f};
+  return e4m3x4(two) & 0xffu;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+  float lo, hi;
+  f16x2_to_f32(e4m3x2_to_f16x2(b), lo, hi);
+  return lo;
+}
+
+// v / s ready for the conversion to E2M1, s an E4M3 number. 16-bit inputs have at most 11 significant bits and s four:
+// the quotient is a border between two codes (three bits) exactly, or at least 2^-11 of itself away from it. The
+// product with the rounded reciprocal is within 2^-22, and rounding it to 19 bits puts exact borders back onto themselves.
+__device__ __forceinline__ float quotient16(float v, float recip) {
+  return __uint_as_float((__float_as_uint(v * recip) + 16u) & ~31u);
+}
+
+// fp32 inputs may lie nearer to a border than that: the code's magnitude by comparing with the borders times s, which
+// are exact (three bits times four); between two codes a tie goes to the even one
+__device__ __forceinline__ float e2m1_by_borders(float v, float s) {
+  const float a = fabsf(v);
+  float r = a > 0.25f * s ? 0.5f : 0.f;
+  r = a >= 0.75f * s ? 1.f : r;
+  r = a > 1.25f * s ? 1.5f : r;
+  r = a >= 1.75f * s ? 2.f : r;
+  r = a > 2.5f * s ? 3.f : r;
+  r = a >= 3.5f * s ? 4.f : r;
+  r = a > 5.f * s ? 6.f : r;
+  return copysignf(r, v);
+}
+
+// LANES threads of 16 values share a block: 1 (blocks of 16) or 2 with 4-bit codes, 2, 4 or 8 with 8-bit codes.
+// HALF: rows are a multiple of 8 values and no more (8 bits), so a row's last thread may have 8.
+template <int TYPE, int LANES, bool FOUR, bool TILED, bool HALF>
+__global__ void __launch_bounds__(kThreads)
+    quantize_kernel(const QuantArgs a, const uint32_t per_row, const uint64_t units, const float inv) {
+  pdl_wait();
+  pdl_trigger();
+  using T = typename Elem<TYPE>::type;
+  const uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  const bool on = u < units;
+  // a row has per_row threads, a multiple of LANES
+  const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
+  const uint32_t j = (uint32_t)(u - row * per_row);
+  const int col = (int)j * kPer;
+  const bool lo = on && col < a.cols, hi = HALF ? on && col + 8 < a.cols : lo;
+  const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride + col;
+  Raw<TYPE, 8> r0, r1;
+  r0.zero();
+  r1.zero();
+  if (lo) r0.load(x);
+  if (hi) r1.load(x + 8);
+  float v[kPer];
+  r0.widen(v);
+  r1.widen(v + 8);
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (FOUR) v[i] *= inv;
+    amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);  // in bits a NaN is above infinity
+  }
+#pragma unroll
+  for (int off = 1; off < LANES; off *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  uint32_t code;
+  uint32_t w[4];
+  if constexpr (FOUR && LANES == 1) {
+    code = e4m3_scale(amax);
+    const float s = e4m3_value(code);
+    const bool ok = code != 0u && code != 0x7fu;
+    const float recip = ok ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      v[i] = !ok ? 0.f : TYPE == ENGRAM_TYPE_F32 ? e2m1_by_borders(v[i], s) : quotient16(v[i], recip);
+  } else {
+    code = FOUR ? pow2_scale(amax, 2, 0x400000u) : pow2_scale(amax, 8, 0x600000u);
+    const float recip = code == 255u ? 0.f : pow2_recip(code);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = code == 255u ? 0.f : v[i] * recip;
+  }
+  if constexpr (FOUR) {
+    w[0] = e2m1x8(v);
+    w[1] = e2m1x8(v + 8);
+    if (lo) *reinterpret_cast<uint2*>(a.codes + (int64_t)row * (a.cols >> 1) + (col >> 1)) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e4m3x4(v + 4 * i);
+    uint8_t* to = a.codes + (int64_t)row * a.cols + col;
+    if (!HALF) {
+      if (lo) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      if (lo) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      if (hi) *reinterpret_cast<uint2*>(to + 8) = make_uint2(w[2], w[3]);
+    }
+  }
+  if (!lo || j % LANES != 0) return;
+  const uint32_t k = j / LANES;
+  if constexpr (TILED) {
+    uint8_t* to = static_cast<uint8_t*>(a.scales);
+    const int64_t groups = scale_groups(a.cols, a.block);
+    to[tiled_scale_at((int64_t)row, k, groups)] = (uint8_t)code;
+    if ((int)(k + 1) * a.block >= a.cols)  // the row's last scale: the rest of its group of four is 0
+      for (uint32_t p = k + 1; p & 3u; ++p) to[tiled_scale_at((int64_t)row, p, groups)] = 0;
+  } else {
+    const int64_t at = (int64_t)row * (per_row / LANES) + k;
+    if (FOUR || a.scale_dtype == ENGRAM_SCALE_E8M0) {
+      static_cast<uint8_t*>(a.scales)[at] = (uint8_t)code;
+    } else {
+      const uint32_t bits = __float_as_uint(widen_scale<ENGRAM_SCALE_E8M0>(code));
+      if (a.scale_dtype == ENGRAM_SCALE_F32) static_cast<uint32_t*>(a.scales)[at] = bits;
+      else static_cast<uint16_t*>(a.scales)[at] = (uint16_t)(bits >> 16);  // a power of two: exact
+    }
+  }
+}
+
+template <int LANES, bool FOUR, bool TILED>
+cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s) {
+  const uint32_t per_row = (uint32_t)((a.cols + a.block - 1) / a.block) * LANES;
+  const uint64_t units = (uint64_t)a.rows * per_row, ctas = (units + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidValue;
+  const float inv = 1.0f / a.scale;
+  return with_type(a.x_type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    auto kern = quantize_kernel<TYPE, LANES, FOUR, TILED, !FOUR>;
+    if (!FOUR && a.cols % 16 == 0) kern = quantize_kernel<TYPE, LANES, FOUR, TILED, false>;
+    return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), 0, s, a, per_row, units, inv);
+  });
+}
+
+// 16 values a thread, as above, in the other direction
+template <int TYPE, bool FOUR, bool NV, bool TILED>
+__global__ void __launch_bounds__(kThreads)
+    dequantize_kernel(const DequantArgs a, const uint32_t per_row, const uint64_t units) {
+  pdl_wait();
+  pdl_trigger();
+  const uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (u >= units) return;
+  const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
+  const int col = (int)(u - row * per_row) * kPer;
+  const bool hi = FOUR || col + 8 < a.cols;
+  const int k = col / a.block;
+  float v[kPer];
+  if constexpr (FOUR) {
+    const int64_t at = TILED ? tiled_scale_at((int64_t)row, k, scale_groups(a.cols, a.block))
+                             : (int64_t)row * (a.cols / a.block) + k;
+    const uint32_t b = static_cast<const uint8_t*>(a.scales)[at];
+    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + (int64_t)row * (a.cols >> 1) + (col >> 1));
+    const float s = (NV ? e4m3_value(b) : widen_scale<ENGRAM_SCALE_E8M0>(b));
+    widen_e2m1x8(w.x, s, v);
+    widen_e2m1x8(w.y, s, v + 8);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] *= a.scale;
+  } else {
+    const int64_t at = (int64_t)row * ((a.cols + a.block - 1) / a.block) + k;
+    float s;
+    if (a.scale_dtype == ENGRAM_SCALE_E8M0) s = widen_scale<ENGRAM_SCALE_E8M0>(static_cast<const uint8_t*>(a.scales)[at]);
+    else if (a.scale_dtype == ENGRAM_SCALE_F32) s = static_cast<const float*>(a.scales)[at];
+    else s = __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.scales)[at] << 16);
+    const uint8_t* from = a.codes + (int64_t)row * a.cols + col;
+    const uint2 w0 = *reinterpret_cast<const uint2*>(from);
+    const uint2 w1 = hi ? *reinterpret_cast<const uint2*>(from + 8) : make_uint2(0u, 0u);
+    widen_e4m3x4(w0.x, s, v);
+    widen_e4m3x4(w0.y, s, v + 4);
+    widen_e4m3x4(w1.x, s, v + 8);
+    widen_e4m3x4(w1.y, s, v + 12);
+  }
+  typename Elem<TYPE>::type* to = static_cast<typename Elem<TYPE>::type*>(a.out) + (int64_t)row * a.cols + col;
+  store_vals<TYPE, 8>(to, v);
+  if (hi) store_vals<TYPE, 8>(to + 8, v + 8);
+}
+
+template <bool FOUR, bool NV, bool TILED>
+cudaError_t launch_dequantize(const DequantArgs& a, cudaStream_t s) {
+  const uint32_t per_row = (uint32_t)((a.cols + kPer - 1) / kPer);
+  const uint64_t units = (uint64_t)a.rows * per_row, ctas = (units + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffffull) return cudaErrorInvalidValue;
+  return with_type(a.out_type, [&](auto t) {
+    return launch_pdl(dequantize_kernel<decltype(t)::value, FOUR, NV, TILED>, dim3((unsigned)ctas), dim3(kThreads), 0,
+                      s, a, per_row, units);
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_quantize4(const QuantArgs& a, cudaStream_t s) {
+  if (a.block == 16) return a.tiled ? launch_quantize<1, true, true>(a, s) : launch_quantize<1, true, false>(a, s);
+  return a.tiled ? launch_quantize<2, true, true>(a, s) : launch_quantize<2, true, false>(a, s);
+}
+
+cudaError_t launch_quantize8(const QuantArgs& a, cudaStream_t s) {
+  switch (a.block) {
+    case 32: return launch_quantize<2, false, false>(a, s);
+    case 64: return launch_quantize<4, false, false>(a, s);
+    default: return launch_quantize<8, false, false>(a, s);
+  }
+}
+
+cudaError_t launch_dequantize4(const DequantArgs& a, cudaStream_t s) {
+  if (a.block == 16)
+    return a.tiled ? launch_dequantize<true, true, true>(a, s) : launch_dequantize<true, true, false>(a, s);
+  return a.tiled ? launch_dequantize<true, false, true>(a, s) : launch_dequantize<true, false, false>(a, s);
+}
+
+cudaError_t launch_dequantize8(const DequantArgs& a, cudaStream_t s) { return launch_dequantize<false, false, false>(a, s); }
+
+}  // namespace engram

@@ -277,5 +277,59 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// ------------------------------------------------------------------------------------------ block-scaled 4-bit MMAs
+// E2M1 operands packed two to a byte, K-major; a 128-byte swizzle row is 256 values of K, and one MMA takes 64 of
+// them (32 bytes, as 16 bf16 values do). Each row's scales stand in tensor memory: row r of a block of 128 in lane
+// r % 32 of column r / 32, four bytes a column, the same in all four groups of 32 lanes.
+
+// Shared-memory descriptor of 512 bytes of scales, 32 rows of 16 bytes one after the other (8-row groups of 128 bytes, no
+// swizzling), as the copy into tensor memory reads them.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
+         (static_cast<uint64_t>(1) << 46);
+}
+
+// 512 bytes of scales from shared memory into 4 columns of tensor memory, written to all four groups of 32 lanes;
+// with PAIR in both CTAs, each from its own shared memory. Ordered before the MMAs this thread issues later.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+  if (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of the block-scaled 4-bit kinds, both operands K-major. e8m0: scales are UE8M0, else
+// UE4M3. `half` (block of 32, two scales an MMA) picks the lower or upper two bytes of a scale column.
+__host__ __device__ constexpr uint32_t idesc_e2m1(int M, int N, bool e8m0, uint32_t half) {
+  return (half * 2u << 4)                           // B scales: byte of the column
+         | (1u << 7)                                // A format: E2M1
+         | (1u << 10)                               // B format: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
+         | (e8m0 ? 1u << 23 : 0u)                   // scale format
+         | (static_cast<uint32_t>(M >> 7) << 27)    // M / 128
+         | (half * 2u << 29);                       // A scales: byte of the column
+}
+
+// D[tmem] (+)= (A[smem] * scales_a) * (B[smem] * scales_b)^T over K = 64. BLOCK16: a scale for 16 values, else for 32.
+template <bool PAIR, bool BLOCK16>
+__device__ __forceinline__ void mma_e2m1(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t a_scales, uint32_t b_scales, uint32_t accumulate) {
+#define ENGRAM_MMA_E2M1(GROUP, KIND)                                                             \
+  asm volatile(                                                                                  \
+      "{\n"                                                                                      \
+      ".reg .pred p;\n"                                                                          \
+      "setp.ne.b32 p, %6, 0;\n"                                                                  \
+      "tcgen05.mma.cta_group::" GROUP "." KIND " [%0], %1, %2, %3, [%4], [%5], p;\n"             \
+      "}\n" ::"r"(d_tmem),                                                                       \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scales), "r"(b_scales), "r"(accumulate)        \
+      : "memory")
+  if (PAIR && BLOCK16) ENGRAM_MMA_E2M1("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else if (PAIR) ENGRAM_MMA_E2M1("2", "kind::mxf4.block_scale.scale_vec::2X");
+  else if (BLOCK16) ENGRAM_MMA_E2M1("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  else ENGRAM_MMA_E2M1("1", "kind::mxf4.block_scale.scale_vec::2X");
+#undef ENGRAM_MMA_E2M1
+}
+
 }  // namespace tc
 }  // namespace engram

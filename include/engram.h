@@ -588,6 +588,106 @@ int engram_grad_clip(const engram_tensor* tensors, int32_t n_tensors, int32_t no
                      float* norm, void* workspace, uint64_t workspace_bytes, engram_stream_t stream);
 
 /*
+ * Block-scaled values in 4 and 8 bits. The pages hold their tables as fp8 codes with block scales and name a 4-bit
+ * quantisation of activations (`fp4_act_quant`) without defining it; the calls below are those of the open microscaled
+ * formats, for the block's operands.
+ *
+ * 4 bits: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign bit), the code of an even column in its byte's low half, and
+ *   block 32: a UE8M0 scale, the smallest 2^e (e >= -127) with max |v| <= 6 * 2^e;
+ *   block 16: an E4M3 scale, max |v| / 6 to the nearest (448 at most); where that is 0 all codes are 0.
+ * 8 bits: E4M3 codes and a scale for each block of 32, 64 or 128 columns (a row's last block may be shorter), the
+ *   smallest 2^e (e >= -127) with max |v| <= 448 * 2^e.
+ * A code is the nearest to v / scale, ties to even, larger ones cut to the largest; the choice is that of exact
+ * arithmetic. A block that holds a NaN or an infinity has the scale NaN and codes of 0, and reads back as NaN.
+ *
+ * Scales of 4-bit rows lie row by row (tiled == 0: [rows][cols / block]) or in the tensor cores' order (tiled != 0):
+ * 512 bytes for each 128 rows and 4 * block columns, scale k of row r at
+ *   ((r / 128) * G + k / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + k % 4,   G = ceil(cols / (4 * block)).
+ * engram_tiled_scales says how many bytes that is (0 for a size that is refused). Scales of a row's last group
+ * past its columns are written as 0; those of rows past the last are not written.
+ *
+ * engram_quantize4
+ *   x         device: rows of cols values of x_type, x_stride values apart (16-byte aligned, x_stride a multiple of 8,
+ *             x_stride >= cols)
+ *   scale     a power of two (finite, positive): v = x / scale, so the codes stand for code * block scale * scale
+ *   codes     device uint8 [rows][cols / 2], 16-byte aligned, written;  scales  device bytes, 16-byte aligned, written
+ * engram_dequantize4: out [rows][cols] of out_type = round(code * block scale * scale), scale finite.
+ * cols a multiple of block (of 32 where tiled), 2^30 at most. rows == 0 is a no-op.
+ * engram_quantize8, engram_dequantize8: the same in 8 bits, without a factor and a tiled order; scales [rows][ceil(cols /
+ * block)] stored as scale_dtype (ENGRAM_SCALE_F32, _BF16 or _E8M0: the same powers of two), aligned to its width; cols
+ * a multiple of 8; codes [rows][cols], 16-byte aligned (a table for engram_lookup, where cols is a head_dim that block
+ * divides; a checkpoint for engram_gate_grad8).
+ * Errors: _INVALID (null, misaligned, negative rows, a stride below its row, unknown types, scale not a power of two),
+ * _UNSUPPORTED (block, cols, scale_dtype, rows * cols >= 2^42), _CUDA.
+ */
+uint64_t engram_tiled_scales(int64_t rows, int32_t cols, int32_t block);
+int engram_quantize4(const void* x, int64_t rows, int32_t cols, int64_t x_stride, int32_t x_type, int32_t block,
+                     float scale, int32_t tiled, uint8_t* codes, uint8_t* scales, engram_stream_t stream);
+int engram_dequantize4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols, int32_t block,
+                       float scale, int32_t tiled, void* out, int32_t out_type, engram_stream_t stream);
+int engram_quantize8(const void* x, int64_t rows, int32_t cols, int64_t x_stride, int32_t x_type, int32_t block,
+                     int32_t scale_dtype, uint8_t* codes, void* scales, engram_stream_t stream);
+int engram_dequantize8(const uint8_t* codes, const void* scales, int64_t rows, int32_t cols, int32_t block,
+                       int32_t scale_dtype, void* out, int32_t out_type, engram_stream_t stream);
+
+/*
+ * The lookup in a 4-bit table (engram-first/lookup page, `ParallelEngramEmbedding.forward` with 4-bit rows): codes
+ * Q [table_rows][dim / 2] (16-byte aligned) and row-by-row scales S [table_rows][dim / block], as engram_quantize4
+ * makes them.
+ *   engram_lookup4           out[t][c][k] = bf16(code * block scale * scale) of row idx[t * idx_stride + c]
+ *   engram_lookup4_operand   the rows as they stand, as the first operand of engram_project4: codes [T][n_cols * dim / 2],
+ *                            tiled scales of T rows of n_cols * dim columns
+ * An id outside [0, table_rows) gives a row of +0. idx as engram_embed; dim a multiple of block, ENGRAM_MAX_EMBED_DIM at
+ * most; for the operand n_cols * dim is a multiple of 32, 2^30 at most. Outputs 16-byte aligned. T == 0 is a no-op.
+ * Errors: _INVALID (null or misaligned, negative sizes, idx_stride < n_cols, scale not finite), _UNSUPPORTED (block,
+ * dim, T * n_cols >= 2^31), _CUDA.
+ */
+int engram_lookup4(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const uint8_t* Q,
+                   const uint8_t* S, int64_t table_rows, int32_t dim, int32_t block, float scale, uint16_t* out,
+                   engram_stream_t stream);
+int engram_lookup4_operand(const int64_t* idx, int64_t idx_stride, int64_t T, int32_t n_cols, const uint8_t* Q,
+                           const uint8_t* S, int64_t table_rows, int32_t dim, int32_t block, uint8_t* codes,
+                           uint8_t* scales, engram_stream_t stream);
+
+/*
+ * The `wkv` projection with both operands in 4 bits (blocks/stack-hashes page, `Engram.forward`, kv = wkv(rows)):
+ *   out[t][n] = bf16_rne(scale * sum_k a[t][k] * w[n][k])     a, w: code * block scale; fp32 accumulation
+ * on the tensor cores' block-scaled 4-bit rate (four times that of bf16).
+ *   a, a_scales  device uint8 [T][K / 2] and tiled scales (engram_quantize4 or engram_lookup4_operand); 16-byte aligned,
+ *                the scales on 128 bytes
+ *   w, w_scales  device uint8 [N][K / 2] and tiled scales, the same block
+ *   scale        finite: the product of the operands' factors
+ *   out          device bf16 [T][N], 16-byte aligned, written
+ * K a multiple of 32, N a multiple of 8 (>= 8), block 16 or 32. Codes and scales of rows past T and N are not used. A wait
+ * that does not end raises ENGRAM_STATUS_TIMEOUT (engram_device_status) instead of hanging. T == 0 is a no-op.
+ * Errors: _INVALID (null, misaligned, scale not finite), _UNSUPPORTED (block, K, N, T >= 2^31), _CUDA.
+ */
+int engram_project4(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales, int64_t T,
+                    int32_t K, int32_t N, int32_t block, float scale, uint16_t* out, engram_stream_t stream);
+
+/* Test hook of engram_project4's failure path (no counterpart in the pages), as engram_project_withhold: the
+ * completion of tile `tile` (counted from 0 per unit of work) is not signalled, so its epilogue's wait runs out. */
+int engram_project4_withhold(const uint8_t* a, const uint8_t* a_scales, const uint8_t* w, const uint8_t* w_scales,
+                             int64_t T, int32_t K, int32_t N, int32_t block, float scale, uint16_t* out, int32_t tile,
+                             engram_stream_t stream);
+
+/*
+ * engram_gate_grad from checkpoints in 8 bits: x and kv as engram_quantize8 left them in the forward pass (half the
+ * memory that bf16 takes until the backward pass), read as they are. The arithmetic is that of engram_gate_grad on the
+ * values that the checkpoints stand for (code * scale), its sums in an order of their own; the same inputs give the same bits.
+ *   x, x_scales    device E4M3 codes [T][hc][dim], UE8M0 scales [T][hc][ceil(dim / block)]
+ *   kv, kv_scales  device E4M3 codes [T][hc + 1][dim], UE8M0 scales [T][hc + 1][ceil(dim / block)]
+ *   block          32, 64 or 128;  dim a multiple of 16
+ * Everything else as engram_gate_grad (codes 16-byte aligned; workspace of engram_gate_grad8_workspace bytes).
+ */
+uint64_t engram_gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim);
+int engram_gate_grad8(const uint8_t* x, const uint8_t* x_scales, const uint8_t* kv, const uint8_t* kv_scales,
+                      int32_t block, const uint16_t* q_weight, const uint16_t* k_weight, const uint16_t* dout,
+                      const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps, uint16_t* dx, uint16_t* dkv,
+                      float* dq_weight, float* dk_weight, void* workspace, uint64_t workspace_bytes,
+                      engram_stream_t stream);
+
+/*
  * Set the L2 fetch granularity limit of the current device's context (cudaLimitMaxL2FetchGranularity:
  * the most bytes L2 fetches from DRAM for one missed sector, a hint; 0, 32, 64 or 128) and return the
  * previous value in *previous (may be NULL). Process-wide for that context and not stream-ordered:
