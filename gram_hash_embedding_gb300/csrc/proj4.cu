@@ -10,8 +10,8 @@
 //   are copied from shared into tensor memory by the thread that issues the MMAs (tcgen05.cp): 128 rows of A and all
 //   BN rows of B in each CTA of the pair.
 // - Tensor memory. Two accumulators of 256 columns leave no column for scales, so they overlap: columns [0, 256) and
-//   [192, 448), scales from 448 on. The epilogue reads the 64 shared columns of a tile first and then lets the next
-//   tile's MMAs start.
+//   [224, 480) (blocks of 32) or [192, 448), scales after them. The epilogue reads the 32 or 64 shared columns of a tile
+//   first and then lets the next tile's MMAs start.
 // Warp 0 loads, warp 1 issues, warps 2-5 are the epilogue. Every wait is bounded (tc_ptx.cuh): a wait that runs
 // out raises ENGRAM_STATUS_TIMEOUT, the CTA stops issuing, waits for its copies and MMAs in flight and exits.
 #include <cstdint>
@@ -34,7 +34,6 @@ constexpr int kGroup = 16;                 // 256-row blocks per tile group
 constexpr uint32_t kABytes = kBM * 128;    // A of a stage
 constexpr uint32_t kChunkBytes = 512;      // scales of 128 rows, four each
 constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;
-constexpr uint32_t kScaleCol = 448;        // first tensor-memory column of the scales
 
 template <bool NV, int BN>
 struct Cfg {
@@ -51,9 +50,12 @@ struct Cfg {
                                      ? (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes))
                                      : 8;
   static constexpr bool kOverlap = BN == 256;
-  static constexpr uint32_t kAcc1 = kOverlap ? 192 : BN;         // column of the second accumulator
+  // columns that the accumulators share: what the scales leave no room for, in chunks of 32
+  static constexpr int kShared = kOverlap ? (NV ? 64 : 32) : 0;
+  static constexpr uint32_t kAcc1 = BN - kShared;                // column of the second accumulator
   static constexpr uint32_t kSaCols = 4 * kChunks, kSbCols = 4 * kBBlocks;  // of a stage; of one group of B
-  static_assert(kScaleCol + kSaCols + kChunks * kSbCols <= 512 && kAcc1 + BN <= kScaleCol, "tensor memory");
+  static constexpr uint32_t kScaleCol = kAcc1 + BN;              // first column of the scales
+  static_assert(kScaleCol + kSaCols + kChunks * kSbCols <= 512, "tensor memory");
   // shared memory: operand ring, scale ring, output staging, barriers and words
   static constexpr uint32_t kScaleOff = kStages * kTileBytes;
   static constexpr uint32_t kEpiOff = kScaleOff + kStages * kStageScaleBytes;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto acc_full = [&](uint32_t a) { return bar(2 * S + (int)a); };
   auto acc_free = [&](uint32_t a) { return bar(2 * S + 2 + (int)a); };
   const uint32_t drain = bar(2 * S + 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;  // uniform in its warp
   const uint32_t q = tc::cluster_ctarank();
   const bool leader = q == 0;
   const int64_t unit = (int64_t)(blockIdx.x / 2), n_units = (int64_t)(gridDim.x / 2);
@@ -180,61 +182,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = issued - (issued < S ? issued : S); i < issued; ++i)
       if (!tc::mbar_wait(empty((uint32_t)(i % S)), (uint32_t)((i / S) & 1), nullptr))
         atomicOr(p.status, (unsigned)ENGRAM_STATUS_TIMEOUT);
-  } else if (warp == 1 && lane == 0 && leader) {
+  } else if (warp == 1 && leader) {
     // ---------------------------------------------------------------- MMA issuer
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     int32_t n = 0;
-    for (int64_t tile = unit; ok && tile < p.n_tiles && !*abort; tile += n_units, ++n) {
+    const uint32_t tile_lo = base >> 4, scale_lo = (base + C::kScaleOff) >> 4;  // of descriptors
+    for (int64_t tile = unit; ok && tile < p.n_tiles; tile += n_units, ++n) {
       const uint32_t acc = n & 1;
       // overlapping accumulators: the tile before must have left the shared columns (and then the one before it is
       // read in full); separate ones: the tile two before must be read
-      const bool free = C::kOverlap ? n == 0 || tc::mbar_wait(acc_free(acc ^ 1u), ((n - 1) >> 1) & 1, abort)
-                                    : tc::mbar_wait(acc_free(acc), ((n >> 1) & 1) ^ 1u, abort);
+      const bool free = C::kOverlap ? n == 0 || tc::warp_mbar_wait(acc_free(acc ^ 1u), ((n - 1) >> 1) & 1, abort)
+                                    : tc::warp_mbar_wait(acc_free(acc), ((n >> 1) & 1) ^ 1u, abort);
       if (!free) {
         raise_timeout(abort, p.status);
         break;
       }
       tc::fence_after_thread_sync();
       const uint32_t d = tmem + acc * C::kAcc1;
-      const uint32_t ta = tmem + kScaleCol, tb = ta + C::kSaCols;
+      const uint32_t ta = tmem + C::kScaleCol, tb = ta + C::kSaCols;
       for (int kb = 0; kb < p.num_kb; ++kb) {
-        if (!tc::mbar_wait(full(stage), phase, abort)) {
+        if (!tc::warp_mbar_wait(full(stage), phase, abort)) {
           raise_timeout(abort, p.status);
           ok = false;
           break;
         }
         tc::fence_after_thread_sync();
-        const uint32_t a0 = base + stage * C::kTileBytes, b0 = a0 + kABytes;
-        const uint32_t s0 = base + C::kScaleOff + stage * C::kStageScaleBytes;
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          tc::copy_scales<true>(ta + 4 * c, tc::scales_desc(s0 + c * kChunkBytes));
-#pragma unroll
-          for (int b = 0; b < C::kBBlocks; ++b)
-            tc::copy_scales<true>(tb + c * C::kSbCols + 4 * b, tc::scales_desc(s0 + C::kSaBytes * (1 + b) + c * kChunkBytes));
-        }
+        const uint32_t a0 = tile_lo + stage * (C::kTileBytes >> 4), b0 = a0 + (kABytes >> 4);
+        const uint32_t s0 = scale_lo + stage * (C::kStageScaleBytes >> 4);
         const int left = p.K - kb * kStageK;
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kMmas; ++k) {
-          if (k * kMmaK < left) {
-            const int c = NV ? k : k / 2;
-            tc::mma_e2m1<true, NV>(d, tc::sw128_kmajor_desc(a0 + 32 * k), tc::sw128_kmajor_desc(b0 + 32 * k),
-                                   tc::idesc_e2m1(2 * kBM, BN, !NV, NV ? 0u : (uint32_t)(k & 1)), ta + 4 * c,
-                                   tb + c * C::kSbCols, (kb | k) != 0 ? 1u : 0u);
+          for (int c = 0; c < C::kChunks; ++c) {
+            tc::copy_scales<true>(ta + 4 * c, tc::desc_of(s0 + 32 * c, tc::kScalesHi));
+#pragma unroll
+            for (int b = 0; b < C::kBBlocks; ++b)
+              tc::copy_scales<true>(tb + c * C::kSbCols + 4 * b,
+                                    tc::desc_of(s0 + (C::kSaBytes >> 4) * (1 + b) + 32 * c, tc::kScalesHi));
           }
+#pragma unroll
+          for (int k = 0; k < kMmas; ++k) {
+            if (k * kMmaK < left) {
+              const int c = NV ? k : k / 2;
+              tc::mma_e2m1<true, NV>(d, tc::desc_of(a0 + 2 * k, tc::kSw128Hi), tc::desc_of(b0 + 2 * k, tc::kSw128Hi),
+                                     tc::idesc_e2m1(2 * kBM, BN, !NV, NV ? 0u : (uint32_t)(k & 1)), ta + 4 * c,
+                                     tb + c * C::kSbCols, (kb | k) != 0 ? 1u : 0u);
+            }
+          }
+          tc::commit_pair_multicast(empty(stage), 3);
         }
-        tc::commit_pair_multicast(empty(stage), 3);
+        __syncwarp();
         if (++stage == S) {
           stage = 0;
           phase ^= 1u;
         }
       }
       if (!ok) break;
-      if (n != p.withhold) tc::commit_pair_multicast(acc_full(acc), 3);
+      if (n != p.withhold && tc::elect_one()) tc::commit_pair_multicast(acc_full(acc), 3);
+      __syncwarp();
     }
-    tc::commit_pair_multicast(drain, 1);
-    if (!tc::mbar_wait(drain, 0, nullptr)) atomicOr(p.status, (unsigned)ENGRAM_STATUS_TIMEOUT);
+    if (tc::elect_one()) tc::commit_pair_multicast(drain, 1);
+    __syncwarp();
+    if (!tc::warp_mbar_wait(drain, 0, nullptr)) atomicOr(p.status, (unsigned)ENGRAM_STATUS_TIMEOUT);
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3;  // tensor-memory lanes [32 * quarter, 32 * quarter + 32)
@@ -281,17 +290,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_free(acc), 0));
       };
-      constexpr int kChunksN = BN / 32;
-      // the columns that the next tile's accumulator shares come first: the last 64 of the first, the first of the second
-      const int first = C::kOverlap && acc == 0 ? kChunksN - 2 : 0;
+      constexpr int kChunksN = BN / 32, kFirst = C::kShared / 32;
+      // the columns that the next tile's accumulator shares come first: the last of the first, the first of the second
+      const int first = acc == 0 ? kChunksN - kFirst : 0;
       float v[32], w[32];
-      tc::tmem_load_32cols(taddr + 32 * first, v);
-      tc::tmem_load_32cols(taddr + 32 * (first + 1), w);
-      if (C::kOverlap) release();
-      put(v, nt * BN + 32 * first, row);
-      put(w, nt * BN + 32 * (first + 1), row);
+      if (C::kOverlap) {
+        tc::tmem_load_32cols(taddr + 32 * first, v);
+        if (kFirst > 1) tc::tmem_load_32cols(taddr + 32 * (first + 1), w);
+        release();
+        put(v, nt * BN + 32 * first, row);
+        if (kFirst > 1) put(w, nt * BN + 32 * (first + 1), row);
+      }
 #pragma unroll 1
-      for (int i = 2; i < kChunksN; ++i) {
+      for (int i = kFirst; i < kChunksN; ++i) {
         const int c = (first + i) % kChunksN;
         tc::tmem_load_32cols(taddr + 32 * c, v);
         put(v, nt * BN + 32 * c, row);

@@ -282,11 +282,31 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
 // them (32 bytes, as 16 bf16 values do). Each row's scales stand in tensor memory: row r of a block of 128 in lane
 // r % 32 of column r / 32, four bytes a column, the same in all four groups of 32 lanes.
 
-// Shared-memory descriptor of 512 bytes of scales, 32 rows of 16 bytes one after the other (8-row groups of 128 bytes, no
-// swizzling), as the copy into tensor memory reads them.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 32) |
-         (static_cast<uint64_t>(1) << 46);
+// Shared-memory descriptors as a low word, the address / 16 (14 bits; no leading-dimension offset), and a constant high
+// word: a loop that issues MMAs then adds to one 32-bit register instead of packing fields. kSw128Hi: a K-major operand
+// as sw128_kmajor_desc describes it. kScalesHi: 512 bytes of scales, 32 rows of 16 bytes one after the other (8-row
+// groups of 128 bytes, no swizzling), as the copy into tensor memory reads them.
+constexpr uint32_t kSw128Hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kScalesHi = (128u >> 4) | (1u << 14);
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// One lane of a converged warp. A loop that waits and issues runs in the whole warp and branches on this around what it
+// issues: the operands then stay in the warp's uniform registers. Block-scaled MMAs and copies of scales last 128 and
+// some 30 cycles, and issued from a loop of one thread (lane == 0) each took its operands through that thread's registers,
+// which was slower than the MMAs themselves (16,384 x 6,144 x 25,600: 1,182 us, now 746).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n"
+      ".reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n"
+      "}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
 // 512 bytes of scales from shared memory into 4 columns of tensor memory, written to all four groups of 32 lanes;
@@ -297,6 +317,11 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
   else
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// mbar_wait by a whole converged warp, with one answer for all its lanes
+__device__ __forceinline__ bool warp_mbar_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
 // Instruction descriptor of the block-scaled 4-bit kinds, both operands K-major. e8m0: scales are UE8M0, else
