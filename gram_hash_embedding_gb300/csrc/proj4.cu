@@ -34,6 +34,8 @@ constexpr int kGroup = 16;                 // 256-row blocks per tile group
 constexpr uint32_t kABytes = kBM * 128;    // A of a stage
 constexpr uint32_t kChunkBytes = 512;      // scales of 128 rows, four each
 constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;
+constexpr int kSms = 152;
+constexpr uint64_t kSettleNs = 100000;     // after a wait has run out: far longer than a load or an MMA takes
 
 template <bool NV, int BN>
 struct Cfg {
@@ -375,12 +377,248 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, to, p);
 }
 
+// ------------------------------------------------------------------------------------------------
+// Few tokens: the weights are all there is to read, so they take the rows of the MMAs (128 weight rows a CTA, TP >= T
+// token columns, cta_group::1) and no row of a tile is wasted on tokens that do not exist. Every CTA has one tile of 128
+// weight rows and, where the tiles alone are too few for the GPU, a part of K: the CTAs of a cluster split it, leave their
+// fp32 sums in shared memory and add them up in a fixed order, each for some of the tokens. All CTAs are resident at once
+// (3 or 2 an SM), so they share DRAM evenly whatever SM they are on.
+template <bool NV, int TP>
+struct Few {
+  static constexpr int kChunks = NV ? 4 : 2;
+  static constexpr uint32_t kScaleBytes = kChunks * kChunkBytes;    // of the weights' or the tokens' rows, a stage
+  static constexpr uint32_t kTileBytes = kABytes + TP * 128;        // weights, then tokens
+  static constexpr uint32_t kTxBytes = kTileBytes + 2 * kScaleBytes;
+  static constexpr int kStages = 3;
+  static constexpr uint32_t kAccCols = TP < 32 ? 32 : TP;           // columns are read 32 at a time
+  static constexpr uint32_t kSaCol = kAccCols, kSbCol = kSaCol + 4 * kChunks;
+  static constexpr uint32_t kTmemCols = kSbCol + 4 * kChunks <= 64 ? 64 : kSbCol + 4 * kChunks <= 128 ? 128 : 256;
+  static constexpr uint32_t kScaleOff = kStages * kTileBytes;
+  static constexpr uint32_t kBarOff = kScaleOff + kStages * 2 * kScaleBytes;  // full[S], empty[S], done
+  static constexpr uint32_t kTmemSlotOff = kBarOff + 8 * (2 * kStages + 1);
+  static constexpr uint32_t kAbortOff = kTmemSlotOff + 4;
+  static constexpr uint32_t kSmemBytes = kAbortOff + 4 + 1024;
+  static constexpr int kPerSm = 232448 / (kSmemBytes + 1024) < 512 / (int)kTmemCols ? 232448 / (kSmemBytes + 1024)
+                                                                                    : 512 / (int)kTmemCols;
+  static_assert(TP * 128 * 4 <= kStages * kTileBytes, "the sums take the operands' place");
+  static_assert(kSbCol + 4 * kChunks <= kTmemCols && kPerSm >= 2, "tensor memory");
+};
+
+template <bool NV, int TP>
+__global__ void __launch_bounds__(kThreads)
+    project4_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+                        const __grid_constant__ CUtensorMap tmSw, const __grid_constant__ CUtensorMap tmSt,
+                        const Params p, uint16_t* __restrict__ out, const int split) {
+  using C = Few<NV, TP>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = tc::smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // the same offset in every CTA of a cluster
+  uint8_t* gbase = smem_raw + (base - raw);
+  volatile int* abort = reinterpret_cast<volatile int*>(gbase + C::kAbortOff);
+  const uint32_t* tmem_slot = reinterpret_cast<const uint32_t*>(gbase + C::kTmemSlotOff);
+  auto full = [&](uint32_t s) { return base + C::kBarOff + 8u * s; };
+  auto empty = [&](uint32_t s) { return base + C::kBarOff + 8u * (S + s); };
+  const uint32_t done = base + C::kBarOff + 16u * S;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = split > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int32_t tile = (int32_t)(blockIdx.x / split);
+  const int kb0 = (int)((int64_t)p.num_kb * rank / split), kb1 = (int)((int64_t)p.num_kb * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < S; ++s) {
+      tc::mbar_init(full(s), 1);
+      tc::mbar_init(empty(s), 1);
+    }
+    tc::mbar_init(done, 1);
+    *abort = 0;
+    tc::fence_barrier_init();
+    tc::tma_prefetch_descriptor(&tmW);
+    tc::tma_prefetch_descriptor(&tmT);
+    tc::tma_prefetch_descriptor(&tmSw);
+    tc::tma_prefetch_descriptor(&tmSt);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 1) {
+    tc::tmem_alloc(base + C::kTmemSlotOff, C::kTmemCols);
+    tc::tmem_relinquish_alloc_permit();
+  }
+  tc::fence_before_thread_sync();
+  __syncthreads();
+  tc::fence_after_thread_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loader
+    if (lane == 0) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint32_t i = (uint32_t)(kb - kb0), stage = i % S;
+        if (!tc::mbar_wait(empty(stage), ((i / S) & 1u) ^ 1u, abort)) {
+          raise_timeout(abort, p.status);
+          break;
+        }
+        const uint32_t dst = base + stage * C::kTileBytes, sdst = base + C::kScaleOff + stage * 2 * C::kScaleBytes;
+        tc::mbar_arrive_expect_tx(full(stage), C::kTxBytes);
+        tc::tma_load_2d(dst, &tmW, full(stage), kb * (kStageK / 2), tile * 128);
+        tc::tma_load_2d(sdst, &tmSw, full(stage), 0, tile * p.groups + kb * C::kChunks);
+        tc::tma_load_2d(dst + kABytes, &tmT, full(stage), kb * (kStageK / 2), 0);
+        tc::tma_load_2d(sdst + C::kScaleBytes, &tmSt, full(stage), 0, kb * C::kChunks);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t ta = tmem + C::kSaCol, tb = tmem + C::kSbCol;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t i = (uint32_t)(kb - kb0), stage = i % S;
+      if (!tc::warp_mbar_wait(full(stage), (i / S) & 1u, abort)) {
+        raise_timeout(abort, p.status);
+        break;
+      }
+      tc::fence_after_thread_sync();
+      const uint32_t a0 = (base + stage * C::kTileBytes) >> 4, b0 = a0 + (kABytes >> 4);
+      const uint32_t s0 = (base + C::kScaleOff + stage * 2 * C::kScaleBytes) >> 4;
+      const int left = p.K - kb * kStageK;
+      if (tc::elect_one()) {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          tc::copy_scales<false>(ta + 4 * c, tc::desc_of(s0 + 32 * c, tc::kScalesHi));
+          tc::copy_scales<false>(tb + 4 * c, tc::desc_of(s0 + (C::kScaleBytes >> 4) + 32 * c, tc::kScalesHi));
+        }
+#pragma unroll
+        for (int k = 0; k < kMmas; ++k) {
+          if (k * kMmaK < left) {
+            const int c = NV ? k : k / 2;
+            tc::mma_e2m1<false, NV>(tmem, tc::desc_of(a0 + 2 * k, tc::kSw128Hi), tc::desc_of(b0 + 2 * k, tc::kSw128Hi),
+                                    tc::idesc_e2m1(kBM, TP, !NV, NV ? 0u : (uint32_t)(k & 1)), ta + 4 * c, tb + 4 * c,
+                                    ((kb - kb0) | k) != 0 ? 1u : 0u);
+          }
+        }
+        tc::commit(empty(stage));
+      }
+      __syncwarp();
+    }
+    // Every MMA issued has completed, and with it every load that was waited for. After a wait that ran out loads may
+    // still be landing: those of the stages filled and not consumed.
+    if (rank != 0 || p.withhold != 0) {
+      if (tc::elect_one()) tc::commit(done);
+    }
+    __syncwarp();
+  }
+  // the sums, one weight row a thread, take the place of the operands
+  float* sums = reinterpret_cast<float*>(gbase);  // [T][128]
+  if (warp >= 2) {
+    const int quarter = warp & 3;
+    if (tc::warp_mbar_wait(done, 0, abort)) {
+      tc::fence_after_thread_sync();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < TP; c += 32) {
+        if (c >= p.T) break;
+        float v[32];
+        tc::tmem_load_32cols(taddr + c, v);
+#pragma unroll
+        for (int t = 0; t < 32; ++t)
+          if (c + t < p.T && t < TP) sums[(c + t) * 128 + quarter * 32 + lane] = v[t];
+      }
+    } else {
+      raise_timeout(abort, p.status);
+    }
+  }
+  tc::fence_before_thread_sync();
+  if (split > 1) tc::cluster_sync();
+  else __syncthreads();
+  const int64_t n = (int64_t)tile * 128 + 4 * lane;
+  if (!*abort && n < p.N) {
+    for (int t = rank * (kThreads / 32) + warp; t < p.T; t += split * (kThreads / 32)) {
+      const uint32_t at = base + (uint32_t)(t * 512 + lane * 16);
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < split; ++r) {
+        const float4 v = split > 1 ? tc::ld_cluster_v4(tc::map_to_rank(at, (uint32_t)r))
+                                   : *reinterpret_cast<const float4*>(sums + t * 128 + lane * 4);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+      }
+      *reinterpret_cast<uint2*>(out + (int64_t)t * p.N + n) =
+          make_uint2(tc::f32x2_to_bf16x2(s.x * p.scale, s.y * p.scale), tc::f32x2_to_bf16x2(s.z * p.scale, s.w * p.scale));
+    }
+  }
+  if (*abort) {  // loads and MMAs may still be in flight: let them end before the memory is given up
+    const uint64_t t0 = tc::global_timer_ns();
+    while (tc::global_timer_ns() - t0 < kSettleNs) {}
+  }
+  if (split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
+  else __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <bool NV, int TP>
+cudaError_t launch_few(const Project4Args& a, cudaStream_t s, int32_t withhold) {
+  using C = Few<NV, TP>;
+  Params p = {};
+  p.T = a.T;
+  p.K = a.K;
+  p.N = a.N;
+  p.num_kb = (a.K + kStageK - 1) / kStageK;
+  p.n_ntile = (a.N + 127) / 128;
+  p.groups = (int32_t)scale_groups(a.K, a.block);
+  p.scale = a.scale;
+  p.withhold = withhold;
+  cudaError_t e = device_status_word(&p.status);
+  if (e != cudaSuccess) return e;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, i32 = CU_TENSOR_MAP_DATA_TYPE_INT32;
+  const uint64_t kb = (uint64_t)a.K / 2;
+  CUtensorMap tw, tt, tsw, tst;
+  if (!tensor_map_2d(&tw, u8, a.w, (uint64_t)a.N, kb, kb, 128, 128, sw) ||
+      !tensor_map_2d(&tt, u8, a.a, (uint64_t)a.T, kb, kb, TP, 128, sw) ||
+      !tensor_map_2d(&tsw, i32, a.ws, (uint64_t)p.n_ntile * p.groups, 128, 512, C::kChunks, 128, none) ||
+      !tensor_map_2d(&tst, i32, a.as, (uint64_t)p.groups, 128, 512, C::kChunks, 128, none))
+    return cudaErrorInvalidValue;
+  auto kern = project4_few_kernel<NV, TP>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  // the longest split of K that leaves every CTA a stage and all of them resident
+  int split = 8;
+  while (split > 1 && (split > p.num_kb || (int64_t)p.n_ntile * split > (int64_t)kSms * C::kPerSm)) split /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = ENGRAM_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  cfg.gridDim = dim3((unsigned)(p.n_ntile * split));
+  return cudaLaunchKernelEx(&cfg, kern, tw, tt, tsw, tst, p, a.out, split);
+}
+
+template <bool NV>
+cudaError_t launch_kind(const Project4Args& a, cudaStream_t s, int32_t withhold) {
+  if (a.T <= 16) return launch_few<NV, 16>(a, s, withhold);
+  if (a.T <= 32) return launch_few<NV, 32>(a, s, withhold);
+  if (a.T <= 64) return launch_few<NV, 64>(a, s, withhold);
+  if (a.T <= 128) return launch_few<NV, 128>(a, s, withhold);
+  // wide tiles, unless narrow ones fill the waves of pairs better
+  auto waves = [&](int64_t bn) { return ((a.T + 255) / 256 * ((a.N + bn - 1) / bn) + kSms / 2 - 1) / (kSms / 2) * bn; };
+  return waves(128) * 10 < waves(256) * 9 ? launch_pairs<NV, 128>(a, s, withhold) : launch_pairs<NV, 256>(a, s, withhold);
+}
+
 }  // namespace
 
 cudaError_t launch_project4(const Project4Args& a, cudaStream_t s, int32_t withhold) {
-  const int64_t wide = (a.T + 255) / 256 * ((a.N + 255) / 256);
-  if (wide < 76) return a.block == 16 ? launch_pairs<true, 128>(a, s, withhold) : launch_pairs<false, 128>(a, s, withhold);
-  return a.block == 16 ? launch_pairs<true, 256>(a, s, withhold) : launch_pairs<false, 256>(a, s, withhold);
+  return a.block == 16 ? launch_kind<true>(a, s, withhold) : launch_kind<false>(a, s, withhold);
 }
 
 }  // namespace engram

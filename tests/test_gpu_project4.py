@@ -58,7 +58,13 @@ SHAPES = [
     (1, 32, 8),         # the smallest
     (1, 6144, 520),     # one token
     (2, 96, 1000),      # K over one and a half MMAs
+    (16, 2080, 3000),   # few tokens: K split over the CTAs of a cluster, in odd parts
+    (17, 6144, 136),
     (33, 288, 264),     # K past one stage by half an MMA
+    (64, 768, 25608),   # more row blocks of w than CTAs fit at once
+    (65, 1120, 4000),
+    (129, 512, 1000),
+    (200, 2048, 9000),
     (300, 544, 520),    # ragged everywhere
     (257, 1024, 2056),
     (1000, 3 * 256, 1032),
