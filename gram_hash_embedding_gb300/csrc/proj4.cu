@@ -12,8 +12,9 @@
 // - Tensor memory. Two accumulators of 256 columns leave no column for scales, so they overlap: columns [0, 256) and
 //   [224, 480) (blocks of 32) or [192, 448), scales after them. The epilogue reads the 32 or 64 shared columns of a tile
 //   first and then lets the next tile's MMAs start.
-// Warp 0 loads, warp 1 issues, warps 2-5 are the epilogue. Every wait is bounded (tc_ptx.cuh): a wait that runs
+// Warp 0 loads, warp 1 issues, warps 2-9 are the epilogue. Every wait is bounded (tc_ptx.cuh): a wait that runs
 // out raises ENGRAM_STATUS_TIMEOUT, the CTA stops issuing, waits for its copies and MMAs in flight and exits.
+#include <algorithm>
 #include <cstdint>
 
 #include "engram_internal.cuh"
@@ -29,7 +30,7 @@ constexpr int kBM = 128;                   // tile rows of one CTA (tokens)
 constexpr int kStageK = 256;               // values of K a stage: one 128-byte swizzle row
 constexpr int kMmaK = 64;                  // values of K an MMA
 constexpr int kMmas = kStageK / kMmaK;     // MMAs a stage
-constexpr int kThreads = 192;              // 6 warps: loader, MMA, 4 epilogue
+constexpr int kThreads = 192;              // few tokens: loader, MMA, 4 epilogue warps
 constexpr int kGroup = 16;                 // 256-row blocks per tile group
 constexpr uint32_t kABytes = kBM * 128;    // A of a stage
 constexpr uint32_t kChunkBytes = 512;      // scales of 128 rows, four each
@@ -37,26 +38,32 @@ constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;
 constexpr int kSms = 152;
 constexpr uint64_t kSettleNs = 100000;     // after a wait has run out: far longer than a load or an MMA takes
 
-template <bool NV, int BN>
+// EW: epilogue warps, one or two for each quarter of the tensor-memory lanes
+template <bool NV, int BN, int EW>
 struct Cfg {
+  static constexpr int kThreads = 64 + 32 * EW;
   static constexpr int kChunks = NV ? 4 : 2;                     // groups of four scales in a stage's K
   static constexpr int kBBlocks = BN / 128;                      // blocks of 128 rows of B
   static constexpr uint32_t kBBytes = (BN / 2) * 128;            // this CTA's half of B
+  static constexpr int kBBox = BN > 256 ? (BN - 256) / 2 : BN / 2;  // rows of B a load
   static constexpr uint32_t kSaBytes = kChunks * kChunkBytes;
   static constexpr uint32_t kSbBytes = kBBlocks * kSaBytes;
   static constexpr uint32_t kTileBytes = kABytes + kBBytes;      // 1024-byte multiples
   static constexpr uint32_t kStageScaleBytes = kSaBytes + kSbBytes;
   static constexpr uint32_t kTxBytes = 2 * (kTileBytes + kStageScaleBytes);  // both CTAs of the pair
-  static constexpr uint32_t kEpiBytes = 4 * 2 * kEpiChunkBytes;
+  static constexpr uint32_t kEpiBytes = EW * 2 * kEpiChunkBytes;
   static constexpr int kStages = (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes)) < 8
                                      ? (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes))
                                      : 8;
+  // widths of the MMAs that make up a tile's columns, and accumulators: two that overlap, two apart, or one
+  static constexpr int kN0 = BN < 256 ? BN : 256, kN1 = BN - kN0;
   static constexpr bool kOverlap = BN == 256;
+  static constexpr int kAccs = BN > 256 ? 1 : 2;
   // columns that the accumulators share: what the scales leave no room for, in chunks of 32
   static constexpr int kShared = kOverlap ? (NV ? 64 : 32) : 0;
   static constexpr uint32_t kAcc1 = BN - kShared;                // column of the second accumulator
   static constexpr uint32_t kSaCols = 4 * kChunks, kSbCols = 4 * kBBlocks;  // of a stage; of one group of B
-  static constexpr uint32_t kScaleCol = kAcc1 + BN;              // first column of the scales
+  static constexpr uint32_t kScaleCol = kAccs == 2 ? kAcc1 + BN : BN;  // first column of the scales
   static_assert(kScaleCol + kSaCols + kChunks * kSbCols <= 512, "tensor memory");
   // shared memory: operand ring, scale ring, output staging, barriers and words
   static constexpr uint32_t kScaleOff = kStages * kTileBytes;
@@ -95,12 +102,12 @@ __device__ __forceinline__ void raise_timeout(volatile int* abort, unsigned int*
   atomicOr(status, (unsigned)ENGRAM_STATUS_TIMEOUT);
 }
 
-template <bool NV, int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool NV, int BN, int EW>
+__global__ void __launch_bounds__(64 + 32 * EW, 1)
     project4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
                     const __grid_constant__ CUtensorMap tmO, const Params p) {
-  using C = Cfg<NV, BN>;
+  using C = Cfg<NV, BN, EW>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -126,7 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(acc_full(a), 1);
-      tc::mbar_init(acc_free(a), 8);  // one arrival per epilogue warp of the pair
+      tc::mbar_init(acc_free(a), 2 * EW);  // one arrival per epilogue warp of the pair
     }
     tc::mbar_init(drain, 1);
     *abort = 0;
@@ -155,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t tile = unit; tile < p.n_tiles && !*abort; tile += n_units) {
       int32_t mt, nt;
       tile_coords(p, tile, mt, nt);
-      const int32_t arow = (mt * 2 + (int32_t)q) * kBM, brow = nt * BN + (int32_t)q * (BN / 2);
+      // a CTA holds its half of the columns of each of the tile's MMAs
+      const int32_t arow = (mt * 2 + (int32_t)q) * kBM, brow = nt * BN + (int32_t)q * (C::kN0 / 2);
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!tc::mbar_wait(empty(stage), phase ^ 1u, abort)) {
           raise_timeout(abort, p.status);
@@ -166,7 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t fb = tc::map_to_rank(full(stage), 0);
         if (leader) tc::mbar_arrive_expect_tx(full(stage), C::kTxBytes);
         tc::tma_load_2d_pair(a_dst, &tmA, fb, kb * (kStageK / 2), arow);
-        tc::tma_load_2d_pair(a_dst + kABytes, &tmB, fb, kb * (kStageK / 2), brow);
+#pragma unroll
+        for (int b = 0; b < C::kN0 / 2; b += C::kBBox)
+          tc::tma_load_2d_pair(a_dst + kABytes + b * 128, &tmB, fb, kb * (kStageK / 2), brow + b);
+#pragma unroll
+        for (int b = 0; b < C::kN1 / 2; b += C::kBBox)
+          tc::tma_load_2d_pair(a_dst + kABytes + (C::kN0 / 2 + b) * 128, &tmB, fb, kb * (kStageK / 2),
+                               nt * BN + C::kN0 + (int32_t)q * (C::kN1 / 2) + b);
         // past a row's last group a box reads the next rows' groups, which no MMA uses
         tc::tma_load_2d_pair(s_dst, &tmSa, fb, 0, (mt * 2 + (int32_t)q) * p.groups + kb * C::kChunks);
 #pragma unroll
@@ -191,11 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int32_t n = 0;
     const uint32_t tile_lo = base >> 4, scale_lo = (base + C::kScaleOff) >> 4;  // of descriptors
     for (int64_t tile = unit; ok && tile < p.n_tiles; tile += n_units, ++n) {
-      const uint32_t acc = n & 1;
+      const uint32_t acc = C::kAccs == 2 ? n & 1 : 0;
       // overlapping accumulators: the tile before must have left the shared columns (and then the one before it is
-      // read in full); separate ones: the tile two before must be read
+      // read in full); separate ones: the tile two before must be read; a single one: the tile before
       const bool free = C::kOverlap ? n == 0 || tc::warp_mbar_wait(acc_free(acc ^ 1u), ((n - 1) >> 1) & 1, abort)
-                                    : tc::warp_mbar_wait(acc_free(acc), ((n >> 1) & 1) ^ 1u, abort);
+                                    : tc::warp_mbar_wait(acc_free(acc), ((n / C::kAccs) & 1) ^ 1u, abort);
       if (!free) {
         raise_timeout(abort, p.status);
         break;
@@ -226,9 +240,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kMmas; ++k) {
             if (k * kMmaK < left) {
               const int c = NV ? k : k / 2;
+              const uint32_t half = NV ? 0u : (uint32_t)(k & 1), more = (kb | k) != 0 ? 1u : 0u;
               tc::mma_e2m1<true, NV>(d, tc::desc_of(a0 + 2 * k, tc::kSw128Hi), tc::desc_of(b0 + 2 * k, tc::kSw128Hi),
-                                     tc::idesc_e2m1(2 * kBM, BN, !NV, NV ? 0u : (uint32_t)(k & 1)), ta + 4 * c,
-                                     tb + c * C::kSbCols, (kb | k) != 0 ? 1u : 0u);
+                                     tc::idesc_e2m1(2 * kBM, C::kN0, !NV, half), ta + 4 * c, tb + c * C::kSbCols, more);
+              if (C::kN1 > 0)
+                tc::mma_e2m1<true, NV>(d + C::kN0, tc::desc_of(a0 + 2 * k, tc::kSw128Hi),
+                                       tc::desc_of(b0 + C::kN0 / 2 * 8 + 2 * k, tc::kSw128Hi),
+                                       tc::idesc_e2m1(2 * kBM, C::kN1 > 0 ? C::kN1 : 128, !NV, half), ta + 4 * c,
+                                       tb + c * C::kSbCols + C::kN0 / 32, more);
             }
           }
           tc::commit_pair_multicast(empty(stage), 3);
@@ -249,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 2) {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int quarter = warp & 3;  // tensor-memory lanes [32 * quarter, 32 * quarter + 32)
-    const uint32_t staging = base + C::kEpiOff + (uint32_t)quarter * 2u * kEpiChunkBytes;
+    const int part = (warp - 2) >> 2;  // the warp's share of the columns: every other chunk of 32
+    const uint32_t staging = base + C::kEpiOff + (uint32_t)(warp - 2) * 2u * kEpiChunkBytes;
     int32_t n = 0, sent = 0;
     // 32 columns of the warp's 32 rows: scaled, rounded, through a swizzled chunk of shared memory, out by TMA
     auto put = [&](const float (&v)[32], int col, int32_t row) {
@@ -275,12 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     for (int64_t tile = unit; tile < p.n_tiles; tile += n_units, ++n) {
-      const uint32_t acc = n & 1;
+      const uint32_t acc = C::kAccs == 2 ? n & 1 : 0;
       int32_t mt, nt;
       tile_coords(p, tile, mt, nt);
       int ok = 1;
       if (lane == 0) {
-        ok = tc::mbar_wait(acc_full(acc), (n >> 1) & 1, abort) ? 1 : 0;
+        ok = tc::mbar_wait(acc_full(acc), (n / C::kAccs) & 1, abort) ? 1 : 0;
         if (!ok) raise_timeout(abort, p.status);
       }
       if (__shfl_sync(0xffffffffu, ok, 0) == 0) break;
@@ -292,24 +312,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_free(acc), 0));
       };
-      constexpr int kChunksN = BN / 32, kFirst = C::kShared / 32;
+      constexpr int kChunksN = BN / 32, kParts = EW / 4;
+      static_assert(kChunksN % kParts == 0, "columns");
+      constexpr int kFirst = C::kShared / 32;  // shared chunks
       // the columns that the next tile's accumulator shares come first: the last of the first, the first of the second
-      const int first = acc == 0 ? kChunksN - kFirst : 0;
-      float v[32], w[32];
-      if (C::kOverlap) {
-        tc::tmem_load_32cols(taddr + 32 * first, v);
-        if (kFirst > 1) tc::tmem_load_32cols(taddr + 32 * (first + 1), w);
-        release();
-        put(v, nt * BN + 32 * first, row);
-        if (kFirst > 1) put(w, nt * BN + 32 * (first + 1), row);
-      }
+      const int first = C::kOverlap && acc == 0 ? kChunksN - C::kShared / 32 : 0;
 #pragma unroll 1
-      for (int i = kFirst; i < kChunksN; ++i) {
+      for (int i = part; i < kChunksN; i += kParts) {
         const int c = (first + i) % kChunksN;
+        float v[32];
         tc::tmem_load_32cols(taddr + 32 * c, v);
+        // the part's last shared chunk has been read (or its first, where the other part has the shared one), or the last
+        if (i == part + (C::kOverlap ? (kFirst > kParts ? kFirst - kParts : 0) : kChunksN - kParts)) release();
         put(v, nt * BN + 32 * c, row);
       }
-      if (!C::kOverlap) release();
     }
     if (lane == 0) tc::bulk_wait_group_0();
     __syncwarp();
@@ -325,9 +341,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool NV, int BN>
+template <bool NV, int BN, int EW>
 cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold) {
-  using C = Cfg<NV, BN>;
+  using C = Cfg<NV, BN, EW>;
   Params p = {};
   p.T = a.T;
   p.K = a.K;
@@ -346,13 +362,13 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
   const uint64_t kb = (uint64_t)a.K / 2;
   CUtensorMap ta, tb, tsa, tsb, to;
   if (!tensor_map_2d(&ta, u8, a.a, (uint64_t)a.T, kb, kb, kBM, 128, sw) ||
-      !tensor_map_2d(&tb, u8, a.w, (uint64_t)a.N, kb, kb, BN / 2, 128, sw) ||
+      !tensor_map_2d(&tb, u8, a.w, (uint64_t)a.N, kb, kb, (uint32_t)C::kBBox, 128, sw) ||
       !tensor_map_2d(&tsa, i32, a.as, (uint64_t)((a.T + 127) / 128) * p.groups, 128, 512, C::kChunks, 128, none) ||
       !tensor_map_2d(&tsb, i32, a.ws, (uint64_t)((a.N + 127) / 128) * p.groups, 128, 512, C::kChunks, 128, none) ||
       !tensor_map_2d(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.T, (uint64_t)a.N, (uint64_t)a.N * 2, 32, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  auto kern = project4_kernel<NV, BN>;
+  auto kern = project4_kernel<NV, BN, EW>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -363,7 +379,7 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -610,9 +626,17 @@ cudaError_t launch_kind(const Project4Args& a, cudaStream_t s, int32_t withhold)
   if (a.T <= 32) return launch_few<NV, 32>(a, s, withhold);
   if (a.T <= 64) return launch_few<NV, 64>(a, s, withhold);
   if (a.T <= 128) return launch_few<NV, 128>(a, s, withhold);
-  // wide tiles, unless narrow ones fill the waves of pairs better
-  auto waves = [&](int64_t bn) { return ((a.T + 255) / 256 * ((a.N + bn - 1) / bn) + kSms / 2 - 1) / (kSms / 2) * bn; };
-  return waves(128) * 10 < waves(256) * 9 ? launch_pairs<NV, 128>(a, s, withhold) : launch_pairs<NV, 256>(a, s, withhold);
+  // wide tiles, unless narrow ones fill the waves of pairs better, or tiles of 384 columns are few enough for one wave
+  // (256 tokens of N = 25,600: 67 of them instead of 100)
+  const int64_t rows = (a.T + 255) / 256, pairs = kSms / 2;
+  auto waves = [&](int64_t bn) { return (rows * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * bn; };
+  // Two epilogue warps a lane quarter where a tile has little K to hide them behind or nothing overlaps them (16,384 x
+  // 1,024 x 5,120: 57 us against 62; of K = 6,144 one is 3% faster)
+  const bool two = a.K <= 1024;
+  if (waves(128) <= 128 || waves(128) * 10 < std::min(waves(256), waves(384)) * 9)
+    return two ? launch_pairs<NV, 128, 8>(a, s, withhold) : launch_pairs<NV, 128, 4>(a, s, withhold);
+  if (waves(384) == 384 && waves(256) > 256) return launch_pairs<NV, 384, 8>(a, s, withhold);
+  return two ? launch_pairs<NV, 256, 8>(a, s, withhold) : launch_pairs<NV, 256, 4>(a, s, withhold);
 }
 
 }  // namespace

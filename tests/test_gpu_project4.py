@@ -65,6 +65,8 @@ SHAPES = [
     (65, 1120, 4000),
     (129, 512, 1000),
     (200, 2048, 9000),
+    (200, 544, 20008),  # one wave of the widest tiles
+    (300, 96, 12008),
     (300, 544, 520),    # ragged everywhere
     (257, 1024, 2056),
     (1000, 3 * 256, 1032),
