@@ -1025,44 +1025,55 @@ def engram_gate_grad(x: torch.Tensor, kv: torch.Tensor, q_weight: torch.Tensor, 
 
 
 # ----------------------------------------------------------------------------- low-bit operators
+# As with the training operators, Python's share is most of a small call: one check for each tensor that the caller
+# gives, none for those made here.
 _E8M0 = getattr(torch, "float8_e8m0fnu", torch.uint8)
-_SCALE4_DTYPE = {32: _E8M0, 16: torch.float8_e4m3fn}  # by the block's length
+_E4M3 = torch.float8_e4m3fn
+_SCALE4_DTYPE = {32: _E8M0, 16: _E4M3}  # by the block's length
 _SCALE8_DTYPE = {SCALE_F32: torch.float32, SCALE_BF16: torch.bfloat16, SCALE_E8M0: _E8M0}
+_U8 = torch.uint8
 
 
-def _bytes(t: torch.Tensor, n: int, name: str, dtypes=(torch.uint8,)) -> int:
-    """The pointer of a contiguous CUDA tensor of n one-byte values of uint8 or one of `dtypes`."""
-    if not isinstance(t, torch.Tensor) or (t.dtype is not torch.uint8 and t.dtype not in dtypes):
-        raise TypeError(f"{name} must be uint8{''.join(f' or {d}' for d in dtypes if d is not torch.uint8)}, got "
+def _bytes(t: torch.Tensor, n: int, name: str, dtype: torch.dtype = torch.uint8) -> int:
+    """The pointer of a contiguous CUDA tensor of n one-byte values, uint8 or `dtype`."""
+    try:
+        if (t.dtype is _U8 or t.dtype is dtype) and t.is_cuda and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or (t.dtype is not _U8 and t.dtype is not dtype):
+        raise TypeError(f"{name} must be {_U8}{'' if dtype is _U8 else f' or {dtype}'}, got "
                         f"{getattr(t, 'dtype', type(t).__name__)}")
     _size(t, n, name)
     return _dev(t, t.dtype, name)
 
 
-def _block4(block: int) -> int:
+def _block4(block: int) -> torch.dtype:
+    """The storage type of the scales of blocks of that length."""
     if block not in _SCALE4_DTYPE:
         raise ValueError(f"block must be 32 (UE8M0 scales) or 16 (E4M3 scales), got {block}")
-    return block
+    return _SCALE4_DTYPE[block]
 
 
-def _block8(block: int) -> int:
+def _block8(block: int) -> None:
     if block not in (32, 64, 128):
         raise ValueError(f"block must be 32, 64 or 128, got {block}")
-    return block
 
 
-def _rows_view(x: torch.Tensor, name: str):
-    """x [..., cols] as rows: (pointer, rows, cols, row stride); contiguous, or [rows, cols] with rows a stride apart."""
-    if x.dim() < 1 or x.shape[-1] == 0:
-        raise ValueError(f"{name} must be [..., cols], got {tuple(x.shape)}")
-    cols = _narrow(x.shape[-1], f"the width of {name}")
-    rows = x.numel() // cols
+def _rows_view(x: torch.Tensor, unit: int):
+    """x [..., cols] as rows, cols a multiple of `unit`: (shape, rows, cols, row stride); contiguous, or [rows, cols]
+    with rows a stride apart."""
+    shape = x.shape
+    cols = shape[-1] if shape else 0
+    if cols == 0 or cols % unit:
+        raise ValueError(f"x must be [..., cols] with cols a multiple of {unit}, got {tuple(shape)}")
+    rows = x.numel() // _narrow(cols, "the width of x")
     if x.is_contiguous():
-        return x.data_ptr(), rows, cols, cols
-    if x.dim() != 2 or (cols > 1 and x.stride(1) != 1) or (rows > 1 and x.stride(0) < cols):
-        raise ValueError(f"{name} must be contiguous, or [rows, cols] with only its rows a stride apart, got shape "
-                         f"{tuple(x.shape)} strides {x.stride()}")
-    return x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols
+        return shape, rows, cols, cols
+    if len(shape) != 2 or x.stride(1) != 1 or (rows > 1 and x.stride(0) < cols):
+        raise ValueError(f"x must be contiguous, or [rows, cols] with only its rows a stride apart, got shape "
+                         f"{tuple(shape)} strides {x.stride()}")
+    return shape, rows, cols, x.stride(0) if rows > 1 else cols
 
 
 def engram_tiled_scales(rows: int, cols: int, block: int) -> int:
@@ -1070,15 +1081,28 @@ def engram_tiled_scales(rows: int, cols: int, block: int) -> int:
     return int(_lib().engram_tiled_scales(int(rows), int(cols), int(block)))
 
 
-def _tiled_shape(rows: int, cols: int, block: int) -> tuple:
-    return -(-rows // 128), -(-cols // (4 * block)), 512
+def _tiled_size(rows: int, cols: int, block: int) -> int:
+    return -(-rows // 128) * -(-cols // (4 * block)) * 512
 
 
-def _scales4_size(rows: int, cols: int, block: int, tiled: bool) -> int:
-    if tiled:
-        a, b, c = _tiled_shape(rows, cols, block)
-        return a * b * c
-    return rows * (cols // block)
+def _stream_on(t: torch.Tensor, stream, temps) -> int:
+    """The stream handle of a call on t's memory, which has to be the current device's: launched from another device's
+    stream, the call's pointers would be foreign to it."""
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _launch_stream(stream, temps)
+
+
+def _float_out(out, out_dtype, n: int):
+    """A caller's output of n values of a float type: (type, pointer)."""
+    t = _float_type(out, "out")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    _size(out, n, "out")
+    return t, _dev(out, out.dtype, "out")
 
 
 def engram_quantize4(x: torch.Tensor, block: int = 32, scale: float = 1.0, tiled: bool = False,
@@ -1088,58 +1112,66 @@ def engram_quantize4(x: torch.Tensor, block: int = 32, scale: float = 1.0, tiled
     (32: float8_e8m0fnu) or an E4M3 number (16: float8_e4m3fn). code * block scale * scale stands for x; `scale` is a
     power of two. The scales are [..., cols / block], or with `tiled` in the order engram_project4 reads them
     ([rows / 128, groups of four scales, 512], rounded up; rows past the last are not written). Returns (or fills) codes, scales."""
-    _block4(block)
+    sdt = _block4(block)
     xt = _float_type(x, "x")
-    xp, rows, cols, stride = _rows_view(x, "x")
-    temps = []
-    if cols % (32 if tiled else block):
-        raise ValueError(f"x has {cols} columns, not a multiple of {32 if tiled else block}")
+    shape, rows, cols, stride = _rows_view(x, 32 if tiled else block)
     if codes is None:
-        codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
-        temps.append(codes)
+        codes = torch.empty((rows, cols // 2) if len(shape) == 2 else (*shape[:-1], cols // 2), dtype=_U8, device=x.device)
+        cp = codes.data_ptr()
+    else:
+        cp = _bytes(codes, rows * (cols // 2), "codes")
     if scales is None:
-        shape = _tiled_shape(rows, cols, block) if tiled else (*x.shape[:-1], cols // block)
-        scales = torch.empty(shape, dtype=_SCALE4_DTYPE[block], device=x.device)
-        temps.append(scales)
-    cp = _bytes(codes, rows * (cols // 2), "codes")
-    sp = _bytes(scales, _scales4_size(rows, cols, block, tiled), "scales", (_SCALE4_DTYPE[block],))
-    _check(_lib().engram_quantize4(xp, rows, cols, stride, xt, block, float(scale), int(bool(tiled)), cp, sp,
-                                   _launch_stream(stream, temps)), "engram_quantize4")
+        if tiled:
+            size = (-(-rows // 128), -(-cols // (4 * block)), 512)
+        else:
+            size = (rows, cols // block) if len(shape) == 2 else (*shape[:-1], cols // block)
+        scales = torch.empty(size, dtype=sdt, device=x.device)
+        sp = scales.data_ptr()
+    else:
+        sp = _bytes(scales, _tiled_size(rows, cols, block) if tiled else rows * (cols // block), "scales", sdt)
+    rc = _lib().engram_quantize4(x.data_ptr(), rows, cols, stride, xt, block, float(scale), 1 if tiled else 0, cp, sp,
+                                 _stream_on(x, stream, (codes, scales)))
+    if rc:
+        raise EngramError(rc, "engram_quantize4")
     return codes, scales
 
 
 def engram_dequantize4(codes: torch.Tensor, scales: torch.Tensor, block: int, scale: float = 1.0, tiled: bool = False,
-                       out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, stream=None):
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, stream=None):
     """The values of engram_quantize4's codes uint8 [..., cols / 2] and scales, times `scale`: returns (or fills)
     [..., cols] of out_dtype (bfloat16 unless given; float32, float16)."""
-    _block4(block)
-    cols = 2 * codes.shape[-1]
-    rows = codes.numel() // codes.shape[-1] if codes.shape[-1] else 0
-    if cols % (32 if tiled else block):
+    sdt = _block4(block)
+    shape = codes.shape
+    half = shape[-1] if shape else 0
+    cols = 2 * half
+    if cols == 0 or cols % (32 if tiled else block):
         raise ValueError(f"codes stand for {cols} columns, not a multiple of {32 if tiled else block}")
-    temps = []
+    rows = codes.numel() // half
+    cp = _bytes(codes, rows * half, "codes")
+    sp = _bytes(scales, _tiled_size(rows, cols, block) if tiled else rows * (cols // block), "scales", sdt)
     if out is None:
-        out = torch.empty((*codes.shape[:-1], cols), dtype=out_dtype, device=codes.device)
-        temps.append(out)
-    _size(out, rows * cols, "out")
-    ot = _float_type(out, "out")
-    cp = _bytes(codes, rows * (cols // 2), "codes")
-    sp = _bytes(scales, _scales4_size(rows, cols, block, tiled), "scales", (_SCALE4_DTYPE[block],))
-    _check(_lib().engram_dequantize4(cp, sp, rows, cols, block, float(scale), int(bool(tiled)),
-                                     _dev(out, out.dtype, "out"), ot, _launch_stream(stream, temps)),
-           "engram_dequantize4")
+        out = torch.empty((rows, cols) if len(shape) == 2 else (*shape[:-1], cols), dtype=out_dtype or torch.bfloat16,
+                          device=codes.device)
+        ot, op = _float_type(out, "out"), out.data_ptr()
+    else:
+        ot, op = _float_out(out, out_dtype, rows * cols)
+    rc = _lib().engram_dequantize4(cp, sp, rows, cols, block, float(scale), 1 if tiled else 0, op, ot,
+                                   _stream_on(codes, stream, (out,)))
+    if rc:
+        raise EngramError(rc, "engram_dequantize4")
     return out
 
 
 def _table4(Q: torch.Tensor, S: torch.Tensor, block: int):
-    _block4(block)
-    if Q.dim() != 2:
-        raise ValueError(f"Q must be [rows, dim / 2], got {tuple(Q.shape)}")
-    rows, dim = Q.shape[0], 2 * Q.shape[1]
+    sdt = _block4(block)
+    shape = Q.shape
+    if len(shape) != 2:
+        raise ValueError(f"Q must be [rows, dim / 2], got {tuple(shape)}")
+    rows, half = shape
+    dim = 2 * half
     if dim == 0 or dim % block:
         raise ValueError(f"rows of {dim} values are not whole blocks of {block}")
-    return _bytes(Q, rows * (dim // 2), "Q"), _bytes(S, rows * (dim // block), "S", (_SCALE4_DTYPE[block],)), rows, \
-        _narrow(dim, "the width of Q")
+    return _bytes(Q, rows * half, "Q"), _bytes(S, rows * (dim // block), "S", sdt), rows, _narrow(dim, "the width of Q")
 
 
 def engram_lookup4(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, block: int, scale: float = 1.0,
@@ -1149,13 +1181,16 @@ def engram_lookup4(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, block: i
     `scale`, +0 rows where idx is outside the table."""
     qp, sp, rows, dim = _table4(Q, S, block)
     ip, istride, T, C = _embed_ids(idx)
-    temps = []
     if out is None:
         out = torch.empty((*idx.shape, dim), dtype=torch.bfloat16, device=idx.device)
-        temps.append(out)
-    _size(out, T * C * dim, "out")
-    _check(_lib().engram_lookup4(ip, istride, T, C, qp, sp, rows, dim, block, float(scale),
-                                 _dev(out, torch.bfloat16, "out"), _launch_stream(stream, temps)), "engram_lookup4")
+        op = out.data_ptr()
+    else:
+        _size(out, T * C * dim, "out")
+        op = _dev(out, torch.bfloat16, "out")
+    rc = _lib().engram_lookup4(ip, istride, T, C, qp, sp, rows, dim, block, float(scale), op,
+                               _stream_on(Q, stream, (out,)))
+    if rc:
+        raise EngramError(rc, "engram_lookup4")
     return out
 
 
@@ -1168,17 +1203,20 @@ def engram_lookup4_operand(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, 
     K = _narrow(C * dim, "the operand's width")
     if K == 0 or K % 32:
         raise ValueError(f"{C} rows of {dim} values are not a multiple of 32")
-    temps = []
     if codes is None:
-        codes = torch.empty((T, K // 2), dtype=torch.uint8, device=idx.device)
-        temps.append(codes)
+        codes = torch.empty((T, K // 2), dtype=_U8, device=idx.device)
+        cp = codes.data_ptr()
+    else:
+        cp = _bytes(codes, T * (K // 2), "codes")
     if scales is None:
-        scales = torch.empty(_tiled_shape(T, K, block), dtype=_SCALE4_DTYPE[block], device=idx.device)
-        temps.append(scales)
-    cp = _bytes(codes, T * (K // 2), "codes")
-    op = _bytes(scales, _scales4_size(T, K, block, True), "scales", (_SCALE4_DTYPE[block],))
-    _check(_lib().engram_lookup4_operand(ip, istride, T, C, qp, sp, rows, dim, block, cp, op,
-                                         _launch_stream(stream, temps)), "engram_lookup4_operand")
+        scales = torch.empty((-(-T // 128), -(-K // (4 * block)), 512), dtype=_SCALE4_DTYPE[block], device=idx.device)
+        op = scales.data_ptr()
+    else:
+        op = _bytes(scales, _tiled_size(T, K, block), "scales", _SCALE4_DTYPE[block])
+    rc = _lib().engram_lookup4_operand(ip, istride, T, C, qp, sp, rows, dim, block, cp, op,
+                                       _stream_on(Q, stream, (codes, scales)))
+    if rc:
+        raise EngramError(rc, "engram_lookup4_operand")
     return codes, scales
 
 
@@ -1188,24 +1226,28 @@ def engram_project4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     w uint8 [N, K / 2] with tiled scales, as engram_quantize4(..., tiled=True) (or engram_lookup4_operand for a) makes
     them. Returns (or fills) bf16 [..., N] = bf16(scale * a @ w^T), fp32 accumulation; `scale` is the product of the
     operands' factors."""
-    _block4(block)
-    half = a.shape[-1]
+    sdt = _block4(block)
+    shape = a.shape
+    half = shape[-1] if shape else 0
     K = _narrow(2 * half, "K")
-    if half == 0 or K % 32:
+    if K == 0 or K % 32:
         raise ValueError(f"K is {K}, not a multiple of 32")
-    if w.dim() != 2 or w.shape[1] != half:
-        raise ValueError(f"w must be [N, {half}], got {tuple(w.shape)}")
-    T, N = a.numel() // half, _narrow(w.shape[0], "N")
-    temps = []
+    ws = w.shape
+    if len(ws) != 2 or ws[1] != half:
+        raise ValueError(f"w must be [N, {half}], got {tuple(ws)}")
+    T, N = a.numel() // half, _narrow(ws[0], "N")
+    ap, asp = _bytes(a, T * half, "a"), _bytes(a_scales, _tiled_size(T, K, block), "a_scales", sdt)
+    wp, wsp = _bytes(w, N * half, "w"), _bytes(w_scales, _tiled_size(N, K, block), "w_scales", sdt)
     if out is None:
-        out = torch.empty((*a.shape[:-1], N), dtype=torch.bfloat16, device=a.device)
-        temps.append(out)
-    _size(out, T * N, "out")
-    sd = (_SCALE4_DTYPE[block],)
-    args = (_bytes(a, T * half, "a"), _bytes(a_scales, _scales4_size(T, K, block, True), "a_scales", sd),
-            _bytes(w, N * half, "w"), _bytes(w_scales, _scales4_size(N, K, block, True), "w_scales", sd))
-    _check(_lib().engram_project4(*args, T, K, N, block, float(scale), _dev(out, torch.bfloat16, "out"),
-                                  _launch_stream(stream, temps)), "engram_project4")
+        out = torch.empty((T, N) if len(shape) == 2 else (*shape[:-1], N), dtype=torch.bfloat16, device=a.device)
+        op = out.data_ptr()
+    else:
+        _size(out, T * N, "out")
+        op = _dev(out, torch.bfloat16, "out")
+    rc = _lib().engram_project4(ap, asp, wp, wsp, T, K, N, block, float(scale), op,
+                                _stream_on(w, stream, (out,)))
+    if rc:
+        raise EngramError(rc, "engram_project4")
     return out
 
 
@@ -1220,45 +1262,51 @@ def engram_quantize8(x: torch.Tensor, block: int = 128, scale_dtype: int = SCALE
     if scale_dtype not in _SCALE8_DTYPE:
         raise ValueError(f"scale_dtype must be SCALE_F32, SCALE_BF16 or SCALE_E8M0, got {scale_dtype}")
     xt = _float_type(x, "x")
-    xp, rows, cols, stride = _rows_view(x, "x")
-    if cols % 8:
-        raise ValueError(f"x has {cols} columns, not a multiple of 8")
-    n, temps = -(-cols // block), []
+    shape, rows, cols, stride = _rows_view(x, 8)
+    n = -(-cols // block)
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        temps.append(codes)
+        codes = torch.empty(shape, dtype=_U8, device=x.device)
+        cp = codes.data_ptr()
+    else:
+        cp = _bytes(codes, rows * cols, "codes", _E4M3)
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], n), dtype=_SCALE8_DTYPE[scale_dtype], device=x.device)
-        temps.append(scales)
-    _size(scales, rows * n, "scales")
-    cp = _bytes(codes, rows * cols, "codes", (torch.float8_e4m3fn,))
-    _check(_lib().engram_quantize8(xp, rows, cols, stride, xt, block, scale_dtype, cp,
-                                   _dev_scales(scales, scale_dtype, "scales"), _launch_stream(stream, temps)),
-           "engram_quantize8")
+        scales = torch.empty((rows, n) if len(shape) == 2 else (*shape[:-1], n), dtype=_SCALE8_DTYPE[scale_dtype],
+                             device=x.device)
+        sp = scales.data_ptr()
+    else:
+        _size(scales, rows * n, "scales")
+        sp = _dev_scales(scales, scale_dtype, "scales")
+    rc = _lib().engram_quantize8(x.data_ptr(), rows, cols, stride, xt, block, scale_dtype, cp, sp,
+                                 _stream_on(x, stream, (codes, scales)))
+    if rc:
+        raise EngramError(rc, "engram_quantize8")
     return codes, scales
 
 
 def engram_dequantize8(codes: torch.Tensor, scales: torch.Tensor, block: int, out: torch.Tensor | None = None,
-                       out_dtype: torch.dtype = torch.bfloat16, scale_dtype: int | None = None, stream=None):
-    """The values of engram_quantize8's codes [..., cols] and scales: returns (or fills) [..., cols] of out_dtype."""
+                       out_dtype: torch.dtype | None = None, scale_dtype: int | None = None, stream=None):
+    """The values of engram_quantize8's codes [..., cols] and scales: returns (or fills) [..., cols] of out_dtype
+    (bfloat16 unless given; float32, float16)."""
     _block8(block)
     sdt = _scale_dtype_of(scales, scale_dtype)
     if sdt not in _SCALE8_DTYPE:
         raise ValueError("scales must be float32, bfloat16 or float8_e8m0fnu")
-    cols = _narrow(codes.shape[-1], "the width of codes")
+    shape = codes.shape
+    cols = _narrow(shape[-1] if shape else 0, "the width of codes")
     if cols == 0 or cols % 8:
         raise ValueError(f"codes have {cols} columns, not a multiple of 8")
-    rows, temps = codes.numel() // cols, []
-    if out is None:
-        out = torch.empty(codes.shape, dtype=out_dtype, device=codes.device)
-        temps.append(out)
-    _size(out, rows * cols, "out")
+    rows = codes.numel() // cols
+    cp = _bytes(codes, rows * cols, "codes", _E4M3)
     _size(scales, rows * -(-cols // block), "scales")
-    ot = _float_type(out, "out")
-    cp = _bytes(codes, rows * cols, "codes", (torch.float8_e4m3fn,))
-    _check(_lib().engram_dequantize8(cp, _dev_scales(scales, sdt, "scales"), rows, cols, block, sdt,
-                                     _dev(out, out.dtype, "out"), ot, _launch_stream(stream, temps)),
-           "engram_dequantize8")
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or torch.bfloat16, device=codes.device)
+        ot, op = _float_type(out, "out"), out.data_ptr()
+    else:
+        ot, op = _float_out(out, out_dtype, rows * cols)
+    rc = _lib().engram_dequantize8(cp, _dev_scales(scales, sdt, "scales"), rows, cols, block, sdt, op, ot,
+                                   _stream_on(codes, stream, (out,)))
+    if rc:
+        raise EngramError(rc, "engram_dequantize8")
     return out
 
 
@@ -1277,38 +1325,45 @@ def engram_gate_grad8(x: torch.Tensor, x_scales: torch.Tensor, kv: torch.Tensor,
     with ceil(dim / block) a row). dim a multiple of 16. Returns (or fills) the gradient for the values they stand for,
     as engram_gate_grad: dx bf16 like x, dkv bf16 [..., (hc + 1) * dim], dq_weight and dk_weight float32 [hc, dim]."""
     _block8(block)
-    hc, dim = x.shape[-2:]
+    shape = x.shape
+    if len(shape) < 2 or 0 in shape[-2:]:
+        raise ValueError(f"x must be [..., hc, dim], got {tuple(shape)}")
+    hc, dim = shape[-2:]
     _narrow(max(hc, dim), "hc or dim")
-    if hc == 0 or dim == 0:
-        raise ValueError(f"x must be [..., hc, dim], got {tuple(x.shape)}")
     T, n = x.numel() // (hc * dim), -(-dim // block)
     bf, f32, dev = torch.bfloat16, torch.float32, x.device
-    temps = []
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=bf, device=dev)
-        temps.append(dx)
-    if dkv is None:
-        dkv = torch.empty((*x.shape[:-2], (hc + 1) * dim), dtype=bf, device=dev)
-        temps.append(dkv)
-    if dq_weight is None:
-        dq_weight = torch.empty((hc, dim), dtype=f32, device=dev)
-        temps.append(dq_weight)
-    if dk_weight is None:
-        dk_weight = torch.empty((hc, dim), dtype=f32, device=dev)
-        temps.append(dk_weight)
-    e4m3, e8m0 = (torch.float8_e4m3fn,), (_E8M0,)
-    inputs = (_bytes(x, T * hc * dim, "x", e4m3), _bytes(x_scales, T * hc * n, "x_scales", e8m0),
-              _bytes(kv, T * (hc + 1) * dim, "kv", e4m3), _bytes(kv_scales, T * (hc + 1) * n, "kv_scales", e8m0))
-    specs = [(q_weight, bf, hc * dim, "q_weight"), (k_weight, bf, hc * dim, "k_weight"),
-             (dout, bf, T * hc * dim, "dout"), (dx, bf, T * hc * dim, "dx"), (dkv, bf, T * (hc + 1) * dim, "dkv"),
-             (dq_weight, f32, hc * dim, "dq_weight"), (dk_weight, f32, hc * dim, "dk_weight")]
+    inputs = (_bytes(x, T * hc * dim, "x", _E4M3), _bytes(x_scales, T * hc * n, "x_scales", _E8M0),
+              _bytes(kv, T * (hc + 1) * dim, "kv", _E4M3), _bytes(kv_scales, T * (hc + 1) * n, "kv_scales", _E8M0))
+    specs = [(q_weight, bf, hc * dim, "q_weight"), (k_weight, bf, hc * dim, "k_weight"), (dout, bf, T * hc * dim, "dout")]
     if mask is not None:
         specs.append((mask, torch.bool if mask.dtype is torch.bool else torch.uint8, T, "mask"))
     p = _pointers(specs)
-    keep, ws, nbytes = _scratch(workspace, _lib().engram_gate_grad8_workspace(T, hc, dim), dev)
-    temps.append(keep)
-    _check(_lib().engram_gate_grad8(*inputs, block, *p[:3], p[7] if mask is not None else None, T, hc, dim, float(eps),
-                                    *p[3:7], ws, nbytes, _launch_stream(stream, temps)), "engram_gate_grad8")
+    given = []
+    if dx is None:
+        dx = torch.empty(shape, dtype=bf, device=dev)
+    else:
+        given.append((dx, bf, T * hc * dim, "dx"))
+    if dkv is None:
+        dkv = torch.empty((T, (hc + 1) * dim) if len(shape) == 3 else (*shape[:-2], (hc + 1) * dim), dtype=bf, device=dev)
+    else:
+        given.append((dkv, bf, T * (hc + 1) * dim, "dkv"))
+    if dq_weight is None:
+        dq_weight = torch.empty((hc, dim), dtype=f32, device=dev)
+    else:
+        given.append((dq_weight, f32, hc * dim, "dq_weight"))
+    if dk_weight is None:
+        dk_weight = torch.empty((hc, dim), dtype=f32, device=dev)
+    else:
+        given.append((dk_weight, f32, hc * dim, "dk_weight"))
+    if given:
+        _pointers(given)
+    L = _lib()
+    keep, ws, nbytes = _scratch(workspace, L.engram_gate_grad8_workspace(T, hc, dim), dev)
+    rc = L.engram_gate_grad8(*inputs, block, p[0], p[1], p[2], p[3] if mask is not None else None, T, hc, dim, eps,
+                             dx.data_ptr(), dkv.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), ws, nbytes,
+                             _stream_on(x, stream, (dx, dkv, dq_weight, dk_weight, keep)))
+    if rc:
+        raise EngramError(rc, "engram_gate_grad8")
     return dx, dkv, dq_weight, dk_weight
 
 

@@ -94,16 +94,12 @@ __device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
 
-// 8 E4M3 codes of a checkpoint times their block's scale, a power of two: exact
-__device__ __forceinline__ Vec8 widen8(const uint2& v, float s) {
+// 8 E4M3 codes of a checkpoint, without their block's scale
+__device__ __forceinline__ Vec8 widen8(const uint2& v) {
   const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
   Vec8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), lo, hi);
-    r.p[i] = __fmul2_rn(make_float2(lo, hi), make_float2(s, s));
-  }
+  for (int i = 0; i < 4; ++i) f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), r.p[i].x, r.p[i].y);
   return r;
 }
 
@@ -261,22 +257,26 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
       sc_next[2 * HPT] = __ldg(ks + (HC - g0) * n_blocks);
     }
   };
-  // a thread's 8 values of copy i (of its group), of that copy's key, and of the value
+  // A thread's 8 values of copy i (of its group), of that copy's key, and of the value; with Q8 without their scales,
+  // which are one power of two for all 8 and go into the sums and the copy's scalars: multiplied in there, they change
+  // no rounding.
   auto packed = [&](int st, int j) {  // row j of the checkpoints' rows
     return reinterpret_cast<const uint2*>(smem + st * stage_vecs + HC * nv)[j * nv + me];
   };
   auto h_of = [&](int st, int i) {
-    if constexpr (Q8) return widen8(packed(st, g0 + i), widen_scale<ENGRAM_SCALE_E8M0>(sc[i]));
+    if constexpr (Q8) return widen8(packed(st, g0 + i));
     else return widen8(slot(st, g0 + i));
   };
   auto k_of = [&](int st, int i) {
-    if constexpr (Q8) return widen8(packed(st, HC + g0 + i), widen_scale<ENGRAM_SCALE_E8M0>(sc[HPT + i]));
+    if constexpr (Q8) return widen8(packed(st, HC + g0 + i));
     else return widen8(slot(st, kK + g0 + i));
   };
   auto v_of = [&](int st) {
-    if constexpr (Q8) return widen8(packed(st, 2 * HC), widen_scale<ENGRAM_SCALE_E8M0>(sc[2 * HPT]));
+    if constexpr (Q8) return widen8(packed(st, 2 * HC));
     else return widen8(slot(st, 3 * HC));
   };
+  auto h_scale = [&](int i) { return widen_scale<ENGRAM_SCALE_E8M0>(sc[i]); };
+  auto k_scale = [&](int i) { return widen_scale<ENGRAM_SCALE_E8M0>(sc[HPT + i]); };
   // one thread starts a token's copies
   uint32_t last = ~0u;  // (that thread's) bit st: the parity of the stage's last copies
   auto fetch = [&](int64_t t, int st, bool open) {
@@ -403,6 +403,13 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: another vector's
+          if constexpr (Q8) {
+            const float hs = h_scale(i), ks = k_scale(i);
+            s[4 * i] = s[4 * i] * hs * hs;
+            s[4 * i + 1] = s[4 * i + 1] * ks * ks;
+            s[4 * i + 2] = s[4 * i + 2] * hs * ks;
+            s[4 * i + 3] *= widen_scale<ENGRAM_SCALE_E8M0>(sc[2 * HPT]);
+          }
         }
       }
       const float mine = warp_reduce_scatter<M>(s, lane);
@@ -449,6 +456,10 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
           const Vec8 h = h_of(st, i), k = k_of(st, i), w = weights(i);
           d[i] = Sum2{0.f, 0.f};
           if (on) d[i] = dot_part(h, k, w);
+          if constexpr (Q8) {
+            d[i].hi = d[i].hi * h_scale(i) * k_scale(i);
+            d[i].lo = d[i].lo * h_scale(i) * k_scale(i);
+          }
         }
         const Sum2 mine2 = warp_reduce_scatter2<HPT>(d, lane);
         float* to2 = red + (((buf * CG + group) * cs + rank) * wg + (warp - group * wg)) * M + 2 * (lane / (32 / HPT));
@@ -489,13 +500,28 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
           const Vec8 h = h_of(st, i), k = k_of(st, i), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           Vec8 dh, dk;
+          // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
+          float cwk = g.y, eh = g.z, cwh = g.y, ek = g.w, chk = g.y;
+          if constexpr (Q8) {
+            const float hs = h_scale(i), ks = k_scale(i);
+            cwk *= ks;
+            eh *= hs;
+            cwh *= hs;
+            ek *= ks;
+            chk = chk * hs * ks;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 cw = __fmul2_rn(both(g.y), w.p[e]);
-            dh.p[e] = __ffma2_rn(cw, k.p[e], __ffma2_rn(both(g.z), h.p[e], u.p[e]));
-            dk.p[e] = __ffma2_rn(cw, h.p[e], __fmul2_rn(both(g.w), k.p[e]));
+            if constexpr (Q8) {
+              dh.p[e] = __ffma2_rn(__fmul2_rn(both(cwk), w.p[e]), k.p[e], __ffma2_rn(both(eh), h.p[e], u.p[e]));
+              dk.p[e] = __ffma2_rn(__fmul2_rn(both(cwh), w.p[e]), h.p[e], __fmul2_rn(both(ek), k.p[e]));
+            } else {
+              const float2 cw = __fmul2_rn(both(g.y), w.p[e]);
+              dh.p[e] = __ffma2_rn(cw, k.p[e], __ffma2_rn(both(g.z), h.p[e], u.p[e]));
+              dk.p[e] = __ffma2_rn(cw, h.p[e], __fmul2_rn(both(g.w), k.p[e]));
+            }
             dv.p[e] = __ffma2_rn(both(g.x), u.p[e], dv.p[e]);
-            dw[i].p[e] = __ffma2_rn(both(g.y), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
+            dw[i].p[e] = __ffma2_rn(both(chk), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
           }
           st8(dxt + i * a.dim, dh);
           st8(dkt + i * a.dim, dk);

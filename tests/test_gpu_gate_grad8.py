@@ -1,7 +1,7 @@
 """The gate's gradient from 8-bit checkpoints (engram_gate_grad8) against the formula in 64 bits on the bf16 values that
 the checkpoints stand for, within engram_gate_grad's bounds (GPU only). The two calls run the same arithmetic on those
-values, but may split a row's columns otherwise (a checkpoint's rows have to start on 16 bytes), so their sums run in
-another order; where both hold a token's rows whole in one CTA the bits are equal."""
+values, but split a row's columns otherwise (a checkpoint's rows have to start on 16 bytes; with 4 copies and more a
+thread has 4 columns), so their sums run in another order; where the split is the same the bits are equal."""
 import numpy as np
 import pytest
 import torch
@@ -49,8 +49,8 @@ def test_gradient_of_the_values(T, hc, dim, block):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
-@pytest.mark.parametrize("T,hc,dim", [(700, 8, 96), (1500, 1, 64), (37, 4, 256), (200, 2, 272)])
-def test_whole_rows_give_the_bits_of_the_values_gradient(T, hc, dim):
+@pytest.mark.parametrize("T,hc,dim", [(1500, 1, 64), (200, 2, 272)])
+def test_whole_rows_of_few_copies_give_the_bits_of_the_values_gradient(T, hc, dim):
     args = G._inputs(np.random.default_rng(T + dim), T, hc, dim)
     xq, kq, back = _checkpoints(args, 32)
     got, exp = _run8(xq, kq, back, 32), G._run(back)
