@@ -28,6 +28,21 @@ __device__ __forceinline__ int64_t id_at(const Lookup4Args& a, N e) {
   return (int64_t)t * a.idx_stride + (int64_t)(e - t * (uint32_t)a.n_cols);
 }
 
+// 16 bf16 values, 32 bytes at once where the address allows; evicted first, so that rows that ids repeat stay in L2 longer
+__device__ __forceinline__ void st_row32(uint16_t* to, const float* v) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = bf16x2_rn(v[2 * i], v[2 * i + 1]);
+  if ((reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+    asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    __stcs(reinterpret_cast<uint4*>(to), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(reinterpret_cast<uint4*>(to) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+
 // A unit is 16 values: 8 bytes of codes, 32 of output. N: the type that numbers units (32 bits where they fit).
 template <bool NV, typename N>
 __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, uint16_t* __restrict__ out, const N units) {
@@ -68,13 +83,11 @@ __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, 
     const float s = scale4(b[i], NV);
     widen_e2m1x8(w[i].x, s, v);
     widen_e2m1x8(w[i].y, s, v + 8);
+    if (a.scale != 1.0f) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] *= a.scale;
-    uint4 lo = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
-    uint4 hi = make_uint4(bf16x2_rn(v[8], v[9]), bf16x2_rn(v[10], v[11]), bf16x2_rn(v[12], v[13]), bf16x2_rn(v[14], v[15]));
-    uint4* to = reinterpret_cast<uint4*>(out + (int64_t)u * 16);
-    to[0] = lo;
-    to[1] = hi;
+      for (int e = 0; e < 16; ++e) v[e] *= a.scale;
+    }
+    st_row32(out + (int64_t)u * 16, v);
   }
 }
 

@@ -58,9 +58,11 @@ __device__ __forceinline__ void widen_e2m1x8(uint32_t w, float s, float* v) {
       : "r"(w));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f16x2_to_f32(h[i], v[2 * i], v[2 * i + 1]);
-    v[2 * i] *= s;
-    v[2 * i + 1] *= s;
+    float2 f;
+    f16x2_to_f32(h[i], f.x, f.y);
+    f = __fmul2_rn(f, make_float2(s, s));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 

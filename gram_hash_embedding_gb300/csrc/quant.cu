@@ -54,12 +54,11 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
   return lo;
 }
 
-// v / s ready for the conversion to E2M1, s an E4M3 number. 16-bit inputs have at most 11 significant bits and s four:
-// the quotient is a border between two codes (three bits) exactly, or at least 2^-11 of itself away from it. The
-// product with the rounded reciprocal is within 2^-22, and rounding it to 19 bits puts exact borders back onto themselves.
-__device__ __forceinline__ float quotient16(float v, float recip) {
-  return __uint_as_float((__float_as_uint(v * recip) + 16u) & ~31u);
-}
+// v / s for the conversion to E2M1, s an E4M3 number, two values at a time. 16-bit inputs have at most 11 significant bits
+// and s four: the quotient is a border between two codes (three bits) exactly, or at least 2^-11 of itself away from it.
+// With the reciprocal in two parts (lo: what the rounding of hi lost) one fma's rounding is all that is off, so exact
+// borders stay exact and the others on their side.
+__device__ __forceinline__ float2 quotient2(float2 v, float2 hi, float2 lo) { return __ffma2_rn(v, hi, __fmul2_rn(v, lo)); }
 
 // fp32 inputs may lie nearer to a border than that: the code's magnitude by comparing with the borders times s, which
 // are exact (three bits times four); between two codes a tie goes to the even one
@@ -75,9 +74,50 @@ __device__ __forceinline__ float e2m1_by_borders(float v, float s) {
   return copysignf(r, v);
 }
 
+// 16 consecutive values of x as loaded: one access of 32 bytes for 16-bit types where the address allows
+template <int TYPE>
+struct Raw16 {
+  Raw<TYPE, 8> a, b;
+  __device__ __forceinline__ void load(const typename Elem<TYPE>::type* p, bool second) {
+    if (TYPE != ENGRAM_TYPE_F32 && second && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+      asm("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(a.a.x), "=r"(a.a.y), "=r"(a.a.z), "=r"(a.a.w), "=r"(b.a.x), "=r"(b.a.y), "=r"(b.a.z), "=r"(b.a.w)
+          : "l"(p)
+          : "memory");
+    } else {
+      a.load(p);
+      if (second) b.load(p + 8);
+    }
+  }
+  // bits of the largest magnitude as fp32; a NaN counts as the largest
+  __device__ __forceinline__ uint32_t amax(const float* v) const {
+    if constexpr (TYPE == ENGRAM_TYPE_F32) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);  // in bits a NaN is above infinity
+      return m;
+    } else {
+      using T2 = std::conditional_t<TYPE == ENGRAM_TYPE_BF16, __nv_bfloat162, __half2>;
+      const T2* x = reinterpret_cast<const T2*>(&a.a);
+      const T2* y = reinterpret_cast<const T2*>(&b.a);
+      T2 m = __hmax2_nan(__habs2(x[0]), __habs2(y[0]));
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __hmax2_nan(__habs2(x[i]), __habs2(y[i])));
+      const auto top = __hmax_nan(low_of(m), high_of(m));
+      return __float_as_uint(Elem<TYPE>::load(&top));
+    }
+  }
+  static __device__ __forceinline__ __nv_bfloat16 low_of(__nv_bfloat162 v) { return __low2bfloat16(v); }
+  static __device__ __forceinline__ __nv_bfloat16 high_of(__nv_bfloat162 v) { return __high2bfloat16(v); }
+  static __device__ __forceinline__ __half low_of(__half2 v) { return __low2half(v); }
+  static __device__ __forceinline__ __half high_of(__half2 v) { return __high2half(v); }
+};
+
 // LANES threads of 16 values share a block: 1 (blocks of 16) or 2 with 4-bit codes, 2, 4 or 8 with 8-bit codes.
 // HALF: rows are a multiple of 8 values and no more (8 bits), so a row's last thread may have 8.
-template <int TYPE, int LANES, bool FOUR, bool TILED, bool HALF>
+// LINEAR: rows follow one another without a gap and are whole blocks, so values, codes and scales need no row number (its
+// division was a tenth of the instructions, and blocks of 16 are bound by them).
+template <int TYPE, int LANES, bool FOUR, bool TILED, bool HALF, bool LINEAR>
 __global__ void __launch_bounds__(kThreads)
     quantize_kernel(const QuantArgs a, const uint32_t per_row, const uint64_t units, const float inv) {
   pdl_wait();
@@ -86,50 +126,63 @@ __global__ void __launch_bounds__(kThreads)
   const uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
   const bool on = u < units;
   // a row has per_row threads, a multiple of LANES
-  const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
-  const uint32_t j = (uint32_t)(u - row * per_row);
-  const int col = (int)j * kPer;
-  const bool lo = on && col < a.cols, hi = HALF ? on && col + 8 < a.cols : lo;
+  uint64_t row = 0, j = u;
+  if constexpr (!LINEAR) {
+    row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
+    j = u - row * per_row;
+  }
+  const int64_t col = (int64_t)j * kPer;
+  const bool lo = on && (LINEAR || col < a.cols), hi = HALF ? lo && col + 8 < a.cols : lo;
   const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride + col;
-  Raw<TYPE, 8> r0, r1;
-  r0.zero();
-  r1.zero();
-  if (lo) r0.load(x);
-  if (hi) r1.load(x + 8);
+  Raw16<TYPE> r;
+  r.a.zero();
+  r.b.zero();
+  if (lo) r.load(x, hi);
   float v[kPer];
-  r0.widen(v);
-  r1.widen(v + 8);
-  uint32_t amax = 0;
+  r.a.widen(v);
+  r.b.widen(v + 8);
+  uint32_t amax = r.amax(v);
+  if (FOUR && inv != 1.0f) {  // the tensor's factor
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (FOUR) v[i] *= inv;
-    amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);  // in bits a NaN is above infinity
+    for (int i = 0; i < kPer; ++i) v[i] *= inv;
+    amax = __float_as_uint(__uint_as_float(amax) * inv) & 0x7fffffffu;
   }
 #pragma unroll
   for (int off = 1; off < LANES; off *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   uint32_t code;
   uint32_t w[4];
+  float2* const v2 = reinterpret_cast<float2*>(v);
   if constexpr (FOUR && LANES == 1) {
     code = e4m3_scale(amax);
     const float s = e4m3_value(code);
     const bool ok = code != 0u && code != 0x7fu;
-    const float recip = ok ? __frcp_rn(s) : 0.f;
+    if constexpr (TYPE == ENGRAM_TYPE_F32) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      v[i] = !ok ? 0.f : TYPE == ENGRAM_TYPE_F32 ? e2m1_by_borders(v[i], s) : quotient16(v[i], recip);
+      for (int i = 0; i < kPer; ++i) v[i] = ok ? e2m1_by_borders(v[i], s) : 0.f;
+    } else {
+      // scale 0 or NaN: the codes are 0 (a product with 0 would keep NaN and signs)
+      const float h = __frcp_rz(ok ? s : 1.f), l = __fmaf_rn(-h, s, 1.f) * h;  // l >= 0: -0 stays -0
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) v2[i] = quotient2(v2[i], make_float2(h, h), make_float2(l, l));
+      w[0] = ok ? e2m1x8(v) : 0u;
+      w[1] = ok ? e2m1x8(v + 8) : 0u;
+    }
   } else {
     code = FOUR ? pow2_scale(amax, 2, 0x400000u) : pow2_scale(amax, 8, 0x600000u);
-    const float recip = code == 255u ? 0.f : pow2_recip(code);
+    const float f = pow2_recip(min(code, 253u));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = code == 255u ? 0.f : v[i] * recip;
+    for (int i = 0; i < kPer / 2; ++i) v2[i] = __fmul2_rn(v2[i], make_float2(f, f));
   }
+  const bool nan = (!FOUR || LANES > 1) && code == 255u;  // codes of 0
   if constexpr (FOUR) {
-    w[0] = e2m1x8(v);
-    w[1] = e2m1x8(v + 8);
+    if constexpr (LANES > 1 || TYPE == ENGRAM_TYPE_F32) {
+      w[0] = nan ? 0u : e2m1x8(v);
+      w[1] = nan ? 0u : e2m1x8(v + 8);
+    }
     if (lo) *reinterpret_cast<uint2*>(a.codes + (int64_t)row * (a.cols >> 1) + (col >> 1)) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3x4(v + 4 * i);
+    for (int i = 0; i < 4; ++i) w[i] = nan ? 0u : e4m3x4(v + 4 * i);
     uint8_t* to = a.codes + (int64_t)row * a.cols + col;
     if (!HALF) {
       if (lo) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -139,13 +192,13 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   if (!lo || j % LANES != 0) return;
-  const uint32_t k = j / LANES;
+  const uint64_t k = j / LANES;
   if constexpr (TILED) {
     uint8_t* to = static_cast<uint8_t*>(a.scales);
     const int64_t groups = scale_groups(a.cols, a.block);
     to[tiled_scale_at((int64_t)row, k, groups)] = (uint8_t)code;
-    if ((int)(k + 1) * a.block >= a.cols)  // the row's last scale: the rest of its group of four is 0
-      for (uint32_t p = k + 1; p & 3u; ++p) to[tiled_scale_at((int64_t)row, p, groups)] = 0;
+    if ((int64_t)(k + 1) * a.block >= a.cols)  // the row's last scale: the rest of its group of four is 0
+      for (uint64_t p = k + 1; p & 3u; ++p) to[tiled_scale_at((int64_t)row, p, groups)] = 0;
   } else {
     const int64_t at = (int64_t)row * (per_row / LANES) + k;
     if (FOUR || a.scale_dtype == ENGRAM_SCALE_E8M0) {
@@ -166,10 +219,31 @@ cudaError_t launch_quantize(const QuantArgs& a, cudaStream_t s) {
   const float inv = 1.0f / a.scale;
   return with_type(a.x_type, [&](auto t) {
     constexpr int TYPE = decltype(t)::value;
-    auto kern = quantize_kernel<TYPE, LANES, FOUR, TILED, !FOUR>;
-    if (!FOUR && a.cols % 16 == 0) kern = quantize_kernel<TYPE, LANES, FOUR, TILED, false>;
+    auto kern = quantize_kernel<TYPE, LANES, FOUR, TILED, !FOUR, false>;
+    if (!FOUR && a.cols % 16 == 0) kern = quantize_kernel<TYPE, LANES, FOUR, TILED, false, false>;
+    if constexpr (!TILED)
+      if (a.cols % a.block == 0 && (a.x_stride == a.cols || a.rows == 1))
+        kern = quantize_kernel<TYPE, LANES, FOUR, TILED, false, true>;
     return launch_pdl(kern, dim3((unsigned)ctas), dim3(kThreads), 0, s, a, per_row, units, inv);
   });
+}
+
+// 16 values to consecutive places: 32 bytes at once for 16-bit types where the address allows
+template <int TYPE>
+__device__ __forceinline__ void store16(typename Elem<TYPE>::type* to, const float* v, bool second) {
+  if constexpr (TYPE != ENGRAM_TYPE_F32) {
+    if (second && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack2<TYPE>(v[2 * i], v[2 * i + 1]);
+      asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+                   "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                   : "memory");
+      return;
+    }
+  }
+  store_vals<TYPE, 8>(to, v);
+  if (second) store_vals<TYPE, 8>(to + 8, v + 8);
 }
 
 // 16 values a thread, as above, in the other direction
@@ -180,23 +254,29 @@ __global__ void __launch_bounds__(kThreads)
   pdl_trigger();
   const uint64_t u = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
   if (u >= units) return;
-  const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
-  const int col = (int)(u - row * per_row) * kPer;
-  const bool hi = FOUR || col + 8 < a.cols;
-  const int k = col / a.block;
   float v[kPer];
   if constexpr (FOUR) {
-    const int64_t at = TILED ? tiled_scale_at((int64_t)row, k, scale_groups(a.cols, a.block))
-                             : (int64_t)row * (a.cols / a.block) + k;
+    int64_t at = NV ? u : u >> 1;  // rows are whole blocks
+    if constexpr (TILED) {
+      const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
+      const uint32_t j = (uint32_t)(u - row * per_row);
+      at = tiled_scale_at((int64_t)row, NV ? j : j >> 1, scale_groups(a.cols, a.block));
+    }
+    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + 8 * u);
     const uint32_t b = static_cast<const uint8_t*>(a.scales)[at];
-    const uint2 w = *reinterpret_cast<const uint2*>(a.codes + (int64_t)row * (a.cols >> 1) + (col >> 1));
-    const float s = (NV ? e4m3_value(b) : widen_scale<ENGRAM_SCALE_E8M0>(b));
+    const float s = NV ? e4m3_value(b) : widen_scale<ENGRAM_SCALE_E8M0>(b);
     widen_e2m1x8(w.x, s, v);
     widen_e2m1x8(w.y, s, v + 8);
+    if (a.scale != 1.0f) {  // code * block scale is exact, so this rounds once
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] *= a.scale;
+      for (int i = 0; i < kPer; ++i) v[i] *= a.scale;
+    }
+    store16<TYPE>(static_cast<typename Elem<TYPE>::type*>(a.out) + 16 * u, v, true);
   } else {
-    const int64_t at = (int64_t)row * ((a.cols + a.block - 1) / a.block) + k;
+    const uint64_t row = units <= 0xffffffffull ? (uint32_t)u / per_row : u / per_row;
+    const int col = (int)(u - row * per_row) * kPer;
+    const bool hi = col + 8 < a.cols;
+    const int64_t at = (int64_t)row * ((a.cols + a.block - 1) / a.block) + col / a.block;
     float s;
     if (a.scale_dtype == ENGRAM_SCALE_E8M0) s = widen_scale<ENGRAM_SCALE_E8M0>(static_cast<const uint8_t*>(a.scales)[at]);
     else if (a.scale_dtype == ENGRAM_SCALE_F32) s = static_cast<const float*>(a.scales)[at];
@@ -208,10 +288,8 @@ __global__ void __launch_bounds__(kThreads)
     widen_e4m3x4(w0.y, s, v + 4);
     widen_e4m3x4(w1.x, s, v + 8);
     widen_e4m3x4(w1.y, s, v + 12);
+    store16<TYPE>(static_cast<typename Elem<TYPE>::type*>(a.out) + (int64_t)row * a.cols + col, v, hi);
   }
-  typename Elem<TYPE>::type* to = static_cast<typename Elem<TYPE>::type*>(a.out) + (int64_t)row * a.cols + col;
-  store_vals<TYPE, 8>(to, v);
-  if (hi) store_vals<TYPE, 8>(to + 8, v + 8);
 }
 
 template <bool FOUR, bool NV, bool TILED>
