@@ -772,27 +772,36 @@ uint64_t engram_gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
   return engram::gate_grad_workspace(T, hc, dim);
 }
 
-// the checks that both kinds of inputs share, and the call
-static int gate_grad(const engram::GateGradArgs& a, uint64_t need, void* workspace, uint64_t workspace_bytes,
-                     engram_stream_t stream, int64_t withhold) {
+// the checks that both kinds of inputs share; x and kv: bf16 values, or the codes of checkpoints
+static int check_gate_grad(const void* x, const void* kv, const engram::GateGradArgs& a, uint64_t need,
+                           const void* workspace, uint64_t workspace_bytes) {
   if (a.T < 0) return ENGRAM_ERR_INVALID;
   if (!gate_grad_shape_ok(a.T, a.hc, a.dim)) return ENGRAM_ERR_UNSUPPORTED;
   if (a.qw == nullptr || a.kw == nullptr || a.dq == nullptr || a.dk == nullptr || !aligned(a.qw, 16) ||
       !aligned(a.kw, 16) || !aligned(a.dq, 16) || !aligned(a.dk, 16))
     return ENGRAM_ERR_INVALID;
   if (a.T > 0) {
-    if (a.x == nullptr || a.kv == nullptr || a.dout == nullptr || a.dx == nullptr || a.dkv == nullptr ||
-        workspace == nullptr)
+    if (x == nullptr || kv == nullptr || a.dout == nullptr || a.dx == nullptr || a.dkv == nullptr || workspace == nullptr)
       return ENGRAM_ERR_INVALID;
-    if (!aligned(a.x, 16) || !aligned(a.kv, 16) || !aligned(a.dout, 16) || !aligned(a.dx, 16) || !aligned(a.dkv, 16) ||
+    if (!aligned(x, 16) || !aligned(kv, 16) || !aligned(a.dout, 16) || !aligned(a.dx, 16) || !aligned(a.dkv, 16) ||
         !aligned(workspace, 256) || workspace_bytes < need)
       return ENGRAM_ERR_INVALID;
   }
+  return ENGRAM_OK;
+}
+
+static std::vector<Span> gate_grad_writes(const engram::GateGradArgs& a, const void* workspace, uint64_t workspace_bytes) {
   const uint64_t w = (uint64_t)a.hc * a.dim * 4;
+  return {span(a.dx, (uint64_t)a.T * a.hc * a.dim * 2), span(a.dkv, (uint64_t)a.T * (a.hc + 1) * a.dim * 2),
+          span(a.dq, w), span(a.dk, w), span(workspace, a.T > 0 ? workspace_bytes : 0)};
+}
+
+static int gate_grad(const engram::GateGradArgs& a, void* workspace, uint64_t workspace_bytes, engram_stream_t stream,
+                     int64_t withhold) {
+  const int rc = check_gate_grad(a.x, a.kv, a, engram_gate_grad_workspace(a.T, a.hc, a.dim), workspace, workspace_bytes);
+  if (rc != ENGRAM_OK) return rc;
   return launched(launch_rc(engram::launch_gate_grad(a, workspace, (cudaStream_t)stream, withhold)),
-                  (cudaStream_t)stream,
-                  {span(a.dx, (uint64_t)a.T * a.hc * a.dim * 2), span(a.dkv, (uint64_t)a.T * (a.hc + 1) * a.dim * 2),
-                   span(a.dq, w), span(a.dk, w), span(workspace, a.T > 0 ? workspace_bytes : 0)});
+                  (cudaStream_t)stream, gate_grad_writes(a, workspace, workspace_bytes));
 }
 
 int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight, const uint16_t* k_weight,
@@ -800,7 +809,7 @@ int engram_gate_grad(const uint16_t* x, const uint16_t* kv, const uint16_t* q_we
                      uint16_t* dx, uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
                      uint64_t workspace_bytes, engram_stream_t stream) {
   const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
-  return gate_grad(a, engram_gate_grad_workspace(T, hc, dim), workspace, workspace_bytes, stream, -1);
+  return gate_grad(a, workspace, workspace_bytes, stream, -1);
 }
 
 int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint16_t* q_weight,
@@ -810,7 +819,7 @@ int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint1
                               engram_stream_t stream) {
   if (token < 0) return ENGRAM_ERR_INVALID;
   const engram::GateGradArgs a{x, kv, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight, dk_weight};
-  return gate_grad(a, engram_gate_grad_workspace(T, hc, dim), workspace, workspace_bytes, stream, token);
+  return gate_grad(a, workspace, workspace_bytes, stream, token);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -985,7 +994,18 @@ int engram_project4_withhold(const uint8_t* a, const uint8_t* a_scales, const ui
 
 uint64_t engram_gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim) {
   if (T <= 0 || !gate_grad_shape_ok(T, hc, dim) || dim % 16 != 0) return 0;
-  return engram::gate_grad_workspace(T, hc, dim, true);
+  return engram::gate_grad8_workspace(T, hc, dim);
+}
+
+static int gate_grad8(const engram::GateGrad8Args& a, void* workspace, uint64_t workspace_bytes, engram_stream_t stream,
+                      int64_t withhold) {
+  if (!block8_ok(a.block) || a.g.dim % 16 != 0) return ENGRAM_ERR_UNSUPPORTED;
+  if (a.g.T > 0 && (a.xs == nullptr || a.kvs == nullptr)) return ENGRAM_ERR_INVALID;
+  const int rc = check_gate_grad(a.x, a.kv, a.g, engram_gate_grad8_workspace(a.g.T, a.g.hc, a.g.dim), workspace,
+                                 workspace_bytes);
+  if (rc != ENGRAM_OK) return rc;
+  return launched(launch_rc(engram::launch_gate_grad8(a, workspace, (cudaStream_t)stream, withhold)),
+                  (cudaStream_t)stream, gate_grad_writes(a.g, workspace, workspace_bytes));
 }
 
 int engram_gate_grad8(const uint8_t* x, const uint8_t* x_scales, const uint8_t* kv, const uint8_t* kv_scales,
@@ -993,11 +1013,20 @@ int engram_gate_grad8(const uint8_t* x, const uint8_t* x_scales, const uint8_t* 
                       const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps, uint16_t* dx, uint16_t* dkv,
                       float* dq_weight, float* dk_weight, void* workspace, uint64_t workspace_bytes,
                       engram_stream_t stream) {
-  if (!block8_ok(block) || dim % 16 != 0) return ENGRAM_ERR_UNSUPPORTED;
-  if (T > 0 && (x_scales == nullptr || kv_scales == nullptr)) return ENGRAM_ERR_INVALID;
-  const engram::GateGradArgs a{x,  kv, q_weight, k_weight, dout,      mask,      T,        hc,        dim,
-                               eps, dx, dkv,      dq_weight, dk_weight, x_scales, kv_scales, block};
-  return gate_grad(a, engram_gate_grad8_workspace(T, hc, dim), workspace, workspace_bytes, stream, -1);
+  const engram::GateGrad8Args a{{nullptr, nullptr, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight,
+                                 dk_weight}, x, x_scales, kv, kv_scales, block};
+  return gate_grad8(a, workspace, workspace_bytes, stream, -1);
+}
+
+int engram_gate_grad8_withhold(const uint8_t* x, const uint8_t* x_scales, const uint8_t* kv, const uint8_t* kv_scales,
+                               int32_t block, const uint16_t* q_weight, const uint16_t* k_weight, const uint16_t* dout,
+                               const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps, uint16_t* dx,
+                               uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
+                               uint64_t workspace_bytes, int64_t token, engram_stream_t stream) {
+  if (token < 0) return ENGRAM_ERR_INVALID;
+  const engram::GateGrad8Args a{{nullptr, nullptr, q_weight, k_weight, dout, mask, T, hc, dim, eps, dx, dkv, dq_weight,
+                                 dk_weight}, x, x_scales, kv, kv_scales, block};
+  return gate_grad8(a, workspace, workspace_bytes, stream, token);
 }
 
 namespace {

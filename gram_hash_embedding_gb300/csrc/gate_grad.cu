@@ -32,8 +32,8 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "dequant.cuh"
 #include "engram_internal.cuh"
+#include "gate_grad.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
 #include "train.cuh"
@@ -41,157 +41,7 @@
 namespace engram {
 namespace {
 
-constexpr int kSms = 152;
-constexpr int kMaxSmem = 226 << 10;
-constexpr uint64_t kSettleNs = 100000;  // after a wait has run out: far longer than a store to another SM takes
-
-struct CopyGrad {
-  float gate, c, ea, eb, m;  // gate, c, e / A, e / B, |dot|
-};
-
-// The scalars of one residual copy from its four sums
-__device__ __forceinline__ CopyGrad copy_grad(float sh, float sk, float sd, float su, float rd, float eps,
-                                              float inv_sqrt_dim) {
-  const float ra = rsqrtf(sh * rd + eps), rb = rsqrtf(sk * rd + eps);
-  const float r = ra * rb * inv_sqrt_dim;
-  const float dot = sd * r;
-  // a NaN dot stays one and makes the gate and all of the copy's gradients NaN (fmaxf would take the bound for it)
-  const float m = fabsf(dot), bounded = m < 1e-6f ? 1e-6f : m, ri = rsqrtf(bounded);  // 1 / |z|
-  CopyGrad g;
-  g.m = m;
-  // from exp(-|z|), so that neither the gate nor 1 - gate cancels: gate (1 - gate) = x / (1 + x)^2
-  const float x = expf(-bounded * ri), y = __frcp_rn(1.0f + x);
-  g.gate = dot < 0.f ? x * y : y;
-  const float ddot = m < 1e-6f ? 0.f : su * (x * y * y) * (0.5f * ri);
-  const float e = ddot * dot * rd;
-  g.c = ddot * r;
-  g.ea = e * ra * ra;
-  g.eb = e * rb * rb;
-  return g;
-}
-
-// 8 bf16 values as 4 pairs: the arithmetic runs two values an instruction (the packed fp32 forms), which
-// round like the single ones
-struct Vec8 {
-  float2 p[4];
-};
-
-__device__ __forceinline__ Vec8 widen8(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  Vec8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-  return r;
-}
-
-__device__ __forceinline__ void st8(uint16_t* p, const Vec8& v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = pack2<ENGRAM_TYPE_BF16>(v.p[i].x, v.p[i].y);
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
-
-// 8 E4M3 codes of a checkpoint, without their block's scale
-__device__ __forceinline__ Vec8 widen8(const uint2& v) {
-  const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
-  Vec8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), r.p[i].x, r.p[i].y);
-  return r;
-}
-
-// one row's part of a token into shared memory, counted in bytes on `bar`
-__device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-// Sums of N values over the warp, N a power of two <= 32: lane l ends with the total of value
-// l / (32 / N), in N - 1 + log2(32 / N) shuffles instead of 5 N.
-template <int N>
-__device__ __forceinline__ float warp_reduce_scatter(float (&s)[N], int lane) {
-#pragma unroll
-  for (int w = N / 2, off = 16; w >= 1; w /= 2, off /= 2) {
-    const bool up = lane & off;
-#pragma unroll
-    for (int j = 0; j < w; ++j) {
-      const float give = up ? s[j] : s[j + w];
-      const float keep = up ? s[j + w] : s[j];
-      s[j] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-    }
-  }
-  float r = s[0];
-#pragma unroll
-  for (int off = 16 / N; off >= 1; off /= 2) r += __shfl_xor_sync(0xffffffffu, r, off);
-  return r;
-}
-
-// A sum and what its roundings lost, so far: twice the precision of fp32. Where sum(h w key) cancels to almost
-// nothing, the gate's slope (1 / sqrt of it) magnifies its error, and a few such tokens set the error of the weights'
-// gradients: up to 1e-3 of them at widths of some hundred columns. So a token with a copy of |dot| < kSmallDot has
-// that sum formed once more in this way (for every token it cost 687 instead of 538 us at 16,384 tokens of
-// 4 x 5,120).
-constexpr float kSmallDot = 0.03125f;
-struct Sum2 {
-  float hi, lo;
-};
-
-__device__ __forceinline__ Sum2 add2(const Sum2& a, const Sum2& b) {
-  Sum2 r;
-  r.hi = __fadd_rn(a.hi, b.hi);
-  const float z = __fsub_rn(r.hi, a.hi);
-  r.lo = __fadd_rn(__fadd_rn(a.lo, b.lo), __fadd_rn(__fsub_rn(a.hi, __fsub_rn(r.hi, z)), __fsub_rn(b.hi, z)));
-  return r;
-}
-
-// one thread's part of sum(h w key): h * key and q_weight * k_weight are exact (bf16 factors), their product comes in
-// two parts, and both are summed
-__device__ __forceinline__ Sum2 dot_part(const Vec8& h, const Vec8& k, const Vec8& w) {
-  float2 hi = {}, lo = {};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 hk = __fmul2_rn(h.p[e], k.p[e]), term = __fmul2_rn(hk, w.p[e]);
-    const float2 sum = __fadd2_rn(hi, term), z = __fadd2_rn(sum, minus(hi));
-    lo = __fadd2_rn(lo, __ffma2_rn(hk, w.p[e], minus(term)));
-    lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(hi, minus(__fadd2_rn(sum, minus(z)))), __fadd2_rn(term, minus(z))));
-    hi = sum;
-  }
-  return add2(Sum2{hi.x, lo.x}, Sum2{hi.y, lo.y});
-}
-
-// warp_reduce_scatter for N sums of that kind
-template <int N>
-__device__ __forceinline__ Sum2 warp_reduce_scatter2(Sum2 (&s)[N], int lane) {
-#pragma unroll
-  for (int w = N / 2, off = 16; w >= 1; w /= 2, off /= 2) {
-    const bool up = lane & off;
-#pragma unroll
-    for (int j = 0; j < w; ++j) {
-      const Sum2 give = up ? s[j] : s[j + w];
-      const Sum2 keep = up ? s[j + w] : s[j];
-      s[j] = add2(keep, Sum2{__shfl_xor_sync(0xffffffffu, give.hi, off), __shfl_xor_sync(0xffffffffu, give.lo, off)});
-    }
-  }
-  Sum2 r = s[0];
-#pragma unroll
-  for (int off = 16 / N; off >= 1; off /= 2)
-    r = add2(r, Sum2{__shfl_xor_sync(0xffffffffu, r.hi, off), __shfl_xor_sync(0xffffffffu, r.lo, off)});
-  return r;
-}
-
-// Write v to the same shared variable of CTA `rank` and count its 4 bytes on that CTA's mbarrier. Unlike a
-// cluster barrier's release this waits for none of the thread's global stores.
-__device__ __forceinline__ void send(float* p, uint32_t bar, uint32_t rank, float v) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(
-                   tc::map_to_rank(tc::smem_u32(p), rank)),
-               "f"(v), "r"(tc::map_to_rank(bar, rank))
-               : "memory");
-}
+using namespace gate;
 
 // the most threads of a CTA: what the registers allow
 constexpr int max_threads(int hc, int cg) { return hc <= 2 ? 640 : (cg == 1 ? 320 : 384); }
@@ -201,11 +51,8 @@ constexpr int max_threads(int hc, int cg) { return hc <= 2 ? 640 : (cg == 1 ? 32
 // WHOLE: a CTA has whole rows. It brings each tensor's rows of a token, which lie together, by one copy: three for
 // 3 HC + 1 (9,557 tokens of 8 x 464: 80 -> 68 us), and has no cluster's code. One kernel for both kinds took 8,192 tokens
 // of 4 x 2,048 136 us instead of 122 and, two CTAs a token, 16,384 of 4 x 5,120 556 instead of 545.
-// Q8: x and kv are checkpoints in 8 bits (engram_gate_grad8): their rows are half as long, a stage holds dout's rows, then
-// theirs, and a thread reads the scales of its columns one token ahead (a byte for each of its rows). The values are
-// widened where bf16 ones are: the same arithmetic on the values that the checkpoints stand for.
 // withhold: the token whose sums the cluster's first CTA does not send (the test hook; -1: none)
-template <int HC, int CG, int S, bool WHOLE, bool Q8>
+template <int HC, int CG, int S, bool WHOLE>
 __global__ void __launch_bounds__(max_threads(HC, CG))
     gate_grad_kernel(const GateGradArgs a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
                      float* __restrict__ part, unsigned int* __restrict__ status, const int64_t withhold) {
@@ -213,8 +60,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   pdl_trigger();
   constexpr int kArrays = 3 * HC + 1;   // rows of a token: h and dout of the copies, their keys, the value
   const int cs = WHOLE ? 1 : ctas;      // CTAs of the cluster
-  // a stage's rows of dout and of the keys
-  constexpr int kU = Q8 ? 0 : WHOLE ? HC : 2 * HC, kK = WHOLE ? 2 * HC : HC;
+  constexpr int kU = WHOLE ? HC : 2 * HC, kK = WHOLE ? 2 * HC : HC;  // a stage's rows of dout and of the keys
   constexpr int N = 4 * HC;             // sums of a token
   constexpr int HPT = HC / CG;          // copies of a thread
   constexpr int M = 4 * HPT;            // sums of a warp
@@ -229,8 +75,7 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   const uint32_t rank = blockIdx.x % cs;
   const int per_group = nthr / CG, group = CG == 1 ? 0 : tid / per_group, gt = tid - group * per_group;
   const int g0 = group * HPT, wg = nw / CG;  // its first copy, and the warps of a group
-  const int stage_vecs = Q8 ? (2 * HC + 1) * nv / 2 + HC * nv : kArrays * nv;  // (Q8: nv is even)
-  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)S * stage_vecs);  // [CG - 1][2][per_group]
+  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)S * kArrays * nv);  // [CG - 1][2][per_group]
   float* red = reinterpret_cast<float*>(dvp + (CG - 1) * 2 * per_group);     // [2][CG][cs][wg][M]
   const int cnt = min(nv, (a.dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
   const bool on = gt < cnt;
@@ -239,76 +84,18 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   const int64_t col = row0 + 8 * gt;
   const int64_t gcol = (int64_t)g0 * a.dim + col;  // the thread's place in its first copy
   const uint32_t bar0 = tc::smem_u32(bars);
-  auto slot = [&](int st, int j) -> const uint4& { return smem[st * stage_vecs + j * nv + me]; };
-  // the scales of a token's checkpoint at the thread's columns: its copies', their keys', the value's
-  constexpr int kScales = Q8 ? 2 * HPT + 1 : 1;
-  uint32_t sc[kScales], sc_next[kScales];
-  const int64_t n_blocks = Q8 ? (a.dim + a.block - 1) / a.block : 0, my_block = Q8 ? (row0 + 8 * me) / a.block : 0;
-  auto fetch_scales = [&](int64_t t, bool open) {
-    if constexpr (Q8) {
-      if (!open) return;
-      const uint8_t* xs = a.xs + (t * HC + g0) * n_blocks + my_block;
-      const uint8_t* ks = a.kvs + (t * (HC + 1) + g0) * n_blocks + my_block;
-#pragma unroll
-      for (int i = 0; i < HPT; ++i) {
-        sc_next[i] = __ldg(xs + i * n_blocks);
-        sc_next[HPT + i] = __ldg(ks + i * n_blocks);
-      }
-      sc_next[2 * HPT] = __ldg(ks + (HC - g0) * n_blocks);
-    }
-  };
-  // A thread's 8 values of copy i (of its group), of that copy's key, and of the value; with Q8 without their scales,
-  // which are one power of two for all 8 and go into the sums and the copy's scalars: multiplied in there, they change
-  // no rounding.
-  auto packed = [&](int st, int j) {  // row j of the checkpoints' rows
-    return reinterpret_cast<const uint2*>(smem + st * stage_vecs + HC * nv)[j * nv + me];
-  };
-  auto h_of = [&](int st, int i) {
-    if constexpr (Q8) return widen8(packed(st, g0 + i));
-    else return widen8(slot(st, g0 + i));
-  };
-  auto k_of = [&](int st, int i) {
-    if constexpr (Q8) return widen8(packed(st, HC + g0 + i));
-    else return widen8(slot(st, kK + g0 + i));
-  };
-  auto v_of = [&](int st) {
-    if constexpr (Q8) return widen8(packed(st, 2 * HC));
-    else return widen8(slot(st, 3 * HC));
-  };
-  auto h_scale = [&](int i) { return widen_scale<ENGRAM_SCALE_E8M0>(sc[i]); };
-  auto k_scale = [&](int i) { return widen_scale<ENGRAM_SCALE_E8M0>(sc[HPT + i]); };
+  auto slot = [&](int st, int j) -> const uint4& { return smem[(st * kArrays + j) * nv + me]; };
   // one thread starts a token's copies
   uint32_t last = ~0u;  // (that thread's) bit st: the parity of the stage's last copies
   auto fetch = [&](int64_t t, int st, bool open) {
     if (t >= a.T || dead) return;
     last ^= 1u << st;
     const uint32_t bytes = 16 * cnt, bar = bar0 + 16 + 8 * st;
-    uint4* to = smem + (size_t)st * stage_vecs;
-    const uint16_t* u = a.dout + t * HC * a.dim + row0;
-    if constexpr (Q8) {
-      uint8_t* in = reinterpret_cast<uint8_t*>(to + HC * nv);  // the rows of x, then those of kv
-      const uint32_t part = 8 * cnt;
-      tc::mbar_arrive_expect_tx(bar, bytes * HC + (open ? part * (2 * HC + 1) : 0));
-      const uint8_t* h = static_cast<const uint8_t*>(a.x) + t * HC * a.dim + row0;
-      const uint8_t* k = static_cast<const uint8_t*>(a.kv) + t * (HC + 1) * a.dim + row0;
-      if (WHOLE) {
-        copy_row(to, u, bytes * HC, bar);
-        if (open) {
-          copy_row(in, h, part * HC, bar);
-          copy_row(in + 8 * HC * nv, k, part * (HC + 1), bar);
-        }
-        return;
-      }
-      for (int i = 0; i < HC; ++i) copy_row(to + i * nv, u + (int64_t)i * a.dim, bytes, bar);
-      if (open) {
-        for (int i = 0; i < HC; ++i) copy_row(in + 8 * i * nv, h + (int64_t)i * a.dim, part, bar);
-        for (int i = 0; i <= HC; ++i) copy_row(in + 8 * (HC + i) * nv, k + (int64_t)i * a.dim, part, bar);
-      }
-      return;
-    }
+    uint4* to = smem + (size_t)st * kArrays * nv;
     tc::mbar_arrive_expect_tx(bar, bytes * (open ? kArrays : HC));
-    const uint16_t* h = static_cast<const uint16_t*>(a.x) + t * HC * a.dim + row0;
-    const uint16_t* k = static_cast<const uint16_t*>(a.kv) + t * (HC + 1) * a.dim + row0;
+    const uint16_t* u = a.dout + t * HC * a.dim + row0;
+    const uint16_t* h = a.x + t * HC * a.dim + row0;
+    const uint16_t* k = a.kv + t * (HC + 1) * a.dim + row0;
     if (WHOLE) {
       copy_row(to + kU * nv, u, bytes * HC, bar);
       if (open) {
@@ -361,7 +148,6 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   for (int j = 0; j < S; ++j) open |= open_at(cluster + (int64_t)j * nc) << j;
   if (tid == 0)
     for (int j = 0; j < S - 1; ++j) fetch(cluster + (int64_t)j * nc, j, (open >> j) & 1);
-  fetch_scales(cluster, open & 1);
   int st = 0, buf = 0;
   uint32_t phase = 0;   // bit b: the parity of bars[b]'s current phase
   auto wait = [&](int b) {
@@ -373,11 +159,6 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
   };
   for (int64_t t = cluster; t < a.T; t += nc) {
     const uint32_t next = open_at(t + (int64_t)S * nc);
-    if constexpr (Q8) {
-#pragma unroll
-      for (int i = 0; i < kScales; ++i) sc[i] = sc_next[i];
-      fetch_scales(t + nc, (open >> 1) & 1);
-    }
     wait(2 + st);
     // the stage of the token before is free once every thread has passed this token's first barrier
     auto refill = [&]() {
@@ -388,10 +169,10 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
     if (open & 1) {
       float s[M];
       {
-        const Vec8 v = v_of(st);
+        const Vec8 v = widen8(slot(st, 3 * HC));
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = h_of(st, i), k = k_of(st, i), u = widen8(slot(st, kU + g0 + i));
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           float2 q[4] = {};
 #pragma unroll
@@ -403,13 +184,6 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[4 * i + e] = on ? q[e].x + q[e].y : 0.f;  // past the row: another vector's
-          if constexpr (Q8) {
-            const float hs = h_scale(i), ks = k_scale(i);
-            s[4 * i] = s[4 * i] * hs * hs;
-            s[4 * i + 1] = s[4 * i + 1] * ks * ks;
-            s[4 * i + 2] = s[4 * i + 2] * hs * ks;
-            s[4 * i + 3] *= widen_scale<ENGRAM_SCALE_E8M0>(sc[2 * HPT]);
-          }
         }
       }
       const float mine = warp_reduce_scatter<M>(s, lane);
@@ -453,13 +227,9 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
         Sum2 d[HPT];
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
-          const Vec8 h = h_of(st, i), k = k_of(st, i), w = weights(i);
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), w = weights(i);
           d[i] = Sum2{0.f, 0.f};
           if (on) d[i] = dot_part(h, k, w);
-          if constexpr (Q8) {
-            d[i].hi = d[i].hi * h_scale(i) * k_scale(i);
-            d[i].lo = d[i].lo * h_scale(i) * k_scale(i);
-          }
         }
         const Sum2 mine2 = warp_reduce_scatter2<HPT>(d, lane);
         float* to2 = red + (((buf * CG + group) * cs + rank) * wg + (warp - group * wg)) * M + 2 * (lane / (32 / HPT));
@@ -497,31 +267,16 @@ __global__ void __launch_bounds__(max_threads(HC, CG))
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
           const float4 g = scal[buf][g0 + i];  // gate, c, -e / A, -e / B
-          const Vec8 h = h_of(st, i), k = k_of(st, i), u = widen8(slot(st, kU + g0 + i));
+          const Vec8 h = widen8(slot(st, g0 + i)), k = widen8(slot(st, kK + g0 + i)), u = widen8(slot(st, kU + g0 + i));
           const Vec8 w = weights(i);
           Vec8 dh, dk;
-          // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
-          float cwk = g.y, eh = g.z, cwh = g.y, ek = g.w, chk = g.y;
-          if constexpr (Q8) {
-            const float hs = h_scale(i), ks = k_scale(i);
-            cwk *= ks;
-            eh *= hs;
-            cwh *= hs;
-            ek *= ks;
-            chk = chk * hs * ks;
-          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if constexpr (Q8) {
-              dh.p[e] = __ffma2_rn(__fmul2_rn(both(cwk), w.p[e]), k.p[e], __ffma2_rn(both(eh), h.p[e], u.p[e]));
-              dk.p[e] = __ffma2_rn(__fmul2_rn(both(cwh), w.p[e]), h.p[e], __fmul2_rn(both(ek), k.p[e]));
-            } else {
-              const float2 cw = __fmul2_rn(both(g.y), w.p[e]);
-              dh.p[e] = __ffma2_rn(cw, k.p[e], __ffma2_rn(both(g.z), h.p[e], u.p[e]));
-              dk.p[e] = __ffma2_rn(cw, h.p[e], __fmul2_rn(both(g.w), k.p[e]));
-            }
+            const float2 cw = __fmul2_rn(both(g.y), w.p[e]);
+            dh.p[e] = __ffma2_rn(cw, k.p[e], __ffma2_rn(both(g.z), h.p[e], u.p[e]));
+            dk.p[e] = __ffma2_rn(cw, h.p[e], __fmul2_rn(both(g.w), k.p[e]));
             dv.p[e] = __ffma2_rn(both(g.x), u.p[e], dv.p[e]);
-            dw[i].p[e] = __ffma2_rn(both(chk), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
+            dw[i].p[e] = __ffma2_rn(both(g.y), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
           }
           st8(dxt + i * a.dim, dh);
           st8(dkt + i * a.dim, dk);
@@ -630,8 +385,6 @@ __global__ void __launch_bounds__(THREADS) gate_weight_finish_kernel(const GateG
   *reinterpret_cast<float4*>(a.dk + j) = make_float4(s.x * lo(q.x), s.y * hi(q.x), s.z * lo(q.y), s.w * hi(q.y));
 }
 
-inline uint64_t round256(uint64_t b) { return (b + 255) & ~(uint64_t)255; }
-
 // the threads that an SM's registers hold
 constexpr int resident_threads(int hc) { return hc == 1 ? 896 : hc == 2 ? 736 : 384; }
 
@@ -644,7 +397,7 @@ struct Shape {
 // shared memory (8 copies: in two groups of threads; of more than 12,000 columns or so: in one, and two stages); more
 // CTAs a token when there are too few tokens for every SM. Few clusters rather than many when every cluster would see
 // few tokens: each leaves hc * dim partial sums behind.
-Shape shape_of(int64_t T, int32_t hc, int32_t dim, bool q8) {
+Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   Shape s;
   const int nvec = dim / 8;
   auto set = [&](int cs, int cg, int stages) {
@@ -652,10 +405,9 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, bool q8) {
     s.cg = cg;
     s.stages = stages;
     s.nv = (nvec + cs - 1) / cs;
-    if (q8) s.nv += s.nv & 1;  // rows of 8-byte vectors on 16-byte boundaries
     const int per_group = (s.nv + 31) / 32 * 32;
     s.threads = per_group * cg;
-    s.smem = (int64_t)stages * (q8 ? 32 * hc + 8 : (3 * hc + 1) * 16) * s.nv + (cg - 1) * per_group * 32ll +
+    s.smem = (int64_t)stages * (3 * hc + 1) * s.nv * 16 + (cg - 1) * per_group * 32ll +
              2ll * cs * (s.threads / 32) * 4 * (hc / cg) * 4;
     return s.threads <= max_threads(hc, cg) && s.smem <= kMaxSmem;
   };
@@ -681,10 +433,10 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, bool q8) {
   return s;
 }
 
-template <int HC, int CG, int S, bool WHOLE, bool Q8>
+template <int HC, int CG, int S, bool WHOLE>
 cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, int* parts, int64_t withhold,
                          cudaStream_t s) {
-  auto kern = gate_grad_kernel<HC, CG, S, WHOLE, Q8>;
+  auto kern = gate_grad_kernel<HC, CG, S, WHOLE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -726,24 +478,21 @@ cudaError_t launch_shape(const GateGradArgs& a, const Shape& sh, float* part, in
 
 }  // namespace
 
-uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim, bool q8) {
-  return round256((uint64_t)shape_of(T, hc, dim, q8).clusters * hc * dim * 4);
+uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim) {
+  return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
 }
 
 cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s, int64_t withhold) {
   float* part = static_cast<float*>(workspace);
   int parts = 0;
   if (a.T > 0) {
-    const Shape sh = shape_of(a.T, a.hc, a.dim, a.xs != nullptr);
+    const Shape sh = shape_of(a.T, a.hc, a.dim);
     cudaError_t e = cudaErrorInvalidValue;
     auto launch = [&](auto hc, auto cg, auto stages) {
       constexpr int HC = decltype(hc)::value, CG = decltype(cg)::value, S = decltype(stages)::value;
-      if constexpr (S == 3) {  // with two stages rows are too wide for one CTA
-        if (sh.cs == 1 && a.xs != nullptr) return launch_shape<HC, CG, S, true, true>(a, sh, part, &parts, withhold, s);
-        if (sh.cs == 1) return launch_shape<HC, CG, S, true, false>(a, sh, part, &parts, withhold, s);
-      }
-      if (a.xs != nullptr) return launch_shape<HC, CG, S, false, true>(a, sh, part, &parts, withhold, s);
-      return launch_shape<HC, CG, S, false, false>(a, sh, part, &parts, withhold, s);
+      if constexpr (S == 3)  // with two stages rows are too wide for one CTA
+        if (sh.cs == 1) return launch_shape<HC, CG, S, true>(a, sh, part, &parts, withhold, s);
+      return launch_shape<HC, CG, S, false>(a, sh, part, &parts, withhold, s);
     };
     using std::integral_constant;
     const integral_constant<int, 1> one;
@@ -759,11 +508,15 @@ cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_
     }
     if (e != cudaSuccess) return e;
   }
+  return launch_gate_weight_finish(a, part, parts, s);
+}
+
+cudaError_t launch_gate_weight_finish(const GateGradArgs& a, const float* part, int parts, cudaStream_t s) {
   const int n = a.hc * a.dim;
   if (parts > 256)
-    return launch_pdl(gate_weight_finish_kernel<8, 1024>, dim3((n + 31) / 32), dim3(1024), 0, s, a, (const float*)part,
+    return launch_pdl(gate_weight_finish_kernel<8, 1024>, dim3((n + 31) / 32), dim3(1024), 0, s, a, part,
                       parts);
-  return launch_pdl(gate_weight_finish_kernel<32, 256>, dim3((n + 127) / 128), dim3(256), 0, s, a, (const float*)part,
+  return launch_pdl(gate_weight_finish_kernel<32, 256>, dim3((n + 127) / 128), dim3(256), 0, s, a, part,
                     parts);
 }
 

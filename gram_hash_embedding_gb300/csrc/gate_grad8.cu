@@ -1,0 +1,560 @@
+// The gradient of the Engram gate from activation checkpoints in 8 bits (sm_103a): the formulas of gate_grad.cu on the
+// values code * scale that engram_quantize8 left of x and kv.
+//
+// Design: as there, a cluster of CTAs takes whole tokens in turn, bulk copies bring a token's rows into shared memory, a
+// thread owns 8 columns of every copy from the first token to the last, and per token there is one exchange of 4 hc sums.
+// The codes halve what is read (0.79 of the bytes in all), but each value has to be widened twice, and with one token at a
+// time that chain (sums, exchange, scalars, outputs) took longer than the memory: 16,384 tokens of 4 x 5,120 677 us, floor
+// 434. So the chain is cut in two and runs over two tokens at a time:
+//   - the threads form the sums of token i + 1 and send them, then write the outputs of token i, whose scalars are ready;
+//   - a warp of its own gathers a token's sums, forms its scalars while the others work, and starts the copies of the
+//     tokens ahead.
+// They meet on mbarriers; nothing waits for all threads of a CTA. A block's scale is one power of two for all 8 values of a
+// thread's row, so it goes into the sums and the scalars instead of the values: it changes no rounding there.
+//
+// What may be written while another role, or another CTA of the cluster, still reads (tokens here are open ones, c their
+// number): a thread sends sums c + 2 after it has seen the scalars of c, which need the sums c of every CTA, which these sent
+// after they had seen the scalars of c - 2; so four halves of the sums' buffer are enough. Scalars c + 2 need every thread's
+// sums c + 2, sent after its outputs of c: two. The sums formed once more (below) of the second token after need the same:
+// two.
+#include <algorithm>
+#include <cstdint>
+#include <type_traits>
+
+#include "dequant.cuh"
+#include "engram_internal.cuh"
+#include "gate_grad.cuh"
+#include "proj.cuh"
+#include "tc_ptx.cuh"
+#include "train.cuh"
+
+namespace engram {
+namespace {
+
+using namespace gate;
+
+constexpr int kMaxStages = 5;
+
+// the most threads that own columns: what the registers allow, with one warp more for the scalars
+constexpr int max_owners(int hc) { return hc == 1 ? 736 : hc == 2 ? 608 : 352; }
+
+// 8 E4M3 codes, without their block's scale
+__device__ __forceinline__ Vec8 widen_codes(const uint2& v) {
+  const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), r.p[i].x, r.p[i].y);
+  return r;
+}
+
+// A checkpoint's scale 2^(b - 127). A NaN (255) comes out as infinity: the codes of such a block are 0, and 0 times it is a
+// NaN again.
+__device__ __forceinline__ float pow2(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
+
+// HC copies in CG groups of threads, HC / CG copies each of the same columns (8 copies in one thread leave too few threads
+// on an SM). WHOLE: a CTA has whole rows, which lie together: three copies a token instead of 3 HC + 1.
+// stages: tokens in shared memory. withhold: the token whose sums the cluster's first CTA does not send (the test hook).
+template <int HC, int CG, bool WHOLE>
+__global__ void __launch_bounds__(max_owners(HC) + 32)
+    gate_grad8_kernel(const GateGrad8Args a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
+                      const int stages, float* __restrict__ part, unsigned int* __restrict__ status,
+                      const int64_t withhold) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int N = 4 * HC;              // sums of a token
+  constexpr int HPT = HC / CG;           // copies of a thread
+  constexpr int M = 4 * HPT;             // sums of a warp
+  constexpr bool kKeepW = HPT <= 4;      // the weights stay in registers; 8 copies read them again (L1, L2)
+  constexpr int kStageVecs2 = 4 * HC + 1;  // a stage, in halves of 16 bytes for each vector: dout's rows, then the codes'
+  extern __shared__ uint4 smem[];
+  __shared__ float4 scal[2][HC];
+  __shared__ int again[2];
+  __shared__ volatile int dead;  // a wait has run out: nothing more is fetched or sent, the results are not to be used
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4 + 2 + 2 + 1];
+  const int dim = a.g.dim;
+  const int64_t T = a.g.T;
+  const int cs = WHOLE ? 1 : ctas;
+  const int tid = threadIdx.x, owners = blockDim.x - 32, lane = tid & 31, warp = tid >> 5, nw = owners >> 5;
+  const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
+  const uint32_t rank = blockIdx.x % cs;
+  const int per_group = owners / CG, group = CG == 1 ? 0 : min(tid / per_group, CG - 1), gt = tid - group * per_group;
+  const int g0 = group * HPT, wg = nw / CG;  // its first copy, and the warps of a group
+  const int stage_vecs = kStageVecs2 * nv / 2;  // nv is even
+  float4* dvp = reinterpret_cast<float4*>(smem + (size_t)stages * stage_vecs);  // [2][CG - 1][2][per_group]
+  float* red = reinterpret_cast<float*>(dvp + 2 * (CG - 1) * 2 * per_group);    // [4][CG][cs][wg][M]
+  const int parts_of_group = cs * wg, red_half = CG * parts_of_group * M;
+  float* red2 = red + 4 * red_half;                                             // [2][CG][cs][wg][2 HPT]
+  const int red2_half = CG * parts_of_group * 2 * HPT;
+  const int cnt = min(nv, (dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
+  const int64_t row0 = 8 * (int64_t)rank * nv;           // its first column
+  const uint32_t bar0 = tc::smem_u32(bars);
+  const uint32_t kFull = 0, kEmpty = kMaxStages, kSums = 2 * kMaxStages, kScal = kSums + 4, kSums2 = kScal + 2, kScal2 = kSums2 + 2;
+  auto bar = [&](uint32_t i) { return bar0 + 8 * i; };
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (!dead && !tc::mbar_wait(bar(b), parity, const_cast<const volatile int*>(&dead))) {
+      dead = 1;
+      atomicOr(status, ENGRAM_STATUS_TIMEOUT);
+    }
+  };
+  auto open_at = [&](int64_t t) { return t < T && (a.g.mask == nullptr || a.g.mask[t] != 0); };
+
+  if (tid == 0) {
+    dead = 0;
+    for (int i = 0; i < kMaxStages; ++i) {
+      tc::mbar_init(bar(kFull + i), 1);
+      tc::mbar_init(bar(kEmpty + i), nw);
+    }
+    for (uint32_t i = kSums; i <= kScal2; ++i)
+      tc::mbar_init(bar(i), WHOLE && (i < kScal || i == kSums2 || i == kSums2 + 1) ? nw : 1);
+    tc::fence_barrier_init();
+  }
+  if (cs > 1) tc::cluster_sync();  // every CTA's barriers exist before another CTA sends to them
+  else __syncthreads();
+
+  if (warp == nw) {
+    // ------------------------------------------------------------ copies and scalars
+    uint32_t last = ~0u;  // bit s: the parity of the stage's last copies
+    auto fetch = [&](int64_t t, int s, bool open) {
+      if (t >= T || dead) return;
+      last ^= 1u << s;
+      const uint32_t b = bar(kFull + s), bytes = 16 * cnt, codes = 8 * cnt;
+      tc::mbar_arrive_expect_tx(b, bytes * HC + (open ? codes * (2 * HC + 1) : 0));
+      uint8_t* to = reinterpret_cast<uint8_t*>(smem + (size_t)s * stage_vecs);
+      uint8_t* in = to + 16 * HC * nv;  // the rows of x, then those of kv
+      const uint16_t* u = a.g.dout + t * HC * dim + row0;
+      const uint8_t* h = a.x + t * HC * dim + row0;
+      const uint8_t* k = a.kv + t * (HC + 1) * dim + row0;
+      if constexpr (WHOLE) {
+        copy_row(to, u, bytes * HC, b);
+        if (open) {
+          copy_row(in, h, codes * HC, b);
+          copy_row(in + 8 * HC * nv, k, codes * (HC + 1), b);
+        }
+      }
+      if constexpr (!WHOLE) {
+        for (int i = 0; i < HC; ++i) copy_row(to + 16 * i * nv, u + (int64_t)i * dim, bytes, b);
+        if (open) {
+          for (int i = 0; i < HC; ++i) copy_row(in + 8 * i * nv, h + (int64_t)i * dim, codes, b);
+          for (int i = 0; i <= HC; ++i) copy_row(in + 8 * (HC + i) * nv, k + (int64_t)i * dim, codes, b);
+        }
+      }
+    };
+    // bit j of `open`: the mask of the cluster's token j places on
+    uint32_t open = 0;
+    for (int j = 0; j < stages; ++j) open |= (open_at(cluster + (int64_t)j * nc) ? 1u : 0u) << j;
+    if (lane == 0)
+      for (int s = 0; s < stages; ++s) fetch(cluster + (int64_t)s * nc, s, (open >> s) & 1);
+    uint32_t c = 0, c2 = 0;  // open tokens, and those whose sums were formed once more
+    int s = 0, ps = stages - 1;   // stages of the token and of the one before
+    uint32_t pass = 0;            // how often the ring has gone round before the token before
+    for (int64_t t = cluster; t < T; t += nc) {
+      const uint32_t next = open_at(t + (int64_t)stages * nc) ? 1u : 0u;
+      if (open & 1) {
+        const uint32_t b = c & 1;
+        if (!WHOLE && lane == 0 && !dead)
+          tc::mbar_arrive_expect_tx(bar(kSums + (c & 3)), (uint32_t)(cs * nw * M * 4));
+        wait(kSums + (c & 3), (c >> 2) & 1);
+        // lane l: every (32 / N)-th part of sum l % N by the warps of its copy's group, which lie together
+        const float* from = red + (c & 3) * red_half + (lane % N / M) * parts_of_group * M + lane % M;
+        float sum = 0.f;
+#pragma unroll 5
+        for (int j = lane / N; j < parts_of_group; j += 32 / N) sum += from[j * M];
+#pragma unroll
+        for (int off = N; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        float f[4];  // the sums of copy lane % HC
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __shfl_sync(0xffffffffu, sum, 4 * (lane % HC) + e);
+        CopyGrad g = copy_grad(f[0], f[1], f[2], f[3], rd, a.g.eps, inv_sqrt_dim);
+        if (lane < HC) scal[b][lane] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+        // the same sums in the same order in every CTA of the cluster, so the same answer
+        const bool any = __any_sync(0xffffffffu, g.m < kSmallDot);
+        if (lane == 0) again[b] = any;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(kScal + b));
+        if (any) {  // sum(h w key) once more, in twice the precision
+          const uint32_t b2 = c2 & 1;
+          if (!WHOLE && lane == 0 && !dead)
+            tc::mbar_arrive_expect_tx(bar(kSums2 + b2), (uint32_t)(cs * nw * 2 * HPT * 4));
+          wait(kSums2 + b2, (c2 >> 1) & 1);
+          const float* from2 = red2 + b2 * red2_half + (lane % HC / HPT) * parts_of_group * 2 * HPT + 2 * (lane % HPT);
+          Sum2 sum2 = {0.f, 0.f};
+          for (int j = lane / HC; j < parts_of_group; j += 32 / HC)
+            sum2 = add2(sum2, Sum2{from2[j * 2 * HPT], from2[j * 2 * HPT + 1]});
+#pragma unroll
+          for (int off = HC; off < 32; off *= 2)
+            sum2 = add2(sum2, Sum2{__shfl_xor_sync(0xffffffffu, sum2.hi, off), __shfl_xor_sync(0xffffffffu, sum2.lo, off)});
+          g = copy_grad(f[0], f[1], sum2.hi + sum2.lo, f[3], rd, a.g.eps, inv_sqrt_dim);
+          if (lane < HC) scal[b][lane] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(kScal2));
+          ++c2;
+        }
+        ++c;
+      }
+      if (t != cluster) {  // the stage of the token before, once its outputs are written
+        if (lane == 0 && t + (int64_t)(stages - 1) * nc < T) {
+          wait(kEmpty + ps, pass & 1);
+          fetch(t + (int64_t)(stages - 1) * nc, ps, (open >> (stages - 1)) & 1);
+        }
+        __syncwarp();
+      }
+      ps = s;
+      if (++s == stages) s = 0;
+      if (ps == 0 && t != cluster) ++pass;
+      open = open >> 1 | next << (stages - 1);
+    }
+    if (dead && lane == 0)  // copies may still be on their way into this CTA's memory
+      for (int s = 0; s < stages; ++s)
+        if (cluster + (int64_t)s * nc < T) tc::mbar_wait(bar(kFull + s), (last >> s) & 1, nullptr);
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ owners of columns
+    const bool on = gt < cnt;
+    const int me = min(gt, cnt - 1);  // threads past the row read its last vector and use nothing of it
+    const int64_t col = row0 + 8 * gt;
+    const int64_t gcol = (int64_t)g0 * dim + col;  // the thread's place in its first copy
+    const int64_t n_blocks = (dim + a.block - 1) / a.block, my_block = (row0 + 8 * me) / a.block;
+    auto u_of = [&](int s, int i) { return widen8(smem[s * stage_vecs + (g0 + i) * nv + me]); };
+    auto codes = [&](int s, int j) {  // row j of the checkpoints' rows
+      return widen_codes(reinterpret_cast<const uint2*>(smem + s * stage_vecs + HC * nv)[j * nv + me]);
+    };
+    // the scales at the thread's columns: its copies', their keys', the value's
+    struct Scales {
+      uint32_t h[HPT], k[HPT], v;
+    };
+    auto load_scales = [&](Scales& s, int64_t t) {
+      const uint8_t* xs = a.xs + (t * HC + g0) * n_blocks + my_block;
+      const uint8_t* ks = a.kvs + (t * (HC + 1) + g0) * n_blocks + my_block;
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        s.h[i] = __ldg(xs + i * n_blocks);
+        s.k[i] = __ldg(ks + i * n_blocks);
+      }
+      s.v = __ldg(ks + (HC - g0) * n_blocks);
+    };
+    auto load_weights = [&](int i) {
+      Vec8 w = {};
+      if (on) {
+        const Vec8 q = widen8(__ldg(reinterpret_cast<const uint4*>(a.g.qw + gcol + (int64_t)i * dim)));
+        const Vec8 k = widen8(__ldg(reinterpret_cast<const uint4*>(a.g.kw + gcol + (int64_t)i * dim)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.p[e] = __fmul2_rn(q.p[e], k.p[e]);
+      }
+      return w;
+    };
+    Vec8 w_kept[kKeepW ? HPT : 1];
+    if constexpr (kKeepW) {
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) w_kept[i] = load_weights(i);
+    }
+    auto weights = [&](int i) {
+      if constexpr (kKeepW) return w_kept[i];
+      else return load_weights(i);
+    };
+    Vec8 dw[HPT] = {};
+    // the sums of token t, open token number c, from stage s
+    auto sums = [&](int64_t t, uint32_t c, int s, const Scales& sc) {
+      float m[M] = {};
+      if (on) {  // past the row: another thread's vector
+        const Vec8 v = codes(s, 2 * HC);
+        const float vs = pow2(sc.v);
+#pragma unroll
+        for (int i = 0; i < HPT; ++i) {
+          const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), u = u_of(s, i);
+          const Vec8 w = weights(i);
+          float2 q[4] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            q[0] = __ffma2_rn(h.p[e], h.p[e], q[0]);
+            q[1] = __ffma2_rn(k.p[e], k.p[e], q[1]);
+            q[2] = __ffma2_rn(__fmul2_rn(h.p[e], k.p[e]), w.p[e], q[2]);
+            q[3] = __ffma2_rn(u.p[e], v.p[e], q[3]);
+          }
+          const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+          m[4 * i] = (q[0].x + q[0].y) * hs * hs;
+          m[4 * i + 1] = (q[1].x + q[1].y) * ks * ks;
+          m[4 * i + 2] = (q[2].x + q[2].y) * hs * ks;
+          m[4 * i + 3] = (q[3].x + q[3].y) * vs;
+        }
+      }
+      const float mine = warp_reduce_scatter<M>(m, lane);
+      const bool sent = !dead && (t != withhold || rank != 0);
+      float* to = red + (c & 3) * red_half + ((group * cs + rank) * wg + (warp - group * wg)) * M + lane / (32 / M);
+      if constexpr (WHOLE) {  // (a launch without clusters has no asynchronous stores to a CTA of one)
+        if (lane % (32 / M) == 0) *to = mine;
+        __syncwarp();
+        if (lane == 0 && sent) tc::mbar_arrive(bar(kSums + (c & 3)));
+      } else if (lane % (32 / M) == 0 && sent) {
+        for (int r = 0; r < cs; ++r) send(to, bar(kSums + (c & 3)), r, mine);
+      }
+    };
+    bool open = open_at(cluster), next_open = open_at(cluster + nc);
+    Scales sc = {}, ahead = {};  // of the token, and of the next one
+    if (open) load_scales(sc, cluster);
+    if (next_open) load_scales(ahead, cluster + nc);
+    if (cluster < T) wait(kFull, 0);
+    if (open) sums(cluster, 0, 0, sc);
+    uint32_t c = 0, c2 = 0, pass = 0;  // open tokens, those whose sums were formed once more, rounds of the ring
+    uint32_t odd = 0;                  // CG > 1: the token's half of dvp, and its barrier
+    int s = 0;
+    for (int64_t t = cluster; t < T; t += nc) {
+      const bool then_open = open_at(t + 2 * (int64_t)nc);
+      Scales beyond = {};  // of the token after the next: on their way while this one's outputs are formed
+      const int ns = s + 1 == stages ? 0 : s + 1;
+      if (t + nc < T) {
+        wait(kFull + ns, (ns == 0 ? pass + 1 : pass) & 1);
+        if (next_open) sums(t + nc, c + (open ? 1 : 0), ns, ahead);
+        if (then_open) load_scales(beyond, t + 2 * (int64_t)nc);
+      }
+      uint16_t* dxt = a.g.dx + t * HC * dim + gcol;
+      uint16_t* dkt = a.g.dkv + t * (HC + 1) * dim + gcol;
+      if (open) {
+        const uint32_t b = c & 1;
+        wait(kScal + b, (c >> 1) & 1);
+        if (again[b]) {  // sum(h w key) once more, in twice the precision
+          Sum2 d[HPT];
+#pragma unroll
+          for (int i = 0; i < HPT; ++i) {
+            const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), w = weights(i);
+            const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+            d[i] = Sum2{0.f, 0.f};
+            if (on) d[i] = dot_part(h, k, w);
+            d[i].hi = d[i].hi * hs * ks;
+            d[i].lo = d[i].lo * hs * ks;
+          }
+          const Sum2 mine = warp_reduce_scatter2<HPT>(d, lane);
+          float* to = red2 + (c2 & 1) * red2_half + ((group * cs + rank) * wg + (warp - group * wg)) * 2 * HPT +
+                      2 * (lane / (32 / HPT));
+          if constexpr (WHOLE) {
+            if (lane % (32 / HPT) == 0) {
+              to[0] = mine.hi;
+              to[1] = mine.lo;
+            }
+            __syncwarp();
+            if (lane == 0 && !dead) tc::mbar_arrive(bar(kSums2 + (c2 & 1)));
+          } else if (lane % (32 / HPT) == 0 && !dead) {
+            for (int r = 0; r < cs; ++r) {
+              send(to, bar(kSums2 + (c2 & 1)), r, mine.hi);
+              send(to + 1, bar(kSums2 + (c2 & 1)), r, mine.lo);
+            }
+          }
+          wait(kScal2, c2 & 1);
+          ++c2;
+        }
+        Vec8 dv = {};
+        float4* mine = dvp + odd * (CG - 1) * 2 * per_group;
+        if (on) {
+#pragma unroll
+          for (int i = 0; i < HPT; ++i) {
+            const float4 g = scal[b][g0 + i];  // gate, c, -e / A, -e / B
+            const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), u = u_of(s, i);
+            const Vec8 w = weights(i);
+            const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+            // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
+            const float cwk = g.y * ks, eh = g.z * hs, cwh = g.y * hs, ek = g.w * ks, chk = g.y * hs * ks;
+            Vec8 dh, dk;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              dh.p[e] = __ffma2_rn(__fmul2_rn(both(cwk), w.p[e]), k.p[e], __ffma2_rn(both(eh), h.p[e], u.p[e]));
+              dk.p[e] = __ffma2_rn(__fmul2_rn(both(cwh), w.p[e]), h.p[e], __fmul2_rn(both(ek), k.p[e]));
+              dv.p[e] = __ffma2_rn(both(g.x), u.p[e], dv.p[e]);
+              dw[i].p[e] = __ffma2_rn(both(chk), __fmul2_rn(h.p[e], k.p[e]), dw[i].p[e]);
+            }
+            st8(dxt + i * dim, dh);
+            st8(dkt + i * dim, dk);
+          }
+          if (group > 0) {
+            mine[(2 * group - 2) * per_group + gt] = make_float4(dv.p[0].x, dv.p[0].y, dv.p[1].x, dv.p[1].y);
+            mine[(2 * group - 1) * per_group + gt] = make_float4(dv.p[2].x, dv.p[2].y, dv.p[3].x, dv.p[3].y);
+          }
+        }
+        if constexpr (CG > 1) {  // the other groups go on; group 0 waits for their parts of the value's gradient
+          if (odd) {
+            if (group > 0) asm volatile("bar.arrive 2, %0;" ::"r"(owners) : "memory");
+            else asm volatile("bar.sync 2, %0;" ::"r"(owners) : "memory");
+          } else {
+            if (group > 0) asm volatile("bar.arrive 1, %0;" ::"r"(owners) : "memory");
+            else asm volatile("bar.sync 1, %0;" ::"r"(owners) : "memory");
+          }
+        }
+        if (group == 0 && on) {
+#pragma unroll
+          for (int g = 0; g < CG - 1; ++g) {
+            const float4 lo = mine[2 * g * per_group + gt], hi = mine[(2 * g + 1) * per_group + gt];
+            dv.p[0] = __fadd2_rn(dv.p[0], make_float2(lo.x, lo.y));
+            dv.p[1] = __fadd2_rn(dv.p[1], make_float2(lo.z, lo.w));
+            dv.p[2] = __fadd2_rn(dv.p[2], make_float2(hi.x, hi.y));
+            dv.p[3] = __fadd2_rn(dv.p[3], make_float2(hi.z, hi.w));
+          }
+          st8(a.g.dkv + (t * (HC + 1) + HC) * dim + col, dv);
+        }
+        ++c;
+      } else if (on) {  // masked: dout passes through, whatever the checkpoints hold
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < HPT; ++i) {
+          *reinterpret_cast<uint4*>(dxt + i * dim) = smem[s * stage_vecs + (g0 + i) * nv + me];
+          *reinterpret_cast<uint4*>(dkt + i * dim) = z;
+        }
+        if (group == 0) *reinterpret_cast<uint4*>(a.g.dkv + (t * (HC + 1) + HC) * dim + col) = z;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kEmpty + s));
+      odd ^= 1;
+      sc = ahead;
+      ahead = beyond;
+      open = next_open;
+      next_open = then_open;
+      s = ns;
+      if (s == 0) ++pass;
+    }
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        float* to = part + (int64_t)cluster * HC * dim + gcol + (int64_t)i * dim;
+        const float2* d = dw[i].p;
+        *reinterpret_cast<float4*>(to) = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
+        *reinterpret_cast<float4*>(to + 4) = make_float4(d[2].x, d[2].y, d[3].x, d[3].y);
+      }
+    }
+  }
+  __syncthreads();
+  if (dead) {  // sums may still be on their way into another CTA's memory
+    const uint64_t t0 = tc::global_timer_ns();
+    while (tc::global_timer_ns() - t0 < kSettleNs) {}
+  }
+  if (cs > 1) tc::cluster_sync();  // no CTA leaves while another may send to it
+}
+
+// the threads that an SM's registers hold
+constexpr int resident_threads(int hc) { return hc == 1 ? 672 : hc == 2 ? 640 : 384; }
+
+struct Shape {
+  int cs, cg, nv, owners, stages;  // CTAs per cluster, groups of copies, vectors and column-owning threads per CTA
+  int64_t smem, clusters;
+};
+
+// As in gate_grad.cu: the smallest cluster (with one exception) whose CTAs hold their columns in registers and three
+// stages of shared memory, more CTAs a token when there are too few tokens for every SM; then as many stages, up to
+// kMaxStages, as cost no CTA its place on an SM.
+Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
+  Shape s;
+  const int nvec = dim / 8;
+  auto set = [&](int cs, int cg, int stages) {
+    s.cs = cs;
+    s.cg = cg;
+    s.stages = stages;
+    s.nv = (nvec + cs - 1) / cs;
+    s.nv += s.nv & 1;  // rows of codes begin on 16 bytes
+    const int per_group = (s.nv + 31) / 32 * 32, hpt = hc / cg;
+    s.owners = per_group * cg;
+    s.smem = (int64_t)stages * (4 * hc + 1) * s.nv * 8 + 2ll * (cg - 1) * per_group * 32 +
+             (int64_t)cs * (s.owners / 32) * 4 * (4 * 4 * hpt + 2 * 2 * hpt);
+    return s.owners <= max_owners(hc) && s.smem <= kMaxSmem;
+  };
+  const int cg = hc == 8 ? 2 : 1;
+  int cs = 1;
+  while (cs < 8 && !set(cs, cg, 3)) cs *= 2;
+  while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
+  // CTAs resident on an SM, by shared memory and registers
+  auto resident = [&]() {
+    return std::max<int64_t>(
+        1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / (s.owners + 32)));
+  };
+  if (!set(cs, cg, 3)) {
+    if (!set(cs, 1, 3)) set(cs, 1, 2);  // 8 copies of more than 12,000 columns or so
+  } else if (cs < 8) {
+    const int64_t columns = s.nv * resident();
+    set(cs * 2, cg, 3);
+    if (s.nv * resident() * 5 < columns * 7) set(cs, cg, 3);
+  }
+  const int64_t fit = resident();
+  while (s.stages < kMaxStages) {
+    const Shape before = s;
+    if (set(s.cs, s.cg, s.stages + 1) && resident() == fit) continue;
+    s = before;
+    break;
+  }
+  s.clusters = std::min({T, std::max<int64_t>(1, kSms * fit / s.cs), std::max<int64_t>(kSms / s.cs, (T + 3) / 4)});
+  return s;
+}
+
+template <int HC, int CG, bool WHOLE>
+cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
+                         cudaStream_t s) {
+  auto kern = gate_grad8_kernel<HC, CG, WHOLE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
+  if (e != cudaSuccess) return e;
+  const int threads = sh.owners + 32;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = ENGRAM_PDL;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = sh.cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = sh.smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  // CTAs that hold whole rows launch without the attribute: as clusters of one, 8 at most are resident on an SM
+  cfg.numAttrs = sh.cs > 1 ? 2 : 1;
+  // no more clusters than can be resident: one that had to wait would run its share of the tokens alone
+  cfg.gridDim = dim3((unsigned)(sh.clusters * sh.cs));
+  int64_t clusters = sh.clusters;
+  if (sh.cs > 1 && clusters > 1) {
+    int resident = 0;
+    e = cudaOccupancyMaxActiveClusters(&resident, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    clusters = std::max<int64_t>(1, std::min<int64_t>(clusters, resident));
+  } else if (clusters > kSms) {
+    int resident = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, sh.smem);
+    if (e != cudaSuccess) return e;
+    clusters = std::min<int64_t>(clusters, std::max<int64_t>(1, resident) * kSms);
+  }
+  unsigned int* status = nullptr;
+  e = device_status_word(&status);
+  if (e != cudaSuccess) return e;
+  *parts = (int)clusters;
+  cfg.gridDim = dim3((unsigned)(clusters * sh.cs));
+  return cudaLaunchKernelEx(&cfg, kern, a, 1.0f / (float)a.g.dim, (float)(1.0 / sqrt((double)a.g.dim)), sh.nv, sh.cs,
+                            sh.stages, part, status, withhold);
+}
+
+template <int HC, int CG>
+cudaError_t launch_copies(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
+                          cudaStream_t s) {
+  if constexpr (HC / CG < 8)  // with 8 copies a thread rows are too wide for one CTA
+    if (sh.cs == 1) return launch_shape<HC, CG, true>(a, sh, part, parts, withhold, s);
+  return launch_shape<HC, CG, false>(a, sh, part, parts, withhold, s);
+}
+
+}  // namespace
+
+uint64_t gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim) {
+  return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
+}
+
+cudaError_t launch_gate_grad8(const GateGrad8Args& a, void* workspace, cudaStream_t s, int64_t withhold) {
+  float* part = static_cast<float*>(workspace);
+  int parts = 0;
+  if (a.g.T > 0) {
+    const Shape sh = shape_of(a.g.T, a.g.hc, a.g.dim);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.g.hc) {
+      case 1: e = launch_copies<1, 1>(a, sh, part, &parts, withhold, s); break;
+      case 2: e = launch_copies<2, 1>(a, sh, part, &parts, withhold, s); break;
+      case 4: e = launch_copies<4, 1>(a, sh, part, &parts, withhold, s); break;
+      case 8:
+        e = sh.cg == 2 ? launch_copies<8, 2>(a, sh, part, &parts, withhold, s)
+                       : launch_copies<8, 1>(a, sh, part, &parts, withhold, s);
+        break;
+    }
+    if (e != cudaSuccess) return e;
+  }
+  return launch_gate_weight_finish(a.g, part, parts, s);
+}
+
+}  // namespace engram

@@ -14,7 +14,9 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFly = 4;  // units in flight a thread
+// Units in flight a thread: rows read back (65,536 x 24 of 128 values: 1, 2, 4 and 8 take 110, 93, 94 and 95 us; small calls
+// take 2.5 us with 2 and 3.0 with 4), and rows gathered as they stand (16,384 x 24 of 256: 24, 20, 19 and 22 us)
+constexpr int kFlyValues = 2, kFlyOperand = 4;
 
 __device__ __forceinline__ float scale4(uint32_t b, bool nv) {
   return nv ? widen_scale<ENGRAM_SCALE_E4M3>(b) : widen_scale<ENGRAM_SCALE_E8M0>(b);
@@ -50,11 +52,11 @@ __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, 
   pdl_trigger();
   const uint32_t per_row = a.dim / 16;
   const int64_t spr = a.dim / a.block;
-  const N u0 = (N)blockIdx.x * (kThreads * kFly) + threadIdx.x;
-  int64_t r[kFly];
-  uint32_t k[kFly];
+  const N u0 = (N)blockIdx.x * (kThreads * kFlyValues) + threadIdx.x;
+  int64_t r[kFlyValues];
+  uint32_t k[kFlyValues];
 #pragma unroll
-  for (int i = 0; i < kFly; ++i) {
+  for (int i = 0; i < kFlyValues; ++i) {
     const N u = u0 + i * kThreads;
     r[i] = -1;
     k[i] = 0;
@@ -64,10 +66,10 @@ __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, 
       r[i] = a.idx[id_at<N>(a, e)];
     }
   }
-  uint2 w[kFly];
-  uint32_t b[kFly];
+  uint2 w[kFlyValues];
+  uint32_t b[kFlyValues];
 #pragma unroll
-  for (int i = 0; i < kFly; ++i) {
+  for (int i = 0; i < kFlyValues; ++i) {
     w[i] = make_uint2(0u, 0u);
     b[i] = 0u;
     if (r[i] >= 0 && r[i] < a.table_rows) {
@@ -76,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, 
     }
   }
 #pragma unroll
-  for (int i = 0; i < kFly; ++i) {
+  for (int i = 0; i < kFlyValues; ++i) {
     const N u = u0 + i * kThreads;
     if (u >= units) continue;
     float v[16];
@@ -91,8 +93,9 @@ __global__ void __launch_bounds__(kThreads) lookup4_kernel(const Lookup4Args a, 
   }
 }
 
-// A unit is a piece of 32 values where dim allows (BYTES = 16), else of 16 (BYTES = 8), with its scales.
-template <bool NV, int BYTES, typename N>
+// A unit is a piece of 32 values where dim allows (BYTES = 16), else of 16 (BYTES = 8), with its scales; with WORDS (rows of
+// whole groups of four scales, on 4-byte boundaries) the first piece of each group moves the group's four at once.
+template <bool NV, int BYTES, bool WORDS, typename N>
 __global__ void __launch_bounds__(kThreads)
     lookup4_operand_kernel(const Lookup4Args a, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, const N units) {
   pdl_wait();
@@ -103,43 +106,69 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t spr = a.dim / a.block;
   const int64_t groups = scale_groups((int64_t)a.n_cols * a.dim, a.block);
   const int64_t all = spr * a.n_cols;  // scales of a token
-  const N u0 = (N)blockIdx.x * (kThreads * kFly) + threadIdx.x;
+  const N u0 = (N)blockIdx.x * (kThreads * kFlyOperand) + threadIdx.x;
+  int64_t r[kFlyOperand];
+  uint32_t k[kFlyOperand];
 #pragma unroll
-  for (int i = 0; i < kFly; ++i) {
+  for (int i = 0; i < kFlyOperand; ++i) {
+    const N u = u0 + i * kThreads;
+    r[i] = -1;
+    k[i] = 0;
+    if (u < units) {
+      const N e = u / per_row;
+      k[i] = (uint32_t)(u - e * per_row);
+      r[i] = a.idx[id_at<N>(a, e)];
+    }
+  }
+  V w[kFlyOperand];
+  uint32_t b[kFlyOperand];
+#pragma unroll
+  for (int i = 0; i < kFlyOperand; ++i) {
+    w[i] = V{};
+    b[i] = 0;
+    if (r[i] >= 0 && r[i] < a.table_rows) {
+      w[i] = __ldg(reinterpret_cast<const V*>(a.Q + r[i] * (a.dim >> 1)) + k[i]);
+      const uint8_t* s = a.S + r[i] * spr + (int64_t)k[i] * kScales;
+      if constexpr (WORDS) {
+        if (k[i] % (4 / kScales) == 0) b[i] = __ldg(reinterpret_cast<const uint32_t*>(s));
+      } else {
+        b[i] = __ldg(s);
+        if (kScales > 1) b[i] |= (uint32_t)__ldg(s + 1) << 8;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFlyOperand; ++i) {
     const N u = u0 + i * kThreads;
     if (u >= units) continue;
+    *reinterpret_cast<V*>(codes + (int64_t)u * BYTES) = w[i];
     const N e = u / per_row;
-    const uint32_t k = (uint32_t)(u - e * per_row);
-    const int64_t r = a.idx[id_at<N>(a, e)];
-    const bool ok = r >= 0 && r < a.table_rows;
-    V w = {};
-    if (ok) w = __ldg(reinterpret_cast<const V*>(a.Q + r * (a.dim >> 1)) + k);
-    *reinterpret_cast<V*>(codes + (int64_t)u * BYTES) = w;
     const int64_t t = (int64_t)(e / (uint32_t)a.n_cols);
-    const int64_t c = (int64_t)e - t * a.n_cols;
+    const int64_t at = ((int64_t)e - t * a.n_cols) * spr + (int64_t)k[i] * kScales;
+    if constexpr (WORDS) {
+      if (k[i] % (4 / kScales) == 0) *reinterpret_cast<uint32_t*>(scales + tiled_scale_at(t, at, groups)) = b[i];
+    } else {
 #pragma unroll
-    for (int j = 0; j < kScales; ++j) {
-      const int64_t at = c * spr + (int64_t)k * kScales + j;
-      scales[tiled_scale_at(t, at, groups)] = ok ? __ldg(a.S + r * spr + (int64_t)k * kScales + j) : 0;
-      if (at == all - 1)  // the token's last scale: the rest of its group of four is 0
-        for (int64_t p = at + 1; p & 3; ++p) scales[tiled_scale_at(t, p, groups)] = 0;
+      for (int j = 0; j < kScales; ++j) scales[tiled_scale_at(t, at + j, groups)] = (uint8_t)(b[i] >> (8 * j));
+      if (at + kScales == all)  // the token's last scale: the rest of its group of four is 0
+        for (int64_t p = all; p & 3; ++p) scales[tiled_scale_at(t, p, groups)] = 0;
     }
   }
 }
 
 template <typename F>
-cudaError_t with_units(int64_t units, F&& f) {
-  const int64_t ctas = (units + kThreads * kFly - 1) / (kThreads * kFly);
+cudaError_t with_units(int64_t units, int fly, F&& f) {
+  const int64_t per_cta = kThreads * fly, ctas = (units + per_cta - 1) / per_cta;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   // a CTA's last unit must be numbered as well
-  if (ctas * (kThreads * kFly) <= 0xffffffffll) return f((uint32_t)units, (unsigned)ctas);
+  if (ctas * per_cta <= 0xffffffffll) return f((uint32_t)units, (unsigned)ctas);
   return f((uint64_t)units, (unsigned)ctas);
 }
 
 }  // namespace
 
 cudaError_t launch_lookup4(const Lookup4Args& a, uint16_t* out, cudaStream_t s) {
-  return with_units(a.T * a.n_cols * (a.dim / 16), [&](auto units, unsigned ctas) {
+  return with_units(a.T * a.n_cols * (a.dim / 16), kFlyValues, [&](auto units, unsigned ctas) {
     using N = decltype(units);
     auto kern = a.block == 16 ? lookup4_kernel<true, N> : lookup4_kernel<false, N>;
     return launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, s, a, out, units);
@@ -148,10 +177,14 @@ cudaError_t launch_lookup4(const Lookup4Args& a, uint16_t* out, cudaStream_t s) 
 
 cudaError_t launch_lookup4_operand(const Lookup4Args& a, uint8_t* codes, uint8_t* scales, cudaStream_t s) {
   const int bytes = a.dim % 32 == 0 ? 16 : 8;
-  return with_units(a.T * a.n_cols * (a.dim / (2 * bytes)), [&](auto units, unsigned ctas) {
+  return with_units(a.T * a.n_cols * (a.dim / (2 * bytes)), kFlyOperand, [&](auto units, unsigned ctas) {
     using N = decltype(units);
-    auto kern = lookup4_operand_kernel<false, 16, N>;
-    if (a.block == 16) kern = bytes == 16 ? lookup4_operand_kernel<true, 16, N> : lookup4_operand_kernel<true, 8, N>;
+    const bool words = a.dim % (4 * a.block) == 0 && (reinterpret_cast<uintptr_t>(a.S) & 3) == 0;
+    auto kern = words ? lookup4_operand_kernel<false, 16, true, N> : lookup4_operand_kernel<false, 16, false, N>;
+    if (a.block == 16)
+      kern = words         ? lookup4_operand_kernel<true, 16, true, N>
+             : bytes == 16 ? lookup4_operand_kernel<true, 16, false, N>
+                           : lookup4_operand_kernel<true, 8, false, N>;
     return launch_pdl(kern, dim3(ctas), dim3(kThreads), 0, s, a, codes, scales, units);
   });
 }

@@ -60,18 +60,12 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
 // borders stay exact and the others on their side.
 __device__ __forceinline__ float2 quotient2(float2 v, float2 hi, float2 lo) { return __ffma2_rn(v, hi, __fmul2_rn(v, lo)); }
 
-// fp32 inputs may lie nearer to a border than that: the code's magnitude by comparing with the borders times s, which
-// are exact (three bits times four); between two codes a tie goes to the even one
-__device__ __forceinline__ float e2m1_by_borders(float v, float s) {
-  const float a = fabsf(v);
-  float r = a > 0.25f * s ? 0.5f : 0.f;
-  r = a >= 0.75f * s ? 1.f : r;
-  r = a > 1.25f * s ? 1.5f : r;
-  r = a >= 1.75f * s ? 2.f : r;
-  r = a > 2.5f * s ? 3.f : r;
-  r = a >= 3.5f * s ? 4.f : r;
-  r = a > 5.f * s ? 6.f : r;
-  return copysignf(r, v);
+// fp32 inputs may lie nearer to a border than that: t, the rounded quotient, may be a border that v / s only comes near.
+// The remainder v - t s is exact and tells on which side: t becomes a neighbour whose last bit is set, which no border's
+// is, on the quotient's side of every border.
+__device__ __forceinline__ float beside_borders(float t, float rest, float v) {
+  const int bits = __float_as_int(t) + ((__float_as_int(rest) ^ __float_as_int(v)) >> 31);  // one less where t is too large
+  return rest != 0.f ? __int_as_float(bits | 1) : t;
 }
 
 // 16 consecutive values of x as loaded: one access of 32 bytes for 16-bit types where the address allows
@@ -156,17 +150,20 @@ __global__ void __launch_bounds__(kThreads)
     code = e4m3_scale(amax);
     const float s = e4m3_value(code);
     const bool ok = code != 0u && code != 0x7fu;
-    if constexpr (TYPE == ENGRAM_TYPE_F32) {
+    // scale 0 or NaN: the codes are 0 (a product with 0 would keep NaN and signs)
+    const float h = __frcp_rz(ok ? s : 1.f), l = __fmaf_rn(-h, s, 1.f) * h;  // l >= 0: -0 stays -0
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = ok ? e2m1_by_borders(v[i], s) : 0.f;
-    } else {
-      // scale 0 or NaN: the codes are 0 (a product with 0 would keep NaN and signs)
-      const float h = __frcp_rz(ok ? s : 1.f), l = __fmaf_rn(-h, s, 1.f) * h;  // l >= 0: -0 stays -0
-#pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) v2[i] = quotient2(v2[i], make_float2(h, h), make_float2(l, l));
-      w[0] = ok ? e2m1x8(v) : 0u;
-      w[1] = ok ? e2m1x8(v + 8) : 0u;
+    for (int i = 0; i < kPer / 2; ++i) {
+      const float2 t = quotient2(v2[i], make_float2(h, h), make_float2(l, l));
+      if constexpr (TYPE == ENGRAM_TYPE_F32) {
+        const float2 rest = __ffma2_rn(t, make_float2(-s, -s), v2[i]);
+        v2[i] = make_float2(beside_borders(t.x, rest.x, v2[i].x), beside_borders(t.y, rest.y, v2[i].y));
+      } else {
+        v2[i] = t;
+      }
     }
+    w[0] = ok ? e2m1x8(v) : 0u;
+    w[1] = ok ? e2m1x8(v + 8) : 0u;
   } else {
     code = FOUR ? pow2_scale(amax, 2, 0x400000u) : pow2_scale(amax, 8, 0x600000u);
     const float f = pow2_recip(min(code, 253u));
@@ -175,7 +172,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const bool nan = (!FOUR || LANES > 1) && code == 255u;  // codes of 0
   if constexpr (FOUR) {
-    if constexpr (LANES > 1 || TYPE == ENGRAM_TYPE_F32) {
+    if constexpr (LANES > 1) {
       w[0] = nan ? 0u : e2m1x8(v);
       w[1] = nan ? 0u : e2m1x8(v + 8);
     }

@@ -207,21 +207,27 @@ cudaError_t launch_embed_grad(const EmbedGradArgs& a, void* workspace, cudaStrea
 
 // -------------------------------------------------------------------------------- the gate's gradient
 struct GateGradArgs {
-  const void *x, *kv;  // bf16, or E4M3 codes with the scales below
-  const uint16_t *qw, *kw, *dout;
+  const uint16_t *x, *kv, *qw, *kw, *dout;
   const uint8_t* mask;  // may be null
   int64_t T;
   int32_t hc, dim;
   float eps;
   uint16_t *dx, *dkv;
   float *dq, *dk;
-  // checkpoints in 8 bits: a UE8M0 scale for each `block` columns of a row (null: x and kv are bf16)
-  const uint8_t *xs = nullptr, *kvs = nullptr;
-  int32_t block = 0;
 };
-uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim, bool q8 = false);
+uint64_t gate_grad_workspace(int64_t T, int32_t hc, int32_t dim);
 // withhold >= 0: the test hook of engram_gate_grad_withhold
 cudaError_t launch_gate_grad(const GateGradArgs& a, void* workspace, cudaStream_t s, int64_t withhold = -1);
+
+// The same from checkpoints in 8 bits (gate_grad8.cu): E4M3 codes [T][hc][dim] and [T][hc + 1][dim] with a UE8M0 scale for
+// each `block` columns of a row. `g`: the rest of the arguments (its x and kv unused).
+struct GateGrad8Args {
+  GateGradArgs g;
+  const uint8_t *x, *xs, *kv, *kvs;
+  int32_t block;
+};
+uint64_t gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim);
+cudaError_t launch_gate_grad8(const GateGrad8Args& a, void* workspace, cudaStream_t s, int64_t withhold = -1);
 
 // ------------------------------------------------------------------------- gradient norm and clipping
 uint64_t grad_norm_workspace(int32_t n_tensors);

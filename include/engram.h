@@ -687,6 +687,14 @@ int engram_gate_grad8(const uint8_t* x, const uint8_t* x_scales, const uint8_t* 
                       float* dq_weight, float* dk_weight, void* workspace, uint64_t workspace_bytes,
                       engram_stream_t stream);
 
+/* Test hook of engram_gate_grad8's failure path (no counterpart in the pages), as engram_gate_grad_withhold: the sums of
+ * token `token` (one whose mask is open) are not sent in full, so the wait for them runs out. */
+int engram_gate_grad8_withhold(const uint8_t* x, const uint8_t* x_scales, const uint8_t* kv, const uint8_t* kv_scales,
+                               int32_t block, const uint16_t* q_weight, const uint16_t* k_weight, const uint16_t* dout,
+                               const uint8_t* mask, int64_t T, int32_t hc, int32_t dim, float eps, uint16_t* dx,
+                               uint16_t* dkv, float* dq_weight, float* dk_weight, void* workspace,
+                               uint64_t workspace_bytes, int64_t token, engram_stream_t stream);
+
 /*
  * Set the L2 fetch granularity limit of the current device's context (cudaLimitMaxL2FetchGranularity:
  * the most bytes L2 fetches from DRAM for one missed sector, a hint; 0, 32, 64 or 128) and return the

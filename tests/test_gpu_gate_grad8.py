@@ -1,7 +1,8 @@
 """The gate's gradient from 8-bit checkpoints (engram_gate_grad8) against the formula in 64 bits on the bf16 values that
-the checkpoints stand for, within engram_gate_grad's bounds (GPU only). The two calls run the same arithmetic on those
-values, but split a row's columns otherwise (a checkpoint's rows have to start on 16 bytes; with 4 copies and more a
-thread has 4 columns), so their sums run in another order; where the split is the same the bits are equal."""
+the checkpoints stand for, within engram_gate_grad's bounds (GPU only): the same arithmetic on those values, its sums in an
+order of their own."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +10,7 @@ import torch
 import gram_hash_embedding_gb300 as geng
 from tests import gpu_helpers as H
 from tests import test_gpu_gate_grad as G
+from tests import train_ref as R
 
 pytestmark = pytest.mark.gpu
 
@@ -49,13 +51,60 @@ def test_gradient_of_the_values(T, hc, dim, block):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
-@pytest.mark.parametrize("T,hc,dim", [(1500, 1, 64), (200, 2, 272)])
-def test_whole_rows_of_few_copies_give_the_bits_of_the_values_gradient(T, hc, dim):
-    args = G._inputs(np.random.default_rng(T + dim), T, hc, dim)
-    xq, kq, back = _checkpoints(args, 32)
-    got, exp = _run8(xq, kq, back, 32), G._run(back)
-    assert torch.equal(got[0].view(torch.int16), exp[0].view(torch.int16))
-    assert torch.equal(got[1].view(torch.int16), exp[1].view(torch.int16))
+@pytest.mark.parametrize("T,hc,dim", [(4000, 4, 256), (3000, 8, 640), (2500, 2, 1040), (1200, 1, 5120), (900, 4, 5120),
+                                      (400, 8, 5120)])
+def test_many_tokens_a_cluster(T, hc, dim):
+    """Rings and buffers go round several times, over runs of masked and of open tokens."""
+    rng = np.random.default_rng(T + dim)
+    args = G._inputs(rng, T, hc, dim)
+    args[5] = torch.from_numpy(np.repeat(rng.random(-(-T // 50)) < 0.7, 50)[:T] ^ (rng.random(T) < 0.1))
+    xq, kq, back = _checkpoints(args, 128)
+    got = _run8(xq, kq, back, 128)
+    G._check(back, got, f"T={T} hc={hc} dim={dim}")
+    assert all(torch.equal(a, b) for a, b in zip(got, _run8(xq, kq, back, 128)))
+
+
+@pytest.mark.parametrize("T,hc,dim", [(1500, 1, 64), (900, 2, 1040), (700, 1, 5120), (600, 2, 5120), (400, 4, 1024),
+                                      (500, 8, 256)])
+def test_small_dots(T, hc, dim):
+    """Keys nearly orthogonal to h, where sum(h w key) is formed once more in twice the precision: dot is held to the
+    error of the mean squares alone. Tokens with a copy of |dot| outside [1e-5, 0.03] are masked out."""
+    rng = np.random.default_rng(T + dim)
+    args = G._inputs(rng, T, hc, dim, masked=0.0)
+    x, q, k = G._f64(args[0]), G._f64(args[2]), G._f64(args[3])
+    kv = rng.standard_normal((T, hc + 1, dim))
+    key = kv[:, :hc]
+    key -= (x * q * k * key).sum(-1, keepdims=True) / (x * x * q * k * q * k).sum(-1, keepdims=True) * (x * q * k)
+    args[1] = G._bf(kv.reshape(T, -1))
+    xq, kq, back = _checkpoints(args, 128)
+    dot = np.abs(R.gate_grad(G._f64(back[0]), G._f64(back[1]), q, k, G._f64(args[4]), np.ones(T, bool), G.EPS)[5][..., 0])
+    back[5] = torch.from_numpy(((dot > 1e-5) & (dot < 0.03)).all(1))
+    assert back[5].sum() >= 5
+    got = _run8(xq, kq, back, 128)
+    G._check(back, got, "small dots", small=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, _run8(xq, kq, back, 128)))
+
+
+@pytest.mark.parametrize("T,hc,dim", [(300, 4, 5120), (300, 2, 256), (160, 8, 1024)])
+def test_withheld_sums_time_out_and_the_next_call_is_right(T, hc, dim):
+    args = G._inputs(np.random.default_rng(T), T, hc, dim, masked=0.0)
+    xq, kq, back = _checkpoints(args, 128)
+    L = geng._lib()
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    L.engram_gate_grad8_withhold.argtypes = [P, P, P, P, I32, P, P, P, P, I64, I32, I32, ctypes.c_float, P, P, P, P, P,
+                                             ctypes.c_uint64, I64, P]
+    L.engram_gate_grad8_withhold.restype = ctypes.c_int
+    dev = [a.cuda() for a in back[2:5]]
+    outs = [torch.empty((T, hc, dim), dtype=torch.bfloat16, device="cuda"),
+            torch.empty((T, (hc + 1) * dim), dtype=torch.bfloat16, device="cuda"),
+            torch.empty((hc, dim), device="cuda"), torch.empty((hc, dim), device="cuda")]
+    ws = torch.empty(geng.engram_gate_grad8_workspace(T, hc, dim), dtype=torch.uint8, device="cuda")
+    rc = L.engram_gate_grad8_withhold(*[t.data_ptr() for t in (*xq, *kq)], 128, *[t.data_ptr() for t in dev], None, T, hc,
+                                      dim, G.EPS, *[t.data_ptr() for t in outs], ws.data_ptr(), ws.numel(), T // 2,
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == geng.OK and geng.engram_device_status() == geng.STATUS_TIMEOUT
+    G._check(back, _run8(xq, kq, back, 128), "after the timeout")
+    assert geng.engram_device_status() == 0
 
 
 def test_masked_tokens_and_nan():
