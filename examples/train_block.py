@@ -2,11 +2,12 @@
 embedding rows, the `wkv` projection and the gate forward, then their gradients, the global norm with
 clipping and a plain gradient step.
 
-    python examples/train_block.py [--steps 20] [--tokens 4096] [--dim 1024]
+    python examples/train_block.py [--steps 20] [--tokens 4096] [--dim 1024] [--checkpoint8]
 
 The table is fp32 and read as bf16 (the lookup rounds); only the rows that a step's tokens hash to
 get a gradient, so its size does not depend on the table's. The projection's two gradients are plain
-matrix products and run as torch matmuls.
+matrix products and run as torch matmuls. With --checkpoint8 the residual copies and the keys and values wait
+for the backward pass in 8 bits instead of bf16.
 """
 import argparse
 import os
@@ -37,8 +38,16 @@ class Block:
         kv = geng.engram_project(emb, self.wkv)
         return geng.engram_gate(x, kv, self.q, self.k, mask), emb, kv
 
-    def gradients(self, x, ids, mask, emb, kv, dout):
-        dx, dkv, dq, dk = geng.engram_gate_grad(x, kv, self.q, self.k, dout, mask)
+    def checkpoint(self, x, kv):
+        """x and kv in 8 bits, rows of dim values, for gradients(saved=...): half the memory until the backward pass."""
+        return geng.engram_quantize8(x) + geng.engram_quantize8(kv.view(kv.shape[0], self.hc + 1, self.dim))
+
+    def gradients(self, x, ids, mask, emb, kv, dout, saved=None):
+        """From x and kv, or from what checkpoint() made of them (then x and kv are not read)."""
+        if saved is None:
+            dx, dkv, dq, dk = geng.engram_gate_grad(x, kv, self.q, self.k, dout, mask)
+        else:
+            dx, dkv, dq, dk = geng.engram_gate_grad8(*saved, self.q, self.k, dout, mask=mask)
         dwkv = dkv.t() @ emb
         rows, drows, count = geng.engram_embed_grad(ids, dkv @ self.wkv, self.table.shape[0])
         return dx, {"wkv": dwkv, "q": dq, "k": dk, "rows": drows}, rows, count
@@ -56,7 +65,7 @@ class Block:
 
 
 def train(steps: int = 20, tokens: int = 4096, dim: int = 1024, hc: int = 4, lr: float = 0.5, max_norm: float = 4.0,
-          log=print):
+          log=print, checkpoint8: bool = False):
     """Fit the layer's output to that of another layer with the same tokens; returns the losses."""
     wl = synth.make_workload(5)  # two layers, 24 columns of rows a token, small tables
     lay = wl.layout
@@ -80,7 +89,10 @@ def train(steps: int = 20, tokens: int = 4096, dim: int = 1024, hc: int = 4, lr:
         diff = out.float() - target
         losses.append(float(diff.square().mean()))
         dout = (diff * (2 / dim)).bfloat16()  # of the squared error summed over tokens and copies
-        _, grads, rows, count = student.gradients(x, ids, mask, emb, kv, dout)
+        saved = student.checkpoint(x, kv) if checkpoint8 else None
+        if saved:
+            kv = None  # in a stack of layers x goes as well
+        _, grads, rows, count = student.gradients(x, ids, mask, emb, kv, dout, saved)
         norm = student.step(grads, rows, count, lr, max_norm)
         log(f"step {step}: loss {losses[-1]:.5f}, gradient norm {float(norm):.3f}, {int(count)} rows")
     hasher.close()
@@ -92,7 +104,8 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--tokens", type=int, default=4096)
     ap.add_argument("--dim", type=int, default=1024)
+    ap.add_argument("--checkpoint8", action="store_true")
     a = ap.parse_args()
     synth.build()
     geng.build()
-    train(a.steps, a.tokens, a.dim)
+    train(a.steps, a.tokens, a.dim, checkpoint8=a.checkpoint8)

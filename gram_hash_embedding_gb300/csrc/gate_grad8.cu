@@ -24,6 +24,7 @@
 #include "dequant.cuh"
 #include "engram_internal.cuh"
 #include "gate_grad.cuh"
+#include "launch_cache.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
 #include "train.cuh"
@@ -482,8 +483,8 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
 template <int HC, int CG, bool WHOLE>
 cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
                          cudaStream_t s) {
-  auto kern = gate_grad8_kernel<HC, CG, WHOLE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sh.smem);
+  constexpr auto kern = gate_grad8_kernel<HC, CG, WHOLE>;
+  cudaError_t e = allow_smem<kern>((int)sh.smem);
   if (e != cudaSuccess) return e;
   const int threads = sh.owners + 32;
   cudaLaunchConfig_t cfg = {};

@@ -1,0 +1,46 @@
+// What a launch asks the runtime about its kernel, asked once per device: the dynamic shared memory a kernel may use and
+// how many of its clusters fit at once. Asked at every call they were a quarter of a small call's host time.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace engram {
+
+constexpr int kCachedDevices = 64;
+
+inline cudaError_t current_device(int* dev) {
+  const cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return e;
+  return *dev >= 0 && *dev < kCachedDevices ? cudaSuccess : cudaErrorInvalidDevice;
+}
+
+// allow kernel KERN `bytes` of dynamic shared memory on the current device
+template <auto KERN>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<int> allowed[kCachedDevices];
+  int dev = 0;
+  cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  if (allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) allowed[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
+
+// clusters of KERN that fit on the current device at once, for a configuration that is always the same
+template <auto KERN>
+cudaError_t resident_clusters(int* n, const cudaLaunchConfig_t& cfg) {
+  static std::atomic<int> known[kCachedDevices];
+  int dev = 0;
+  cudaError_t e = current_device(&dev);
+  if (e != cudaSuccess) return e;
+  *n = known[dev].load(std::memory_order_relaxed);
+  if (*n > 0) return cudaSuccess;
+  e = cudaOccupancyMaxActiveClusters(n, KERN, &cfg);
+  if (e == cudaSuccess) known[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
+}  // namespace engram

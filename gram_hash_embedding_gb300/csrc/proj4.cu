@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "engram_internal.cuh"
+#include "launch_cache.cuh"
 #include "lowbit.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
@@ -368,8 +369,8 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
       !tensor_map_2d(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.T, (uint64_t)a.N, (uint64_t)a.N * 2, 32, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  auto kern = project4_kernel<NV, BN, EW>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  constexpr auto kern = project4_kernel<NV, BN, EW>;
+  e = allow_smem<kern>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -386,7 +387,7 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
   cfg.numAttrs = 2;
   cfg.gridDim = dim3(2);
   int units = 0;
-  e = cudaOccupancyMaxActiveClusters(&units, kern, &cfg);
+  e = resident_clusters<kern>(&units, cfg);
   if (e != cudaSuccess) return e;
   if (units < 1) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3((unsigned)(2 * (p.n_tiles < units ? p.n_tiles : units)));
@@ -597,8 +598,8 @@ cudaError_t launch_few(const Project4Args& a, cudaStream_t s, int32_t withhold) 
       !tensor_map_2d(&tsw, i32, a.ws, (uint64_t)p.n_ntile * p.groups, 128, 512, C::kChunks, 128, none) ||
       !tensor_map_2d(&tst, i32, a.as, (uint64_t)p.groups, 128, 512, C::kChunks, 128, none))
     return cudaErrorInvalidValue;
-  auto kern = project4_few_kernel<NV, TP>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  constexpr auto kern = project4_few_kernel<NV, TP>;
+  e = allow_smem<kern>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   // the longest split of K that leaves every CTA a stage and all of them resident
   int split = 8;
