@@ -4,14 +4,19 @@
 // cores (tcgen05.mma .block_scale, K = 64 an instruction, four times the bf16 rate).
 //
 // Design (GB300): the shape of the bf16 projection (proj.cu): persistent CTA pairs, 256 x BN output tiles by M = 256
-// MMAs of the pair's leader, operands by TMA in 128-byte swizzled rows (256 values of K: one stage), an
-// accumulator in each CTA's tensor memory while the epilogue empties the tile before. What differs:
+// MMAs of the pair's leader, operands by TMA in 128-byte swizzled rows (256 values of K: one stage), accumulators in the
+// CTAs' tensor memory. What differs:
 // - Scales. A stage's scales come in the tensor cores' order (512 bytes for 128 rows and four scales of each) by TMA, and
 //   are copied from shared into tensor memory by the thread that issues the MMAs (tcgen05.cp): 128 rows of A and all
 //   BN rows of B in each CTA of the pair.
-// - Tensor memory. Two accumulators of 256 columns leave no column for scales, so they overlap: columns [0, 256) and
-//   [224, 480) (blocks of 32) or [192, 448), scales after them. The epilogue reads the 32 or 64 shared columns of a tile
-//   first and then lets the next tile's MMAs start.
+// - Issue. A stage is 512 cycles of MMAs where the bf16 one is 1,024, and has copies besides: see elect_one (tc_ptx.cuh).
+// - Tiles. Two accumulators of 256 columns leave no column of tensor memory for scales. So 256 and 384 columns have one, and
+//   the epilogue takes all of it into registers, already rounded, before it stores anything: the next tile's MMAs wait
+//   for that much. 128 columns have two.
+// What bounds it: the L2-to-SM rate of the operands (114 B/ns an SM; tiles of 384 columns need 16% less of it for the same
+// flops than tiles of 256) and, in a stream of calls, the power cap: 16,384 x 6,144 x 25,600 with blocks of 32 takes 771 us
+// alone and 781 under the cap at 1.9 GHz (6.6 PFLOP/s, 3.4 times the bf16 GEMM's burst rate), with blocks of 16 848. Two
+// accumulators of 256 columns that overlap by 32 to 64 took 750 alone, 796 and 857 under the cap.
 // Warp 0 loads, warp 1 issues, warps 2-9 are the epilogue. Every wait is bounded (tc_ptx.cuh): a wait that runs
 // out raises ENGRAM_STATUS_TIMEOUT, the CTA stops issuing, waits for its copies and MMAs in flight and exits.
 #include <algorithm>
@@ -32,6 +37,8 @@ constexpr int kStageK = 256;               // values of K a stage: one 128-byte 
 constexpr int kMmaK = 64;                  // values of K an MMA
 constexpr int kMmas = kStageK / kMmaK;     // MMAs a stage
 constexpr int kThreads = 192;              // few tokens: loader, MMA, 4 epilogue warps
+constexpr int kEpiWarps = 8;               // pairs: two for each quarter of the tensor-memory lanes
+constexpr int kPairThreads = 64 + 32 * kEpiWarps;
 constexpr int kGroup = 16;                 // 256-row blocks per tile group
 constexpr uint32_t kABytes = kBM * 128;    // A of a stage
 constexpr uint32_t kChunkBytes = 512;      // scales of 128 rows, four each
@@ -39,10 +46,8 @@ constexpr uint32_t kEpiChunkBytes = 32 * 32 * 2;
 constexpr int kSms = 152;
 constexpr uint64_t kSettleNs = 100000;     // after a wait has run out: far longer than a load or an MMA takes
 
-// EW: epilogue warps, one or two for each quarter of the tensor-memory lanes
-template <bool NV, int BN, int EW>
+template <bool NV, int BN>
 struct Cfg {
-  static constexpr int kThreads = 64 + 32 * EW;
   static constexpr int kChunks = NV ? 4 : 2;                     // groups of four scales in a stage's K
   static constexpr int kBBlocks = BN / 128;                      // blocks of 128 rows of B
   static constexpr uint32_t kBBytes = (BN / 2) * 128;            // this CTA's half of B
@@ -52,19 +57,15 @@ struct Cfg {
   static constexpr uint32_t kTileBytes = kABytes + kBBytes;      // 1024-byte multiples
   static constexpr uint32_t kStageScaleBytes = kSaBytes + kSbBytes;
   static constexpr uint32_t kTxBytes = 2 * (kTileBytes + kStageScaleBytes);  // both CTAs of the pair
-  static constexpr uint32_t kEpiBytes = EW * 2 * kEpiChunkBytes;
+  static constexpr uint32_t kEpiBytes = kEpiWarps * 2 * kEpiChunkBytes;
   static constexpr int kStages = (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes)) < 8
                                      ? (int)((232448 - 1024 - 512 - kEpiBytes) / (kTileBytes + kStageScaleBytes))
                                      : 8;
-  // widths of the MMAs that make up a tile's columns, and accumulators: two that overlap, two apart, or one
+  // widths of the MMAs that make up a tile's columns, and accumulators
   static constexpr int kN0 = BN < 256 ? BN : 256, kN1 = BN - kN0;
-  static constexpr bool kOverlap = BN == 256;
-  static constexpr int kAccs = BN > 256 ? 1 : 2;
-  // columns that the accumulators share: what the scales leave no room for, in chunks of 32
-  static constexpr int kShared = kOverlap ? (NV ? 64 : 32) : 0;
-  static constexpr uint32_t kAcc1 = BN - kShared;                // column of the second accumulator
+  static constexpr int kAccs = BN <= 128 ? 2 : 1;
   static constexpr uint32_t kSaCols = 4 * kChunks, kSbCols = 4 * kBBlocks;  // of a stage; of one group of B
-  static constexpr uint32_t kScaleCol = kAccs == 2 ? kAcc1 + BN : BN;  // first column of the scales
+  static constexpr uint32_t kScaleCol = kAccs * BN;              // first column of the scales
   static_assert(kScaleCol + kSaCols + kChunks * kSbCols <= 512, "tensor memory");
   // shared memory: operand ring, scale ring, output staging, barriers and words
   static constexpr uint32_t kScaleOff = kStages * kTileBytes;
@@ -103,12 +104,12 @@ __device__ __forceinline__ void raise_timeout(volatile int* abort, unsigned int*
   atomicOr(status, (unsigned)ENGRAM_STATUS_TIMEOUT);
 }
 
-template <bool NV, int BN, int EW>
-__global__ void __launch_bounds__(64 + 32 * EW, 1)
+template <bool NV, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
     project4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
                     const __grid_constant__ CUtensorMap tmO, const Params p) {
-  using C = Cfg<NV, BN, EW>;
+  using C = Cfg<NV, BN>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = tc::smem_u32(smem_raw);
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
     }
     for (int a = 0; a < 2; ++a) {
       tc::mbar_init(acc_full(a), 1);
-      tc::mbar_init(acc_free(a), 2 * EW);  // one arrival per epilogue warp of the pair
+      tc::mbar_init(acc_free(a), 2 * kEpiWarps);  // one arrival per epilogue warp of the pair
     }
     tc::mbar_init(drain, 1);
     *abort = 0;
@@ -207,16 +208,14 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
     const uint32_t tile_lo = base >> 4, scale_lo = (base + C::kScaleOff) >> 4;  // of descriptors
     for (int64_t tile = unit; ok && tile < p.n_tiles; tile += n_units, ++n) {
       const uint32_t acc = C::kAccs == 2 ? n & 1 : 0;
-      // overlapping accumulators: the tile before must have left the shared columns (and then the one before it is
-      // read in full); separate ones: the tile two before must be read; a single one: the tile before
-      const bool free = C::kOverlap ? n == 0 || tc::warp_mbar_wait(acc_free(acc ^ 1u), ((n - 1) >> 1) & 1, abort)
-                                    : tc::warp_mbar_wait(acc_free(acc), ((n / C::kAccs) & 1) ^ 1u, abort);
+      // the tile that had this accumulator before has been read
+      const bool free = tc::warp_mbar_wait(acc_free(acc), ((n / C::kAccs) & 1) ^ 1u, abort);
       if (!free) {
         raise_timeout(abort, p.status);
         break;
       }
       tc::fence_after_thread_sync();
-      const uint32_t d = tmem + acc * C::kAcc1;
+      const uint32_t d = tmem + acc * BN;
       const uint32_t ta = tmem + C::kScaleCol, tb = ta + C::kSaCols;
       for (int kb = 0; kb < p.num_kb; ++kb) {
         if (!tc::warp_mbar_wait(full(stage), phase, abort)) {
@@ -272,22 +271,17 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
     const int part = (warp - 2) >> 2;  // the warp's share of the columns: every other chunk of 32
     const uint32_t staging = base + C::kEpiOff + (uint32_t)(warp - 2) * 2u * kEpiChunkBytes;
     int32_t n = 0, sent = 0;
-    // 32 columns of the warp's 32 rows: scaled, rounded, through a swizzled chunk of shared memory, out by TMA
-    auto put = [&](const float (&v)[32], int col, int32_t row) {
+    // 32 columns of the warp's 32 rows, in bf16, through a swizzled chunk of shared memory, out by TMA
+    auto put = [&](const uint32_t (&v)[16], int col, int32_t row) {
       const uint32_t chunk = staging + (uint32_t)(sent & 1) * kEpiChunkBytes;
       ++sent;
       if (lane == 0) tc::bulk_wait_group_read_1();
       __syncwarp();
       const uint32_t to = chunk + (uint32_t)lane * 64u;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float* w = v + 8 * g;
+      for (int g = 0; g < 4; ++g)
         tc::st_shared_v4(to + (uint32_t)((g ^ ((lane >> 1) & 3)) * 16),
-                         make_uint4(tc::f32x2_to_bf16x2(w[0] * p.scale, w[1] * p.scale),
-                                    tc::f32x2_to_bf16x2(w[2] * p.scale, w[3] * p.scale),
-                                    tc::f32x2_to_bf16x2(w[4] * p.scale, w[5] * p.scale),
-                                    tc::f32x2_to_bf16x2(w[6] * p.scale, w[7] * p.scale)));
-      }
+                         make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
       tc::fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) {
@@ -306,26 +300,35 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
       }
       if (__shfl_sync(0xffffffffu, ok, 0) == 0) break;
       tc::fence_after_thread_sync();
-      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + acc * C::kAcc1;
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN;
       const int32_t row = (mt * 2 + (int32_t)q) * kBM + quarter * 32;  // TMA stores skip rows past T
-      auto release = [&]() {
+      constexpr int kMine = BN / 32 / (kEpiWarps / 4);  // chunks of 32 columns, every other one
+      auto take = [&](int i, uint32_t (&to)[16]) {
+        float v[32];
+        tc::tmem_load_32cols(taddr + 32 * (2 * i + part), v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) to[e] = tc::f32x2_to_bf16x2(v[2 * e] * p.scale, v[2 * e + 1] * p.scale);
+      };
+      if (C::kAccs == 1 && tile + n_units < p.n_tiles) {
+        // the warp's columns into registers before anything is stored: the next tile's MMAs wait for no more
+        uint32_t held[kMine][16];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) take(i, held[i]);
         tc::fence_before_thread_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_free(acc), 0));
-      };
-      constexpr int kChunksN = BN / 32, kParts = EW / 4;
-      static_assert(kChunksN % kParts == 0, "columns");
-      constexpr int kFirst = C::kShared / 32;  // shared chunks
-      // the columns that the next tile's accumulator shares come first: the last of the first, the first of the second
-      const int first = C::kOverlap && acc == 0 ? kChunksN - C::kShared / 32 : 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) put(held[i], nt * BN + 32 * (2 * i + part), row);
+      } else {  // no next tile, or another accumulator for it
 #pragma unroll 1
-      for (int i = part; i < kChunksN; i += kParts) {
-        const int c = (first + i) % kChunksN;
-        float v[32];
-        tc::tmem_load_32cols(taddr + 32 * c, v);
-        // the part's last shared chunk has been read (or its first, where the other part has the shared one), or the last
-        if (i == part + (C::kOverlap ? (kFirst > kParts ? kFirst - kParts : 0) : kChunksN - kParts)) release();
-        put(v, nt * BN + 32 * c, row);
+        for (int i = 0; i < kMine; ++i) {
+          uint32_t held[16];
+          take(i, held);
+          put(held, nt * BN + 32 * (2 * i + part), row);
+        }
+        tc::fence_before_thread_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::map_to_rank(acc_free(acc), 0));
       }
     }
     if (lane == 0) tc::bulk_wait_group_0();
@@ -342,9 +345,9 @@ __global__ void __launch_bounds__(64 + 32 * EW, 1)
   }
 }
 
-template <bool NV, int BN, int EW>
+template <bool NV, int BN>
 cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold) {
-  using C = Cfg<NV, BN, EW>;
+  using C = Cfg<NV, BN>;
   Params p = {};
   p.T = a.T;
   p.K = a.K;
@@ -369,7 +372,7 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
       !tensor_map_2d(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.T, (uint64_t)a.N, (uint64_t)a.N * 2, 32, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  constexpr auto kern = project4_kernel<NV, BN, EW>;
+  constexpr auto kern = project4_kernel<NV, BN>;
   e = allow_smem<kern>(C::kSmemBytes);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -380,7 +383,7 @@ cudaError_t launch_pairs(const Project4Args& a, cudaStream_t s, int32_t withhold
   attr[1].val.clusterDim.x = 2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -627,17 +630,17 @@ cudaError_t launch_kind(const Project4Args& a, cudaStream_t s, int32_t withhold)
   if (a.T <= 32) return launch_few<NV, 32>(a, s, withhold);
   if (a.T <= 64) return launch_few<NV, 64>(a, s, withhold);
   if (a.T <= 128) return launch_few<NV, 128>(a, s, withhold);
-  // wide tiles, unless narrow ones fill the waves of pairs better, or tiles of 384 columns are few enough for one wave
-  // (256 tokens of N = 25,600: 67 of them instead of 100)
-  const int64_t rows = (a.T + 255) / 256, pairs = kSms / 2;
-  auto waves = [&](int64_t bn) { return (rows * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * bn; };
-  // Two epilogue warps a lane quarter where a tile has little K to hide them behind or nothing overlaps them (16,384 x
-  // 1,024 x 5,120: 57 us against 62; of K = 6,144 one is 3% faster)
-  const bool two = a.K <= 1024;
-  if (waves(128) <= 128 || waves(128) * 10 < std::min(waves(256), waves(384)) * 9)
-    return two ? launch_pairs<NV, 128, 8>(a, s, withhold) : launch_pairs<NV, 128, 4>(a, s, withhold);
-  if (waves(384) == 384 && waves(256) > 256) return launch_pairs<NV, 384, 8>(a, s, withhold);
-  return two ? launch_pairs<NV, 256, 8>(a, s, withhold) : launch_pairs<NV, 256, 4>(a, s, withhold);
+  // The width of tile that takes least: waves of tiles over the pairs, each so many stages of K and what a tile costs
+  // besides, in units of 10 ns as measured at K = 256 to 6,144 (narrow tiles read the rows of A more often, wide ones leave
+  // more of the epilogue uncovered). At 16,384 x 6,144 x 25,600 under the power cap: 384 columns 781 us, 256 820; at K =
+  // 1,024 and N = 5,120 58 and 54, 128 columns 63; at 777 x 1,056 x 1,992 11, 8 and 7; 256 tokens of the first 23, 24, 27.
+  const int64_t rows = (a.T + 255) / 256, pairs = kSms / 2, stages = (a.K + kStageK - 1) / kStageK;
+  auto cost = [&](int64_t bn, int64_t stage, int64_t tile) {
+    return (rows * ((a.N + bn - 1) / bn) + pairs - 1) / pairs * (stages * stage + tile);
+  };
+  const int64_t narrow = cost(128, 27, 76), middle = cost(256, 30, 189), wide = cost(384, 43, 315);
+  if (narrow <= std::min(middle, wide)) return launch_pairs<NV, 128>(a, s, withhold);
+  return middle <= wide ? launch_pairs<NV, 256>(a, s, withhold) : launch_pairs<NV, 384>(a, s, withhold);
 }
 
 }  // namespace
