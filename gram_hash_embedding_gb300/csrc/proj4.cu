@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncwarp();
     }
-    // Every MMA issued has completed, and with it every load that was waited for. After a wait that ran out loads may
-    // still be landing: those of the stages filled and not consumed.
+    // arrives once every MMA above has completed, and with them the loads that they waited for
     if (rank != 0 || p.withhold != 0) {
       if (tc::elect_one()) tc::commit(done);
     }
@@ -547,8 +546,18 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   tc::fence_before_thread_sync();
-  if (split > 1) tc::cluster_sync();
-  else __syncthreads();
+  __syncthreads();
+  // Tensor memory goes back before this CTA waits for others of its cluster: what another kernel's CTA on this SM waits for
+  // then never depends on a CTA elsewhere, which might wait for that kernel in turn.
+  if (*abort) {  // loads and MMAs may still be in flight: let them end before the memory is given up
+    const uint64_t t0 = tc::global_timer_ns();
+    while (tc::global_timer_ns() - t0 < kSettleNs) {}
+  }
+  if (warp == 1) {
+    tc::fence_after_thread_sync();
+    tc::tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (split > 1) tc::cluster_sync();  // every CTA's sums are there
   const int64_t n = (int64_t)tile * 128 + 4 * lane;
   if (!*abort && n < p.N) {
     for (int t = rank * (kThreads / 32) + warp; t < p.T; t += split * (kThreads / 32)) {
@@ -566,16 +575,7 @@ __global__ void __launch_bounds__(kThreads)
           make_uint2(tc::f32x2_to_bf16x2(s.x * p.scale, s.y * p.scale), tc::f32x2_to_bf16x2(s.z * p.scale, s.w * p.scale));
     }
   }
-  if (*abort) {  // loads and MMAs may still be in flight: let them end before the memory is given up
-    const uint64_t t0 = tc::global_timer_ns();
-    while (tc::global_timer_ns() - t0 < kSettleNs) {}
-  }
   if (split > 1) tc::cluster_sync();  // no CTA leaves while another reads its sums
-  else __syncthreads();
-  if (warp == 1) {
-    tc::fence_after_thread_sync();
-    tc::tmem_dealloc(tmem, C::kTmemCols);
-  }
 }
 
 template <bool NV, int TP>

@@ -158,3 +158,23 @@ def test_no_tokens():
     got = geng.engram_gate_grad8(e, e[..., :1], torch.empty((0, 3, 64), dtype=torch.uint8, device="cuda"),
                                  torch.empty((0, 3, 1), dtype=torch.uint8, device="cuda"), w, w, e.bfloat16(), block=64)
     assert got[0].shape == (0, 2, 64) and got[1].shape == (0, 192) and (got[2] == 0).all() and (got[3] == 0).all()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 codes: the last tokens' gradients, against the formula on these tokens alone (every other token masked)."""
+    T, hc, dim, n = 1_100_000, 4, 1024, 24
+    args = G._inputs(np.random.default_rng(3), n, hc, dim, masked=0.0)
+    xq, kq, back = _checkpoints(args, 128)
+    x = torch.zeros((T, hc, dim), dtype=torch.uint8, device="cuda")
+    kv = torch.zeros((T, hc + 1, dim), dtype=torch.uint8, device="cuda")
+    xs = torch.full((T, hc, dim // 128), 127, dtype=torch.uint8, device="cuda")
+    ks = torch.full((T, hc + 1, dim // 128), 127, dtype=torch.uint8, device="cuda")
+    x[-n:], kv[-n:] = xq[0], kq[0]
+    xs[-n:], ks[-n:] = xq[1].view(torch.uint8), kq[1].view(torch.uint8)
+    dout = torch.ones((T, hc, dim), dtype=torch.bfloat16, device="cuda")
+    dout[-n:] = args[4].cuda()
+    mask = torch.zeros(T, dtype=torch.bool, device="cuda")
+    mask[-n:] = True
+    got = geng.engram_gate_grad8(x, xs, kv, ks, args[2].cuda(), args[3].cuda(), dout, mask=mask, dx=dout)
+    assert (got[0][: -n : 4099] == 1).all() and (got[1][: -n : 4099] == 0).all()
+    G._check(back, [got[0][-n:], got[1][-n:], got[2], got[3]], "last tokens")

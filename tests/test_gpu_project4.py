@@ -144,6 +144,54 @@ def test_chain_from_ids_and_from_values():
     assert torch.equal(kv2, kv) and torch.equal(kv3, kv) and torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("block", [32, 16])
+@pytest.mark.parametrize("T", [20, 100, 300])
+def test_a_nan_block_stays_in_its_row_and_column(block, T):
+    """A NaN or an infinity among the values makes its block's scale NaN: that token's outputs are NaN, a weight's
+    likewise its column, and every other output is as without it."""
+    K, N = 320, 776
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, w = torch.randn((T, K), generator=g, device="cuda"), torch.randn((N, K), generator=g, device="cuda")
+    run = lambda: geng.engram_project4(*geng.engram_quantize4(x, block, tiled=True),  # noqa: E731
+                                       *geng.engram_quantize4(w, block, tiled=True), block)
+    want = run()
+    x[7, 100], x[T - 1, 319], w[300, 0] = float("nan"), float("-inf"), float("inf")
+    got = run()
+    nan = torch.zeros((T, N), dtype=torch.bool, device="cuda")
+    nan[7], nan[T - 1], nan[:, 300] = True, True, True
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
+
+
+def test_outputs_beyond_32_bits():
+    """More than 2^32 outputs: the last rows and columns are in place."""
+    T, K, N, block = 170_000, 64, 25608, 32
+    rng = np.random.default_rng(1)
+    w, sw, vw = _operand(rng, N, K, block)
+    x = torch.randn((T, K), device="cuda")
+    a, sa = geng.engram_quantize4(x, block, tiled=True)
+    got = geng.engram_project4(a, sa, w, sw, block)
+    va = geng.engram_dequantize4(a, sa, block, tiled=True, out_dtype=torch.float32)
+    for rows in (slice(0, 3), slice(T // 2, T // 2 + 3), slice(T - 300, T)):
+        _check(got[rows], va[rows].double(), vw, 1.0, K, str(rows))
+
+
+def test_calls_of_several_streams_at_once():
+    """Few-token calls of different sizes and one of many tokens, in flight together."""
+    rng = np.random.default_rng(5)
+    block, K, N = 16, 1024, 6000
+    w, sw, vw = _operand(rng, N, K, block)
+    ops = [_operand(rng, T, K, block) for T in (1, 20, 50, 128, 700)]
+    want = [geng.engram_project4(a, sa, w, sw, block) for a, sa, _ in ops]
+    streams = [torch.cuda.Stream() for _ in ops]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = []
+        for (a, sa, _), s in zip(ops, streams):
+            got.append(geng.engram_project4(a, sa, w, sw, block, stream=s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_graph_replays_with_new_inputs():
     T, K, N, block = 70, 512, 776, 16
     rng = np.random.default_rng(9)

@@ -189,3 +189,23 @@ def test_other_stream_and_graph():
         x.copy_(torch.randn((300, 512), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
         graph.replay()
         assert torch.equal(out, geng.engram_dequantize4(*geng.engram_quantize4(x, 16), 16))
+
+
+def test_values_beyond_32_bits():
+    """More than 2^32 values: the last rows, there and back."""
+    rows, cols = 68_000_000, 64
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn((40, cols), device="cuda").bfloat16()
+    x[-40:] = tail
+    for block in (32, 16):
+        for tiled in (False, True):
+            codes, scales = geng.engram_quantize4(x, block, tiled=tiled)
+            c, s = geng.engram_quantize4(tail, block)
+            assert torch.equal(codes[-40:], c)
+            back = geng.engram_dequantize4(codes, scales, block, tiled=tiled)
+            assert torch.equal(back[-40:], geng.engram_dequantize4(c, s, block))
+            del codes, scales, back
+    codes, scales = geng.engram_quantize8(x, 32)
+    c, s = geng.engram_quantize8(tail, 32)
+    assert torch.equal(codes[-40:], c) and torch.equal(scales[-40:].view(torch.uint8), s.view(torch.uint8))
+    assert torch.equal(geng.engram_dequantize8(codes, scales, 32)[-40:], geng.engram_dequantize8(c, s, 32))
