@@ -66,11 +66,13 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
 
 // one row's part of a token into shared memory, counted in bytes on `bar`
-__device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(bar)
+__device__ __forceinline__ void copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
                : "memory");
+}
+__device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t bytes, uint32_t bar) {
+  copy_row(tc::smem_u32(dst), src, bytes, bar);
 }
 
 // Sums of N values over the warp, N a power of two <= 32: lane l ends with the total of value

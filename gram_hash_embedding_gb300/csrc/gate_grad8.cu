@@ -5,12 +5,17 @@
 // thread owns 8 columns of every copy from the first token to the last, and per token there is one exchange of 4 hc sums.
 // The codes halve what is read (0.79 of the bytes in all), but each value has to be widened twice, and with one token at a
 // time that chain (sums, exchange, scalars, outputs) took longer than the memory: 16,384 tokens of 4 x 5,120 677 us, floor
-// 434. So the chain is cut in two and runs over two tokens at a time:
+// 434. So the chain is cut in two and runs over two tokens at a time, with warps of their own for what the chain waits for:
 //   - the threads form the sums of token i + 1 and send them, then write the outputs of token i, whose scalars are ready;
-//   - a warp of its own gathers a token's sums, forms its scalars while the others work, and starts the copies of the
-//     tokens ahead.
+//   - a warp gathers a token's sums and forms its scalars while the others work;
+//   - a warp starts the copies of the tokens ahead and puts their scales, widened, and their mask beside them (loaded by
+//     the threads that use them, a token or two ahead, they cost 40 registers and their latency).
 // They meet on mbarriers; nothing waits for all threads of a CTA. A block's scale is one power of two for all 8 values of a
 // thread's row, so it goes into the sums and the scalars instead of the values: it changes no rounding there.
+// Measured: 16,384 of 4 x 5,120 448 us (0.97 of the floor; the scalars' and the copies' work in one warp and scales loaded
+// by the owners: 506), 4,096 of 8 x 5,120 262 (floor 208), 16,384 of 1 x 5,120 167 (136), 8,192 of 4 x 2,048 103 (87).
+// Wide rows are bound by DRAM; with few copies a token takes 1.6 us or more whatever its width, the pace of the copying warp
+// and of the exchange (three or four tokens in the chain at a time: no gain).
 //
 // What may be written while another role, or another CTA of the cluster, still reads (tokens here are open ones, c their
 // number): a thread sends sums c + 2 after it has seen the scalars of c, which need the sums c of every CTA, which these sent
@@ -36,8 +41,8 @@ using namespace gate;
 
 constexpr int kMaxStages = 5;
 
-// the most threads that own columns: what the registers allow, with one warp more for the scalars
-constexpr int max_owners(int hc) { return hc == 1 ? 736 : hc == 2 ? 608 : 352; }
+// the most threads that own columns: what the registers allow, with two warps more for scalars and copies
+constexpr int max_owners(int hc) { return hc == 1 ? 704 : hc == 2 ? 576 : 320; }
 
 // 8 E4M3 codes, without their block's scale
 __device__ __forceinline__ Vec8 widen_codes(const uint2& v) {
@@ -52,11 +57,17 @@ __device__ __forceinline__ Vec8 widen_codes(const uint2& v) {
 // NaN again.
 __device__ __forceinline__ float pow2(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
 
+// A block's scales in shared memory: those of the copies of x, of their keys, of the value, in records of 16-byte multiples
+__host__ __device__ constexpr int record(int hc) { return hc == 1 ? 4 : hc == 2 ? 8 : hc == 4 ? 12 : 20; }
+
+// the most blocks of scales that nv vectors of a row touch
+__host__ __device__ constexpr int blocks_of(int nv, int cs, int block) { return (8 * nv - 1) / block + (cs > 1 ? 2 : 1); }
+
 // HC copies in CG groups of threads, HC / CG copies each of the same columns (8 copies in one thread leave too few threads
 // on an SM). WHOLE: a CTA has whole rows, which lie together: three copies a token instead of 3 HC + 1.
 // stages: tokens in shared memory. withhold: the token whose sums the cluster's first CTA does not send (the test hook).
 template <int HC, int CG, bool WHOLE>
-__global__ void __launch_bounds__(max_owners(HC) + 32)
+__global__ void __launch_bounds__(max_owners(HC) + 64)
     gate_grad8_kernel(const GateGrad8Args a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
                       const int stages, float* __restrict__ part, unsigned int* __restrict__ status,
                       const int64_t withhold) {
@@ -69,13 +80,13 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
   constexpr int kStageVecs2 = 4 * HC + 1;  // a stage, in halves of 16 bytes for each vector: dout's rows, then the codes'
   extern __shared__ uint4 smem[];
   __shared__ float4 scal[2][HC];
-  __shared__ int again[2];
+  __shared__ int again[2], open_in[kMaxStages];
   __shared__ volatile int dead;  // a wait has run out: nothing more is fetched or sent, the results are not to be used
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4 + 2 + 2 + 1];
   const int dim = a.g.dim;
   const int64_t T = a.g.T;
   const int cs = WHOLE ? 1 : ctas;
-  const int tid = threadIdx.x, owners = blockDim.x - 32, lane = tid & 31, warp = tid >> 5, nw = owners >> 5;
+  const int tid = threadIdx.x, owners = blockDim.x - 64, lane = tid & 31, warp = tid >> 5, nw = owners >> 5;
   const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
   const uint32_t rank = blockIdx.x % cs;
   const int per_group = owners / CG, group = CG == 1 ? 0 : min(tid / per_group, CG - 1), gt = tid - group * per_group;
@@ -86,8 +97,12 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
   const int parts_of_group = cs * wg, red_half = CG * parts_of_group * M;
   float* red2 = red + 4 * red_half;                                             // [2][CG][cs][wg][2 HPT]
   const int red2_half = CG * parts_of_group * 2 * HPT;
+  constexpr int kRec = record(HC);
+  float* scs = red2 + 2 * red2_half;                                            // [stages][blocks][kRec]
+  const int scs_stage = blocks_of(nv, cs, a.block) * kRec;
   const int cnt = min(nv, (dim >> 3) - (int)rank * nv);  // this CTA's vectors of a row
   const int64_t row0 = 8 * (int64_t)rank * nv;           // its first column
+  const int b0 = (int)(row0 / a.block);                  // its first block of scales
   const uint32_t bar0 = tc::smem_u32(bars);
   const uint32_t kFull = 0, kEmpty = kMaxStages, kSums = 2 * kMaxStages, kScal = kSums + 4, kSums2 = kScal + 2, kScal2 = kSums2 + 2;
   auto bar = [&](uint32_t i) { return bar0 + 8 * i; };
@@ -97,7 +112,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
       atomicOr(status, ENGRAM_STATUS_TIMEOUT);
     }
   };
-  auto open_at = [&](int64_t t) { return t < T && (a.g.mask == nullptr || a.g.mask[t] != 0); };
+  auto mask_of = [&](int64_t t) { return t >= T ? 0u : a.g.mask == nullptr ? 1u : (uint32_t)a.g.mask[t]; };
 
   if (tid == 0) {
     dead = 0;
@@ -112,45 +127,115 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
   if (cs > 1) tc::cluster_sync();  // every CTA's barriers exist before another CTA sends to them
   else __syncthreads();
 
-  if (warp == nw) {
-    // ------------------------------------------------------------ copies and scalars
+  if (warp == nw + 1) {
+    // ------------------------------------------------------------ copies
     uint32_t last = ~0u;  // bit s: the parity of the stage's last copies
-    auto fetch = [&](int64_t t, int s, bool open) {
-      if (t >= T || dead) return;
-      last ^= 1u << s;
-      const uint32_t b = bar(kFull + s), bytes = 16 * cnt, codes = 8 * cnt;
-      tc::mbar_arrive_expect_tx(b, bytes * HC + (open ? codes * (2 * HC + 1) : 0));
-      uint8_t* to = reinterpret_cast<uint8_t*>(smem + (size_t)s * stage_vecs);
-      uint8_t* in = to + 16 * HC * nv;  // the rows of x, then those of kv
-      const uint16_t* u = a.g.dout + t * HC * dim + row0;
-      const uint8_t* h = a.x + t * HC * dim + row0;
-      const uint8_t* k = a.kv + t * (HC + 1) * dim + row0;
-      if constexpr (WHOLE) {
-        copy_row(to, u, bytes * HC, b);
-        if (open) {
-          copy_row(in, h, codes * HC, b);
-          copy_row(in + 8 * HC * nv, k, codes * (HC + 1), b);
-        }
-      }
-      if constexpr (!WHOLE) {
-        for (int i = 0; i < HC; ++i) copy_row(to + 16 * i * nv, u + (int64_t)i * dim, bytes, b);
-        if (open) {
-          for (int i = 0; i < HC; ++i) copy_row(in + 8 * i * nv, h + (int64_t)i * dim, codes, b);
-          for (int i = 0; i <= HC; ++i) copy_row(in + 8 * (HC + i) * nv, k + (int64_t)i * dim, codes, b);
-        }
-      }
+    // The fewer instructions a token takes here the better: this warp sets the pace of narrow rows. What a lane copies lies a
+    // fixed step from that of the token before: a row to a lane, or three runs of rows where a CTA has them whole.
+    constexpr int kRows = 2 * HC + 1, kDouts = WHOLE ? 1 : HC, kCopies = WHOLE ? 3 : HC + kRows;
+    const uint8_t* src = nullptr;
+    int64_t step = 0;
+    uint32_t bytes = 0, dst = 0;
+    if (lane < kDouts) {
+      src = reinterpret_cast<const uint8_t*>(a.g.dout + ((int64_t)cluster * HC + lane) * dim + row0);
+      step = 2ll * nc * HC * dim;
+      bytes = 16 * cnt * (WHOLE ? HC : 1);
+      dst = 16 * lane * nv;
+    } else if (lane < kCopies) {
+      const int i = lane - kDouts;  // row of the checkpoints (WHOLE: 0 those of x, 1 those of kv)
+      const bool kv = i >= (WHOLE ? 1 : HC);
+      const int r = WHOLE ? 0 : kv ? i - HC : i, rows = kv ? HC + 1 : HC;
+      src = (kv ? a.kv : a.x) + ((int64_t)cluster * rows + r) * dim + row0;
+      step = (int64_t)nc * rows * dim;
+      bytes = 8 * cnt * (WHOLE ? rows : 1);
+      dst = 16 * HC * nv + 8 * (WHOLE ? (kv ? HC : 0) : i) * nv;
+    }
+    const uint32_t dout_bytes = 16 * cnt * HC, code_bytes = 8 * cnt * kRows;
+    // The scales are too short to be copied in bulk: a lane takes every 32nd unit of a token's, a byte or (rows on 4-byte
+    // boundaries) four, the first kAhead of them before the stage is empty. (With those of two or three tokens on their way
+    // the kernel was slower: more instructions.)
+    constexpr int kAhead = 8;
+    const int n_blocks = (dim + a.block - 1) / a.block;
+    const int nb = (int)((row0 + 8 * cnt - 1) / a.block) - b0 + 1;  // this CTA's blocks of a row
+    const bool words = n_blocks % 4 == 0 && b0 % 4 == 0 &&
+                       ((reinterpret_cast<uintptr_t>(a.xs) | reinterpret_cast<uintptr_t>(a.kvs)) & 3) == 0;
+    const int per_row = words ? (nb + 3) / 4 : nb, units = kRows * per_row;
+    auto from_of = [&](int64_t t, int u) {
+      const int r = u / per_row;
+      return (r < HC ? a.xs + (t * HC + r) * n_blocks : a.kvs + (t * (HC + 1) + (r - HC)) * n_blocks) + b0 +
+             (u - r * per_row) * (words ? 4 : 1);
     };
-    // bit j of `open`: the mask of the cluster's token j places on
-    uint32_t open = 0;
-    for (int j = 0; j < stages; ++j) open |= (open_at(cluster + (int64_t)j * nc) ? 1u : 0u) << j;
-    if (lane == 0)
-      for (int s = 0; s < stages; ++s) fetch(cluster + (int64_t)s * nc, s, (open >> s) & 1);
-    uint32_t c = 0, c2 = 0;  // open tokens, and those whose sums were formed once more
-    int s = 0, ps = stages - 1;   // stages of the token and of the one before
-    uint32_t pass = 0;            // how often the ring has gone round before the token before
+    auto to_of = [&](int u) {  // the unit's place in its first record, and how many blocks it is
+      const int r = u / per_row, k = (u - r * per_row) * (words ? 4 : 1);
+      return make_int2(k * kRec + r, words ? min(4, nb - k) : 1);
+    };
+    auto load = [&](const uint8_t* from) {
+      return words ? __ldg(reinterpret_cast<const uint32_t*>(from)) : (uint32_t)__ldg(from);
+    };
+    auto store = [&](int s, int2 at, uint32_t v) {
+      float* to = scs + s * scs_stage + at.x;
+      to[0] = pow2(v & 255u);
+#pragma unroll
+      for (int e = 1; e < 4; ++e)
+        if (e < at.y) to[e * kRec] = pow2((v >> (8 * e)) & 255u);
+    };
+    const uint8_t* from[kAhead];
+    uint32_t early[kAhead];
+    int2 to[kAhead];
+    const int nj = min(kAhead, (units + 31) / 32);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int u = min(lane + 32 * j, units - 1);
+      from[j] = from_of(cluster, u);
+      to[j] = to_of(u);
+    }
+    const int64_t step_x = (int64_t)nc * HC * n_blocks, step_kv = (int64_t)nc * (HC + 1) * n_blocks;
+    uint32_t coming = mask_of(cluster);  // asked for a token before it is needed
+    int s = 0;
+    uint32_t pass = 0;  // how often the ring has gone round
+    const uint32_t stage_bytes = 16 * stage_vecs, dst0 = tc::smem_u32(smem) + dst;
     for (int64_t t = cluster; t < T; t += nc) {
-      const uint32_t next = open_at(t + (int64_t)stages * nc) ? 1u : 0u;
-      if (open & 1) {
+      const bool open = coming != 0;
+      coming = mask_of(t + nc);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j < nj) {
+          if (open) early[j] = load(from[j]);
+          from[j] += min(lane + 32 * j, units - 1) < HC * per_row ? step_x : step_kv;
+        }
+      }
+      if (pass > 0) wait(kEmpty + s, (pass - 1) & 1);
+      if (__any_sync(0xffffffffu, dead)) break;  // the same for all lanes
+      const uint32_t b = bar(kFull + s);
+      // (bytes may arrive before they are expected: the phase ends with lane 0's arrival at the earliest)
+      if (lane < (open ? kCopies : kDouts)) copy_row(dst0 + s * stage_bytes, src, bytes, b);
+      src += step;
+      last ^= 1u << s;
+      if (open) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (j < nj && lane + 32 * j < units) store(s, to[j], early[j]);
+        for (int u = lane + 32 * kAhead; u < units; u += 32) store(s, to_of(u), load(from_of(t, u)));
+      }
+      if (lane == 0) open_in[s] = open;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_expect_tx(b, dout_bytes + (open ? code_bytes : 0));
+      if (++s == stages) {
+        s = 0;
+        ++pass;
+      }
+    }
+    if (dead && lane == 0)  // copies may still be on their way into this CTA's memory
+      for (int s = 0; s < stages; ++s)
+        if (cluster + (int64_t)s * nc < T) tc::mbar_wait(bar(kFull + s), (last >> s) & 1, nullptr);
+    __syncwarp();
+  } else if (warp == nw) {
+    // ------------------------------------------------------------ scalars
+    uint32_t c = 0, c2 = 0;  // open tokens, and those whose sums were formed once more
+    uint32_t open = mask_of(cluster), coming = mask_of(cluster + nc);
+    for (int64_t t = cluster; t < T; t += nc) {
+      const uint32_t then = mask_of(t + 2 * (int64_t)nc);
+      if (open != 0) {
         const uint32_t b = c & 1;
         if (!WHOLE && lane == 0 && !dead)
           tc::mbar_arrive_expect_tx(bar(kSums + (c & 3)), (uint32_t)(cs * nw * M * 4));
@@ -192,46 +277,43 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
         }
         ++c;
       }
-      if (t != cluster) {  // the stage of the token before, once its outputs are written
-        if (lane == 0 && t + (int64_t)(stages - 1) * nc < T) {
-          wait(kEmpty + ps, pass & 1);
-          fetch(t + (int64_t)(stages - 1) * nc, ps, (open >> (stages - 1)) & 1);
-        }
-        __syncwarp();
-      }
-      ps = s;
-      if (++s == stages) s = 0;
-      if (ps == 0 && t != cluster) ++pass;
-      open = open >> 1 | next << (stages - 1);
+      open = coming;
+      coming = then;
     }
-    if (dead && lane == 0)  // copies may still be on their way into this CTA's memory
-      for (int s = 0; s < stages; ++s)
-        if (cluster + (int64_t)s * nc < T) tc::mbar_wait(bar(kFull + s), (last >> s) & 1, nullptr);
-    __syncwarp();
   } else {
     // ------------------------------------------------------------ owners of columns
     const bool on = gt < cnt;
     const int me = min(gt, cnt - 1);  // threads past the row read its last vector and use nothing of it
     const int64_t col = row0 + 8 * gt;
     const int64_t gcol = (int64_t)g0 * dim + col;  // the thread's place in its first copy
-    const int64_t n_blocks = (dim + a.block - 1) / a.block, my_block = (row0 + 8 * me) / a.block;
+    const float* my_scales = scs + ((int)((row0 + 8 * me) / a.block) - b0) * kRec;
     auto u_of = [&](int s, int i) { return widen8(smem[s * stage_vecs + (g0 + i) * nv + me]); };
     auto codes = [&](int s, int j) {  // row j of the checkpoints' rows
       return widen_codes(reinterpret_cast<const uint2*>(smem + s * stage_vecs + HC * nv)[j * nv + me]);
     };
     // the scales at the thread's columns: its copies', their keys', the value's
     struct Scales {
-      uint32_t h[HPT], k[HPT], v;
+      float h[HPT], k[HPT], v;
     };
-    auto load_scales = [&](Scales& s, int64_t t) {
-      const uint8_t* xs = a.xs + (t * HC + g0) * n_blocks + my_block;
-      const uint8_t* ks = a.kvs + (t * (HC + 1) + g0) * n_blocks + my_block;
+    auto scales_of = [&](int s) {
+      const float* from = my_scales + s * scs_stage;
+      Scales r;
+      if constexpr (HPT == 1) {
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        r.h[0] = f.x, r.k[0] = f.y, r.v = f.z;
+      } else if constexpr (HPT == 2) {
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        r.h[0] = f.x, r.h[1] = f.y, r.k[0] = f.z, r.k[1] = f.w, r.v = from[4];
+      } else {
 #pragma unroll
-      for (int i = 0; i < HPT; ++i) {
-        s.h[i] = __ldg(xs + i * n_blocks);
-        s.k[i] = __ldg(ks + i * n_blocks);
+        for (int i = 0; i < HPT; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(from + g0 + i), g = *reinterpret_cast<const float4*>(from + HC + g0 + i);
+          r.h[i] = f.x, r.h[i + 1] = f.y, r.h[i + 2] = f.z, r.h[i + 3] = f.w;
+          r.k[i] = g.x, r.k[i + 1] = g.y, r.k[i + 2] = g.z, r.k[i + 3] = g.w;
+        }
+        r.v = from[2 * HC];
       }
-      s.v = __ldg(ks + (HC - g0) * n_blocks);
+      return r;
     };
     auto load_weights = [&](int i) {
       Vec8 w = {};
@@ -254,11 +336,11 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
     };
     Vec8 dw[HPT] = {};
     // the sums of token t, open token number c, from stage s
-    auto sums = [&](int64_t t, uint32_t c, int s, const Scales& sc) {
+    auto sums = [&](int64_t t, uint32_t c, int s) {
       float m[M] = {};
       if (on) {  // past the row: another thread's vector
+        const Scales sc = scales_of(s);
         const Vec8 v = codes(s, 2 * HC);
-        const float vs = pow2(sc.v);
 #pragma unroll
         for (int i = 0; i < HPT; ++i) {
           const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), u = u_of(s, i);
@@ -271,11 +353,11 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
             q[2] = __ffma2_rn(__fmul2_rn(h.p[e], k.p[e]), w.p[e], q[2]);
             q[3] = __ffma2_rn(u.p[e], v.p[e], q[3]);
           }
-          const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+          const float hs = sc.h[i], ks = sc.k[i];
           m[4 * i] = (q[0].x + q[0].y) * hs * hs;
           m[4 * i + 1] = (q[1].x + q[1].y) * ks * ks;
           m[4 * i + 2] = (q[2].x + q[2].y) * hs * ks;
-          m[4 * i + 3] = (q[3].x + q[3].y) * vs;
+          m[4 * i + 3] = (q[3].x + q[3].y) * sc.v;
         }
       }
       const float mine = warp_reduce_scatter<M>(m, lane);
@@ -289,23 +371,18 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
         for (int r = 0; r < cs; ++r) send(to, bar(kSums + (c & 3)), r, mine);
       }
     };
-    bool open = open_at(cluster), next_open = open_at(cluster + nc);
-    Scales sc = {}, ahead = {};  // of the token, and of the next one
-    if (open) load_scales(sc, cluster);
-    if (next_open) load_scales(ahead, cluster + nc);
     if (cluster < T) wait(kFull, 0);
-    if (open) sums(cluster, 0, 0, sc);
+    bool open = cluster < T && open_in[0] != 0, next_open = false;
+    if (open) sums(cluster, 0, 0);
     uint32_t c = 0, c2 = 0, pass = 0;  // open tokens, those whose sums were formed once more, rounds of the ring
     uint32_t odd = 0;                  // CG > 1: the token's half of dvp, and its barrier
     int s = 0;
     for (int64_t t = cluster; t < T; t += nc) {
-      const bool then_open = open_at(t + 2 * (int64_t)nc);
-      Scales beyond = {};  // of the token after the next: on their way while this one's outputs are formed
       const int ns = s + 1 == stages ? 0 : s + 1;
       if (t + nc < T) {
         wait(kFull + ns, (ns == 0 ? pass + 1 : pass) & 1);
-        if (next_open) sums(t + nc, c + (open ? 1 : 0), ns, ahead);
-        if (then_open) load_scales(beyond, t + 2 * (int64_t)nc);
+        next_open = open_in[ns] != 0;
+        if (next_open) sums(t + nc, c + (open ? 1 : 0), ns);
       }
       uint16_t* dxt = a.g.dx + t * HC * dim + gcol;
       uint16_t* dkt = a.g.dkv + t * (HC + 1) * dim + gcol;
@@ -314,10 +391,11 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
         wait(kScal + b, (c >> 1) & 1);
         if (again[b]) {  // sum(h w key) once more, in twice the precision
           Sum2 d[HPT];
+          const Scales sc = scales_of(s);
 #pragma unroll
           for (int i = 0; i < HPT; ++i) {
             const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), w = weights(i);
-            const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+            const float hs = sc.h[i], ks = sc.k[i];
             d[i] = Sum2{0.f, 0.f};
             if (on) d[i] = dot_part(h, k, w);
             d[i].hi = d[i].hi * hs * ks;
@@ -345,12 +423,13 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
         Vec8 dv = {};
         float4* mine = dvp + odd * (CG - 1) * 2 * per_group;
         if (on) {
+          const Scales sc = scales_of(s);
 #pragma unroll
           for (int i = 0; i < HPT; ++i) {
             const float4 g = scal[b][g0 + i];  // gate, c, -e / A, -e / B
             const Vec8 h = codes(s, g0 + i), k = codes(s, HC + g0 + i), u = u_of(s, i);
             const Vec8 w = weights(i);
-            const float hs = pow2(sc.h[i]), ks = pow2(sc.k[i]);
+            const float hs = sc.h[i], ks = sc.k[i];
             // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
             const float cwk = g.y * ks, eh = g.z * hs, cwh = g.y * hs, ek = g.w * ks, chk = g.y * hs * ks;
             Vec8 dh, dk;
@@ -402,10 +481,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(kEmpty + s));
       odd ^= 1;
-      sc = ahead;
-      ahead = beyond;
       open = next_open;
-      next_open = then_open;
       s = ns;
       if (s == 0) ++pass;
     }
@@ -428,7 +504,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 32)
 }
 
 // the threads that an SM's registers hold
-constexpr int resident_threads(int hc) { return hc == 1 ? 672 : hc == 2 ? 640 : 384; }
+constexpr int resident_threads(int hc) { return hc == 1 ? 768 : hc == 2 ? 640 : 384; }
 
 struct Shape {
   int cs, cg, nv, owners, stages;  // CTAs per cluster, groups of copies, vectors and column-owning threads per CTA
@@ -438,9 +514,10 @@ struct Shape {
 // As in gate_grad.cu: the smallest cluster (with one exception) whose CTAs hold their columns in registers and three
 // stages of shared memory, more CTAs a token when there are too few tokens for every SM; then as many stages, up to
 // kMaxStages, as cost no CTA its place on an SM.
-Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
+Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   Shape s;
   const int nvec = dim / 8;
+  int32_t of = 32;  // the smallest blocks, so that what the workspace holds does not depend on them
   auto set = [&](int cs, int cg, int stages) {
     s.cs = cs;
     s.cg = cg;
@@ -450,7 +527,8 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
     const int per_group = (s.nv + 31) / 32 * 32, hpt = hc / cg;
     s.owners = per_group * cg;
     s.smem = (int64_t)stages * (4 * hc + 1) * s.nv * 8 + 2ll * (cg - 1) * per_group * 32 +
-             (int64_t)cs * (s.owners / 32) * 4 * (4 * 4 * hpt + 2 * 2 * hpt);
+             (int64_t)cs * (s.owners / 32) * 4 * (4 * 4 * hpt + 2 * 2 * hpt) +
+             4ll * stages * blocks_of(s.nv, cs, of) * record(hc);
     return s.owners <= max_owners(hc) && s.smem <= kMaxSmem;
   };
   const int cg = hc == 8 ? 2 : 1;
@@ -460,7 +538,7 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
   // CTAs resident on an SM, by shared memory and registers
   auto resident = [&]() {
     return std::max<int64_t>(
-        1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / (s.owners + 32)));
+        1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / (s.owners + 64)));
   };
   if (!set(cs, cg, 3)) {
     if (!set(cs, 1, 3)) set(cs, 1, 2);  // 8 copies of more than 12,000 columns or so
@@ -470,6 +548,7 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim) {
     if (s.nv * resident() * 5 < columns * 7) set(cs, cg, 3);
   }
   const int64_t fit = resident();
+  of = block;
   while (s.stages < kMaxStages) {
     const Shape before = s;
     if (set(s.cs, s.cg, s.stages + 1) && resident() == fit) continue;
@@ -486,7 +565,7 @@ cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, i
   constexpr auto kern = gate_grad8_kernel<HC, CG, WHOLE>;
   cudaError_t e = allow_smem<kern>((int)sh.smem);
   if (e != cudaSuccess) return e;
-  const int threads = sh.owners + 32;
+  const int threads = sh.owners + 64;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -535,14 +614,14 @@ cudaError_t launch_copies(const GateGrad8Args& a, const Shape& sh, float* part, 
 }  // namespace
 
 uint64_t gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim) {
-  return round256((uint64_t)shape_of(T, hc, dim).clusters * hc * dim * 4);
+  return round256((uint64_t)shape_of(T, hc, dim, 32).clusters * hc * dim * 4);
 }
 
 cudaError_t launch_gate_grad8(const GateGrad8Args& a, void* workspace, cudaStream_t s, int64_t withhold) {
   float* part = static_cast<float*>(workspace);
   int parts = 0;
   if (a.g.T > 0) {
-    const Shape sh = shape_of(a.g.T, a.g.hc, a.g.dim);
+    const Shape sh = shape_of(a.g.T, a.g.hc, a.g.dim, a.block);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.g.hc) {
       case 1: e = launch_copies<1, 1>(a, sh, part, &parts, withhold, s); break;
