@@ -1085,12 +1085,13 @@ def _tiled_size(rows: int, cols: int, block: int) -> int:
     return -(-rows // 128) * -(-cols // (4 * block)) * 512
 
 
-def _stream_on(t: torch.Tensor, stream, temps) -> int:
-    """The stream handle of a call on t's memory, which has to be the current device's: launched from another device's
-    stream, the call's pointers would be foreign to it."""
+def _stream_on(inputs, stream, temps) -> int:
+    """The stream handle of a call whose tensors all have to be on the current device: launched from another device's
+    stream, their pointers would be foreign to it."""
     dev = torch.cuda.current_device()
-    if t.get_device() != dev:
-        raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    for t in (*inputs, *temps):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
     return _launch_stream(stream, temps)
@@ -1130,7 +1131,7 @@ def engram_quantize4(x: torch.Tensor, block: int = 32, scale: float = 1.0, tiled
     else:
         sp = _bytes(scales, _tiled_size(rows, cols, block) if tiled else rows * (cols // block), "scales", sdt)
     rc = _lib().engram_quantize4(x.data_ptr(), rows, cols, stride, xt, block, float(scale), 1 if tiled else 0, cp, sp,
-                                 _stream_on(x, stream, (codes, scales)))
+                                 _stream_on((x,), stream, (codes, scales)))
     if rc:
         raise EngramError(rc, "engram_quantize4")
     return codes, scales
@@ -1156,7 +1157,7 @@ def engram_dequantize4(codes: torch.Tensor, scales: torch.Tensor, block: int, sc
     else:
         ot, op = _float_out(out, out_dtype, rows * cols)
     rc = _lib().engram_dequantize4(cp, sp, rows, cols, block, float(scale), 1 if tiled else 0, op, ot,
-                                   _stream_on(codes, stream, (out,)))
+                                   _stream_on((codes, scales), stream, (out,)))
     if rc:
         raise EngramError(rc, "engram_dequantize4")
     return out
@@ -1188,7 +1189,7 @@ def engram_lookup4(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, block: i
         _size(out, T * C * dim, "out")
         op = _dev(out, torch.bfloat16, "out")
     rc = _lib().engram_lookup4(ip, istride, T, C, qp, sp, rows, dim, block, float(scale), op,
-                               _stream_on(Q, stream, (out,)))
+                               _stream_on((idx, Q, S), stream, (out,)))
     if rc:
         raise EngramError(rc, "engram_lookup4")
     return out
@@ -1214,7 +1215,7 @@ def engram_lookup4_operand(idx: torch.Tensor, Q: torch.Tensor, S: torch.Tensor, 
     else:
         op = _bytes(scales, _tiled_size(T, K, block), "scales", _SCALE4_DTYPE[block])
     rc = _lib().engram_lookup4_operand(ip, istride, T, C, qp, sp, rows, dim, block, cp, op,
-                                       _stream_on(Q, stream, (codes, scales)))
+                                       _stream_on((idx, Q, S), stream, (codes, scales)))
     if rc:
         raise EngramError(rc, "engram_lookup4_operand")
     return codes, scales
@@ -1245,7 +1246,7 @@ def engram_project4(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
         _size(out, T * N, "out")
         op = _dev(out, torch.bfloat16, "out")
     rc = _lib().engram_project4(ap, asp, wp, wsp, T, K, N, block, float(scale), op,
-                                _stream_on(w, stream, (out,)))
+                                _stream_on((a, a_scales, w, w_scales), stream, (out,)))
     if rc:
         raise EngramError(rc, "engram_project4")
     return out
@@ -1277,7 +1278,7 @@ def engram_quantize8(x: torch.Tensor, block: int = 128, scale_dtype: int = SCALE
         _size(scales, rows * n, "scales")
         sp = _dev_scales(scales, scale_dtype, "scales")
     rc = _lib().engram_quantize8(x.data_ptr(), rows, cols, stride, xt, block, scale_dtype, cp, sp,
-                                 _stream_on(x, stream, (codes, scales)))
+                                 _stream_on((x,), stream, (codes, scales)))
     if rc:
         raise EngramError(rc, "engram_quantize8")
     return codes, scales
@@ -1304,7 +1305,7 @@ def engram_dequantize8(codes: torch.Tensor, scales: torch.Tensor, block: int, ou
     else:
         ot, op = _float_out(out, out_dtype, rows * cols)
     rc = _lib().engram_dequantize8(cp, _dev_scales(scales, sdt, "scales"), rows, cols, block, sdt, op, ot,
-                                   _stream_on(codes, stream, (out,)))
+                                   _stream_on((codes, scales), stream, (out,)))
     if rc:
         raise EngramError(rc, "engram_dequantize8")
     return out
@@ -1361,7 +1362,8 @@ def engram_gate_grad8(x: torch.Tensor, x_scales: torch.Tensor, kv: torch.Tensor,
     keep, ws, nbytes = _scratch(workspace, L.engram_gate_grad8_workspace(T, hc, dim), dev)
     rc = L.engram_gate_grad8(*inputs, block, p[0], p[1], p[2], p[3] if mask is not None else None, T, hc, dim, eps,
                              dx.data_ptr(), dkv.data_ptr(), dq_weight.data_ptr(), dk_weight.data_ptr(), ws, nbytes,
-                             _stream_on(x, stream, (dx, dkv, dq_weight, dk_weight, keep)))
+                             _stream_on((x, x_scales, kv, kv_scales, q_weight, k_weight, dout, mask), stream,
+                                        (dx, dkv, dq_weight, dk_weight, keep)))
     if rc:
         raise EngramError(rc, "engram_gate_grad8")
     return dx, dkv, dq_weight, dk_weight

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
   const int64_t row0 = 8 * (int64_t)rank * nv;           // its first column
   const int b0 = (int)(row0 / a.block);                  // its first block of scales
   const uint32_t bar0 = tc::smem_u32(bars);
-  const uint32_t kFull = 0, kEmpty = kMaxStages, kSums = 2 * kMaxStages, kScal = kSums + 4, kSums2 = kScal + 2, kScal2 = kSums2 + 2;
+  const uint32_t kFull = 0, kEmpty = kMaxStages, kSums = 2 * kMaxStages, kScal = kSums + 4, kSums2 = kScal + 2;
+  const uint32_t kScal2 = kSums2 + 2;
   auto bar = [&](uint32_t i) { return bar0 + 8 * i; };
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (!dead && !tc::mbar_wait(bar(b), parity, const_cast<const volatile int*>(&dead))) {
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
       } else {
 #pragma unroll
         for (int i = 0; i < HPT; i += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(from + g0 + i), g = *reinterpret_cast<const float4*>(from + HC + g0 + i);
+          const float4 f = *reinterpret_cast<const float4*>(from + g0 + i);
+          const float4 g = *reinterpret_cast<const float4*>(from + HC + g0 + i);
           r.h[i] = f.x, r.h[i + 1] = f.y, r.h[i + 2] = f.z, r.h[i + 3] = f.w;
           r.k[i] = g.x, r.k[i + 1] = g.y, r.k[i + 2] = g.z, r.k[i + 3] = g.w;
         }

@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kThreads)
     four |= __shfl_xor_sync(0xffffffffu, four, 2 * LANES);
     if (!on || threadIdx.x % (4 * LANES) != 0) return;
     const uint32_t r = by_row((uint32_t)u), k = ((uint32_t)u - r * per_row) / LANES;
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) + tiled_scale_at((int64_t)r, k, scale_groups(a.cols, a.block))) =
-        four;
+    uint8_t* to = static_cast<uint8_t*>(a.scales) + tiled_scale_at((int64_t)r, k, scale_groups(a.cols, a.block));
+    *reinterpret_cast<uint32_t*>(to) = four;
     return;
   }
   if (!lo || j % LANES != 0) return;

@@ -207,3 +207,19 @@ def test_gate_grad8_binding_sizes():
             geng.engram_gate_grad8(*args, w, w, x.to(torch.bfloat16), block=64, **ok)
     with pytest.raises(TypeError, match="x must be"):
         geng.engram_gate_grad8(x.to(torch.bfloat16), _fake(3, 2, 1), k, _fake(3, 3, 1), w, w, x, block=64, **ok)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    class On:
+        def __init__(self, index):
+            self.index, self.device = index, f"cuda:{index}"
+
+        def get_device(self):
+            return self.index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(geng, "_raw_stream", lambda dev: 7)
+    assert geng._stream_on((On(0), None), None, (On(0),)) == 7
+    for inputs, temps in (((On(1),), ()), ((On(0), On(1)), ()), ((On(0),), (On(1),)), ((None, On(0)), (On(0), On(1)))):
+        with pytest.raises(ValueError, match="cuda:1, the current device is cuda:0"):
+            geng._stream_on(inputs, None, temps)
