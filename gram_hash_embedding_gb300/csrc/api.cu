@@ -823,7 +823,7 @@ int engram_gate_grad_withhold(const uint16_t* x, const uint16_t* kv, const uint1
 }
 
 // ------------------------------------------------------------------------------------------------
-// Low-bit operators (quant.cu, lookup4.cu, proj4.cu, and gate_grad.cu from checkpoints)
+// Low-bit operators (quant.cu, lookup4.cu, proj4.cu, gate_grad8.cu)
 namespace {
 inline bool block8_ok(int32_t block) { return block == 32 || block == 64 || block == 128; }
 
