@@ -178,3 +178,21 @@ def test_offsets_beyond_32_bits():
     got = geng.engram_gate_grad8(x, xs, kv, ks, args[2].cuda(), args[3].cuda(), dout, mask=mask, dx=dout)
     assert (got[0][: -n : 4099] == 1).all() and (got[1][: -n : 4099] == 0).all()
     G._check(back, [got[0][-n:], got[1][-n:], got[2], got[3]], "last tokens")
+
+
+@pytest.mark.parametrize("block", [32, 64])
+@pytest.mark.parametrize("T,hc,dim", [(900, 1, 5120), (700, 2, 5120), (600, 4, 2048), (400, 4, 5120), (200, 8, 5120)])
+def test_scales_at_any_address(T, hc, dim, block):
+    """Scales are read by words where they lie on 4-byte boundaries, else by bytes: the same bits."""
+    args = G._inputs(np.random.default_rng(T + block), T, hc, dim)
+    xq, kq, back = _checkpoints(args, block)
+    want = _run8(xq, kq, back, block)
+    G._check(back, want, f"T={T} hc={hc} dim={dim} block={block}")
+    for off in (1, 2):
+        moved = []
+        for _, s in (xq, kq):
+            room = torch.full((s.numel() + 8,), 255, dtype=torch.uint8, device="cuda")
+            room[off:off + s.numel()] = s.view(torch.uint8).flatten()
+            moved.append(room[off:off + s.numel()].view(s.shape))
+        got = _run8((xq[0], moved[0]), (kq[0], moved[1]), back, block)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
