@@ -27,9 +27,9 @@
 #include <cstdint>
 #include <type_traits>
 
-#include "dequant.cuh"
 #include "engram_internal.cuh"
 #include "gate_grad.cuh"
+#include "gate_grad8.cuh"
 #include "launch_cache.cuh"
 #include "proj.cuh"
 #include "tc_ptx.cuh"
@@ -44,19 +44,6 @@ constexpr int kMaxStages = 5;
 
 // the most threads that own columns: what the registers allow, with two warps more for scalars and copies
 constexpr int max_owners(int hc) { return hc == 1 ? 704 : hc == 2 ? 576 : 320; }
-
-// 8 E4M3 codes, without their block's scale
-__device__ __forceinline__ Vec8 widen_codes(const uint2& v) {
-  const uint32_t w[4] = {v.x, v.x >> 16, v.y, v.y >> 16};
-  Vec8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f16x2_to_f32(e4m3x2_to_f16x2(w[i] & 0xffffu), r.p[i].x, r.p[i].y);
-  return r;
-}
-
-// A checkpoint's scale 2^(b - 127). A NaN (255) comes out as infinity: the codes of such a block are 0, and 0 times it is a
-// NaN again.
-__device__ __forceinline__ float pow2(uint32_t b) { return __uint_as_float(max(b << 23, 0x00400000u)); }
 
 // A block's scales in shared memory: those of the copies of x, of their keys, of the value, in records of 16-byte multiples
 __host__ __device__ constexpr int record(int hc) { return hc == 1 ? 4 : hc == 2 ? 8 : hc == 4 ? 12 : 20; }
@@ -617,13 +604,19 @@ cudaError_t launch_copies(const GateGrad8Args& a, const Shape& sh, float* part, 
 }  // namespace
 
 uint64_t gate_grad8_workspace(int64_t T, int32_t hc, int32_t dim) {
-  return round256((uint64_t)shape_of(T, hc, dim, 32).clusters * hc * dim * 4);
+  const int64_t clusters = shape_of(T, hc, dim, 32).clusters, ctas = gate_grad8_rows_parts(T, hc, dim);
+  return round256((uint64_t)std::max(clusters, ctas) * hc * dim * 4);
 }
 
 cudaError_t launch_gate_grad8(const GateGrad8Args& a, void* workspace, cudaStream_t s, int64_t withhold) {
   float* part = static_cast<float*>(workspace);
   int parts = 0;
-  if (a.g.T > 0) {
+  // (the test hook is this file's kernel's)
+  if (a.g.T > 0 && withhold < 0) parts = gate_grad8_rows_parts(a.g.T, a.g.hc, a.g.dim);
+  if (parts > 0) {
+    const cudaError_t e = launch_gate_grad8_rows(a, part, parts, s);
+    if (e != cudaSuccess) return e;
+  } else if (a.g.T > 0) {
     const Shape sh = shape_of(a.g.T, a.g.hc, a.g.dim, a.block);
     cudaError_t e = cudaErrorInvalidValue;
     switch (a.g.hc) {

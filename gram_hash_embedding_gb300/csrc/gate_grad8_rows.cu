@@ -1,0 +1,307 @@
+// The gradient of the Engram gate from 8-bit checkpoints, rows that a warp holds (sm_103a): the formulas and the arithmetic
+// of gate_grad8.cu for narrow rows, where that kernel's barriers, exchange and copying warp took 1.6 us a token and CTA
+// whatever the width.
+//
+// Design: G lanes take a token, each VECS vectors of 8 columns of every copy; its sums stay in those lanes (a reduction that
+// scatters, then four shuffles that bring each copy's sums together), lane c forms the scalars of copy c, and the token's
+// rows never leave registers. No barriers but the warp's; many warps an SM cover one another's loads. The weights' product
+// lies in shared memory, the weights' gradients in registers until the end, where a CTA adds them up in a fixed order.
+#include <algorithm>
+#include <cstdint>
+
+#include "dequant.cuh"
+#include "engram_internal.cuh"
+#include "gate_grad.cuh"
+#include "gate_grad8.cuh"
+#include "launch_cache.cuh"
+#include "train.cuh"
+
+namespace engram {
+namespace {
+
+using namespace gate;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// CTAs on an SM: what the registers of HC * VECS vectors allow
+constexpr int resident_ctas(int vectors) { return vectors == 1 ? 4 : vectors == 2 ? 3 : vectors <= 4 ? 2 : 1; }
+
+// Sums of N values over the G lanes of a token: lane p ends with the totals of values p N / G and after (N >= G), or of value
+// p / (G / N), in s[0] and after.
+template <int N, int G>
+__device__ __forceinline__ void group_reduce_scatter(float (&s)[N], int lane) {
+  int off = G / 2;
+#pragma unroll
+  for (int w = N / 2; w >= (N > G ? N / G : 1); w /= 2, off /= 2) {
+    const bool up = lane & off;
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const float give = up ? s[j] : s[j + w];
+      const float keep = up ? s[j + w] : s[j];
+      s[j] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+    }
+  }
+#pragma unroll
+  for (int o = G / N / 2; o >= 1; o /= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+}
+
+// what is formed from the value after this is formed anew
+__device__ __forceinline__ void again(uint32_t& v) { asm volatile("" : "+r"(v)); }
+__device__ __forceinline__ void again(uint2& v) { asm volatile("" : "+r"(v.x), "+r"(v.y)); }
+__device__ __forceinline__ void again(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+
+template <int HC, int VECS, int G>
+__global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
+    gate_grad8_rows_kernel(const GateGrad8Args a, const float rd, const float inv_sqrt_dim, float* __restrict__ part) {
+  pdl_wait();
+  pdl_trigger();
+  static_assert(VECS == 1 || G == 32, "a lane has more vectors where a token has a whole warp");
+  constexpr int N = 4 * HC, kTokens = 32 / G;  // sums of a token, tokens of a warp
+  extern __shared__ float4 w_smem[];           // [HC][dim] q_weight * k_weight; at the end the CTA's sums
+  __shared__ float4 scal[kWarps][kTokens][HC];
+  float* const w_of = reinterpret_cast<float*>(w_smem);
+  const int dim = a.g.dim, nvec = dim / 8, n_blocks = (dim + a.block - 1) / a.block;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, p = lane % G, sub = lane / G, first = sub * G;
+  const int64_t T = a.g.T;
+  for (int i = threadIdx.x; i < HC * dim; i += kThreads)
+    w_of[i] = __uint_as_float((uint32_t)a.g.qw[i] << 16) * __uint_as_float((uint32_t)a.g.kw[i] << 16);
+  __syncthreads();
+  bool on[VECS];
+  int col[VECS], block[VECS];
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    on[v] = p + G * v < nvec;
+    col[v] = 8 * min(p + G * v, nvec - 1);  // lanes past the row: its last vector's scales and weights, values of 0
+    block[v] = col[v] / a.block;
+  }
+  auto weights = [&](int i, int v) {
+    const float4* from = w_smem + (i * dim + col[v]) / 4;
+    const float4 x = from[0], y = from[1];
+    Vec8 w;
+    w.p[0] = make_float2(x.x, x.y), w.p[1] = make_float2(x.z, x.w);
+    w.p[2] = make_float2(y.x, y.y), w.p[3] = make_float2(y.z, y.w);
+    return w;
+  };
+  Vec8 dw[HC][VECS] = {};
+  const int64_t stride = (int64_t)gridDim.x * kWarps * kTokens;
+  for (int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; base < T; base += stride) {
+    const int64_t t = base + sub;
+    const bool in = t < T, open = in && (a.g.mask == nullptr || a.g.mask[t] != 0);
+    const int64_t row = in ? t : base;
+    uint4 u[HC][VECS] = {};
+    uint2 h[HC][VECS] = {}, k[HC + 1][VECS] = {};
+    uint32_t hs[HC][VECS] = {}, ks[HC + 1][VECS] = {};
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      if (in && on[v]) {
+        const uint16_t* from = a.g.dout + row * HC * dim + col[v];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) u[i][v] = __ldg(reinterpret_cast<const uint4*>(from + i * dim));
+      }
+      if (open && on[v]) {
+        const uint8_t *x = a.x + row * HC * dim + col[v], *kv = a.kv + row * (HC + 1) * dim + col[v];
+        const uint8_t *xs = a.xs + row * HC * n_blocks + block[v], *kvs = a.kvs + row * (HC + 1) * n_blocks + block[v];
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          h[i][v] = __ldg(reinterpret_cast<const uint2*>(x + i * dim));
+          hs[i][v] = __ldg(xs + i * n_blocks);
+        }
+#pragma unroll
+        for (int i = 0; i <= HC; ++i) {
+          k[i][v] = __ldg(reinterpret_cast<const uint2*>(kv + i * dim));
+          ks[i][v] = __ldg(kvs + i * n_blocks);
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, open)) {
+      float m[N];
+#pragma unroll
+      for (int i = 0; i < HC; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[4 * i + e] = 0.f;
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+          const Vec8 hv = widen_codes(h[i][v]), kv = widen_codes(k[i][v]), vv = widen_codes(k[HC][v]), uv = widen8(u[i][v]);
+          const Vec8 w = weights(i, v);
+          float2 q[4] = {};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            q[0] = __ffma2_rn(hv.p[e], hv.p[e], q[0]);
+            q[1] = __ffma2_rn(kv.p[e], kv.p[e], q[1]);
+            q[2] = __ffma2_rn(__fmul2_rn(hv.p[e], kv.p[e]), w.p[e], q[2]);
+            q[3] = __ffma2_rn(uv.p[e], vv.p[e], q[3]);
+          }
+          const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
+          m[4 * i] += (q[0].x + q[0].y) * a0 * a0;
+          m[4 * i + 1] += (q[1].x + q[1].y) * a1 * a1;
+          m[4 * i + 2] += (q[2].x + q[2].y) * a0 * a1;
+          m[4 * i + 3] += (q[3].x + q[3].y) * pow2(ks[HC][v]);
+        }
+      }
+      group_reduce_scatter<N, G>(m, lane);
+      // widened once more for the outputs: kept as fp32 through the reduction they do not fit in registers
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          again(h[i][v]);
+          again(k[i][v]);
+          again(u[i][v]);
+          again(hs[i][v]);
+          again(ks[i][v]);
+        }
+      }
+      const int c = p % HC;
+      float f[4];  // the sums of copy c
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        constexpr int kEach = N > G ? N / G : 1, kLanes = N > G ? 1 : G / N;  // values a lane, lanes a value
+        f[e] = __shfl_sync(0xffffffffu, m[e % kEach], first + (4 * c + e) / kEach * kLanes);
+      }
+      CopyGrad g = copy_grad(f[0], f[1], f[2], f[3], rd, a.g.eps, inv_sqrt_dim);
+      const uint32_t small = __ballot_sync(0xffffffffu, open && g.m < kSmallDot);
+      if (small != 0u) {  // sum(h w key) once more, in twice the precision, for the tokens that need it
+        Sum2 mine = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          Sum2 d = {0.f, 0.f};
+#pragma unroll
+          for (int v = 0; v < VECS; ++v) {
+            const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
+            Sum2 one = dot_part(widen_codes(h[i][v]), widen_codes(k[i][v]), weights(i, v));
+            one.hi = one.hi * a0 * a1;
+            one.lo = one.lo * a0 * a1;
+            d = add2(d, one);
+          }
+#pragma unroll
+          for (int off = G / 2; off >= 1; off /= 2)
+            d = add2(d, Sum2{__shfl_xor_sync(0xffffffffu, d.hi, off), __shfl_xor_sync(0xffffffffu, d.lo, off)});
+          if (i == c) mine = d;
+        }
+        const uint32_t lanes = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << first;
+        if ((small & lanes) != 0u) g = copy_grad(f[0], f[1], mine.hi + mine.lo, f[3], rd, a.g.eps, inv_sqrt_dim);
+      }
+      if (p < HC) scal[warp][sub][p] = make_float4(g.gate, g.c, -g.ea, -g.eb);
+    }
+    __syncwarp();
+    uint16_t* const dx = a.g.dx + row * HC * dim;
+    uint16_t* const dkv = a.g.dkv + row * (HC + 1) * dim;
+    if (open) {
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        if (!on[v]) continue;
+        Vec8 dv = {};
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          const float4 g = scal[warp][sub][i];  // gate, c, -e / A, -e / B
+          const Vec8 hv = widen_codes(h[i][v]), kv = widen_codes(k[i][v]), uv = widen8(u[i][v]), w = weights(i, v);
+          const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
+          // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
+          const float cwk = g.y * a1, eh = g.z * a0, cwh = g.y * a0, ek = g.w * a1, chk = g.y * a0 * a1;
+          Vec8 dh, dk;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            dh.p[e] = __ffma2_rn(__fmul2_rn(both(cwk), w.p[e]), kv.p[e], __ffma2_rn(both(eh), hv.p[e], uv.p[e]));
+            dk.p[e] = __ffma2_rn(__fmul2_rn(both(cwh), w.p[e]), hv.p[e], __fmul2_rn(both(ek), kv.p[e]));
+            dv.p[e] = __ffma2_rn(both(g.x), uv.p[e], dv.p[e]);
+            dw[i][v].p[e] = __ffma2_rn(both(chk), __fmul2_rn(hv.p[e], kv.p[e]), dw[i][v].p[e]);
+          }
+          st8(dx + i * dim + col[v], dh);
+          st8(dkv + i * dim + col[v], dk);
+        }
+        st8(dkv + HC * dim + col[v], dv);
+      }
+    } else if (in) {  // masked: dout passes through, whatever the checkpoints hold
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int v = 0; v < VECS; ++v) {
+        if (!on[v]) continue;
+#pragma unroll
+        for (int i = 0; i < HC; ++i) {
+          *reinterpret_cast<uint4*>(dx + i * dim + col[v]) = u[i][v];
+          *reinterpret_cast<uint4*>(dkv + i * dim + col[v]) = z;
+        }
+        *reinterpret_cast<uint4*>(dkv + HC * dim + col[v]) = z;
+      }
+    }
+    __syncwarp();  // the scalars have been read
+  }
+  // the CTA's sums: the tokens of a warp, then the warps in order
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < HC; ++i)
+#pragma unroll
+    for (int v = 0; v < VECS; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int off = G; off < 32; off *= 2) {
+          float2& d = dw[i][v].p[e];
+          d.x += __shfl_xor_sync(0xffffffffu, d.x, off);
+          d.y += __shfl_xor_sync(0xffffffffu, d.y, off);
+        }
+  for (int from = 0; from < kWarps; ++from) {
+    if (warp == from && sub == 0) {
+#pragma unroll
+      for (int i = 0; i < HC; ++i)
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+          if (!on[v]) continue;
+          float2* to = reinterpret_cast<float2*>(w_of + i * dim + col[v]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = from == 0 ? dw[i][v].p[e] : __fadd2_rn(to[e], dw[i][v].p[e]);
+        }
+    }
+    __syncthreads();
+  }
+  float4* to = reinterpret_cast<float4*>(part + (int64_t)blockIdx.x * HC * dim);
+  for (int i = threadIdx.x; i < HC * dim / 4; i += kThreads) to[i] = w_smem[i];
+}
+
+template <int HC, int VECS, int G>
+cudaError_t launch_rows(const GateGrad8Args& a, float* part, int parts, cudaStream_t s) {
+  return launch_pdl(gate_grad8_rows_kernel<HC, VECS, G>, dim3((unsigned)parts), dim3(kThreads), (size_t)HC * a.g.dim * 4, s, a,
+                    1.0f / (float)a.g.dim, (float)(1.0 / sqrt((double)a.g.dim)), part);
+}
+
+template <int HC, int VECS>
+cudaError_t launch_vecs(const GateGrad8Args& a, float* part, int parts, cudaStream_t s) {
+  if constexpr (VECS == 1) {
+    if (a.g.dim <= 64) return launch_rows<HC, 1, 8>(a, part, parts, s);
+    if (a.g.dim <= 128) return launch_rows<HC, 1, 16>(a, part, parts, s);
+  }
+  return launch_rows<HC, VECS, 32>(a, part, parts, s);
+}
+
+template <int HC>
+cudaError_t launch_copies(const GateGrad8Args& a, float* part, int parts, cudaStream_t s) {
+  if (a.g.dim <= 256) return launch_vecs<HC, 1>(a, part, parts, s);
+  if constexpr (HC <= 4)
+    if (a.g.dim <= 512) return launch_vecs<HC, 2>(a, part, parts, s);
+  if constexpr (HC <= 2)
+    if (a.g.dim <= 1024) return launch_vecs<HC, 4>(a, part, parts, s);
+  return cudaErrorInvalidValue;
+}
+
+int vectors_of(int32_t dim) { return dim <= 256 ? 1 : dim <= 512 ? 2 : 4; }
+
+}  // namespace
+
+// CTAs, each with its part of the weights' gradients; 0: the rows are not narrow enough
+int gate_grad8_rows_parts(int64_t T, int32_t hc, int32_t dim) {
+  if (dim > 1024 || hc * vectors_of(dim) > 8) return 0;
+  const int tokens = kWarps * (dim <= 64 ? 4 : dim <= 128 ? 2 : 1);
+  return (int)std::min<int64_t>((T + tokens - 1) / tokens, (int64_t)kSms * resident_ctas(hc * vectors_of(dim)));
+}
+
+cudaError_t launch_gate_grad8_rows(const GateGrad8Args& a, float* part, int parts, cudaStream_t s) {
+  switch (a.g.hc) {
+    case 1: return launch_copies<1>(a, part, parts, s);
+    case 2: return launch_copies<2>(a, part, parts, s);
+    case 4: return launch_copies<4>(a, part, parts, s);
+    case 8: return launch_copies<8>(a, part, parts, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace engram
