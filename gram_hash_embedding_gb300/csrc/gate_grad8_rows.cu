@@ -4,8 +4,12 @@
 //
 // Design: G lanes take a token, each VECS vectors of 8 columns of every copy; its sums stay in those lanes (a reduction that
 // scatters, then four shuffles that bring each copy's sums together), lane c forms the scalars of copy c, and the token's
-// rows never leave registers. No barriers but the warp's; many warps an SM cover one another's loads. The weights' product
-// lies in shared memory, the weights' gradients in registers until the end, where a CTA adds them up in a fixed order.
+// rows stay in registers as they came. No barriers but the warp's; many warps an SM cover one another's loads. The weights'
+// product lies in shared memory, the weights' gradients in registers until the end, where a CTA adds them up in a fixed order.
+// Rows of more vectors than that leave too few warps an SM, and gate_grad8.cu is as fast (4 x 512, 2 x 1,024).
+// Measured, 32,768 tokens (in brackets gate_grad8.cu, then the floor): 4 copies of 64, 128 and 256 columns 23, 40 and 63 us
+// (99, 94, 85; 11, 22, 43), 1 of 256, 512 and 1,024 23, 38 and 68 (40, 56, 80; 14, 27, 55), 2 of 512 67 (80; 47), 8 of 128 and
+// 256 97 and 141 (163, 152; 42, 83); 1,000 tokens of 4 x 256 12 (16). Bound by instructions and the loads' latency.
 #include <algorithm>
 #include <cstdint>
 
@@ -23,8 +27,9 @@ using namespace gate;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-// CTAs on an SM: what the registers of HC * VECS vectors allow
-constexpr int resident_ctas(int vectors) { return vectors == 1 ? 4 : vectors == 2 ? 3 : vectors <= 4 ? 2 : 1; }
+// CTAs on an SM: what the registers of HC * VECS vectors allow. With one or two the next token's loads are in flight while
+// one is worked on (32,768 of 1 x 512: 38 us, without 47); four with that took 168 registers and more time.
+constexpr int resident_ctas(int vectors) { return vectors == 1 ? 3 : vectors <= 4 ? 2 : 1; }
 
 // Sums of N values over the G lanes of a token: lane p ends with the totals of values p N / G and after (N >= G), or of value
 // p / (G / N), in s[0] and after.
@@ -84,35 +89,66 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
   };
   Vec8 dw[HC][VECS] = {};
   const int64_t stride = (int64_t)gridDim.x * kWarps * kTokens;
-  for (int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * kTokens; base < T; base += stride) {
+  struct Token {
+    uint4 u[HC][VECS];
+    uint2 h[HC][VECS], k[HC + 1][VECS];
+    uint32_t hs[HC][VECS], ks[HC + 1][VECS];
+    bool open;
+  };
+  auto load = [&](Token& r, int64_t base) {
     const int64_t t = base + sub;
-    const bool in = t < T, open = in && (a.g.mask == nullptr || a.g.mask[t] != 0);
-    const int64_t row = in ? t : base;
-    uint4 u[HC][VECS] = {};
-    uint2 h[HC][VECS] = {}, k[HC + 1][VECS] = {};
-    uint32_t hs[HC][VECS] = {}, ks[HC + 1][VECS] = {};
+    const bool in = t < T;
+    r.open = in && (a.g.mask == nullptr || a.g.mask[t] != 0);
+    const uint4 z4 = make_uint4(0u, 0u, 0u, 0u);
+    const uint2 z2 = make_uint2(0u, 0u);
 #pragma unroll
     for (int v = 0; v < VECS; ++v) {
-      if (in && on[v]) {
-        const uint16_t* from = a.g.dout + row * HC * dim + col[v];
+      const bool some = in && on[v], all = r.open && on[v];
+      const uint16_t* from = a.g.dout + t * HC * dim + col[v];
+      const uint8_t *x = a.x + t * HC * dim + col[v], *kv = a.kv + t * (HC + 1) * dim + col[v];
+      const uint8_t *xs = a.xs + t * HC * n_blocks + block[v], *kvs = a.kvs + t * (HC + 1) * n_blocks + block[v];
+      // A branch around a vector's loads where there is one; with more of them a choice at each load, which keeps the loads
+      // of all vectors in flight together (32,768 of 1 x 1,024: 67 us, with branches 79; of 8 x 128 101, with a branch 85).
+      if constexpr (VECS == 1) {
 #pragma unroll
-        for (int i = 0; i < HC; ++i) u[i][v] = __ldg(reinterpret_cast<const uint4*>(from + i * dim));
-      }
-      if (open && on[v]) {
-        const uint8_t *x = a.x + row * HC * dim + col[v], *kv = a.kv + row * (HC + 1) * dim + col[v];
-        const uint8_t *xs = a.xs + row * HC * n_blocks + block[v], *kvs = a.kvs + row * (HC + 1) * n_blocks + block[v];
+        for (int i = 0; i <= HC; ++i) {
+          if (i < HC) r.u[i][v] = z4, r.h[i][v] = z2, r.hs[i][v] = 0u;
+          r.k[i][v] = z2, r.ks[i][v] = 0u;
+        }
+        if (some) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i) r.u[i][v] = __ldg(reinterpret_cast<const uint4*>(from + i * dim));
+        }
+        if (all) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i) {
+            r.h[i][v] = __ldg(reinterpret_cast<const uint2*>(x + i * dim));
+            r.hs[i][v] = __ldg(xs + i * n_blocks);
+          }
+#pragma unroll
+          for (int i = 0; i <= HC; ++i) {
+            r.k[i][v] = __ldg(reinterpret_cast<const uint2*>(kv + i * dim));
+            r.ks[i][v] = __ldg(kvs + i * n_blocks);
+          }
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          h[i][v] = __ldg(reinterpret_cast<const uint2*>(x + i * dim));
-          hs[i][v] = __ldg(xs + i * n_blocks);
+          r.u[i][v] = some ? __ldg(reinterpret_cast<const uint4*>(from + i * dim)) : z4;
+          r.h[i][v] = all ? __ldg(reinterpret_cast<const uint2*>(x + i * dim)) : z2;
+          r.hs[i][v] = all ? __ldg(xs + i * n_blocks) : 0u;
         }
 #pragma unroll
         for (int i = 0; i <= HC; ++i) {
-          k[i][v] = __ldg(reinterpret_cast<const uint2*>(kv + i * dim));
-          ks[i][v] = __ldg(kvs + i * n_blocks);
+          r.k[i][v] = all ? __ldg(reinterpret_cast<const uint2*>(kv + i * dim)) : z2;
+          r.ks[i][v] = all ? __ldg(kvs + i * n_blocks) : 0u;
         }
       }
     }
+  };
+  auto step = [&](Token& r, int64_t base) {
+    const int64_t t = base + sub;
+    const bool in = t < T, open = r.open;
     if (__any_sync(0xffffffffu, open)) {
       float m[N];
 #pragma unroll
@@ -121,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
         for (int e = 0; e < 4; ++e) m[4 * i + e] = 0.f;
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
-          const Vec8 hv = widen_codes(h[i][v]), kv = widen_codes(k[i][v]), vv = widen_codes(k[HC][v]), uv = widen8(u[i][v]);
+          const Vec8 hv = widen_codes(r.h[i][v]), kv = widen_codes(r.k[i][v]);
+          const Vec8 vv = widen_codes(r.k[HC][v]), uv = widen8(r.u[i][v]);
           const Vec8 w = weights(i, v);
           float2 q[4] = {};
 #pragma unroll
@@ -131,11 +168,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
             q[2] = __ffma2_rn(__fmul2_rn(hv.p[e], kv.p[e]), w.p[e], q[2]);
             q[3] = __ffma2_rn(uv.p[e], vv.p[e], q[3]);
           }
-          const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
+          const float a0 = pow2(r.hs[i][v]), a1 = pow2(r.ks[i][v]);
           m[4 * i] += (q[0].x + q[0].y) * a0 * a0;
           m[4 * i + 1] += (q[1].x + q[1].y) * a1 * a1;
           m[4 * i + 2] += (q[2].x + q[2].y) * a0 * a1;
-          m[4 * i + 3] += (q[3].x + q[3].y) * pow2(ks[HC][v]);
+          m[4 * i + 3] += (q[3].x + q[3].y) * pow2(r.ks[HC][v]);
         }
       }
       group_reduce_scatter<N, G>(m, lane);
@@ -144,11 +181,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
       for (int v = 0; v < VECS; ++v) {
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          again(h[i][v]);
-          again(k[i][v]);
-          again(u[i][v]);
-          again(hs[i][v]);
-          again(ks[i][v]);
+          again(r.h[i][v]);
+          again(r.k[i][v]);
+          again(r.u[i][v]);
+          again(r.hs[i][v]);
+          again(r.ks[i][v]);
         }
       }
       const int c = p % HC;
@@ -167,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
           Sum2 d = {0.f, 0.f};
 #pragma unroll
           for (int v = 0; v < VECS; ++v) {
-            const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
-            Sum2 one = dot_part(widen_codes(h[i][v]), widen_codes(k[i][v]), weights(i, v));
+            const float a0 = pow2(r.hs[i][v]), a1 = pow2(r.ks[i][v]);
+            Sum2 one = dot_part(widen_codes(r.h[i][v]), widen_codes(r.k[i][v]), weights(i, v));
             one.hi = one.hi * a0 * a1;
             one.lo = one.lo * a0 * a1;
             d = add2(d, one);
@@ -184,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
       if (p < HC) scal[warp][sub][p] = make_float4(g.gate, g.c, -g.ea, -g.eb);
     }
     __syncwarp();
-    uint16_t* const dx = a.g.dx + row * HC * dim;
-    uint16_t* const dkv = a.g.dkv + row * (HC + 1) * dim;
+    uint16_t* const dx = a.g.dx + t * HC * dim;
+    uint16_t* const dkv = a.g.dkv + t * (HC + 1) * dim;
     if (open) {
 #pragma unroll
       for (int v = 0; v < VECS; ++v) {
@@ -194,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
           const float4 g = scal[warp][sub][i];  // gate, c, -e / A, -e / B
-          const Vec8 hv = widen_codes(h[i][v]), kv = widen_codes(k[i][v]), uv = widen8(u[i][v]), w = weights(i, v);
-          const float a0 = pow2(hs[i][v]), a1 = pow2(ks[i][v]);
+          const Vec8 hv = widen_codes(r.h[i][v]), kv = widen_codes(r.k[i][v]), uv = widen8(r.u[i][v]), w = weights(i, v);
+          const float a0 = pow2(r.hs[i][v]), a1 = pow2(r.ks[i][v]);
           // the factors of w k and of h in dh, of w h and of k in dk, and of h k in the weights' sums
           const float cwk = g.y * a1, eh = g.z * a0, cwh = g.y * a0, ek = g.w * a1, chk = g.y * a0 * a1;
           Vec8 dh, dk;
@@ -218,13 +255,33 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(HC* VECS))
         if (!on[v]) continue;
 #pragma unroll
         for (int i = 0; i < HC; ++i) {
-          *reinterpret_cast<uint4*>(dx + i * dim + col[v]) = u[i][v];
+          *reinterpret_cast<uint4*>(dx + i * dim + col[v]) = r.u[i][v];
           *reinterpret_cast<uint4*>(dkv + i * dim + col[v]) = z;
         }
         *reinterpret_cast<uint4*>(dkv + HC * dim + col[v]) = z;
       }
     }
     __syncwarp();  // the scalars have been read
+  };
+  int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * kTokens;
+  if constexpr (HC * VECS <= 2) {
+    Token one, two;
+    if (base < T) load(one, base);
+    while (base < T) {
+      load(two, base + stride);
+      step(one, base);
+      base += stride;
+      if (base >= T) break;
+      load(one, base + stride);
+      step(two, base);
+      base += stride;
+    }
+  } else {
+    for (; base < T; base += stride) {
+      Token one;
+      load(one, base);
+      step(one, base);
+    }
   }
   // the CTA's sums: the tokens of a warp, then the warps in order
   __syncthreads();
@@ -276,9 +333,9 @@ cudaError_t launch_vecs(const GateGrad8Args& a, float* part, int parts, cudaStre
 template <int HC>
 cudaError_t launch_copies(const GateGrad8Args& a, float* part, int parts, cudaStream_t s) {
   if (a.g.dim <= 256) return launch_vecs<HC, 1>(a, part, parts, s);
-  if constexpr (HC <= 4)
-    if (a.g.dim <= 512) return launch_vecs<HC, 2>(a, part, parts, s);
   if constexpr (HC <= 2)
+    if (a.g.dim <= 512) return launch_vecs<HC, 2>(a, part, parts, s);
+  if constexpr (HC == 1)
     if (a.g.dim <= 1024) return launch_vecs<HC, 4>(a, part, parts, s);
   return cudaErrorInvalidValue;
 }
@@ -289,7 +346,7 @@ int vectors_of(int32_t dim) { return dim <= 256 ? 1 : dim <= 512 ? 2 : 4; }
 
 // CTAs, each with its part of the weights' gradients; 0: the rows are not narrow enough
 int gate_grad8_rows_parts(int64_t T, int32_t hc, int32_t dim) {
-  if (dim > 1024 || hc * vectors_of(dim) > 8) return 0;
+  if (dim > 1024 || (dim > 256 && hc * vectors_of(dim) > 4)) return 0;
   const int tokens = kWarps * (dim <= 64 ? 4 : dim <= 128 ? 2 : 1);
   return (int)std::min<int64_t>((T + tokens - 1) / tokens, (int64_t)kSms * resident_ctas(hc * vectors_of(dim)));
 }
