@@ -8,15 +8,17 @@
 // 434. So the chain is cut in two and runs over two tokens at a time, with warps of their own for what the chain waits for:
 //   - the threads form the sums of token i + 1 and send them, then write the outputs of token i, whose scalars are ready;
 //   - a warp gathers a token's sums and forms its scalars while the others work;
-//   - a warp starts the copies of the tokens ahead and puts their scales, widened, and their mask beside them (loaded by
-//     the threads that use them, a token or two ahead, they cost 40 registers and their latency).
+//   - a warp (or the same, see shape_of) starts the copies of the tokens ahead and puts their scales, widened, and their
+//     mask beside them (loaded by the threads that use them, a token or two ahead, they cost 40 registers and their latency).
 // They meet on mbarriers; nothing waits for all threads of a CTA. A block's scale is one power of two for all 8 values of a
 // thread's row, so it goes into the sums and the scalars instead of the values: it changes no rounding there.
-// Measured: 16,384 of 4 x 5,120 435 us (the floor; with the scalars' and the copies' work in one warp and scales loaded by
-// the owners 506), 4,096 of 8 x 5,120 256 (floor 208), 16,384 of 1 x 5,120 160 (136), 8,192 of 4 x 2,048 102 (87). Wide rows
+// Measured: 16,384 of 4 x 5,120 434 us (the floor; with the scalars' and the copies' work in one warp and scales loaded by
+// the owners 506), 4,096 of 8 x 5,120 256 (floor 208), 16,384 of 1 x 5,120 164 (136), 8,192 of 4 x 2,048 102 (87). Wide rows
 // are bound by DRAM. With one or two copies a token takes 1.5 us or more whatever its width, the pace of the copying warp and
-// of the exchange, and the bf16 form is faster at some widths (16,384 of 2 x 5,120: 330 for 296). Three or four tokens in the
-// chain at a time, more stages, and two groups of threads of one copy each were no faster there.
+// of the exchange, and the bf16 form is faster at some widths (16,384 of 2 x 5,120: 343 for 296). Three or four tokens in the
+// chain at a time, more stages, and two groups of threads of one copy each were no faster there. Narrow rows: see
+// gate_grad8_rows.cu. (The setup of both control roles stands before their loops, in this order: with the scalars' first, in
+// branches of their own, the compiler's code took 518 us for the 434.)
 //
 // What may be written while another role, or another CTA of the cluster, still reads (tokens here are open ones, c their
 // number): a thread sends sums c + 2 after it has seen the scalars of c, which need the sums c of every CTA, which these sent
@@ -53,8 +55,9 @@ __host__ __device__ constexpr int blocks_of(int nv, int cs, int block) { return 
 
 // HC copies in CG groups of threads, HC / CG copies each of the same columns (8 copies in one thread leave too few threads
 // on an SM). WHOLE: a CTA has whole rows, which lie together: three copies a token instead of 3 HC + 1.
-// stages: tokens in shared memory. withhold: the token whose sums the cluster's first CTA does not send (the test hook).
-template <int HC, int CG, bool WHOLE>
+// stages: tokens in shared memory. kControl: warps for scalars and copies, one each or one for both. withhold: the token
+// whose sums the cluster's first CTA does not send (the test hook).
+template <int HC, int CG, bool WHOLE, int kControl>
 __global__ void __launch_bounds__(max_owners(HC) + 64)
     gate_grad8_kernel(const GateGrad8Args a, const float rd, const float inv_sqrt_dim, const int nv, const int ctas,
                       const int stages, float* __restrict__ part, unsigned int* __restrict__ status,
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
   const int dim = a.g.dim;
   const int64_t T = a.g.T;
   const int cs = WHOLE ? 1 : ctas;
-  const int tid = threadIdx.x, owners = blockDim.x - 64, lane = tid & 31, warp = tid >> 5, nw = owners >> 5;
+  const int tid = threadIdx.x, owners = blockDim.x - 32 * kControl, lane = tid & 31, warp = tid >> 5, nw = owners >> 5;
   const int cluster = blockIdx.x / cs, nc = gridDim.x / cs;
   const uint32_t rank = blockIdx.x % cs;
   const int per_group = owners / CG, group = CG == 1 ? 0 : min(tid / per_group, CG - 1), gt = tid - group * per_group;
@@ -116,7 +119,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
   if (cs > 1) tc::cluster_sync();  // every CTA's barriers exist before another CTA sends to them
   else __syncthreads();
 
-  if (warp == nw + 1) {
+  if (warp >= nw) {
     // ------------------------------------------------------------ copies
     uint32_t last = ~0u;  // bit s: the parity of the stage's last copies
     // The fewer instructions a token takes here the better: this warp sets the pace of narrow rows. What a lane copies lies a
@@ -180,12 +183,13 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
     }
     const int64_t step_x = (int64_t)nc * HC * n_blocks, step_kv = (int64_t)nc * (HC + 1) * n_blocks;
     uint32_t coming = mask_of(cluster);  // asked for a token before it is needed
+    int64_t ct = cluster;                // the next token whose copies start
     int s = 0;
     uint32_t pass = 0;  // how often the ring has gone round
     const uint32_t stage_bytes = 16 * stage_vecs, dst0 = tc::smem_u32(smem) + dst;
-    for (int64_t t = cluster; t < T; t += nc) {
+    auto fetch = [&]() {
       const bool open = coming != 0;
-      coming = mask_of(t + nc);
+      coming = mask_of(ct + nc);
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (j < nj) {
@@ -194,7 +198,10 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
         }
       }
       if (pass > 0) wait(kEmpty + s, (pass - 1) & 1);
-      if (__any_sync(0xffffffffu, dead)) break;  // the same for all lanes
+      if (__any_sync(0xffffffffu, dead)) {  // the same for all lanes
+        ct = T;
+        return;
+      }
       const uint32_t b = bar(kFull + s);
       // (bytes may arrive before they are expected: the phase ends with lane 0's arrival at the earliest)
       if (lane < (open ? kCopies : kDouts)) copy_row(dst0 + s * stage_bytes, src, bytes, b);
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
           if (j < nj && lane + 32 * j < units) store(s, to[j], early[j]);
-        for (int u = lane + 32 * kAhead; u < units; u += 32) store(s, to_of(u), load(from_of(t, u)));
+        for (int u = lane + 32 * kAhead; u < units; u += 32) store(s, to_of(u), load(from_of(ct, u)));
       }
       if (lane == 0) open_in[s] = open;
       __syncwarp();
@@ -213,18 +220,14 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
         s = 0;
         ++pass;
       }
-    }
-    if (dead && lane == 0)  // copies may still be on their way into this CTA's memory
-      for (int s = 0; s < stages; ++s)
-        if (cluster + (int64_t)s * nc < T) tc::mbar_wait(bar(kFull + s), (last >> s) & 1, nullptr);
-    __syncwarp();
-  } else if (warp == nw) {
+      ct += nc;
+    };
     // ------------------------------------------------------------ scalars
     uint32_t c = 0, c2 = 0;  // open tokens, and those whose sums were formed once more
-    uint32_t open = mask_of(cluster), coming = mask_of(cluster + nc);
-    for (int64_t t = cluster; t < T; t += nc) {
+    uint32_t sopen = mask_of(cluster), scoming = mask_of(cluster + nc);
+    auto scalars = [&](int64_t t) {
       const uint32_t then = mask_of(t + 2 * (int64_t)nc);
-      if (open != 0) {
+      if (sopen != 0) {
         const uint32_t b = c & 1;
         if (!WHOLE && lane == 0 && !dead)
           tc::mbar_arrive_expect_tx(bar(kSums + (c & 3)), (uint32_t)(cs * nw * M * 4));
@@ -266,9 +269,27 @@ __global__ void __launch_bounds__(max_owners(HC) + 64)
         }
         ++c;
       }
-      open = coming;
-      coming = then;
+      sopen = scoming;
+      scoming = then;
+    };
+    // ------------------------------------------------------------ in two warps, or in one
+    if (kControl == 2) {
+      if (warp == nw) {
+        for (int64_t t = cluster; t < T; t += nc) scalars(t);
+      } else {
+        while (ct < T) fetch();
+      }
+    } else {
+      for (int i = 0; i < stages && ct < T; ++i) fetch();
+      for (int64_t t = cluster; t < T; t += nc) {
+        scalars(t);
+        if (t != cluster && ct < T) fetch();  // into the stage of the token before, once its outputs are written
+      }
     }
+    if (dead && lane == 0 && (kControl == 1 || warp > nw))  // copies may still be on their way into this CTA's memory
+      for (int s = 0; s < stages; ++s)
+        if (cluster + (int64_t)s * nc < T) tc::mbar_wait(bar(kFull + s), (last >> s) & 1, nullptr);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ owners of columns
     const bool on = gt < cnt;
@@ -498,6 +519,7 @@ constexpr int resident_threads(int hc) { return hc == 1 ? 768 : hc == 2 ? 640 : 
 
 struct Shape {
   int cs, cg, nv, owners, stages;  // CTAs per cluster, groups of copies, vectors and column-owning threads per CTA
+  int control;                     // warps beside these
   int64_t smem, clusters;
 };
 
@@ -507,6 +529,7 @@ struct Shape {
 Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   Shape s;
   const int nvec = dim / 8;
+  s.control = 2;
   int32_t of = 32;  // the smallest blocks, so that what the workspace holds does not depend on them
   auto set = [&](int cs, int cg, int stages) {
     s.cs = cs;
@@ -528,7 +551,7 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   // CTAs resident on an SM, by shared memory and registers
   auto resident = [&]() {
     return std::max<int64_t>(
-        1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / (s.owners + 64)));
+        1, std::min<int64_t>((kMaxSmem + 1024) / (s.smem + 1024), resident_threads(hc) / (s.owners + 32 * s.control)));
   };
   if (!set(cs, cg, 3)) {
     if (!set(cs, 1, 3)) set(cs, 1, 2);  // 8 copies of more than 12,000 columns or so
@@ -536,6 +559,16 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
     const int64_t columns = s.nv * resident();
     set(cs * 2, cg, 3);
     if (s.nv * resident() * 5 < columns * 7) set(cs, cg, 3);
+  }
+  // One warp for scalars and copies where that lets more CTAs on an SM, half as many again with two copies, and there are
+  // tokens to keep them busy (32,768 of 4 x 1,040: 245 us, with two warps 350; of 4 x 512 112 and 123; of 2 x 2,304 267 and
+  // 397; but of 2 x 640, five CTAs for four, 104 and 95, and with one copy always more: that warp is the pace there). Not with
+  // two stages: a token's copies would wait for scalars that wait for sums which need them.
+  if ((hc == 2 || hc == 4) && s.stages >= 3) {
+    const int64_t two = resident();
+    s.control = 1;
+    const int64_t one = resident();
+    if ((hc == 4 ? one <= two : 2 * one < 3 * two) || T < 4 * kSms * two) s.control = 2;
   }
   const int64_t fit = resident();
   of = block;
@@ -549,13 +582,13 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   return s;
 }
 
-template <int HC, int CG, bool WHOLE>
-cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
-                         cudaStream_t s) {
-  constexpr auto kern = gate_grad8_kernel<HC, CG, WHOLE>;
+template <int HC, int CG, bool WHOLE, int CONTROL>
+cudaError_t launch_control(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
+                           cudaStream_t s) {
+  constexpr auto kern = gate_grad8_kernel<HC, CG, WHOLE, CONTROL>;
   cudaError_t e = allow_smem<kern>((int)sh.smem);
   if (e != cudaSuccess) return e;
-  const int threads = sh.owners + 64;
+  const int threads = sh.owners + 32 * CONTROL;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -591,6 +624,14 @@ cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, i
   cfg.gridDim = dim3((unsigned)(clusters * sh.cs));
   return cudaLaunchKernelEx(&cfg, kern, a, 1.0f / (float)a.g.dim, (float)(1.0 / sqrt((double)a.g.dim)), sh.nv, sh.cs,
                             sh.stages, part, status, withhold);
+}
+
+template <int HC, int CG, bool WHOLE>
+cudaError_t launch_shape(const GateGrad8Args& a, const Shape& sh, float* part, int* parts, int64_t withhold,
+                         cudaStream_t s) {
+  if constexpr (HC == 2 || HC == 4)
+    if (sh.control == 1) return launch_control<HC, CG, WHOLE, 1>(a, sh, part, parts, withhold, s);
+  return launch_control<HC, CG, WHOLE, 2>(a, sh, part, parts, withhold, s);
 }
 
 template <int HC, int CG>

@@ -196,3 +196,24 @@ def test_scales_at_any_address(T, hc, dim, block):
             moved.append(room[off:off + s.numel()].view(s.shape))
         got = _run8((xq[0], moved[0]), (kq[0], moved[1]), back, block)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,hc,dim,block", [(3000, 4, 272, 32), (2600, 4, 512, 64), (1800, 4, 1040, 32), (1300, 4, 1280, 128),
+                                            (1900, 2, 1040, 64), (1000, 2, 2304, 32), (1800, 2, 10240, 128)])
+def test_scalars_and_copies_in_one_warp(T, hc, dim, block):
+    rng = np.random.default_rng(T + dim)
+    args = G._inputs(rng, T, hc, dim)
+    args[5] = torch.from_numpy(np.repeat(rng.random(-(-T // 40)) < 0.8, 40)[:T] ^ (rng.random(T) < 0.1))
+    xq, kq, back = _checkpoints(args, block)
+    got = _run8(xq, kq, back, block)
+    G._check(back, got, f"T={T} hc={hc} dim={dim}")
+    assert all(torch.equal(a, b) for a, b in zip(got, _run8(xq, kq, back, block)))
+
+
+@pytest.mark.parametrize("T,hc,dim", [(1800, 4, 1040), (1000, 2, 2304)])
+def test_small_dots_with_one_warp(T, hc, dim):
+    test_small_dots(T, hc, dim)
+
+
+def test_withheld_sums_with_one_warp():
+    test_withheld_sums_time_out_and_the_next_call_is_right(1800, 4, 1040)
