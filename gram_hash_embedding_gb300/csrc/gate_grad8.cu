@@ -523,9 +523,9 @@ struct Shape {
   int64_t smem, clusters;
 };
 
-// As in gate_grad.cu: the smallest cluster (with one exception) whose CTAs hold their columns in registers and three
-// stages of shared memory, more CTAs a token when there are too few tokens for every SM; then as many stages, up to
-// kMaxStages, as cost no CTA its place on an SM.
+// As in gate_grad.cu, but with clusters of 1, 2, 3, 4, 6 or 8: the smallest (with one exception) whose CTAs hold their
+// columns in registers and three stages of shared memory, more CTAs a token when there are too few tokens for every SM; then
+// as many stages, up to kMaxStages, as cost no CTA its place on an SM.
 Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   Shape s;
   const int nvec = dim / 8;
@@ -546,8 +546,10 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   };
   const int cg = hc == 8 ? 2 : 1;
   int cs = 1;
-  while (cs < 8 && !set(cs, cg, 3)) cs *= 2;
-  while (cs < 8 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
+  // (16,384 of 4 x 6,144 in clusters of three 655 us, of four 794; 4,096 of 8 x 7,168 in six 416, in eight 552; but 8,192 of
+  // 1 x 16,384 in three 495, in four 348)
+  while (cs < 8 && !set(cs, cg, 3)) cs += hc == 1 ? cs : cs < 4 ? 1 : 2;
+  while (cs <= 4 && T * cs * 2 <= kSms && nvec / (cs * 2) >= 64) cs *= 2;
   // CTAs resident on an SM, by shared memory and registers
   auto resident = [&]() {
     return std::max<int64_t>(
@@ -555,7 +557,7 @@ Shape shape_of(int64_t T, int32_t hc, int32_t dim, int32_t block) {
   };
   if (!set(cs, cg, 3)) {
     if (!set(cs, 1, 3)) set(cs, 1, 2);  // 8 copies of more than 12,000 columns or so
-  } else if (cs < 8) {
+  } else if (cs <= 4) {
     const int64_t columns = s.nv * resident();
     set(cs * 2, cg, 3);
     if (s.nv * resident() * 5 < columns * 7) set(cs, cg, 3);

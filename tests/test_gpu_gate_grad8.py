@@ -217,3 +217,13 @@ def test_small_dots_with_one_warp(T, hc, dim):
 
 def test_withheld_sums_with_one_warp():
     test_withheld_sums_time_out_and_the_next_call_is_right(1800, 4, 1040)
+
+
+@pytest.mark.parametrize("T,hc,dim", [(400, 4, 6144), (300, 4, 12288), (200, 8, 3584), (150, 8, 7168), (400, 2, 10240),
+                                      (300, 1, 12288)])
+def test_rows_of_three_and_six_ctas(T, hc, dim):
+    args = G._inputs(np.random.default_rng(T + dim), T, hc, dim)
+    xq, kq, back = _checkpoints(args, 64)
+    got = _run8(xq, kq, back, 64)
+    G._check(back, got, f"T={T} hc={hc} dim={dim}")
+    assert all(torch.equal(a, b) for a, b in zip(got, _run8(xq, kq, back, 64)))
